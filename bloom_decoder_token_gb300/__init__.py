@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -72,6 +72,11 @@ class KVC(C.Structure):
                 ("host_buf", P), ("host_bytes", C.c_size_t), ("offload_from", I32)]
 
 
+class KV8C(C.Structure):
+    _fields_ = [("k", P), ("v", P), ("k_scale", P), ("v_scale", P), ("codes", I32),
+                ("batch", I32), ("n_kv", I32), ("max_seq", I32), ("d", I32)]
+
+
 _SIGS = {
     "bloom_kv_bytes": (C.c_size_t, [C.POINTER(Config), I32, I32]),
     "bloom_create": (I32, [C.POINTER(Config), C.POINTER(WeightsC), C.POINTER(P)]),
@@ -104,6 +109,11 @@ _SIGS = {
     "bloom_op_attn_decode": (I32, [P, P, P, P, P, I32, I32, I32, I32, I32, I32, P, P]),
     "bloom_op_lmhead_argmax": (I32, [P, P, I32, I32, I32, P, P, P]),
     "bloom_op_sample": (I32, [P, I32, I32, C.c_int64, P, P, P, P, P]),
+    "bloom_op_logprobs": (I32, [P, I32, I32, C.c_int64, P, I32, P, P, I32, P, P, P]),
+    "bloom_op_kv8_write": (I32, [P, P, P, P, P, I32, P, P, P, P, P]),
+    "bloom_op_kv8_read": (I32, [P, P, P, P, P, I32, P, P, P, P]),
+    "bloom_op_attn_decode_kv8": (I32, [P, P, P, P, P, I32, I32, P, P, C.c_size_t, P, P]),
+    "bloom_op_attn_decode_kv8_workspace": (C.c_size_t, [P, I32, I32]),
     "bloom_op_lmhead_argmax_noalloc": (I32, [P, P, I32, I32, I32, P, P, P]),
 }
 EXPORTS = tuple(_SIGS)
@@ -446,3 +456,188 @@ def op_lmhead_argmax_noalloc(x, emb, logits: bool = True, stream=None):
     check(lib().bloom_op_lmhead_argmax_noalloc(_p(x), _p(emb), M, V, K, _p(tok), _p(lg),
                                                _stream(stream)))
     return tok, lg
+
+
+def _bad(msg: str):
+    raise BloomError(1, msg)
+
+
+def _dev(name: str, t, dtype, shape, device):
+    """A contiguous device tensor of that type and shape, or an error; its address."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        _bad(f"{name}: contiguous {dtype} {tuple(shape)} on {device} expected, "
+             f"got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _rows(name: str, t, dtype, shape, device):
+    return None if t is None else _dev(name, t, dtype, shape, device)
+
+
+class _Here:
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *_):
+        return False
+
+
+_HERE_NOW = _Here()
+
+
+def _on(device, stream):
+    """Context of a call on `stream` (None: the device's current one): its device
+    and the stream are current inside, so what is allocated there belongs to it."""
+    if device.type != "cuda":
+        _bad(f"tensors on a CUDA device expected, got {device}")
+    if stream is None:
+        if device.index == torch.cuda.current_device():
+            return _HERE_NOW
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        _bad(f"stream on {stream.device}, tensors on {device}")
+    return torch.cuda.stream(stream)
+
+
+KV8_BLOCK = 32
+_KV8_CODES = {torch.int8: 0, torch.float8_e4m3fn: 1}
+
+
+class KV8(NamedTuple):
+    """An 8-bit KV cache of one layer: value = code * scale.
+
+    k, v: codes, int8 or float8_e4m3fn [B][n_kv][S][d], d 64 or 128; k_scale,
+    v_scale: float32 [B][n_kv][ceil(S / 32)], one for every 32 slots of a head."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+    @classmethod
+    def empty(cls, batch: int, n_kv: int, max_seq: int, d: int, codes=torch.int8, device="cuda"):
+        """A cache of zeros; codes torch.int8 or torch.float8_e4m3fn."""
+        kv = [torch.zeros(batch, n_kv, max_seq, d, dtype=codes, device=device) for _ in range(2)]
+        sc = [torch.zeros(batch, n_kv, -(-max_seq // KV8_BLOCK), device=device) for _ in range(2)]
+        return cls(*kv, *sc)
+
+    def c(self) -> KV8C:
+        """The C descriptor (bloom_kv8), after checking types, shapes and devices."""
+        k, dev = self.k, self.k.device
+        codes = _KV8_CODES.get(k.dtype)
+        if codes is None or k.dim() != 4:
+            _bad(f"cache codes: int8 or float8_e4m3fn [B][n][S][d] expected, got {k.dtype} "
+                 f"{tuple(k.shape)}")
+        B, n, S, d = k.shape
+        sc = (B, n, -(-S // KV8_BLOCK))
+        return KV8C(_dev("k", k, k.dtype, k.shape, dev), _dev("v", self.v, k.dtype, k.shape, dev),
+                    _dev("k_scale", self.k_scale, torch.float32, sc, dev),
+                    _dev("v_scale", self.v_scale, torch.float32, sc, dev), codes, B, n, S, d)
+
+
+def _kv8_values(name: str, t, shape, device):
+    """(address, strides) of a bf16 [B][T][n][d] view whose d elements lie together."""
+    if t.dtype is not torch.bfloat16 or t.shape != shape or t.device != device or t.stride(3) != 1:
+        _bad(f"{name}: bfloat16 {tuple(shape)} on {device} with unit last stride expected, "
+             f"got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
+    st = [0 if n == 1 else s for n, s in zip(shape, t.stride()[:3])]
+    return t.data_ptr(), (C.c_int64 * 3)(*st)
+
+
+def op_kv8_write(kv: KV8, k, v, start, count=None, mask=None, flag=None, stream=None):
+    """Quantise new keys and values k, v (bf16 [B][T][n][d], any strides that are
+    multiples of 8) into slots start[b] + t of the cache, in place: start int32
+    [B], -1 for an idle row; count int32 [B], tokens of each row (None: T); mask
+    uint8 [B][T], 0 for pad slots; flag int32 [1] that errors are recorded in."""
+    c, dev = kv.c(), kv.k.device
+    if k.dim() != 4:
+        _bad(f"k: [B][T][n][d] expected, got {tuple(k.shape)}")
+    B, T = c.batch, k.shape[1]
+    shape = (B, T, c.n_kv, c.d)
+    kp, ks = _kv8_values("k", k, shape, dev)
+    vp, vs = _kv8_values("v", v, shape, dev)
+    with _on(dev, stream):
+        check(lib().bloom_op_kv8_write(
+            C.byref(c), kp, ks, vp, vs, T, _dev("start", start, torch.int32, (B,), dev),
+            _rows("count", count, torch.int32, (B,), dev),
+            _rows("mask", mask, torch.uint8, (B, T), dev),
+            _rows("flag", flag, torch.int32, (1,), dev), _stream(stream)))
+
+
+def op_kv8_read(kv: KV8, start, T: int, count=None, k=None, v=None, flag=None, stream=None):
+    """Slots start[b] + t, t < T, of the cache as bf16 (k, v) [B][T][n][d]: views
+    given, or new tensors.  Zeros for idle rows (start -1), for t >= count[b]
+    and beyond the cache."""
+    c, dev = kv.c(), kv.k.device
+    if T < 0:
+        _bad(f"T={T}")
+    shape = (c.batch, T, c.n_kv, c.d)
+    with _on(dev, stream):
+        if k is None:
+            k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        if v is None:
+            v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        kp, ks = _kv8_values("k", k, shape, dev)
+        vp, vs = _kv8_values("v", v, shape, dev)
+        check(lib().bloom_op_kv8_read(
+            C.byref(c), kp, ks, vp, vs, T, _dev("start", start, torch.int32, (c.batch,), dev),
+            _rows("count", count, torch.int32, (c.batch,), dev),
+            _rows("flag", flag, torch.int32, (1,), dev), _stream(stream)))
+    return k, v
+
+
+def op_attn_decode_kv8(q, kv: KV8, pos, slopes, lens, o=None, workspace=None, flag=None,
+                       stream=None):
+    """Decode attention over an 8-bit cache: q bf16 [B][T][n][d] for the last T
+    tokens of every row (or [B][n][d], T = 1), whose keys are in the cache; pos
+    int32 [B][S], -1 masked; slopes float32 [n] or None; lens int32 [B], slots
+    filled.  Returns o bf16 [B][T][n * d] (or [B][n * d])."""
+    c, dev = kv.c(), kv.k.device
+    if q.dim() not in (3, 4):
+        _bad(f"q: [B][T][n][d] or [B][n][d] expected, got {tuple(q.shape)}")
+    T, n = (1, q.shape[1]) if q.dim() == 3 else q.shape[1:3]
+    qshape = (c.batch, n, c.d) if q.dim() == 3 else (c.batch, T, n, c.d)
+    oshape = (c.batch, n * c.d) if q.dim() == 3 else (c.batch, T, n * c.d)
+    qp = _dev("q", q, torch.bfloat16, qshape, dev)
+    with _on(dev, stream):
+        L = lib()
+        if o is None:
+            o = torch.empty(oshape, dtype=torch.bfloat16, device=dev)
+        need = L.bloom_op_attn_decode_kv8_workspace(C.byref(c), T, n)
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        check(L.bloom_op_attn_decode_kv8(
+            C.byref(c), qp, _dev("pos", pos, torch.int32, (c.batch, c.max_seq), dev),
+            _rows("slopes", slopes, torch.float32, (n,), dev),
+            _dev("lens", lens, torch.int32, (c.batch,), dev), T, n,
+            _dev("o", o, torch.bfloat16, oshape, dev), _p(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size(),
+            _rows("flag", flag, torch.int32, (1,), dev), _stream(stream)))
+    return o
+
+
+def op_logprobs(logits, tokens=None, top: int = 0, stream=None):
+    """Log probabilities of tokens (int32 [B][J] or [B]; -1: none) under softmax of
+    float32 logits [B][V] (rows may be strided), the rows' entropies, and their
+    `top` <= 32 most probable tokens: (logp like tokens or None, entropy [B],
+    top_ids int32 [B][top], top_logp [B][top])."""
+    dev = logits.device
+    if logits.dtype is not torch.float32 or logits.dim() != 2 or logits.stride(1) != 1:
+        _bad(f"logits: float32 [B][V] with unit last stride expected, got {logits.dtype} "
+             f"{tuple(logits.shape)}, strides {logits.stride()}")
+    B, V = logits.shape
+    if not 0 <= top <= 32:
+        _bad(f"top={top}: 0 to 32 expected")
+    J, tp, logp = 0, None, None
+    if tokens is not None:
+        J = tokens.shape[1] if tokens.dim() == 2 else 1
+        tp = _dev("tokens", tokens, torch.int32, (B, J) if tokens.dim() == 2 else (B,), dev)
+    with _on(dev, stream):
+        if tokens is not None:
+            logp = torch.empty(tokens.shape, device=dev)
+        entropy = torch.empty(B, device=dev)
+        ids = torch.empty(B, top, dtype=torch.int32, device=dev)
+        lps = torch.empty(B, top, device=dev)
+        check(lib().bloom_op_logprobs(logits.data_ptr(), B, V, logits.stride(0) if B > 1 else V, tp,
+                                      J, _p(logp), _p(entropy), top, _p(ids), _p(lps),
+                                      _stream(stream)))
+    return logp, entropy, ids, lps

@@ -1418,6 +1418,174 @@ extern "C" bloom_status bloom_op_sample(const float *logits, int32_t B, int32_t 
     return BLOOM_OK;
 }
 
+extern "C" bloom_status bloom_op_logprobs(const float *logits, int32_t B, int32_t V, int64_t ld,
+                                          const int32_t *tokens, int32_t J, float *logp,
+                                          float *entropy, int32_t top, int32_t *top_ids,
+                                          float *top_logp, void *stream) {
+    g_pdl = true;
+    if (B < 0 || B > 65535 || V < 1 || ld < V || J < 0 || top < 0 || top > kLpMaxTop)
+        return fail(BLOOM_E_INVALID, "B=%d V=%d ld=%lld J=%d top=%d", B, V, (long long)ld, J, top);
+    if (B == 0) return BLOOM_OK;
+    if (!logits || (J && (!tokens || !logp)) || (top && (!top_ids || !top_logp)))
+        return fail(BLOOM_E_INVALID, "null argument");
+    LogprobsArgs a;
+    a.logits = logits;
+    a.ld = ld;
+    a.B = B;
+    a.V = V;
+    a.J = J;
+    a.top = top;
+    a.tokens = tokens;
+    a.logp = logp;
+    a.entropy = entropy;
+    a.top_ids = top_ids;
+    a.top_logp = top_logp;
+    CK(launch_logprobs(a, (cudaStream_t)stream));
+    return BLOOM_OK;
+}
+
+static bloom_status check_kv8(const bloom_kv8 *kv) {
+    if (!kv || !kv->k || !kv->v || !kv->k_scale || !kv->v_scale)
+        return fail(BLOOM_E_INVALID, "null argument");
+    if (kv->codes != BLOOM_KV8_INT8 && kv->codes != BLOOM_KV8_E4M3)
+        return fail(BLOOM_E_INVALID, "codes=%d", kv->codes);
+    if (kv->d != 64 && kv->d != 128) return fail(BLOOM_E_UNSUPPORTED, "d=%d", kv->d);
+    if (kv->batch < 1 || kv->batch > 65535 || kv->n_kv < 1 || kv->n_kv > 65535 || kv->max_seq < 1 ||
+        kv->max_seq > (1 << 30))
+        return fail(BLOOM_E_INVALID, "batch=%d n_kv=%d max_seq=%d", kv->batch, kv->n_kv, kv->max_seq);
+    if (!aligned16(kv->k) || !aligned16(kv->v))
+        return fail(BLOOM_E_INVALID, "codes must be 16-byte aligned");
+    return BLOOM_OK;
+}
+
+// The arguments that the write and the read share: a tile is 32 tokens of a
+// (row, head), at most one more than T / 32 rounded up.
+static bloom_status check_kv8_io(const bloom_kv8 *kv, const void *k, const int64_t *ks,
+                                 const void *v, const int64_t *vs, int32_t T,
+                                 const int32_t *start) {
+    bloom_status st = check_kv8(kv);
+    if (st) return st;
+    if (T < 0 || T > kv->max_seq) return fail(BLOOM_E_INVALID, "T=%d max_seq=%d", T, kv->max_seq);
+    if (T == 0) return BLOOM_OK;
+    if (!k || !v || !ks || !vs || !start) return fail(BLOOM_E_INVALID, "null argument");
+    if (!aligned16(k) || !aligned16(v)) return fail(BLOOM_E_INVALID, "k and v must be 16-byte aligned");
+    for (int i = 0; i < 3; ++i)
+        if (ks[i] % 8 || vs[i] % 8 || ks[i] < 0 || vs[i] < 0)
+            return fail(BLOOM_E_INVALID, "strides must be multiples of 8 elements, not negative");
+    if ((long long)kv->batch * kv->n_kv * (T / 32 + 2) > (1ll << 31))
+        return fail(BLOOM_E_INVALID, "batch=%d n_kv=%d T=%d: too many tiles for a launch", kv->batch,
+                    kv->n_kv, T);
+    return BLOOM_OK;
+}
+
+template <typename A>
+static void kv8_io_args(A &a, const bloom_kv8 *kv, const int64_t *ks, const int64_t *vs, int32_t T,
+                        const int32_t *start, const int32_t *count, int32_t *flag) {
+    a.ks = kv->k_scale;
+    a.vs = kv->v_scale;
+    a.B = kv->batch;
+    a.n = kv->n_kv;
+    a.max_seq = kv->max_seq;
+    a.blocks = (kv->max_seq + BLOOM_KV8_BLOCK - 1) / BLOOM_KV8_BLOCK;
+    a.T = T;
+    for (int i = 0; i < 3; ++i) {
+        a.stride[0][i] = ks[i];
+        a.stride[1][i] = vs[i];
+    }
+    a.start = start;
+    a.count = count;
+    a.err = flag;
+}
+
+extern "C" bloom_status bloom_op_kv8_write(const bloom_kv8 *kv, const void *k,
+                                           const int64_t *k_stride, const void *v,
+                                           const int64_t *v_stride, int32_t T,
+                                           const int32_t *start, const int32_t *count,
+                                           const uint8_t *mask, int32_t *flag, void *stream) {
+    g_pdl = true;
+    bloom_status st = check_kv8_io(kv, k, k_stride, v, v_stride, T, start);
+    if (st || T == 0) return st;
+    Kv8WriteArgs a;
+    kv8_io_args(a, kv, k_stride, v_stride, T, start, count, flag);
+    a.kc = (uint8_t *)kv->k;
+    a.vc = (uint8_t *)kv->v;
+    a.k = (const uint16_t *)k;
+    a.v = (const uint16_t *)v;
+    a.mask = mask;
+    CK(launch_kv8_write(a, kv->d, kv->codes == BLOOM_KV8_E4M3, (cudaStream_t)stream));
+    return BLOOM_OK;
+}
+
+extern "C" bloom_status bloom_op_kv8_read(const bloom_kv8 *kv, void *k, const int64_t *k_stride,
+                                          void *v, const int64_t *v_stride, int32_t T,
+                                          const int32_t *start, const int32_t *count, int32_t *flag,
+                                          void *stream) {
+    g_pdl = true;
+    bloom_status st = check_kv8_io(kv, k, k_stride, v, v_stride, T, start);
+    if (st || T == 0) return st;
+    Kv8ReadArgs a;
+    kv8_io_args(a, kv, k_stride, v_stride, T, start, count, flag);
+    a.kc = (const uint8_t *)kv->k;
+    a.vc = (const uint8_t *)kv->v;
+    a.k = (uint16_t *)k;
+    a.v = (uint16_t *)v;
+    CK(launch_kv8_read(a, kv->d, kv->codes == BLOOM_KV8_E4M3, (cudaStream_t)stream));
+    return BLOOM_OK;
+}
+
+static bloom_status check_attn_kv8(const bloom_kv8 *kv, int32_t T, int32_t n_head) {
+    bloom_status st = check_kv8(kv);
+    if (st) return st;
+    if (n_head < 1 || n_head % kv->n_kv)
+        return fail(BLOOM_E_INVALID, "n_head=%d is not a multiple of n_kv=%d", n_head, kv->n_kv);
+    if (T < 1) return fail(BLOOM_E_INVALID, "T=%d", T);
+    if (T > kKv8MaxT || n_head > 65535)
+        return fail(BLOOM_E_UNSUPPORTED, "T=%d n_head=%d (at most %d tokens)", T, n_head, kKv8MaxT);
+    return BLOOM_OK;
+}
+
+extern "C" size_t bloom_op_attn_decode_kv8_workspace(const bloom_kv8 *kv, int32_t T,
+                                                     int32_t n_head) {
+    if (check_attn_kv8(kv, T, n_head)) return 0;
+    return 0;
+}
+
+extern "C" bloom_status bloom_op_attn_decode_kv8(const bloom_kv8 *kv, const void *q,
+                                                 const int32_t *pos, const float *slopes,
+                                                 const int32_t *lens, int32_t T, int32_t n_head,
+                                                 void *o, void *workspace, size_t workspace_bytes,
+                                                 int32_t *flag, void *stream) {
+    g_pdl = true;
+    bloom_status st = check_attn_kv8(kv, T, n_head);
+    if (st) return st;
+    if (!q || !pos || !lens || !o) return fail(BLOOM_E_INVALID, "null argument");
+    if (!aligned16(q) || !aligned16(o) || !aligned16(workspace))
+        return fail(BLOOM_E_INVALID, "q, o and workspace must be 16-byte aligned");
+    const size_t need = bloom_op_attn_decode_kv8_workspace(kv, T, n_head);
+    if (need && (!workspace || workspace_bytes < need))
+        return fail(BLOOM_E_INVALID, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+    AttnKv8Args a;
+    a.q = (const uint16_t *)q;
+    a.kc = (const uint8_t *)kv->k;
+    a.vc = (const uint8_t *)kv->v;
+    a.ks = kv->k_scale;
+    a.vs = kv->v_scale;
+    a.pos = pos;
+    a.slopes = slopes;
+    a.lens = lens;
+    a.B = kv->batch;
+    a.T = T;
+    a.n = n_head;
+    a.kv = kv->n_kv;
+    a.max_seq = kv->max_seq;
+    a.blocks = (kv->max_seq + BLOOM_KV8_BLOCK - 1) / BLOOM_KV8_BLOCK;
+    a.scale = (float)(1.0 / sqrt((double)kv->d));
+    a.o = (uint16_t *)o;
+    a.err = flag;
+    CK(launch_attn_kv8(a, kv->d, kv->codes == BLOOM_KV8_E4M3, (cudaStream_t)stream));
+    return BLOOM_OK;
+}
+
 extern "C" bloom_status bloom_decode_step_sampled(bloom_model *m, bloom_kv *kv,
                                                   const int32_t *next_tokens, int32_t *out_tokens,
                                                   float *logits, const float *temperature,

@@ -231,6 +231,62 @@ struct SampleArgs {
 };
 cudaError_t launch_sample(const SampleArgs &a, cudaStream_t s);
 
+// Log probabilities of given tokens, entropy and the top alternatives of B rows of
+// float32 logits (k_logprobs.cu); arrays as bloom_op_logprobs describes them.
+struct LogprobsArgs {
+    const float *logits = nullptr;
+    long long ld = 0;
+    int B = 0, V = 0, J = 0, top = 0;
+    const int32_t *tokens = nullptr;   // [B][J]
+    float *logp = nullptr;             // [B][J]
+    float *entropy = nullptr;          // [B] or null
+    int32_t *top_ids = nullptr;        // [B][top]
+    float *top_logp = nullptr;
+};
+constexpr int kLpMaxTop = 32;
+cudaError_t launch_logprobs(const LogprobsArgs &a, cudaStream_t s);
+
+// The 8-bit KV cache (kv8_ops.cuh): codes [B][n][max_seq][d], scales [B][n][blocks].
+// Strides of K (0) and V (1) values are elements from one row, token, head to the next.
+struct Kv8WriteArgs {
+    uint8_t *kc = nullptr, *vc = nullptr;
+    float *ks = nullptr, *vs = nullptr;
+    int B = 0, n = 0, max_seq = 0, blocks = 0, T = 0, tiles = 0;
+    const uint16_t *k = nullptr, *v = nullptr;   // bf16
+    long long stride[2][3] = {};
+    const int *start = nullptr, *count = nullptr;   // [B]; count null: T
+    const uint8_t *mask = nullptr;                  // [B][T] or null
+    int *err = nullptr;
+};
+cudaError_t launch_kv8_write(Kv8WriteArgs a, int d, int e4m3, cudaStream_t s);
+
+struct Kv8ReadArgs {
+    const uint8_t *kc = nullptr, *vc = nullptr;
+    const float *ks = nullptr, *vs = nullptr;
+    int B = 0, n = 0, max_seq = 0, blocks = 0, T = 0, tiles = 0;
+    uint16_t *k = nullptr, *v = nullptr;
+    long long stride[2][3] = {};
+    const int *start = nullptr, *count = nullptr;
+    int *err = nullptr;
+};
+cudaError_t launch_kv8_read(Kv8ReadArgs a, int d, int e4m3, cudaStream_t s);
+
+// Decode attention over the 8-bit cache (k_attn_kv8.cu).
+constexpr int kKv8MaxT = 32;        // new tokens a row
+struct AttnKv8Args {
+    const uint16_t *q = nullptr;                 // [B][T][n][d]
+    const uint8_t *kc = nullptr, *vc = nullptr;  // [B][kv][max_seq][d]
+    const float *ks = nullptr, *vs = nullptr;    // [B][kv][blocks]
+    const int *pos = nullptr;                    // [B][max_seq], -1 masked
+    const float *slopes = nullptr;               // [n] or null
+    const int *lens = nullptr;                   // [B]
+    int B = 0, T = 0, n = 0, kv = 0, max_seq = 0, blocks = 0;
+    float scale = 0.f;                           // 1 / sqrt(d)
+    uint16_t *o = nullptr;                       // [B][T][n][d]
+    int *err = nullptr;
+};
+cudaError_t launch_attn_kv8(const AttnKv8Args &a, int d, int e4m3, cudaStream_t s);
+
 struct AttnPrefillArgs {
     const uint16_t *q = nullptr;     // [B*T][n][d], prompt i's tokens at rows i*T ..
     const uint16_t *k = nullptr;     // [rows][n][max_seq][d] (the cache)

@@ -411,6 +411,103 @@ bloom_status bloom_op_sample(const float *logits, int32_t B, int32_t V, int64_t 
                              const float *temperature, const float *top_p, const float *u,
                              int32_t *out_tokens, void *stream);
 
+/* Log probabilities of given tokens, with entropy and top alternatives, of B rows
+ * of float32 logits (row b at logits + b * ld, ld >= V; device), natural
+ * logarithms of softmax(logits):
+ *   logp[b][j]  of tokens[b][j] (device int32 [B][J]); a token -1 (no token: an
+ *               idle row of a decode step) gets 0, any other value outside
+ *               [0, V) NaN;
+ *   entropy[b]  = -sum p log p, or NULL for none;
+ *   top_ids[b][i], top_logp[b][i], i < top: the tokens with the highest logits,
+ *               highest first, equal logits in index order.
+ * As in bloom_op_sample, NaN logits take no part, nor do -inf ones: their
+ * tokens' logp is -inf and they are never top alternatives; places left over
+ * get id -1 and -inf.  A row where nothing takes part has entropy 0.  +inf
+ * logits share the whole mass.  Sums are float32.  tokens / logp may be NULL
+ * with J = 0, top_ids / top_logp with top = 0.  BLOOM_E_INVALID for null
+ * pointers, B outside 0..65535, V < 1, ld < V, J < 0, top outside 0..32 (B = 0
+ * does nothing). */
+bloom_status bloom_op_logprobs(const float *logits, int32_t B, int32_t V, int64_t ld,
+                               const int32_t *tokens, int32_t J, float *logp, float *entropy,
+                               int32_t top, int32_t *top_ids, float *top_logp, void *stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit KV cache of one layer: codes with one float32 scale for every
+ * BLOOM_KV8_BLOCK slots of a (row, head), K and V apart; value = code * scale.
+ * Half the bytes of the bf16 cache for decode attention to read.
+ * ------------------------------------------------------------------------ */
+enum { BLOOM_KV8_INT8 = 0, BLOOM_KV8_E4M3 = 1 };
+#define BLOOM_KV8_BLOCK 32
+
+typedef struct {
+    void *k, *v;               /* codes [batch][n_kv][max_seq][d], 16-byte aligned, device */
+    float *k_scale, *v_scale;  /* [batch][n_kv][ceil(max_seq / BLOOM_KV8_BLOCK)], device */
+    int32_t codes;             /* BLOOM_KV8_INT8: -127..127; BLOOM_KV8_E4M3: finite e4m3 */
+    int32_t batch, n_kv, max_seq;
+    int32_t d;                 /* 64 or 128 */
+} bloom_kv8;
+
+/* `flag` of the three calls below: a device int32 word, or NULL, that a kernel
+ * ORs a bit of bloom_check_device into when it meets a bad value (2: a slot
+ * beyond the cache; 8: a bounded wait expired, the call's output is invalid). */
+
+/* Quantise new keys and values into the cache: token t of row b goes to slot
+ * start[b] + t, t < count[b] (count NULL: T; clamped to 0..T).  k and v: bf16,
+ * element (b, t, head, e) at b * stride[0] + t * stride[1] + head * stride[2] +
+ * e, strides in elements, multiples of 8, k_stride and v_stride HOST arrays of
+ * three (views of a fused QKV row, of [B][T][n][d] and of a bf16 cache's
+ * [B][n][S][d] all fit); k and v 16-byte aligned.  start, count: device int32
+ * [batch]; mask: device uint8 [batch][T] or NULL.
+ *  - A block's scale is the smallest power of two, 2^-126 at least, with
+ *    amax <= 127 * scale (int8) or 448 * scale (e4m3) over its tokens, 0 if all
+ *    are 0; codes are value / scale rounded half to even.
+ *  - A block that holds tokens already (slots below start[b]) keeps its scale
+ *    unless the new tokens need a larger one: then the codes it holds are
+ *    rounded again in the larger scale.  A block whose first slot is written
+ *    starts afresh, whatever it held.  So a cache need not be cleared, provided
+ *    each row is first written from a slot that is a multiple of 32.
+ *  - mask 0 (a pad slot): the token is stored as zeros and not looked at.
+ *  - start[b] < 0: row b is idle and left as it is, as are all slots that the
+ *    call does not name (but for that second rounding).  Tokens beyond max_seq
+ *    are dropped (flag 2).
+ *  - An infinity or NaN among a block's tokens makes its scale NaN: all of the
+ *    block reads as NaN until it is started afresh.
+ * The values must not overlap the cache.  T = 0 does nothing. */
+bloom_status bloom_op_kv8_write(const bloom_kv8 *kv, const void *k, const int64_t *k_stride,
+                                const void *v, const int64_t *v_stride, int32_t T,
+                                const int32_t *start, const int32_t *count, const uint8_t *mask,
+                                int32_t *flag, void *stream);
+
+/* Read slots start[b] + t, t < T, back as bf16 values (rounded half to even;
+ * exact for scales that bloom_op_kv8_write made) into k and v, addressed as in
+ * bloom_op_kv8_write.  Tokens t >= count[b], of idle rows (start[b] < 0) and
+ * beyond max_seq (flag 2) are written as 0. */
+bloom_status bloom_op_kv8_read(const bloom_kv8 *kv, void *k, const int64_t *k_stride, void *v,
+                               const int64_t *v_stride, int32_t T, const int32_t *start,
+                               const int32_t *count, int32_t *flag, void *stream);
+
+/* Decode attention over the cache for the last T tokens of every row (T = 1: a
+ * decode step; up to 32: drafted tokens checked at once; their keys and values
+ * are in the cache already).  q bf16 [batch][T][n_head][d]; query head j reads
+ * key head j / (n_head / n_kv); pos int32 [batch][max_seq] as in
+ * bloom_op_attn_decode (-1 = masked); slopes float [n_head], or NULL for no
+ * position term; lens device int32 [batch]: slots filled, the new tokens
+ * included.  Query t of row b sees slots [0, lens[b] - T + t]; one that sees
+ * nothing (lens[b] <= 0: an idle row; all masked) gets 0.  lens[b] > max_seq
+ * counts as max_seq (flag 2).  o bf16 [batch][T][n_head * d].  Masked slots and
+ * slots from lens on are never looked at: they may hold anything.  A block with
+ * a NaN scale makes every query that sees a slot of it NaN, in that head.
+ * workspace: device scratch of bloom_op_attn_decode_kv8_workspace() bytes (0:
+ * NULL will do), 16-byte aligned, contents immaterial; calls that may overlap on
+ * the GPU (other streams, graphs that may run at once) need one each. */
+bloom_status bloom_op_attn_decode_kv8(const bloom_kv8 *kv, const void *q, const int32_t *pos,
+                                      const float *slopes, const int32_t *lens, int32_t T,
+                                      int32_t n_head, void *o, void *workspace,
+                                      size_t workspace_bytes, int32_t *flag, void *stream);
+
+/* Bytes of that scratch; 0 also for arguments that the call refuses. */
+size_t bloom_op_attn_decode_kv8_workspace(const bloom_kv8 *kv, int32_t T, int32_t n_head);
+
 /* Tied LM head with fused argmax: logits[m][v] = x[m] . E[v]; out_tokens[m] =
  * lowest index of the row maximum of the float32 logits; out_logits may be
  * NULL.  x bf16 [M][K], E bf16 [V][K]. */
