@@ -1547,7 +1547,7 @@ static bloom_status check_attn_kv8(const bloom_kv8 *kv, int32_t T, int32_t n_hea
 extern "C" size_t bloom_op_attn_decode_kv8_workspace(const bloom_kv8 *kv, int32_t T,
                                                      int32_t n_head) {
     if (check_attn_kv8(kv, T, n_head)) return 0;
-    return 0;
+    return attn_kv8_workspace(n_head, kv->n_kv, T, kv->max_seq, kv->d, device_sms());
 }
 
 extern "C" bloom_status bloom_op_attn_decode_kv8(const bloom_kv8 *kv, const void *q,
@@ -1582,7 +1582,8 @@ extern "C" bloom_status bloom_op_attn_decode_kv8(const bloom_kv8 *kv, const void
     a.scale = (float)(1.0 / sqrt((double)kv->d));
     a.o = (uint16_t *)o;
     a.err = flag;
-    CK(launch_attn_kv8(a, kv->d, kv->codes == BLOOM_KV8_E4M3, (cudaStream_t)stream));
+    a.part = (float *)workspace;
+    CK(launch_attn_kv8(a, kv->d, kv->codes == BLOOM_KV8_E4M3, device_sms(), (cudaStream_t)stream));
     return BLOOM_OK;
 }
 

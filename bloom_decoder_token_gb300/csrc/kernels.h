@@ -284,8 +284,12 @@ struct AttnKv8Args {
     float scale = 0.f;                           // 1 / sqrt(d)
     uint16_t *o = nullptr;                       // [B][T][n][d]
     int *err = nullptr;
+    float *part = nullptr;                       // workspace: attn_kv8_workspace() bytes
+    int part_cols = 0;                           // set by the launch
 };
-cudaError_t launch_attn_kv8(const AttnKv8Args &a, int d, int e4m3, cudaStream_t s);
+constexpr int kAk8MaxPerSm = 4;                  // CTAs per SM that the workspace allows for
+size_t attn_kv8_workspace(int n, int kv, int T, int max_seq, int d, int sms);
+cudaError_t launch_attn_kv8(const AttnKv8Args &a, int d, int e4m3, int sms, cudaStream_t s);
 
 struct AttnPrefillArgs {
     const uint16_t *q = nullptr;     // [B*T][n][d], prompt i's tokens at rows i*T ..
