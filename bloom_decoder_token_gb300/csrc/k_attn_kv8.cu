@@ -23,14 +23,15 @@
 //    M + 14) with a running maximum M of its own, so that scales far apart cost
 //    nothing, rounded to f16 (relative 2^-11; the bf16 result rounds at 2^-8)
 //    and multiplied with exact codes into float32 accumulators.
-//  * Work is cut evenly whatever the lengths: the tiles (128 slots) of all rows and
-//    key heads are numbered in one sequence, and each of as many CTAs as are
-//    resident takes an equal run of it.  A (row, key head) that falls into
-//    several runs leaves partial results, which a second kernel joins in order.
-//  * Each warp takes 32 slots (one scale block) of a tile and keeps its own ring of
-//    stages ahead of it: two bulk copies (K, V) a stage, completing on an
-//    mbarrier, and positions and scales by cp.async.  No barrier of the block
-//    until a (row, key head) ends.
+//  * Work is cut evenly whatever the lengths: the scale blocks (32 slots) of all
+//    rows and key heads are numbered in one sequence, and each resident warp takes
+//    an equal run of it.  A (row, key head) of at most kAk8Short blocks is left
+//    whole; a longer one that falls into several runs leaves partial results,
+//    which a second kernel joins in order.
+//  * A warp keeps its own ring of stages ahead of it, one block each: two bulk copies
+//    (K, V), completing on an mbarrier, and by cp.async positions, scales and, at
+//    the first block of a (row, key head), its queries.  Warps never wait for
+//    one another.
 #include <atomic>
 #include <math.h>
 
@@ -42,8 +43,9 @@
 namespace bloom {
 
 constexpr int kAk8Warps = 4, kAk8Threads = 32 * kAk8Warps;
-constexpr int kAk8Tile = kAk8Warps * kKv8Block;   // slots per tile
-constexpr int kAk8Part = 4;                       // floats beside a partial's accumulator: m, M, l
+constexpr int kAk8Short = 8;      // blocks of a (row, key head) that is never cut
+constexpr int kAk8MinRun = 4;     // blocks a warp takes at least, while there are warps to spare
+constexpr int kAk8Part = 4;       // floats beside a partial's accumulator: m, M, l
 
 // ---- conversions of codes to f16 pairs
 __device__ __forceinline__ uint32_t ak8_s8x2(uint32_t biased, uint32_t sel) {
@@ -89,90 +91,105 @@ __device__ __forceinline__ float ak8_exp2(float x) {
 }
 __device__ __forceinline__ float ak8_finite(float m) { return m == -INFINITY ? 0.f : m; }
 
-// ---- where a tile number lies
+// ---- where a block number lies
 struct Ak8Rows {
     const int *lens;
     int B, max_seq, heads;   // heads: (key head, column chunk) pairs of a row
     __device__ __forceinline__ int len(int b) const { return max(0, min(lens[b], max_seq)); }
-    // tiles of one head of row b; at least one, so that every output is written
-    __device__ __forceinline__ int tiles(int b) const { return max(1, (len(b) + kAk8Tile - 1) / kAk8Tile); }
+    // blocks of one head of row b; at least one, so that every output is written
+    __device__ __forceinline__ int blocks(int b) const { return max(1, (len(b) + kKv8Block - 1) / kKv8Block); }
 };
-// Tiles per head of all rows together, and the row that holds tile number x (with
-// the number of its first tile), by the whole warp.
-__device__ __forceinline__ long long ak8_total(const Ak8Rows &r) {
+__device__ __forceinline__ long long ak8_total(const Ak8Rows &r) {   // by the whole warp
     const int lane = threadIdx.x & 31;
     int t = 0;
-    for (int b = lane; b < r.B; b += 32) t += r.tiles(b);
+    for (int b = lane; b < r.B; b += 32) t += r.blocks(b);
     return (long long)__reduce_add_sync(0xffffffffu, t) * r.heads;
 }
-__device__ __forceinline__ int ak8_find(const Ak8Rows &r, long long x, long long &first) {
-    const int lane = threadIdx.x & 31;
-    long long before = 0;
-    for (int b0 = 0; b0 < r.B; b0 += 32) {
-        const int mine = b0 + lane < r.B ? r.tiles(b0 + lane) : 0;
-        int sum = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += y;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, before + (long long)sum * r.heads > x);
-        if (past) {
-            const int src = __ffs(past) - 1;
-            first = before + (long long)__shfl_sync(0xffffffffu, sum - mine, src) * r.heads;
-            return b0 + src;
-        }
-        before += (long long)__shfl_sync(0xffffffffu, sum, 31) * r.heads;
-    }
-    first = before;
-    return r.B;
-}
-struct Ak8Cursor {   // a tile: row, head, tile of that head
-    int b, head, tile, len, tiles;
+struct Ak8Cursor {   // a block: its row, head, place in that head; the row's length and blocks a head
+    int b, head, blk, len, blocks;
+    // block number x < total, by the whole warp
     __device__ __forceinline__ void at(const Ak8Rows &r, long long x) {
-        long long first;
-        b = ak8_find(r, x, first);
+        const int lane = threadIdx.x & 31;
+        long long before = 0;
+        for (int b0 = 0;; b0 += 32) {
+            const int mine = b0 + lane < r.B ? r.blocks(b0 + lane) : 0;
+            int sum = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += y;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, before + (long long)sum * r.heads > x);
+            if (past || b0 + 32 >= r.B) {
+                const int src = past ? __ffs(past) - 1 : 31;
+                b = b0 + src;
+                x -= before + (long long)__shfl_sync(0xffffffffu, sum - mine, src) * r.heads;
+                break;
+            }
+            before += (long long)__shfl_sync(0xffffffffu, sum, 31) * r.heads;
+        }
         row(r);
-        head = (int)((x - first) / tiles);
-        tile = (int)((x - first) % tiles);
+        head = (int)(x / blocks);
+        blk = (int)(x - (long long)head * blocks);
     }
     __device__ __forceinline__ void row(const Ak8Rows &r) {
         len = b < r.B ? r.len(b) : 0;
-        tiles = b < r.B ? r.tiles(b) : 1;
+        blocks = b < r.B ? r.blocks(b) : 1;
     }
     __device__ __forceinline__ void next(const Ak8Rows &r) {
-        if (++tile < tiles) return;
-        tile = 0;
+        if (++blk < blocks) return;
+        blk = 0;
         if (++head < r.heads) return;
         head = 0;
         ++b;
         row(r);
     }
 };
+// Run k of R: blocks [ak8_cut(k), ak8_cut(k + 1)), equal shares, but that a short
+// (row, head) belongs to the run that its last block falls into.
+__device__ __forceinline__ long long ak8_cut(const Ak8Rows &r, long long k, long long R, long long total,
+                                             Ak8Cursor &c) {
+    long long x = k * total / R;
+    if (x >= total) return total;
+    c.at(r, x);
+    if (c.blocks <= kAk8Short) {
+        x -= c.blk;
+        c.blk = 0;
+    }
+    return x;
+}
+__device__ __forceinline__ long long ak8_runs(long long total, int warps) {
+    return min((long long)warps, (total + kAk8MinRun - 1) / kAk8MinRun);
+}
 
-template <int D, int NT>
-struct Ak8Smem {
-    static constexpr int kStages = 256 / D;
-    uint8_t kv[kAk8Warps][kStages][2][kKv8Block * D];
-    int pos[kAk8Warps][kStages][kKv8Block];
-    float scale[kAk8Warps][kStages][2];
-    uint64_t bar[kAk8Warps][kStages];
-    float stat[kAk8Warps][8 * NT][3];   // m, M, l of a warp
-    // then accumulators [kAk8Warps][columns][D]
+// One stage of a warp's ring, in bytes: K, V, the queries of `cols` columns, positions
+// of the block, positions of the row's last 32 slots, the two scales.
+template <int D>
+struct Ak8Stage {
+    static constexpr int kCount = 256 / D, kQ = 2 * kKv8Block * D;
+    __host__ __device__ static constexpr int pos(int cols) { return kQ + cols * D * 2; }
+    __host__ __device__ static constexpr int bytes(int cols) { return (pos(cols) + 256 + 16 + 127) / 128 * 128; }
+    // the ring of a CTA and an mbarrier per stage
+    __host__ __device__ static constexpr int smem(int cols) { return kAk8Warps * kCount * (bytes(cols) + 8); }
 };
+
+__device__ __forceinline__ void ak8_async4(const void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc_smem(dst)), "l"(src) : "memory");
+}
 
 // Columns of a chunk: query c = t * group + i of a key head, t the token, i the query head.
 template <int D, bool E4M3, int NT>
 __global__ void __launch_bounds__(kAk8Threads, NT == 1 ? 3 : 2) attn_kv8_kernel(const AttnKv8Args a) {
     constexpr int HS = D / 64, VW = D / 32, W = 8 * NT;   // K segments of 16 bytes a lane; V words a key
-    using Smem = Ak8Smem<D, NT>;
-    constexpr int ST = Smem::kStages;
+    using Stage = Ak8Stage<D>;
+    constexpr int ST = Stage::kCount;
     extern __shared__ __align__(128) unsigned char ak8_raw[];
-    Smem &sm = *reinterpret_cast<Smem *>(ak8_raw);
-    float *sm_acc = reinterpret_cast<float *>(ak8_raw + sizeof(Smem));
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, t4 = lane & 3;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
+    const int cols = a.part_cols, sbytes = Stage::bytes(cols);
+    unsigned char *ring = ak8_raw + w * ST * sbytes;
+    uint64_t *bar = reinterpret_cast<uint64_t *>(ak8_raw + kAk8Warps * ST * sbytes) + w * ST;
     if (lane == 0) {
-        for (int i = 0; i < ST; ++i) tc_mbar_init(&sm.bar[w][i], 1);
+        for (int i = 0; i < ST; ++i) tc_mbar_init(&bar[i], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncwarp();
@@ -181,47 +198,59 @@ __global__ void __launch_bounds__(kAk8Threads, NT == 1 ? 3 : 2) attn_kv8_kernel(
 
     const int group = a.n / a.kv, C = group * a.T, chunks = (C + W - 1) / W;
     const Ak8Rows rows{a.lens, a.B, a.max_seq, a.kv * chunks};
-    const long long total = ak8_total(rows), G = min((long long)gridDim.x, total);   // no run is empty
-    if (blockIdx.x >= G) return;
-    const long long x0 = blockIdx.x * total / G, x1 = (blockIdx.x + 1) * total / G;
     if (a.err && blockIdx.x == 0)
-        for (int b = tid; b < a.B; b += kAk8Threads)
+        for (int b = threadIdx.x; b < a.B; b += kAk8Threads)
             if (a.lens[b] > a.max_seq) atomicOr(a.err, kErrSlot);
+    const long long total = ak8_total(rows), R = ak8_runs(total, (int)gridDim.x * kAk8Warps);
+    const int run = w * (int)gridDim.x + (int)blockIdx.x;   // runs spread over the CTAs first
+    if (run >= R) return;
     Ak8Cursor cur, ahead;
-    cur.at(rows, x0);
+    const long long x1 = ak8_cut(rows, run + 1, R, total, ahead);
+    const long long x0 = ak8_cut(rows, run, R, total, cur);
+    if (x0 >= x1) return;
     ahead = cur;
 
-    // the next tile with keys for this warp into stage `st`; one cp.async group, empty at the end
+    // block xa of the run into stage `st`; one cp.async group, empty beyond the end
     long long xa = x0;
     auto issue = [&](int st) {
-        for (; xa < x1; ++xa, ahead.next(rows)) {
-            const int base = ahead.tile * kAk8Tile + w * kKv8Block, n = min(kKv8Block, ahead.len - base);
-            if (n <= 0) continue;
-            const long long bh = (long long)ahead.b * a.kv + ahead.head / chunks;
+        if (xa < x1) {
+            unsigned char *stage = ring + st * sbytes;
+            const int base = ahead.blk * kKv8Block, n = min(kKv8Block, ahead.len - base);   // n <= 0: no keys
+            const int h = ahead.head / chunks;
+            const long long bh = (long long)ahead.b * a.kv + h;
             if (lane == 0) {
-                const uint32_t bar = tc_smem(&sm.bar[w][st]);
-                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(2 * n * D) : "memory");
+                const uint32_t br = tc_smem(&bar[st]);
+                if (n > 0) {
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(br), "r"(2 * n * D) : "memory");
 #pragma unroll
-                for (int v = 0; v < 2; ++v)
-                    asm volatile(
-                        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                            tc_smem(&sm.kv[w][st][v][0])),
-                        "l"((v ? a.vc : a.kc) + (bh * a.max_seq + base) * D), "r"(n * D), "r"(bar)
-                        : "memory");
+                    for (int v = 0; v < 2; ++v)
+                        asm volatile(
+                            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                                tc_smem(stage + v * kKv8Block * D)),
+                            "l"((v ? a.vc : a.kc) + (bh * a.max_seq + base) * D), "r"(n * D), "r"(br)
+                            : "memory");
+                } else {
+                    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(br) : "memory");
+                }
             }
-            if (lane < n)
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc_smem(&sm.pos[w][st][lane])),
-                             "l"(a.pos + (long long)ahead.b * a.max_seq + base + lane)
-                             : "memory");
-            else
-                sm.pos[w][st][lane] = -1;
-            if (lane < 2)
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc_smem(&sm.scale[w][st][lane])),
-                             "l"((lane ? a.vs : a.ks) + bh * a.blocks + base / kKv8Block)
-                             : "memory");
+            int *pos = reinterpret_cast<int *>(stage + Stage::pos(cols));
+            const int *rowpos = a.pos + (long long)ahead.b * a.max_seq;
+            if (lane < n) ak8_async4(pos + lane, rowpos + base + lane);
+            else pos[lane] = -1;
+            if (lane < 2 && n > 0)
+                ak8_async4(pos + 64 + lane, (lane ? a.vs : a.ks) + bh * a.blocks + base / kKv8Block);
+            if (xa == x0 || ahead.blk == 0) {   // the first block of a (row, head) in this run
+                if (ahead.len - 1 - lane >= 0) ak8_async4(pos + 32 + lane, rowpos + ahead.len - 1 - lane);
+                else pos[32 + lane] = -1;
+                const int c0 = ahead.head % chunks * W, nc = min(W, C - c0);
+                for (int i = lane; i < nc * (D / 8); i += 32) {
+                    const int c = c0 + i / (D / 8), e = i % (D / 8) * 8;
+                    cp_async16(stage + Stage::kQ + (i / (D / 8) * D + e) * 2,
+                               a.q + (((long long)ahead.b * a.T + c / group) * a.n + h * group + c % group) * D + e);
+                }
+            }
             ++xa;
             ahead.next(rows);
-            break;
         }
         cp_async_commit();
     };
@@ -232,35 +261,39 @@ __global__ void __launch_bounds__(kAk8Threads, NT == 1 ? 3 : 2) attn_kv8_kernel(
     uint32_t qf[NT][D / 16][2];
     float qinv[NT][2], slope[NT][2], m[NT][2], M[NT][2], l[NT][2], acc[D / 16][NT][4];
     int lim[NT][2];                // slots that a column sees
-    int ref = 0, ref_row = -1, st = 0;
+    int ref = 0, st = 0;
     uint32_t parity = 0;
-    long long seg0 = x0;           // first tile of the current (row, head) in this run
+    long long seg0 = x0;           // first block of the current (row, head) in this run
     bool fresh = true;
     for (long long x = x0; x < x1; ++x) {
         const int chunk = cur.head % chunks, h = cur.head / chunks;
         const int ncol = min(W, C - chunk * W);
+        unsigned char *stage = ring + st * sbytes;
+        const int *pos = reinterpret_cast<const int *>(stage + Stage::pos(cols));
+        // ---- the block's copies
+        cp_async_wait<ST - 1>();
+        const bool ok = __all_sync(0xffffffffu, tc_mbar_wait(&bar[st], parity, 0));
+        if (!ok) {   // report; a second bounded wait, so that no copy lands later; the block is skipped
+            if (a.err) atomicOr(a.err, kErrTimeout);
+            tc_mbar_wait(&bar[st], parity, kTcWaitNs);
+        }
+        __syncwarp();
         if (fresh) {
             fresh = false;
             seg0 = x;
-            if (ref_row != cur.b) {
-                ref_row = cur.b;
-                ref = -1;
-                const int *pos = a.pos + (long long)cur.b * a.max_seq;
-                for (int k0 = cur.len; k0 > 0 && ref < 0; k0 -= 32)
-                    ref = __reduce_max_sync(0xffffffffu, k0 - 1 - lane >= 0 ? pos[k0 - 1 - lane] : -1);
-            }
+            ref = __reduce_max_sync(0xffffffffu, pos[32 + lane]);
+            for (int k0 = cur.len - 32; k0 > 0 && ref < 0; k0 -= 32)   // pads alone at the row's end
+                ref = __reduce_max_sync(0xffffffffu, k0 - 1 - lane >= 0 ? a.pos[(long long)cur.b * a.max_seq + k0 - 1 - lane] : -1);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 // B fragments: column g, elements 64 s + 16 t4 + 4 u + (0, 1 | 2, 3)
-                const int c = chunk * W + nt * 8 + g;
                 uint4 raw[HS][2];
                 uint32_t amax = 0;
 #pragma unroll
                 for (int s = 0; s < HS; ++s) {
                     raw[s][0] = raw[s][1] = make_uint4(0u, 0u, 0u, 0u);
-                    if (c < C) {
-                        const uint4 *q = reinterpret_cast<const uint4 *>(
-                            a.q + (((long long)cur.b * a.T + c / group) * a.n + h * group + c % group) * D + 64 * s + 16 * t4);
+                    if (nt * 8 + g < ncol) {
+                        const uint4 *q = reinterpret_cast<const uint4 *>(stage + Stage::kQ + ((nt * 8 + g) * D + 64 * s + 16 * t4) * 2);
                         raw[s][0] = q[0];
                         raw[s][1] = q[1];
                     }
@@ -303,17 +336,9 @@ __global__ void __launch_bounds__(kAk8Threads, NT == 1 ? 3 : 2) attn_kv8_kernel(
                     for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.f;
             }
         }
-        const int base = cur.tile * kAk8Tile + w * kKv8Block;
-        if (cur.len > base) {   // this warp has keys in the tile: the stage's turn
-            cp_async_wait<ST - 1>();
-            bool ok = tc_mbar_wait(&sm.bar[w][st], parity, 0);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) {   // report; a second bounded wait, so that no copy lands later; the block is skipped
-                if (a.err) atomicOr(a.err, kErrTimeout);
-                tc_mbar_wait(&sm.bar[w][st], parity, kTcWaitNs);
-            }
-            __syncwarp();
-            const uint8_t *ks = &sm.kv[w][st][0][0], *vs = &sm.kv[w][st][1][0];
+        const int base = cur.blk * kKv8Block;
+        {
+            const uint8_t *ks = stage, *vs = stage + kKv8Block * D;
             // ---- scores: 16 slots x columns per mt
             float s[2][NT][4];
 #pragma unroll
@@ -341,7 +366,7 @@ __global__ void __launch_bounds__(kAk8Threads, NT == 1 ? 3 : 2) attn_kv8_kernel(
                     }
             }
             // ---- softmax
-            const float kscale = sm.scale[w][st][0], vscale = sm.scale[w][st][1];
+            const float kscale = reinterpret_cast<const float *>(pos)[64], vscale = reinterpret_cast<const float *>(pos)[65];
             // vscale = mant * 2^ev
             const uint32_t vb = __float_as_uint(vscale), vexp = (vb >> 23) & 255u;
             const float ev = vexp == 255u ? 0.f : vexp == 0u ? -126.f : (float)((int)vexp - 127);
@@ -350,7 +375,7 @@ __global__ void __launch_bounds__(kAk8Threads, NT == 1 ? 3 : 2) attn_kv8_kernel(
             float dp[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                pk[i] = ok ? sm.pos[w][st][8 * i + g] : -1;
+                pk[i] = ok ? pos[8 * i + g] : -1;
                 dp[i] = (float)(pk[i] - ref);
             }
             uint32_t pb[2][NT][2];
@@ -414,7 +439,7 @@ __global__ void __launch_bounds__(kAk8Threads, NT == 1 ? 3 : 2) attn_kv8_kernel(
                         const uint2 r = *reinterpret_cast<const uint2 *>(p);
                         v[i][0] = r.x; v[i][1] = r.y;
                     }
-                    if (!clean && (!ok || sm.pos[w][st][slot] < 0)) {
+                    if (!clean && (!ok || pos[slot] < 0)) {
 #pragma unroll
                         for (int u = 0; u < VW; ++u) v[i][u] = 0;
                     }
@@ -435,19 +460,20 @@ __global__ void __launch_bounds__(kAk8Threads, NT == 1 ? 3 : 2) attn_kv8_kernel(
                     }
                 }
             }
-            __syncwarp();   // the stage has been read
-            issue(st);
-            if (++st == ST) {
-                st = 0;
-                parity ^= 1u;
-            }
+        }
+        __syncwarp();   // the stage has been read
+        issue(st);
+        if (++st == ST) {
+            st = 0;
+            parity ^= 1u;
         }
         const Ak8Cursor here = cur;
         cur.next(rows);
-        if (cur.tile != 0 && x + 1 < x1) continue;
+        if (cur.blk != 0 && x + 1 < x1) continue;
 
-        // ---- the end of a (row, head), or of the run: join the four warps
+        // ---- the end of a (row, head), or of the run
         fresh = true;
+        const bool whole = here.blk + 1 == here.blocks && x - here.blk >= seg0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -457,87 +483,123 @@ __global__ void __launch_bounds__(kAk8Threads, NT == 1 ? 3 : 2) attn_kv8_kernel(
                 sum += __shfl_xor_sync(0xffffffffu, sum, 8);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 16);
                 const int c = nt * 8 + 2 * t4 + e;
-                if (c < ncol) {
-                    if (g == 0) {
-                        sm.stat[w][c][0] = m[nt][e];
-                        sm.stat[w][c][1] = M[nt][e];
-                        sm.stat[w][c][2] = sum;
+                if (c >= ncol) continue;
+                if (whole) {
+                    const int cc = chunk * W + c;
+                    const float inv = sum == 0.f ? 0.f : ak8_exp2(ak8_finite(M[nt][e]) - ak8_finite(m[nt][e])) / sum;
+                    uint4 *o = reinterpret_cast<uint4 *>(
+                        a.o + (((long long)here.b * a.T + cc / group) * a.n + h * group + cc % group) * D + g * (D / 8));
+#pragma unroll
+                    for (int i = 0; i < HS; ++i) {
+                        uint32_t r[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            r[u] = pack_bf2(acc[4 * i + u][nt][e] * 0x1p-14f * inv, acc[4 * i + u][nt][2 + e] * 0x1p-14f * inv);
+                        o[i] = make_uint4(r[0], r[1], r[2], r[3]);
                     }
-                    float2 *dst = reinterpret_cast<float2 *>(sm_acc + (w * ncol + c) * D + g * (D / 8));
+                } else {   // slot 0 of this run: its first (row, head); 1: its last
+                    float *p = a.part + ((long long)(2 * run + (seg0 == x0 ? 0 : 1)) * cols + c) * (D + kAk8Part);
+                    if (g == 0) {
+                        p[D] = m[nt][e];
+                        p[D + 1] = M[nt][e];
+                        p[D + 2] = sum;
+                    }
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i) dst[i] = make_float2(acc[i][nt][e], acc[i][nt][2 + e]);
+                    for (int i = 0; i < D / 32; ++i)
+                        reinterpret_cast<float4 *>(p + g * (D / 8))[i] =
+                            make_float4(acc[2 * i][nt][e], acc[2 * i][nt][2 + e], acc[2 * i + 1][nt][e], acc[2 * i + 1][nt][2 + e]);
                 }
             }
-        __syncthreads();
-        const bool whole = here.tile + 1 == here.tiles && x - here.tile >= seg0;
-        for (int i = tid; i < ncol * D; i += kAk8Threads) {
-            const int c = i / D, d = i % D;
-            float mm = -INFINITY, MM = -INFINITY, ll = 0.f, oo = 0.f;
-#pragma unroll
-            for (int k = 0; k < kAk8Warps; ++k) {
-                mm = fmaxf(mm, sm.stat[k][c][0]);
-                MM = fmaxf(MM, sm.stat[k][c][1]);
-            }
-#pragma unroll
-            for (int k = 0; k < kAk8Warps; ++k) {
-                ll += sm.stat[k][c][2] * ak8_exp2(sm.stat[k][c][0] - ak8_finite(mm));
-                oo += sm_acc[(k * ncol + c) * D + d] * ak8_exp2(sm.stat[k][c][1] - ak8_finite(MM));
-            }
-            if (whole) {
-                const int cc = chunk * W + c;
-                const float o = ll == 0.f ? 0.f : oo * 0x1p-14f * ak8_exp2(ak8_finite(MM) - ak8_finite(mm)) / ll;
-                a.o[(((long long)here.b * a.T + cc / group) * a.n + h * group + cc % group) * D + d] = f2bf(o);
-            } else {   // slot 0 of this CTA: the run's first (row, head); 1: its last
-                float *p = a.part + ((long long)(2 * blockIdx.x + (seg0 == x0 ? 0 : 1)) * a.part_cols + c) * (D + kAk8Part);
-                p[d] = oo;
-                if (d == 0) {
-                    p[D] = mm;
-                    p[D + 1] = MM;
-                    p[D + 2] = ll;
-                }
-            }
-        }
-        __syncthreads();
     }
     cp_async_wait_all();
 }
 
-// Joins the partial results of the (row, head) that CTA blockIdx.x of the kernel
-// above began and did not end, in the order of the runs.
+// Joins the partial results of one (row, head), in the order of the runs.  Block x
+// is the (row, head) x where those are fewer than the runs; else the one that run
+// x began and did not end.  Warps take the partials in turn, lanes D / 32 elements.
 template <int D, int NT>
-__global__ void __launch_bounds__(D) attn_kv8_join_kernel(const AttnKv8Args a, int ctas) {
-    constexpr int W = 8 * NT;
+__global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnKv8Args a, int warps, int by_head) {
+    constexpr int W = 8 * NT, E = D / 32;
+    __shared__ float sm_o[4][D], sm_l[4], sm_m[4][2];
     griddep_launch();
     griddep_wait();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int group = a.n / a.kv, C = group * a.T, chunks = (C + W - 1) / W;
     const Ak8Rows rows{a.lens, a.B, a.max_seq, a.kv * chunks};
-    const long long total = ak8_total(rows), G = min((long long)ctas, total);
-    if (blockIdx.x >= G) return;
-    const long long x0 = blockIdx.x * total / G, x1 = (blockIdx.x + 1) * total / G;
-    Ak8Cursor last;
-    last.at(rows, x1 - 1);
-    const long long first = x1 - 1 - last.tile, end = first + last.tiles;   // tiles of that (row, head)
-    if (first < x0 || end <= x1) return;   // begun by an earlier CTA, or ended here
-    const int c1 = (int)((end * G - 1) / total);                            // the CTA that ends it
-    const int chunk = last.head % chunks, h = last.head / chunks, ncol = min(W, C - chunk * W), d = threadIdx.x;
-    for (int c = blockIdx.y; c < ncol; c += gridDim.y) {
-        auto part = [&](int cta) {
-            return a.part + ((long long)(2 * cta + (cta == (int)blockIdx.x && first != x0)) * a.part_cols + c) * (D + kAk8Part);
+    const long long total = ak8_total(rows), R = ak8_runs(total, warps);
+    int b, head;
+    long long first, end;   // its blocks
+    if (by_head) {
+        b = blockIdx.x / rows.heads;
+        head = blockIdx.x % rows.heads;
+        int before = 0;
+        for (int i = lane; i < b; i += 32) before += rows.blocks(i);
+        const int blocks = rows.blocks(b);
+        if (blocks <= kAk8Short) return;
+        first = (long long)__reduce_add_sync(0xffffffffu, before) * rows.heads + (long long)head * blocks;
+        end = first + blocks;
+    } else {
+        if (blockIdx.x + 1 >= R) return;
+        Ak8Cursor c;
+        const long long x1 = (blockIdx.x + 1) * total / R;
+        c.at(rows, x1);
+        if (c.blocks <= kAk8Short || c.blk == 0) return;   // the cut lies between two
+        b = c.b;
+        head = c.head;
+        first = x1 - c.blk;
+        end = first + c.blocks;
+        if (blockIdx.x * total / R > first) return;        // an earlier run began it
+    }
+    const int r0 = (int)(((first + 1) * R - 1) / total), r1 = (int)((end * R - 1) / total);   // the runs it lies in
+    if (r0 == r1) return;
+    // run r0 may have begun with an earlier (row, head)
+    Ak8Cursor c;
+    const int slot0 = ak8_cut(rows, r0, R, total, c) != first;
+    const int chunk = head % chunks, h = head / chunks, ncol = min(W, C - chunk * W);
+    for (int col = blockIdx.y; col < ncol; col += gridDim.y) {
+        auto part = [&](int r) {
+            return a.part + ((long long)(2 * r + (r == r0 ? slot0 : 0)) * a.part_cols + col) * (D + kAk8Part);
         };
-        float mm = -INFINITY, MM = -INFINITY, ll = 0.f, oo = 0.f;
-        for (int k = blockIdx.x; k <= c1; ++k) {
-            const float *p = part(k);
-            mm = fmaxf(mm, p[D]);
-            MM = fmaxf(MM, p[D + 1]);
+        float mm = -INFINITY, MM = -INFINITY;
+        for (int r = r0 + (int)threadIdx.x; r <= r1; r += 128) {
+            const float2 v = *reinterpret_cast<const float2 *>(part(r) + D);
+            mm = fmaxf(mm, v.x);
+            MM = fmaxf(MM, v.y);
         }
-        for (int k = blockIdx.x; k <= c1; ++k) {
-            const float *p = part(k);
-            ll += p[D + 2] * ak8_exp2(p[D] - ak8_finite(mm));
-            oo += p[d] * ak8_exp2(p[D + 1] - ak8_finite(MM));
+        mm = warp_max(mm);
+        MM = warp_max(MM);
+        __syncthreads();   // the previous column's values have been read
+        if (lane == 0) {
+            sm_m[w][0] = mm;
+            sm_m[w][1] = MM;
         }
-        const int cc = chunk * W + c;
-        const float o = ll == 0.f ? 0.f : oo * 0x1p-14f * ak8_exp2(ak8_finite(MM) - ak8_finite(mm)) / ll;
-        a.o[(((long long)last.b * a.T + cc / group) * a.n + h * group + cc % group) * D + d] = f2bf(o);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            mm = fmaxf(mm, sm_m[i][0]);
+            MM = fmaxf(MM, sm_m[i][1]);
+        }
+        float o[E] = {}, ll = 0.f;
+#pragma unroll 4
+        for (int r = r0 + w; r <= r1; r += 4) {
+            const float *p = part(r);
+            const float4 st = *reinterpret_cast<const float4 *>(p + D);
+            const float f = ak8_exp2(st.y - ak8_finite(MM));
+            ll += st.z * ak8_exp2(st.x - ak8_finite(mm));
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] += p[32 * e + lane] * f;
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) sm_o[w][32 * e + lane] = o[e];
+        if (lane == 0) sm_l[w] = ll;
+        __syncthreads();
+        ll = sm_l[0] + sm_l[1] + sm_l[2] + sm_l[3];
+        const int d = threadIdx.x, cc = chunk * W + col;
+        if (d < D) {
+            const float inv = ll == 0.f ? 0.f : ak8_exp2(ak8_finite(MM) - ak8_finite(mm)) / ll;
+            const float v = (sm_o[0][d] + sm_o[1][d] + sm_o[2][d] + sm_o[3][d]) * 0x1p-14f * inv;
+            a.o[(((long long)b * a.T + cc / group) * a.n + h * group + cc % group) * D + d] = f2bf(v);
+        }
     }
 }
 
@@ -549,32 +611,34 @@ static cudaError_t ak8_launch(AttnKv8Args a, int sms, cudaStream_t s) {
     const auto kern = attn_kv8_kernel<D, E4M3, NT>;
     const int group = a.n / a.kv, C = group * a.T, chunks = (C + W - 1) / W;
     a.part_cols = C < W ? C : W;
-    const size_t smem = sizeof(Ak8Smem<D, NT>) + (size_t)kAk8Warps * a.part_cols * D * 4;
+    const int smem = Ak8Stage<D>::smem(a.part_cols);
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     int per_sm = dev < kDevices ? known[dev][a.part_cols].load(std::memory_order_relaxed) : 0;
     if (per_sm == 0) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)(sizeof(Ak8Smem<D, NT>) + (size_t)kAk8Warps * W * D * 4));
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Ak8Stage<D>::smem(W));
         if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kAk8Threads, smem);
         if (e != cudaSuccess) return e;
         per_sm = per_sm < 1 ? 1 : per_sm > kAk8MaxPerSm ? kAk8MaxPerSm : per_sm;
         if (dev < kDevices) known[dev][a.part_cols].store(per_sm, std::memory_order_relaxed);
     }
-    const long long most = (long long)a.B * a.kv * chunks * ((a.max_seq + kAk8Tile - 1) / kAk8Tile);
-    const int G = (int)(most < (long long)sms * per_sm ? most : (long long)sms * per_sm);
+    const long long heads = (long long)a.B * a.kv * chunks;
+    const long long most = heads * ((a.max_seq + kKv8Block - 1) / kKv8Block);
+    const long long runs = (most + kAk8MinRun - 1) / kAk8MinRun;
+    const int G = (int)(runs < (long long)sms * per_sm ? runs : (long long)sms * per_sm), warps = G * kAk8Warps;
     e = launch_pdl_smem(kern, dim3(G), dim3(kAk8Threads), smem, s, a);
-    // rows of one tile are never cut
-    if (e == cudaSuccess && a.max_seq > kAk8Tile)
-        e = launch_pdl(attn_kv8_join_kernel<D, NT>, dim3(G, a.part_cols < 4 ? a.part_cols : 4), dim3(D), s, a, G);
-    return e;
+    if (e != cudaSuccess || a.max_seq <= kAk8Short * kKv8Block) return e;   // nothing can have been cut
+    const int by_head = heads < warps, blocks = by_head ? (int)heads : warps;
+    int y = 2 * warps / blocks;   // columns apart while that keeps the grid small
+    y = y < 1 ? 1 : y > a.part_cols ? a.part_cols : y;
+    return launch_pdl(attn_kv8_join_kernel<D, NT>, dim3(blocks, y), dim3(128), s, a, warps, by_head);
 }
 
 size_t attn_kv8_workspace(int n, int kv, int T, int max_seq, int d, int sms) {
     const int C = n / kv * T, W = C <= 8 ? 8 : 16;
-    if (max_seq <= kAk8Tile) return 0;
-    return (size_t)sms * kAk8MaxPerSm * 2 * (C < W ? C : W) * (d + kAk8Part) * 4;
+    if (max_seq <= kAk8Short * kKv8Block) return 0;
+    return (size_t)sms * kAk8MaxPerSm * kAk8Warps * 2 * (C < W ? C : W) * (d + kAk8Part) * 4;
 }
 
 cudaError_t launch_attn_kv8(const AttnKv8Args &a, int d, int e4m3, int sms, cudaStream_t s) {
