@@ -1541,6 +1541,9 @@ static bloom_status check_attn_kv8(const bloom_kv8 *kv, int32_t T, int32_t n_hea
     if (T < 1) return fail(BLOOM_E_INVALID, "T=%d", T);
     if (T > kKv8MaxT || n_head > 65535)
         return fail(BLOOM_E_UNSUPPORTED, "T=%d n_head=%d (at most %d tokens)", T, n_head, kKv8MaxT);
+    if (!attn_kv8_fits(kv->batch, n_head, kv->n_kv, T, kv->max_seq))
+        return fail(BLOOM_E_UNSUPPORTED, "batch=%d n_kv=%d max_seq=%d: 2^31 slots or more", kv->batch,
+                    kv->n_kv, kv->max_seq);
     return BLOOM_OK;
 }
 

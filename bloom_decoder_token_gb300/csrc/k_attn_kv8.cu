@@ -20,20 +20,24 @@
 //    scores are float32 sums of exact products.
 //  * The softmax is one pass: running maxima and sums in float32, in powers of
 //    two.  The weight of V_k carries the block's V scale: exp2(s_k + log2 scale -
-//    M + 14) with a running maximum M of its own, so that scales far apart cost
-//    nothing, rounded to f16 (relative 2^-11; the bf16 result rounds at 2^-8)
-//    and multiplied with exact codes into float32 accumulators.
+//    M) with a reference M of its own, so that scales far apart cost nothing,
+//    rounded to f16 (relative 2^-11; the bf16 result rounds at 2^-8) and
+//    multiplied with exact codes into float32 accumulators.  Both references
+//    move, and what was summed is rescaled, only when a score passes one by
+//    more than 2^8.
 //  * Work is cut evenly whatever the lengths: the scale blocks (32 slots) of all
 //    rows and key heads are numbered in one sequence, and each resident warp takes
 //    an equal run of it.  A (row, key head) of at most kAk8Short blocks is left
 //    whole; a longer one that falls into several runs leaves partial results,
 //    which a second kernel joins in order.
-//  * A warp keeps its own ring of stages ahead of it, one block each: two bulk copies
-//    (K, V), completing on an mbarrier, and by cp.async positions, scales and, at
-//    the first block of a (row, key head), its queries.  Warps never wait for
-//    one another.
+//  * A warp keeps its own ring of stages ahead of it, one block each: K and V by TMA
+//    (swizzled by the row's width, and the slots dealt to the fragments' rows, so
+//    that the fragment loads meet no bank twice), and by cp.async positions,
+//    scales and, at the first block of a (row, key head), its queries.  Warps
+//    never wait for one another.
 #include <atomic>
 #include <math.h>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -69,7 +73,7 @@ __device__ __forceinline__ uint32_t ak8_bias(uint32_t w) { return E4M3 ? w : w ^
 
 __device__ __forceinline__ void ak8_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -99,38 +103,37 @@ struct Ak8Rows {
     // blocks of one head of row b; at least one, so that every output is written
     __device__ __forceinline__ int blocks(int b) const { return max(1, (len(b) + kKv8Block - 1) / kKv8Block); }
 };
-__device__ __forceinline__ long long ak8_total(const Ak8Rows &r) {   // by the whole warp
-    const int lane = threadIdx.x & 31;
+__device__ __forceinline__ int ak8_total(const Ak8Rows &r) {   // by the whole warp
     int t = 0;
-    for (int b = lane; b < r.B; b += 32) t += r.blocks(b);
-    return (long long)__reduce_add_sync(0xffffffffu, t) * r.heads;
+    for (int b = threadIdx.x & 31; b < r.B; b += 32) t += r.blocks(b);
+    return __reduce_add_sync(0xffffffffu, t) * r.heads;
 }
 struct Ak8Cursor {   // a block: its row, head, place in that head; the row's length and blocks a head
     int b, head, blk, len, blocks;
     // block number x < total, by the whole warp
-    __device__ __forceinline__ void at(const Ak8Rows &r, long long x) {
+    __device__ __forceinline__ void at(const Ak8Rows &r, int x) {
         const int lane = threadIdx.x & 31;
-        long long before = 0;
+        int before = 0;
         for (int b0 = 0;; b0 += 32) {
-            const int mine = b0 + lane < r.B ? r.blocks(b0 + lane) : 0;
+            const int mine = b0 + lane < r.B ? r.blocks(b0 + lane) * r.heads : 0;
             int sum = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, sum, o);
                 if (lane >= o) sum += y;
             }
-            const unsigned past = __ballot_sync(0xffffffffu, before + (long long)sum * r.heads > x);
+            const unsigned past = __ballot_sync(0xffffffffu, before + sum > x);
             if (past || b0 + 32 >= r.B) {
                 const int src = past ? __ffs(past) - 1 : 31;
                 b = b0 + src;
-                x -= before + (long long)__shfl_sync(0xffffffffu, sum - mine, src) * r.heads;
+                x -= before + __shfl_sync(0xffffffffu, sum - mine, src);
                 break;
             }
-            before += (long long)__shfl_sync(0xffffffffu, sum, 31) * r.heads;
+            before += __shfl_sync(0xffffffffu, sum, 31);
         }
         row(r);
-        head = (int)(x / blocks);
-        blk = (int)(x - (long long)head * blocks);
+        head = x / blocks;
+        blk = x - head * blocks;
     }
     __device__ __forceinline__ void row(const Ak8Rows &r) {
         len = b < r.B ? r.len(b) : 0;
@@ -145,49 +148,75 @@ struct Ak8Cursor {   // a block: its row, head, place in that head; the row's le
         row(r);
     }
 };
-// Run k of R: blocks [ak8_cut(k), ak8_cut(k + 1)), equal shares, but that a short
-// (row, head) belongs to the run that its last block falls into.
-__device__ __forceinline__ long long ak8_cut(const Ak8Rows &r, long long k, long long R, long long total,
-                                             Ak8Cursor &c) {
-    long long x = k * total / R;
-    if (x >= total) return total;
-    c.at(r, x);
-    if (c.blocks <= kAk8Short) {
-        x -= c.blk;
-        c.blk = 0;
+// The runs: R equal shares of `total` blocks, the first `rem` one longer.
+struct Ak8Runs {
+    int total, R, q, rem;
+    __device__ __forceinline__ Ak8Runs(int t, int warps) : total(t) {
+        R = min(warps, (t + kAk8MinRun - 1) / kAk8MinRun);
+        q = t / R;
+        rem = t - q * R;
     }
-    return x;
-}
-__device__ __forceinline__ long long ak8_runs(long long total, int warps) {
-    return min((long long)warps, (total + kAk8MinRun - 1) / kAk8MinRun);
-}
+    __device__ __forceinline__ int start(int k) const { return k * q + min(k, rem); }
+    __device__ __forceinline__ int of(int x) const {   // the run that block x falls into
+        const int y = x - rem * (q + 1);
+        return y < 0 ? x / (q + 1) : rem + y / q;
+    }
+    // where run k begins in earnest: a short (row, head) belongs to the run of its last block
+    __device__ __forceinline__ int cut(const Ak8Rows &r, int k, Ak8Cursor &c) const {
+        int x = start(k);
+        if (x >= total) return total;
+        c.at(r, x);
+        if (c.blocks <= kAk8Short) {
+            x -= c.blk;
+            c.blk = 0;
+        }
+        return x;
+    }
+};
 
-// One stage of a warp's ring, in bytes: K, V, the queries of `cols` columns, positions
-// of the block, positions of the row's last 32 slots, the two scales.
+struct Ak8Maps {   // K and V codes as rows of D bytes
+    CUtensorMap k, v;
+};
+
+// Shared memory of a CTA: stages of K and V [warps][stages], 1024-byte aligned; beside
+// each stage its queries [cols][D], positions of the block, of the row's last 32
+// slots, slopes [16], scales [2]; an mbarrier per stage.
 template <int D>
-struct Ak8Stage {
-    static constexpr int kCount = 256 / D, kQ = 2 * kKv8Block * D;
-    __host__ __device__ static constexpr int pos(int cols) { return kQ + cols * D * 2; }
-    __host__ __device__ static constexpr int bytes(int cols) { return (pos(cols) + 256 + 16 + 127) / 128 * 128; }
-    // the ring of a CTA and an mbarrier per stage
-    __host__ __device__ static constexpr int smem(int cols) { return kAk8Warps * kCount * (bytes(cols) + 8); }
+struct Ak8Smem {
+    static constexpr int kStages = 256 / D, kStage = 2 * kKv8Block * D, kAll = kAk8Warps * kStages;
+    __host__ __device__ static constexpr int side(int cols) { return cols * D * 2 + 128 + 128 + 64 + 16; }
+    __host__ __device__ static constexpr int bytes(int cols) { return 1024 + kAll * (kStage + side(cols) + 8); }
 };
 
 __device__ __forceinline__ void ak8_async4(const void *dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc_smem(dst)), "l"(src) : "memory");
 }
 
-// Columns of a chunk: query c = t * group + i of a key head, t the token, i the query head.
-template <int D, bool E4M3, int NT>
-__global__ void __launch_bounds__(kAk8Threads, NT == 1 ? 3 : 2) attn_kv8_kernel(const AttnKv8Args a) {
-    constexpr int HS = D / 64, VW = D / 32, W = 8 * NT;   // K segments of 16 bytes a lane; V words a key
-    using Stage = Ak8Stage<D>;
-    constexpr int ST = Stage::kCount;
-    extern __shared__ __align__(128) unsigned char ak8_raw[];
+// The slot (of 8) that row r of a fragment takes.  With 16-byte pieces c of a row at
+// c ^ slot % 8 (D = 128) or c ^ slot / 2 % 4 (D = 64), the eight lanes of a K access
+// (rows 2 i and 2 i + 1, four pieces each) and those of a V access (rows 0, 2, 4, 6
+// or 1, 3, 5, 7, two pieces each; 8 bytes and sixteen lanes at D = 64) cover all banks.
+template <int D>
+__device__ __forceinline__ int ak8_slot(int r) {
+    return (int)((D == 128 ? 0x37621540u : 0x65742130u) >> (4 * r)) & 7;
+}
+
+// Columns of a chunk: query c = t * group + i of a key head, t the token, i the query
+// head.  ONE: a single column in all (T = 1, as many key heads as query heads).
+template <int D, bool E4M3, int NT, bool ONE>
+__global__ void __launch_bounds__(kAk8Threads, NT == 1 ? 3 : 2)
+    attn_kv8_kernel(const __grid_constant__ AttnKv8Args a, const __grid_constant__ Ak8Maps maps) {
+    constexpr int HS = D / 64, VW = D / 32, W = 8 * NT, NE = ONE ? 1 : 2;
+    using Smem = Ak8Smem<D>;
+    constexpr int ST = Smem::kStages;
+    constexpr float kLog2e = 1.4426950408889634f, kSlack = 8.f, kLift = 6.f;   // weights up to 2^15 in f16
+    extern __shared__ __align__(1024) unsigned char ak8_raw[];
+    unsigned char *smem = ak8_raw + ((0u - tc_smem(ak8_raw)) & 1023u);
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
-    const int cols = a.part_cols, sbytes = Stage::bytes(cols);
-    unsigned char *ring = ak8_raw + w * ST * sbytes;
-    uint64_t *bar = reinterpret_cast<uint64_t *>(ak8_raw + kAk8Warps * ST * sbytes) + w * ST;
+    const int cols = a.part_cols, side_bytes = Smem::side(cols);
+    unsigned char *ring = smem + w * ST * Smem::kStage;
+    unsigned char *sides = smem + Smem::kAll * Smem::kStage + w * ST * side_bytes;
+    uint64_t *bar = reinterpret_cast<uint64_t *>(smem + Smem::kAll * (Smem::kStage + side_bytes)) + w * ST;
     if (lane == 0) {
         for (int i = 0; i < ST; ++i) tc_mbar_init(&bar[i], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -196,59 +225,50 @@ __global__ void __launch_bounds__(kAk8Threads, NT == 1 ? 3 : 2) attn_kv8_kernel(
     griddep_launch();
     griddep_wait();
 
-    const int group = a.n / a.kv, C = group * a.T, chunks = (C + W - 1) / W;
+    const int group = ONE ? 1 : a.n / a.kv, C = ONE ? 1 : group * a.T, chunks = ONE ? 1 : (C + W - 1) / W;
     const Ak8Rows rows{a.lens, a.B, a.max_seq, a.kv * chunks};
     if (a.err && blockIdx.x == 0)
         for (int b = threadIdx.x; b < a.B; b += kAk8Threads)
             if (a.lens[b] > a.max_seq) atomicOr(a.err, kErrSlot);
-    const long long total = ak8_total(rows), R = ak8_runs(total, (int)gridDim.x * kAk8Warps);
+    const Ak8Runs runs(ak8_total(rows), (int)gridDim.x * kAk8Warps);
     const int run = w * (int)gridDim.x + (int)blockIdx.x;   // runs spread over the CTAs first
-    if (run >= R) return;
+    if (run >= runs.R) return;
     Ak8Cursor cur, ahead;
-    const long long x1 = ak8_cut(rows, run + 1, R, total, ahead);
-    const long long x0 = ak8_cut(rows, run, R, total, cur);
+    const int x1 = runs.cut(rows, run + 1, ahead), x0 = runs.cut(rows, run, cur);
     if (x0 >= x1) return;
     ahead = cur;
 
     // block xa of the run into stage `st`; one cp.async group, empty beyond the end
-    long long xa = x0;
+    int xa = x0, bh = 0;   // bh: row * key heads + key head of block xa
     auto issue = [&](int st) {
         if (xa < x1) {
-            unsigned char *stage = ring + st * sbytes;
-            const int base = ahead.blk * kKv8Block, n = min(kKv8Block, ahead.len - base);   // n <= 0: no keys
-            const int h = ahead.head / chunks;
-            const long long bh = (long long)ahead.b * a.kv + h;
-            if (lane == 0) {
-                const uint32_t br = tc_smem(&bar[st]);
-                if (n > 0) {
-                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(br), "r"(2 * n * D) : "memory");
-#pragma unroll
-                    for (int v = 0; v < 2; ++v)
-                        asm volatile(
-                            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                                tc_smem(stage + v * kKv8Block * D)),
-                            "l"((v ? a.vc : a.kc) + (bh * a.max_seq + base) * D), "r"(n * D), "r"(br)
-                            : "memory");
-                } else {
-                    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(br) : "memory");
-                }
-            }
-            int *pos = reinterpret_cast<int *>(stage + Stage::pos(cols));
+            unsigned char *stage = ring + st * Smem::kStage, *side = sides + st * side_bytes;
+            int *pos = reinterpret_cast<int *>(side + cols * D * 2);   // [32], [32], slopes, scales
+            const int base = ahead.blk * kKv8Block;
             const int *rowpos = a.pos + (long long)ahead.b * a.max_seq;
-            if (lane < n) ak8_async4(pos + lane, rowpos + base + lane);
-            else pos[lane] = -1;
-            if (lane < 2 && n > 0)
-                ak8_async4(pos + 64 + lane, (lane ? a.vs : a.ks) + bh * a.blocks + base / kKv8Block);
             if (xa == x0 || ahead.blk == 0) {   // the first block of a (row, head) in this run
+                const int h = ONE ? ahead.head : ahead.head / chunks, c0 = (ahead.head - h * chunks) * W;
+                bh = ahead.b * a.kv + h;
                 if (ahead.len - 1 - lane >= 0) ak8_async4(pos + 32 + lane, rowpos + ahead.len - 1 - lane);
                 else pos[32 + lane] = -1;
-                const int c0 = ahead.head % chunks * W, nc = min(W, C - c0);
+                const int nc = ONE ? 1 : min(W, C - c0);
+                if (a.slopes && lane < nc) ak8_async4(pos + 64 + lane, a.slopes + h * group + (c0 + lane) % group);
                 for (int i = lane; i < nc * (D / 8); i += 32) {
                     const int c = c0 + i / (D / 8), e = i % (D / 8) * 8;
-                    cp_async16(stage + Stage::kQ + (i / (D / 8) * D + e) * 2,
+                    cp_async16(side + (i / (D / 8) * D + e) * 2,
                                a.q + (((long long)ahead.b * a.T + c / group) * a.n + h * group + c % group) * D + e);
                 }
             }
+            if (lane == 0) {
+                // slots beyond the row's length come along; they are masked
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(tc_smem(&bar[st])), "r"(Smem::kStage)
+                             : "memory");
+                tc_tma_2d(stage, &maps.k, 0, bh * a.max_seq + base, &bar[st]);
+                tc_tma_2d(stage + kKv8Block * D, &maps.v, 0, bh * a.max_seq + base, &bar[st]);
+            }
+            if (base + lane < ahead.len) ak8_async4(pos + lane, rowpos + base + lane);
+            else pos[lane] = -1;
+            if (lane < 2) ak8_async4(pos + 80 + lane, (lane ? a.vs : a.ks) + (long long)bh * a.blocks + ahead.blk);
             ++xa;
             ahead.next(rows);
         }
@@ -257,19 +277,31 @@ __global__ void __launch_bounds__(kAk8Threads, NT == 1 ? 3 : 2) attn_kv8_kernel(
 #pragma unroll
     for (int i = 0; i < ST; ++i) issue(i);
 
-    constexpr float kLog2e = 1.4426950408889634f;
+    // this lane's places in a stage: K rows g (8 slots further: + 8 D), V slots of rows
+    // 2 t4 and 2 t4 + 1
+    const int slot_g = ak8_slot<D>(g), va = ak8_slot<D>(2 * t4), vb = ak8_slot<D>(2 * t4 + 1);
+    int koff[HS], voff[2];
+    if (D == 128) {
+#pragma unroll
+        for (int i = 0; i < HS; ++i) koff[i] = slot_g * D + ((4 * i + t4) ^ slot_g) * 16;
+        voff[0] = va * D + (g ^ va) * 16;
+        voff[1] = vb * D + (g ^ vb) * 16;
+    } else {   // 8 slots are two periods of the swizzle: the offset is the same
+        koff[0] = slot_g * D + (t4 ^ (slot_g >> 1)) * 16;
+        voff[0] = va * D + ((g >> 1) ^ (va >> 1)) * 16 + (g & 1) * 8;
+        voff[1] = vb * D + ((g >> 1) ^ (vb >> 1)) * 16 + (g & 1) * 8;
+    }
+
     uint32_t qf[NT][D / 16][2];
-    float qinv[NT][2], slope[NT][2], m[NT][2], M[NT][2], l[NT][2], acc[D / 16][NT][4];
-    int lim[NT][2];                // slots that a column sees
-    int ref = 0, st = 0;
+    float qs[NT][NE], slope[NT][NE], m[NT][NE], M[NT][NE], l[NT][NE], acc[D / 16][NT][4];
+    int lim[NT][NE];               // slots that a column sees
+    int chunk = 0, h = 0, ncol = 1, all = 0;   // all: slots that every column sees
+    int ref = 0, st = 0, seg0 = x0;            // seg0: first block of the current (row, head) in this run
     uint32_t parity = 0;
-    long long seg0 = x0;           // first block of the current (row, head) in this run
     bool fresh = true;
-    for (long long x = x0; x < x1; ++x) {
-        const int chunk = cur.head % chunks, h = cur.head / chunks;
-        const int ncol = min(W, C - chunk * W);
-        unsigned char *stage = ring + st * sbytes;
-        const int *pos = reinterpret_cast<const int *>(stage + Stage::pos(cols));
+    for (int x = x0; x < x1; ++x) {
+        unsigned char *stage = ring + st * Smem::kStage;
+        const int *pos = reinterpret_cast<const int *>(sides + st * side_bytes + cols * D * 2);
         // ---- the block's copies
         cp_async_wait<ST - 1>();
         const bool ok = __all_sync(0xffffffffu, tc_mbar_wait(&bar[st], parity, 0));
@@ -281,6 +313,10 @@ __global__ void __launch_bounds__(kAk8Threads, NT == 1 ? 3 : 2) attn_kv8_kernel(
         if (fresh) {
             fresh = false;
             seg0 = x;
+            h = ONE ? cur.head : cur.head / chunks;
+            chunk = cur.head - h * chunks;
+            ncol = ONE ? 1 : min(W, C - chunk * W);
+            all = cur.len - a.T + 1 + (ONE ? 0 : chunk * W / group);
             ref = __reduce_max_sync(0xffffffffu, pos[32 + lane]);
             for (int k0 = cur.len - 32; k0 > 0 && ref < 0; k0 -= 32)   // pads alone at the row's end
                 ref = __reduce_max_sync(0xffffffffu, k0 - 1 - lane >= 0 ? a.pos[(long long)cur.b * a.max_seq + k0 - 1 - lane] : -1);
@@ -293,7 +329,8 @@ __global__ void __launch_bounds__(kAk8Threads, NT == 1 ? 3 : 2) attn_kv8_kernel(
                 for (int s = 0; s < HS; ++s) {
                     raw[s][0] = raw[s][1] = make_uint4(0u, 0u, 0u, 0u);
                     if (nt * 8 + g < ncol) {
-                        const uint4 *q = reinterpret_cast<const uint4 *>(stage + Stage::kQ + ((nt * 8 + g) * D + 64 * s + 16 * t4) * 2);
+                        const uint4 *q = reinterpret_cast<const uint4 *>(
+                            sides + st * side_bytes + ((nt * 8 + g) * D + 64 * s + 16 * t4) * 2);
                         raw[s][0] = q[0];
                         raw[s][1] = q[1];
                     }
@@ -308,10 +345,11 @@ __global__ void __launch_bounds__(kAk8Threads, NT == 1 ? 3 : 2) attn_kv8_kernel(
                 amax = max(amax & 0xffffu, amax >> 16);
                 amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                 amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                // 2^up brings the largest element to [2^14, 2^15); at most 2^126
-                const int up = amax >= 0x7f80u ? 0 : min(126, 14 + 127 - (int)(amax >> 7));
+                // 2^up brings the largest element to [2^14, 2^15); at most 2^120, so that
+                // scale / 2^up is a normal number
+                const int up = amax >= 0x7f80u ? 0 : min(120, 14 + 127 - (int)(amax >> 7));
                 const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
-                float inv = __uint_as_float((uint32_t)(127 - up) << 23);
+                float inv = __uint_as_float((uint32_t)(127 - up) << 23) * (a.scale * kLog2e);
                 if (amax >= 0x7f80u) inv = __uint_as_float(0x7fc00000u);   // every score NaN
 #pragma unroll
                 for (int s = 0; s < HS; ++s)
@@ -322,11 +360,11 @@ __global__ void __launch_bounds__(kAk8Threads, NT == 1 ? 3 : 2) attn_kv8_kernel(
                         qf[nt][4 * s + u][1] = ak8_pack_f16(bf_lo(p[1]) * mul, bf_hi(p[1]) * mul);
                     }
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {   // accumulator columns 2 t4 + e
-                    const int cc = chunk * W + nt * 8 + 2 * t4 + e;
-                    qinv[nt][e] = __shfl_sync(0xffffffffu, inv, (2 * t4 + e) * 4);
-                    slope[nt][e] = a.slopes && cc < C ? a.slopes[h * group + cc % group] * kLog2e : 0.f;
-                    lim[nt][e] = cc < C ? cur.len - a.T + 1 + cc / group : 0;
+                for (int e = 0; e < NE; ++e) {   // accumulator columns 2 t4 + e
+                    const int c = nt * 8 + 2 * t4 + e, cc = chunk * W + c;
+                    qs[nt][e] = __shfl_sync(0xffffffffu, inv, (2 * t4 + e) * 4);
+                    slope[nt][e] = a.slopes && c < ncol ? __int_as_float(pos[64 + c]) * kLog2e : 0.f;
+                    lim[nt][e] = c < ncol ? cur.len - a.T + 1 + (ONE ? 0 : cc / group) : 0;
                     m[nt][e] = M[nt][e] = -INFINITY;
                     l[nt][e] = 0.f;
                 }
@@ -337,101 +375,106 @@ __global__ void __launch_bounds__(kAk8Threads, NT == 1 ? 3 : 2) attn_kv8_kernel(
             }
         }
         const int base = cur.blk * kKv8Block;
-        {
-            const uint8_t *ks = stage, *vs = stage + kKv8Block * D;
-            // ---- scores: 16 slots x columns per mt
-            float s[2][NT][4];
+        // ---- scores: 16 slots x columns per mt
+        float s[2][NT][4];
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
-                uint4 ka[HS], kb[HS];
+        for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
-                for (int i = 0; i < HS; ++i) {
-                    ka[i] = *reinterpret_cast<const uint4 *>(ks + (mt * 16 + g) * D + 64 * i + 16 * t4);
-                    kb[i] = *reinterpret_cast<const uint4 *>(ks + (mt * 16 + 8 + g) * D + 64 * i + 16 * t4);
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
+#pragma unroll
+            for (int i = 0; i < HS; ++i) {
+                const uint4 ka = *reinterpret_cast<const uint4 *>(stage + mt * 16 * D + koff[i]);
+                const uint4 kb = *reinterpret_cast<const uint4 *>(stage + (mt * 16 + 8) * D + koff[i]);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    uint32_t a0, a1, a2, a3;
+                    ak8_widen<E4M3>(ak8_bias<E4M3>((&ka.x)[u]), a0, a2);
+                    ak8_widen<E4M3>(ak8_bias<E4M3>((&kb.x)[u]), a1, a3);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        ak8_mma(s[mt][nt], a0, a1, a2, a3, qf[nt][4 * i + u][0], qf[nt][4 * i + u][1]);
                 }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
-#pragma unroll
-                for (int i = 0; i < HS; ++i)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        uint32_t a0, a1, a2, a3;
-                        ak8_widen<E4M3>(ak8_bias<E4M3>((&ka[i].x)[u]), a0, a2);
-                        ak8_widen<E4M3>(ak8_bias<E4M3>((&kb[i].x)[u]), a1, a3);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            ak8_mma(s[mt][nt], a0, a1, a2, a3, qf[nt][4 * i + u][0], qf[nt][4 * i + u][1]);
-                    }
             }
-            // ---- softmax
-            const float kscale = reinterpret_cast<const float *>(pos)[64], vscale = reinterpret_cast<const float *>(pos)[65];
-            // vscale = mant * 2^ev
-            const uint32_t vb = __float_as_uint(vscale), vexp = (vb >> 23) & 255u;
-            const float ev = vexp == 255u ? 0.f : vexp == 0u ? -126.f : (float)((int)vexp - 127);
-            const float mant = vexp == 255u ? vscale : vexp == 0u ? vscale * 0x1p126f : __uint_as_float((vb & 0x807fffffu) | 0x3f800000u);
-            int pk[4];
-            float dp[4];
+        }
+        const float kscale = __int_as_float(pos[80]), vscale = __int_as_float(pos[81]);
+        // vscale = mant * 2^ev
+        const uint32_t vbits = __float_as_uint(vscale), vexp = (vbits >> 23) & 255u;
+        const float ev = vexp == 255u ? 0.f : vexp == 0u ? -126.f : (float)((int)vexp - 127);
+        const float mant = vexp == 255u ? vscale : vexp == 0u ? vscale * 0x1p126f : __uint_as_float((vbits & 0x807fffffu) | 0x3f800000u);
+        int pk[4];
+        float dp[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                pk[i] = ok ? pos[8 * i + g] : -1;
-                dp[i] = (float)(pk[i] - ref);
-            }
+        for (int i = 0; i < 4; ++i) {
+            pk[i] = pos[8 * i + slot_g];
+            dp[i] = (float)(pk[i] - ref);
+        }
+        // does every column see every slot of the block?
+        const bool clean = __all_sync(0xffffffffu, ok && base + kKv8Block <= all && min(min(pk[0], pk[1]), min(pk[2], pk[3])) >= 0);
+        // ---- softmax, then values: D elements x columns, 16 slots per mt
+        auto rest = [&](auto is_clean) {
+            constexpr bool CLEAN = decltype(is_clean)::value;
             uint32_t pb[2][NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float wt[2][4];
+                bool move = false;
+                float bm[NE];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float f = kscale * qinv[nt][e] * (a.scale * kLog2e);
-                    float bm = -INFINITY;
+                for (int e = 0; e < NE; ++e) {
+                    const float f = kscale * qs[nt][e];
+                    bm[e] = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {   // slot 8 i + g
+                    for (int i = 0; i < 4; ++i) {   // slot 8 i + slot_g
                         float &v = s[i >> 1][nt][2 * (i & 1) + e];
                         v = v * f + slope[nt][e] * dp[i];
-                        if (pk[i] < 0 || base + 8 * i + g >= lim[nt][e]) v = -INFINITY;
-                        bm = fmaxf(bm, v);
+                        if (!CLEAN && (!ok || pk[i] < 0 || base + 8 * i + slot_g >= lim[nt][e])) v = -INFINITY;
+                        bm[e] = fmaxf(bm[e], v);
                     }
-                    bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 4));
-                    bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
-                    bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 16));
-                    const float mn = fmaxf(m[nt][e], bm), Mn = fmaxf(M[nt][e], bm + ev);
-                    const float mf = ak8_finite(mn), Mf = ak8_finite(Mn) - 14.f - ev;
-                    l[nt][e] *= ak8_exp2(m[nt][e] - mf);
-                    if (__any_sync(0xffffffffu, Mn > M[nt][e])) {
+                    move |= bm[e] > m[nt][e] + kSlack || bm[e] + ev > M[nt][e] + kSlack;
+                }
+                if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                    for (int e = 0; e < NE; ++e) {
+                        bm[e] = fmaxf(bm[e], __shfl_xor_sync(0xffffffffu, bm[e], 4));
+                        bm[e] = fmaxf(bm[e], __shfl_xor_sync(0xffffffffu, bm[e], 8));
+                        bm[e] = fmaxf(bm[e], __shfl_xor_sync(0xffffffffu, bm[e], 16));
+                        const float mn = fmaxf(m[nt][e], bm[e]), Mn = fmaxf(M[nt][e], bm[e] + ev);
+                        l[nt][e] *= ak8_exp2(m[nt][e] - ak8_finite(mn));
                         const float r = ak8_exp2(M[nt][e] - ak8_finite(Mn));
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i) {
                             acc[i][nt][e] *= r;
                             acc[i][nt][2 + e] *= r;
                         }
+                        m[nt][e] = mn;
+                        M[nt][e] = Mn;
                     }
-                    m[nt][e] = mn;
-                    M[nt][e] = Mn;
+                }
+#pragma unroll
+                for (int e = 0; e < NE; ++e) {
+                    const float mf = ak8_finite(m[nt][e]), Mf = ak8_finite(M[nt][e]) - kLift - ev;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float v = s[i >> 1][nt][2 * (i & 1) + e];
                         l[nt][e] += ak8_exp2(v - mf);
-                        wt[i >> 1][2 * (i & 1) + e] = v == -INFINITY ? 0.f : ak8_exp2(v - Mf) * mant;
+                        const float p = ak8_exp2(v - Mf) * mant;
+                        wt[i >> 1][2 * (i & 1) + e] = !CLEAN && v == -INFINITY ? 0.f : p;
                     }
                 }
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt) {   // [slot][column] -> [column][slot] fragments
-                    pb[mt][nt][0] = ak8_transpose(ak8_pack_f16(wt[mt][0], wt[mt][1]));
-                    pb[mt][nt][1] = ak8_transpose(ak8_pack_f16(wt[mt][2], wt[mt][3]));
+                    pb[mt][nt][0] = ak8_transpose(ak8_pack_f16(wt[mt][0], ONE ? 0.f : wt[mt][1]));
+                    pb[mt][nt][1] = ak8_transpose(ak8_pack_f16(wt[mt][2], ONE ? 0.f : wt[mt][3]));
                 }
             }
-            // ---- values: D elements x columns, 16 slots per mt
-            // slots that take no part may hold e4m3 NaNs: their codes count as 0
-            const bool clean = !E4M3 || !__any_sync(0xffffffffu, pk[0] < 0 || pk[1] < 0 || pk[2] < 0 || pk[3] < 0);
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt) {
-                uint32_t v[4][VW];   // slots 2 t4 + 0, 1, 8, 9
+                uint32_t v[4][VW];   // slots of rows 2 t4, 2 t4 + 1, and 8 further
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int slot = mt * 16 + 2 * t4 + (i & 1) + 8 * (i >> 1);
-                    const uint8_t *p = vs + slot * D + g * (D / 8);
+                    const unsigned char *p = stage + (kKv8Block + mt * 16 + 8 * (i >> 1)) * D + voff[i & 1];
                     if (D == 128) {
                         const uint4 r = *reinterpret_cast<const uint4 *>(p);
                         v[i][0] = r.x; v[i][1] = r.y; v[i][VW - 2] = r.z; v[i][VW - 1] = r.w;
@@ -439,7 +482,8 @@ __global__ void __launch_bounds__(kAk8Threads, NT == 1 ? 3 : 2) attn_kv8_kernel(
                         const uint2 r = *reinterpret_cast<const uint2 *>(p);
                         v[i][0] = r.x; v[i][1] = r.y;
                     }
-                    if (!clean && (!ok || pos[slot] < 0)) {
+                    // slots that take no part may hold e4m3 NaNs: their codes count as 0
+                    if (E4M3 && !CLEAN && (!ok || pos[mt * 16 + 8 * (i >> 1) + (i & 1 ? vb : va)] < 0)) {
 #pragma unroll
                         for (int u = 0; u < VW; ++u) v[i][u] = 0;
                     }
@@ -460,24 +504,28 @@ __global__ void __launch_bounds__(kAk8Threads, NT == 1 ? 3 : 2) attn_kv8_kernel(
                     }
                 }
             }
-        }
+        };
+        if (clean) rest(std::true_type{});
+        else rest(std::false_type{});
         __syncwarp();   // the stage has been read
         issue(st);
         if (++st == ST) {
             st = 0;
             parity ^= 1u;
         }
-        const Ak8Cursor here = cur;
-        cur.next(rows);
-        if (cur.blk != 0 && x + 1 < x1) continue;
+        const bool ends = cur.blk + 1 == cur.blocks;
+        if (!ends && x + 1 < x1) {
+            ++cur.blk;
+            continue;
+        }
 
         // ---- the end of a (row, head), or of the run
         fresh = true;
-        const bool whole = here.blk + 1 == here.blocks && x - here.blk >= seg0;
+        const bool whole = ends && x - cur.blk >= seg0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < NE; ++e) {
                 float sum = l[nt][e];
                 sum += __shfl_xor_sync(0xffffffffu, sum, 4);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 8);
@@ -488,28 +536,25 @@ __global__ void __launch_bounds__(kAk8Threads, NT == 1 ? 3 : 2) attn_kv8_kernel(
                     const int cc = chunk * W + c;
                     const float inv = sum == 0.f ? 0.f : ak8_exp2(ak8_finite(M[nt][e]) - ak8_finite(m[nt][e])) / sum;
                     uint4 *o = reinterpret_cast<uint4 *>(
-                        a.o + (((long long)here.b * a.T + cc / group) * a.n + h * group + cc % group) * D + g * (D / 8));
+                        a.o + (((long long)cur.b * a.T + cc / group) * a.n + h * group + cc % group) * D + g * (D / 8));
 #pragma unroll
                     for (int i = 0; i < HS; ++i) {
                         uint32_t r[4];
 #pragma unroll
                         for (int u = 0; u < 4; ++u)
-                            r[u] = pack_bf2(acc[4 * i + u][nt][e] * 0x1p-14f * inv, acc[4 * i + u][nt][2 + e] * 0x1p-14f * inv);
+                            r[u] = pack_bf2(acc[4 * i + u][nt][e] * 0x1p-6f * inv, acc[4 * i + u][nt][2 + e] * 0x1p-6f * inv);
                         o[i] = make_uint4(r[0], r[1], r[2], r[3]);
                     }
                 } else {   // slot 0 of this run: its first (row, head); 1: its last
                     float *p = a.part + ((long long)(2 * run + (seg0 == x0 ? 0 : 1)) * cols + c) * (D + kAk8Part);
-                    if (g == 0) {
-                        p[D] = m[nt][e];
-                        p[D + 1] = M[nt][e];
-                        p[D + 2] = sum;
-                    }
+                    if (g == 0) *reinterpret_cast<float4 *>(p + D) = make_float4(m[nt][e], M[nt][e], sum, 0.f);
 #pragma unroll
                     for (int i = 0; i < D / 32; ++i)
                         reinterpret_cast<float4 *>(p + g * (D / 8))[i] =
                             make_float4(acc[2 * i][nt][e], acc[2 * i][nt][2 + e], acc[2 * i + 1][nt][e], acc[2 * i + 1][nt][2 + e]);
                 }
             }
+        cur.next(rows);
     }
     cp_async_wait_all();
 }
@@ -519,120 +564,151 @@ __global__ void __launch_bounds__(kAk8Threads, NT == 1 ? 3 : 2) attn_kv8_kernel(
 // x began and did not end.  Warps take the partials in turn, lanes D / 32 elements.
 template <int D, int NT>
 __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnKv8Args a, int warps, int by_head) {
-    constexpr int W = 8 * NT, E = D / 32;
-    __shared__ float sm_o[4][D], sm_l[4], sm_m[4][2];
+    constexpr int W = 8 * NT, E = D / 32, U = 4;
+    __shared__ float sm_o[4][D], sm_st[4][3];
     griddep_launch();
     griddep_wait();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int group = a.n / a.kv, C = group * a.T, chunks = (C + W - 1) / W;
     const Ak8Rows rows{a.lens, a.B, a.max_seq, a.kv * chunks};
-    const long long total = ak8_total(rows), R = ak8_runs(total, warps);
-    int b, head;
-    long long first, end;   // its blocks
+    int b = by_head ? blockIdx.x / rows.heads : 0, head = 0, before = 0, total = 0;
+    for (int i = lane; i < a.B; i += 32) {
+        const int n = rows.blocks(i);
+        total += n;
+        if (i < b) before += n;
+    }
+    const Ak8Runs runs(__reduce_add_sync(0xffffffffu, total) * rows.heads, warps);
+    int first, end;   // its blocks
     if (by_head) {
-        b = blockIdx.x / rows.heads;
-        head = blockIdx.x % rows.heads;
-        int before = 0;
-        for (int i = lane; i < b; i += 32) before += rows.blocks(i);
+        head = blockIdx.x - b * rows.heads;
         const int blocks = rows.blocks(b);
         if (blocks <= kAk8Short) return;
-        first = (long long)__reduce_add_sync(0xffffffffu, before) * rows.heads + (long long)head * blocks;
+        first = __reduce_add_sync(0xffffffffu, before) * rows.heads + head * blocks;
         end = first + blocks;
     } else {
-        if (blockIdx.x + 1 >= R) return;
+        if (blockIdx.x + 1 >= runs.R) return;
         Ak8Cursor c;
-        const long long x1 = (blockIdx.x + 1) * total / R;
+        const int x1 = runs.start(blockIdx.x + 1);
         c.at(rows, x1);
         if (c.blocks <= kAk8Short || c.blk == 0) return;   // the cut lies between two
         b = c.b;
         head = c.head;
         first = x1 - c.blk;
         end = first + c.blocks;
-        if (blockIdx.x * total / R > first) return;        // an earlier run began it
+        if (runs.start(blockIdx.x) > first) return;        // an earlier run began it
     }
-    const int r0 = (int)(((first + 1) * R - 1) / total), r1 = (int)((end * R - 1) / total);   // the runs it lies in
+    const int r0 = runs.of(first), r1 = runs.of(end - 1);  // the runs it lies in
     if (r0 == r1) return;
-    // run r0 may have begun with an earlier (row, head)
-    Ak8Cursor c;
-    const int slot0 = ak8_cut(rows, r0, R, total, c) != first;
-    const int chunk = head % chunks, h = head / chunks, ncol = min(W, C - chunk * W);
+    const int slot0 = runs.start(r0) != first;             // run r0 began with an earlier (row, head)
+    const int h = head / chunks, chunk = head - h * chunks, ncol = min(W, C - chunk * W);
     for (int col = blockIdx.y; col < ncol; col += gridDim.y) {
-        auto part = [&](int r) {
-            return a.part + ((long long)(2 * r + (r == r0 ? slot0 : 0)) * a.part_cols + col) * (D + kAk8Part);
-        };
-        float mm = -INFINITY, MM = -INFINITY;
-        for (int r = r0 + (int)threadIdx.x; r <= r1; r += 128) {
-            const float2 v = *reinterpret_cast<const float2 *>(part(r) + D);
-            mm = fmaxf(mm, v.x);
-            MM = fmaxf(MM, v.y);
+        // a warp's partials r0 + w, + 4, ..., U of them in flight
+        float m = -INFINITY, M = -INFINITY, l = 0.f, o[E] = {};
+        for (int rr = r0 + w; rr <= r1; rr += 4 * U) {
+            float4 st[U];
+            float v[U][E];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int r = rr + 4 * u;
+                st[u] = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[u][e] = 0.f;
+                if (r <= r1) {
+                    const float *p = a.part + ((long long)(2 * r + (r == r0 ? slot0 : 0)) * a.part_cols + col) * (D + kAk8Part);
+                    st[u] = *reinterpret_cast<const float4 *>(p + D);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) v[u][e] = p[32 * e + lane];
+                }
+            }
+            float mn = m, Mn = M;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                mn = fmaxf(mn, st[u].x);
+                Mn = fmaxf(Mn, st[u].y);
+            }
+            const float mf = ak8_finite(mn), Mf = ak8_finite(Mn), f = ak8_exp2(M - Mf);
+            l *= ak8_exp2(m - mf);
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] *= f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                l += st[u].z * ak8_exp2(st[u].x - mf);
+                const float k = ak8_exp2(st[u].y - Mf);
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] += v[u][e] * k;
+            }
+            m = mn;
+            M = Mn;
         }
-        mm = warp_max(mm);
-        MM = warp_max(MM);
         __syncthreads();   // the previous column's values have been read
-        if (lane == 0) {
-            sm_m[w][0] = mm;
-            sm_m[w][1] = MM;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            mm = fmaxf(mm, sm_m[i][0]);
-            MM = fmaxf(MM, sm_m[i][1]);
-        }
-        float o[E] = {}, ll = 0.f;
-#pragma unroll 4
-        for (int r = r0 + w; r <= r1; r += 4) {
-            const float *p = part(r);
-            const float4 st = *reinterpret_cast<const float4 *>(p + D);
-            const float f = ak8_exp2(st.y - ak8_finite(MM));
-            ll += st.z * ak8_exp2(st.x - ak8_finite(mm));
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[e] += p[32 * e + lane] * f;
-        }
 #pragma unroll
         for (int e = 0; e < E; ++e) sm_o[w][32 * e + lane] = o[e];
-        if (lane == 0) sm_l[w] = ll;
+        if (lane == 0) {
+            sm_st[w][0] = m;
+            sm_st[w][1] = M;
+            sm_st[w][2] = l;
+        }
         __syncthreads();
-        ll = sm_l[0] + sm_l[1] + sm_l[2] + sm_l[3];
         const int d = threadIdx.x, cc = chunk * W + col;
         if (d < D) {
-            const float inv = ll == 0.f ? 0.f : ak8_exp2(ak8_finite(MM) - ak8_finite(mm)) / ll;
-            const float v = (sm_o[0][d] + sm_o[1][d] + sm_o[2][d] + sm_o[3][d]) * 0x1p-14f * inv;
-            a.o[(((long long)b * a.T + cc / group) * a.n + h * group + cc % group) * D + d] = f2bf(v);
+            float mm = -INFINITY, MM = -INFINITY, ll = 0.f, v = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                mm = fmaxf(mm, sm_st[i][0]);
+                MM = fmaxf(MM, sm_st[i][1]);
+            }
+            mm = ak8_finite(mm);
+            MM = ak8_finite(MM);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                ll += sm_st[i][2] * ak8_exp2(sm_st[i][0] - mm);
+                v += sm_o[i][d] * ak8_exp2(sm_st[i][1] - MM);
+            }
+            const float inv = ll == 0.f ? 0.f : ak8_exp2(MM - mm) / ll;
+            a.o[(((long long)b * a.T + cc / group) * a.n + h * group + cc % group) * D + d] = f2bf(v * 0x1p-6f * inv);
         }
     }
 }
 
 // CTAs per SM of a variant with its shared memory, found once per device.
-template <int D, bool E4M3, int NT>
+template <int D, bool E4M3, int NT, bool ONE>
 static cudaError_t ak8_launch(AttnKv8Args a, int sms, cudaStream_t s) {
     constexpr int kDevices = 64, W = 8 * NT;
     static std::atomic<int> known[kDevices][W + 1];
-    const auto kern = attn_kv8_kernel<D, E4M3, NT>;
+    const auto kern = attn_kv8_kernel<D, E4M3, NT, ONE>;
     const int group = a.n / a.kv, C = group * a.T, chunks = (C + W - 1) / W;
     a.part_cols = C < W ? C : W;
-    const int smem = Ak8Stage<D>::smem(a.part_cols);
+    const int smem = Ak8Smem<D>::bytes(a.part_cols);
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     int per_sm = dev < kDevices ? known[dev][a.part_cols].load(std::memory_order_relaxed) : 0;
     if (per_sm == 0) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Ak8Stage<D>::smem(W));
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Ak8Smem<D>::bytes(W));
         if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kAk8Threads, smem);
         if (e != cudaSuccess) return e;
         per_sm = per_sm < 1 ? 1 : per_sm > kAk8MaxPerSm ? kAk8MaxPerSm : per_sm;
         if (dev < kDevices) known[dev][a.part_cols].store(per_sm, std::memory_order_relaxed);
     }
-    const long long heads = (long long)a.B * a.kv * chunks;
-    const long long most = heads * ((a.max_seq + kKv8Block - 1) / kKv8Block);
-    const long long runs = (most + kAk8MinRun - 1) / kAk8MinRun;
+    Ak8Maps maps;
+    const long long slots = (long long)a.B * a.kv * a.max_seq;
+    if (!make_map_rows_u8(&maps.k, a.kc, slots, D, kKv8Block) || !make_map_rows_u8(&maps.v, a.vc, slots, D, kKv8Block))
+        return cudaErrorInvalidValue;
+    const int heads = a.B * a.kv * chunks;
+    const long long most = (long long)heads * a.blocks, runs = (most + kAk8MinRun - 1) / kAk8MinRun;
     const int G = (int)(runs < (long long)sms * per_sm ? runs : (long long)sms * per_sm), warps = G * kAk8Warps;
-    e = launch_pdl_smem(kern, dim3(G), dim3(kAk8Threads), smem, s, a);
-    if (e != cudaSuccess || a.max_seq <= kAk8Short * kKv8Block) return e;   // nothing can have been cut
-    const int by_head = heads < warps, blocks = by_head ? (int)heads : warps;
+    e = launch_pdl_smem(kern, dim3(G), dim3(kAk8Threads), smem, s, a, maps);
+    if (e != cudaSuccess || a.blocks <= kAk8Short) return e;   // nothing can have been cut
+    const int by_head = heads < warps, blocks = by_head ? heads : warps;
     int y = 2 * warps / blocks;   // columns apart while that keeps the grid small
     y = y < 1 ? 1 : y > a.part_cols ? a.part_cols : y;
     return launch_pdl(attn_kv8_join_kernel<D, NT>, dim3(blocks, y), dim3(128), s, a, warps, by_head);
+}
+
+bool attn_kv8_fits(int B, int n, int kv, int T, int max_seq) {
+    const long long C = (long long)n / kv * T, chunks = C <= 8 ? 1 : (C + 15) / 16;
+    return (long long)B * kv * max_seq < (1ll << 31) &&
+           (long long)B * kv * chunks * ((max_seq + kKv8Block - 1) / kKv8Block) < (1ll << 31);
 }
 
 size_t attn_kv8_workspace(int n, int kv, int T, int max_seq, int d, int sms) {
@@ -641,15 +717,17 @@ size_t attn_kv8_workspace(int n, int kv, int T, int max_seq, int d, int sms) {
     return (size_t)sms * kAk8MaxPerSm * kAk8Warps * 2 * (C < W ? C : W) * (d + kAk8Part) * 4;
 }
 
-cudaError_t launch_attn_kv8(const AttnKv8Args &a, int d, int e4m3, int sms, cudaStream_t s) {
+template <int D, bool E4M3>
+static cudaError_t ak8_launch_cols(const AttnKv8Args &a, int sms, cudaStream_t s) {
     // more than 8 columns: two column tiles a pass, or the codes would be read and widened twice
-    const bool wide = a.n / a.kv * a.T > 8;
-    if (d == 64) {
-        if (wide) return e4m3 ? ak8_launch<64, true, 2>(a, sms, s) : ak8_launch<64, false, 2>(a, sms, s);
-        return e4m3 ? ak8_launch<64, true, 1>(a, sms, s) : ak8_launch<64, false, 1>(a, sms, s);
-    }
-    if (wide) return e4m3 ? ak8_launch<128, true, 2>(a, sms, s) : ak8_launch<128, false, 2>(a, sms, s);
-    return e4m3 ? ak8_launch<128, true, 1>(a, sms, s) : ak8_launch<128, false, 1>(a, sms, s);
+    const int C = a.n / a.kv * a.T;
+    if (C == 1) return ak8_launch<D, E4M3, 1, true>(a, sms, s);
+    return C <= 8 ? ak8_launch<D, E4M3, 1, false>(a, sms, s) : ak8_launch<D, E4M3, 2, false>(a, sms, s);
+}
+
+cudaError_t launch_attn_kv8(const AttnKv8Args &a, int d, int e4m3, int sms, cudaStream_t s) {
+    if (d == 64) return e4m3 ? ak8_launch_cols<64, true>(a, sms, s) : ak8_launch_cols<64, false>(a, sms, s);
+    return e4m3 ? ak8_launch_cols<128, true>(a, sms, s) : ak8_launch_cols<128, false>(a, sms, s);
 }
 
 }  // namespace bloom

@@ -111,6 +111,8 @@ cudaError_t launch_linear(const LinearArgs &a, int num_sms, cudaStream_t s);
 bool gemm_make_map(void *map, const void *base, long long rows, long long K, int box_rows);
 // The same for int8 weights [rows][K] (K % 16 == 0): boxes of box_rows x 128 bytes.
 bool gemm_make_map_u8(void *map, const void *base, long long rows, long long K, int box_rows);
+// Whole rows of 64 or 128 bytes, boxes of box_rows of them, swizzled by the row's width.
+bool make_map_rows_u8(void *map, const void *base, long long rows, int row_bytes, int box_rows);
 size_t gemm_map_bytes();
 int gemm_box_rows_x();
 int gemm_box_rows_w();
@@ -288,6 +290,8 @@ struct AttnKv8Args {
     int part_cols = 0;                           // set by the launch
 };
 constexpr int kAk8MaxPerSm = 4;                  // CTAs per SM that the workspace allows for
+// whether blocks and slots can be numbered in 31 bits
+bool attn_kv8_fits(int B, int n, int kv, int T, int max_seq);
 size_t attn_kv8_workspace(int n, int kv, int T, int max_seq, int d, int sms);
 cudaError_t launch_attn_kv8(const AttnKv8Args &a, int d, int e4m3, int sms, cudaStream_t s);
 
