@@ -181,9 +181,9 @@ struct Ak8Maps {   // K and V codes as rows of D bytes
 // Shared memory of a CTA: stages of K and V [warps][stages], 1024-byte aligned; beside
 // each stage its queries [cols][D], positions of the block, of the row's last 32
 // slots, slopes [16], scales [2]; an mbarrier per stage.
-template <int D>
+template <int D, bool ONE>
 struct Ak8Smem {
-    static constexpr int kStages = 256 / D, kStage = 2 * kKv8Block * D, kAll = kAk8Warps * kStages;
+    static constexpr int kStages = (ONE ? 384 : 256) / D, kStage = 2 * kKv8Block * D, kAll = kAk8Warps * kStages;
     __host__ __device__ static constexpr int side(int cols) { return cols * D * 2 + 128 + 128 + 64 + 16; }
     __host__ __device__ static constexpr int bytes(int cols) { return 1024 + kAll * (kStage + side(cols) + 8); }
 };
@@ -204,10 +204,10 @@ __device__ __forceinline__ int ak8_slot(int r) {
 // Columns of a chunk: query c = t * group + i of a key head, t the token, i the query
 // head.  ONE: a single column in all (T = 1, as many key heads as query heads).
 template <int D, bool E4M3, int NT, bool ONE>
-__global__ void __launch_bounds__(kAk8Threads, NT == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kAk8Threads, NT == 1 && !ONE ? 3 : 2)
     attn_kv8_kernel(const __grid_constant__ AttnKv8Args a, const __grid_constant__ Ak8Maps maps) {
     constexpr int HS = D / 64, VW = D / 32, W = 8 * NT, NE = ONE ? 1 : 2;
-    using Smem = Ak8Smem<D>;
+    using Smem = Ak8Smem<D, ONE>;
     constexpr int ST = Smem::kStages;
     constexpr float kLog2e = 1.4426950408889634f, kSlack = 8.f, kLift = 6.f;   // weights up to 2^15 in f16
     extern __shared__ __align__(1024) unsigned char ak8_raw[];
@@ -222,8 +222,8 @@ __global__ void __launch_bounds__(kAk8Threads, NT == 1 ? 3 : 2)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncwarp();
-    griddep_launch();
     griddep_wait();
+    griddep_launch();   // after the wait: what the join kernel finds when it starts is final but for the partials
 
     const int group = ONE ? 1 : a.n / a.kv, C = ONE ? 1 : group * a.T, chunks = ONE ? 1 : (C + W - 1) / W;
     const Ak8Rows rows{a.lens, a.B, a.max_seq, a.kv * chunks};
@@ -567,7 +567,6 @@ __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnKv8Args a,
     constexpr int W = 8 * NT, E = D / 32, U = 4;
     __shared__ float sm_o[4][D], sm_st[4][3];
     griddep_launch();
-    griddep_wait();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int group = a.n / a.kv, C = group * a.T, chunks = (C + W - 1) / W;
     const Ak8Rows rows{a.lens, a.B, a.max_seq, a.kv * chunks};
@@ -578,29 +577,28 @@ __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnKv8Args a,
         if (i < b) before += n;
     }
     const Ak8Runs runs(__reduce_add_sync(0xffffffffu, total) * rows.heads, warps);
-    int first, end;   // its blocks
+    int first = 0, end = 0, blocks = 0;   // its blocks
     if (by_head) {
         head = blockIdx.x - b * rows.heads;
-        const int blocks = rows.blocks(b);
-        if (blocks <= kAk8Short) return;
+        blocks = rows.blocks(b);
         first = __reduce_add_sync(0xffffffffu, before) * rows.heads + head * blocks;
         end = first + blocks;
-    } else {
-        if (blockIdx.x + 1 >= runs.R) return;
+    } else if (blockIdx.x + 1 < runs.R) {
         Ak8Cursor c;
         const int x1 = runs.start(blockIdx.x + 1);
         c.at(rows, x1);
-        if (c.blocks <= kAk8Short || c.blk == 0) return;   // the cut lies between two
         b = c.b;
         head = c.head;
         first = x1 - c.blk;
         end = first + c.blocks;
-        if (runs.start(blockIdx.x) > first) return;        // an earlier run began it
+        // begun by this run, and not just before the cut
+        blocks = c.blk != 0 && runs.start(blockIdx.x) <= first ? c.blocks : 0;
     }
-    const int r0 = runs.of(first), r1 = runs.of(end - 1);  // the runs it lies in
-    if (r0 == r1) return;
+    const int r0 = runs.of(first), r1 = runs.of(max(first, end - 1));   // the runs it lies in
     const int slot0 = runs.start(r0) != first;             // run r0 began with an earlier (row, head)
     const int h = head / chunks, chunk = head - h * chunks, ncol = min(W, C - chunk * W);
+    griddep_wait();                                        // the partials (lengths were final before)
+    if (blocks <= kAk8Short || r0 == r1) return;           // whole
     for (int col = blockIdx.y; col < ncol; col += gridDim.y) {
         // a warp's partials r0 + w, + 4, ..., U of them in flight
         float m = -INFINITY, M = -INFINITY, l = 0.f, o[E] = {};
@@ -678,13 +676,13 @@ static cudaError_t ak8_launch(AttnKv8Args a, int sms, cudaStream_t s) {
     const auto kern = attn_kv8_kernel<D, E4M3, NT, ONE>;
     const int group = a.n / a.kv, C = group * a.T, chunks = (C + W - 1) / W;
     a.part_cols = C < W ? C : W;
-    const int smem = Ak8Smem<D>::bytes(a.part_cols);
+    const int smem = Ak8Smem<D, ONE>::bytes(a.part_cols);
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     int per_sm = dev < kDevices ? known[dev][a.part_cols].load(std::memory_order_relaxed) : 0;
     if (per_sm == 0) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Ak8Smem<D>::bytes(W));
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Ak8Smem<D, ONE>::bytes(W));
         if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kAk8Threads, smem);
         if (e != cudaSuccess) return e;
         per_sm = per_sm < 1 ? 1 : per_sm > kAk8MaxPerSm ? kAk8MaxPerSm : per_sm;
