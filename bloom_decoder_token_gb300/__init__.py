@@ -462,45 +462,43 @@ def _bad(msg: str):
     raise BloomError(1, msg)
 
 
+def _expected(name, t, dtype, shape, device, what="contiguous"):
+    _bad(f"{name}: {what} {dtype} {tuple(shape)} on {device} expected, "
+         f"got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
+
+
 def _dev(name: str, t, dtype, shape, device):
-    """A contiguous device tensor of that type and shape, or an error; its address."""
+    """A contiguous device tensor of that type and shape, or an error; its address
+    (None for None)."""
+    if t is None:
+        return None
     if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        _bad(f"{name}: contiguous {dtype} {tuple(shape)} on {device} expected, "
-             f"got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
+        _expected(name, t, dtype, shape, device)
     return t.data_ptr()
 
 
-def _rows(name: str, t, dtype, shape, device):
-    return None if t is None else _dev(name, t, dtype, shape, device)
-
-
-class _Here:
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *_):
-        return False
-
-
-_HERE_NOW = _Here()
-
-
-def _on(device, stream):
-    """Context of a call on `stream` (None: the device's current one): its device
-    and the stream are current inside, so what is allocated there belongs to it."""
+def _elsewhere(device, stream):
+    """None where a call on `stream` (None: the device's current one) runs on what is
+    current already; else a context that makes its device and stream current, so that
+    what is allocated inside belongs to that stream."""
     if device.type != "cuda":
         _bad(f"tensors on a CUDA device expected, got {device}")
     if stream is None:
         if device.index == torch.cuda.current_device():
-            return _HERE_NOW
+            return None
         stream = torch.cuda.current_stream(device)
     elif stream.device != device:
         _bad(f"stream on {stream.device}, tensors on {device}")
     return torch.cuda.stream(stream)
 
 
+def _raw_stream(device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 KV8_BLOCK = 32
 _KV8_CODES = {torch.int8: 0, torch.float8_e4m3fn: 1}
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
 class KV8(NamedTuple):
@@ -522,25 +520,28 @@ class KV8(NamedTuple):
 
     def c(self) -> KV8C:
         """The C descriptor (bloom_kv8), after checking types, shapes and devices."""
-        k, dev = self.k, self.k.device
-        codes = _KV8_CODES.get(k.dtype)
-        if codes is None or k.dim() != 4:
-            _bad(f"cache codes: int8 or float8_e4m3fn [B][n][S][d] expected, got {k.dtype} "
-                 f"{tuple(k.shape)}")
-        B, n, S, d = k.shape
+        k, v, ks, vs = self
+        codes, shape, dev = _KV8_CODES.get(k.dtype), k.shape, k.device
+        if codes is None or len(shape) != 4 or not k.is_contiguous():
+            _bad(f"cache codes: contiguous int8 or float8_e4m3fn [B][n][S][d] expected, got "
+                 f"{k.dtype} {tuple(shape)}, strides {k.stride()}")
+        B, n, S, d = shape
         sc = (B, n, -(-S // KV8_BLOCK))
-        return KV8C(_dev("k", k, k.dtype, k.shape, dev), _dev("v", self.v, k.dtype, k.shape, dev),
-                    _dev("k_scale", self.k_scale, torch.float32, sc, dev),
-                    _dev("v_scale", self.v_scale, torch.float32, sc, dev), codes, B, n, S, d)
+        return KV8C(k.data_ptr(), _dev("v", v, k.dtype, shape, dev),
+                    _dev("k_scale", ks, _F32, sc, dev), _dev("v_scale", vs, _F32, sc, dev),
+                    codes, B, n, S, d)
 
 
 def _kv8_values(name: str, t, shape, device):
     """(address, strides) of a bf16 [B][T][n][d] view whose d elements lie together."""
-    if t.dtype is not torch.bfloat16 or t.shape != shape or t.device != device or t.stride(3) != 1:
-        _bad(f"{name}: bfloat16 {tuple(shape)} on {device} with unit last stride expected, "
-             f"got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
-    st = [0 if n == 1 else s for n, s in zip(shape, t.stride()[:3])]
-    return t.data_ptr(), (C.c_int64 * 3)(*st)
+    st = t.stride()
+    if t.dtype is not _BF16 or t.shape != shape or t.device != device or st[3] != 1:
+        _expected(name, t, _BF16, shape, device, "unit last stride,")
+    B, T, n, _ = shape      # the stride of a dimension of one element means nothing
+    return t.data_ptr(), _I64x3(st[0] if B > 1 else 0, st[1] if T > 1 else 0, st[2] if n > 1 else 0)
+
+
+_I64x3 = C.c_int64 * 3
 
 
 def op_kv8_write(kv: KV8, k, v, start, count=None, mask=None, flag=None, stream=None):
@@ -555,12 +556,15 @@ def op_kv8_write(kv: KV8, k, v, start, count=None, mask=None, flag=None, stream=
     shape = (B, T, c.n_kv, c.d)
     kp, ks = _kv8_values("k", k, shape, dev)
     vp, vs = _kv8_values("v", v, shape, dev)
-    with _on(dev, stream):
-        check(lib().bloom_op_kv8_write(
-            C.byref(c), kp, ks, vp, vs, T, _dev("start", start, torch.int32, (B,), dev),
-            _rows("count", count, torch.int32, (B,), dev),
-            _rows("mask", mask, torch.uint8, (B, T), dev),
-            _rows("flag", flag, torch.int32, (1,), dev), _stream(stream)))
+    sp, cp = _dev("start", start, _I32, (B,), dev), _dev("count", count, _I32, (B,), dev)
+    mp, fp = _dev("mask", mask, _U8, (B, T), dev), _dev("flag", flag, _I32, (1,), dev)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return op_kv8_write(kv, k, v, start, count, mask, flag)
+    st = lib().bloom_op_kv8_write(C.byref(c), kp, ks, vp, vs, T, sp, cp, mp, fp, _raw_stream(dev))
+    if st:
+        check(st)
 
 
 def op_kv8_read(kv: KV8, start, T: int, count=None, k=None, v=None, flag=None, stream=None):
@@ -570,18 +574,24 @@ def op_kv8_read(kv: KV8, start, T: int, count=None, k=None, v=None, flag=None, s
     c, dev = kv.c(), kv.k.device
     if T < 0:
         _bad(f"T={T}")
-    shape = (c.batch, T, c.n_kv, c.d)
-    with _on(dev, stream):
-        if k is None:
-            k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        if v is None:
-            v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        kp, ks = _kv8_values("k", k, shape, dev)
-        vp, vs = _kv8_values("v", v, shape, dev)
-        check(lib().bloom_op_kv8_read(
-            C.byref(c), kp, ks, vp, vs, T, _dev("start", start, torch.int32, (c.batch,), dev),
-            _rows("count", count, torch.int32, (c.batch,), dev),
-            _rows("flag", flag, torch.int32, (1,), dev), _stream(stream)))
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return op_kv8_read(kv, start, T, count, k, v, flag)
+    B = c.batch
+    shape = (B, T, c.n_kv, c.d)
+    if k is None:
+        k = torch.empty(shape, dtype=_BF16, device=dev)
+    if v is None:
+        v = torch.empty(shape, dtype=_BF16, device=dev)
+    kp, ks = _kv8_values("k", k, shape, dev)
+    vp, vs = _kv8_values("v", v, shape, dev)
+    st = lib().bloom_op_kv8_read(
+        C.byref(c), kp, ks, vp, vs, T, _dev("start", start, _I32, (B,), dev),
+        _dev("count", count, _I32, (B,), dev), _dev("flag", flag, _I32, (1,), dev),
+        _raw_stream(dev))
+    if st:
+        check(st)
     return k, v
 
 
@@ -590,28 +600,42 @@ def op_attn_decode_kv8(q, kv: KV8, pos, slopes, lens, o=None, workspace=None, fl
     """Decode attention over an 8-bit cache: q bf16 [B][T][n][d] for the last T
     tokens of every row (or [B][n][d], T = 1), whose keys are in the cache; pos
     int32 [B][S], -1 masked; slopes float32 [n] or None; lens int32 [B], slots
-    filled.  Returns o bf16 [B][T][n * d] (or [B][n * d])."""
+    filled.  Returns o bf16 [B][T][n * d] (or [B][n * d]).  workspace: uint8,
+    bloom_op_attn_decode_kv8_workspace() bytes, None to allocate it."""
     c, dev = kv.c(), kv.k.device
-    if q.dim() not in (3, 4):
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return op_attn_decode_kv8(q, kv, pos, slopes, lens, o, workspace, flag)
+    B, d = c.batch, c.d
+    if q.dim() == 4:
+        T, n = q.shape[1:3]
+        qp, oshape = _dev("q", q, _BF16, (B, T, n, d), dev), (B, T, n * d)
+    elif q.dim() == 3:
+        T, n = 1, q.shape[1]
+        qp, oshape = _dev("q", q, _BF16, (B, n, d), dev), (B, n * d)
+    else:
         _bad(f"q: [B][T][n][d] or [B][n][d] expected, got {tuple(q.shape)}")
-    T, n = (1, q.shape[1]) if q.dim() == 3 else q.shape[1:3]
-    qshape = (c.batch, n, c.d) if q.dim() == 3 else (c.batch, T, n, c.d)
-    oshape = (c.batch, n * c.d) if q.dim() == 3 else (c.batch, T, n * c.d)
-    qp = _dev("q", q, torch.bfloat16, qshape, dev)
-    with _on(dev, stream):
-        L = lib()
-        if o is None:
-            o = torch.empty(oshape, dtype=torch.bfloat16, device=dev)
-        need = L.bloom_op_attn_decode_kv8_workspace(C.byref(c), T, n)
-        if workspace is None and need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        check(L.bloom_op_attn_decode_kv8(
-            C.byref(c), qp, _dev("pos", pos, torch.int32, (c.batch, c.max_seq), dev),
-            _rows("slopes", slopes, torch.float32, (n,), dev),
-            _dev("lens", lens, torch.int32, (c.batch,), dev), T, n,
-            _dev("o", o, torch.bfloat16, oshape, dev), _p(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size(),
-            _rows("flag", flag, torch.int32, (1,), dev), _stream(stream)))
+    pp, sp = _dev("pos", pos, _I32, (B, c.max_seq), dev), _dev("slopes", slopes, _F32, (n,), dev)
+    lp, fp = _dev("lens", lens, _I32, (B,), dev), _dev("flag", flag, _I32, (1,), dev)
+    L, cr = lib(), C.byref(c)
+    if o is None:
+        o = torch.empty(oshape, dtype=_BF16, device=dev)
+    wp, wn = None, 0
+    if workspace is not None:
+        if workspace.dtype is not _U8 or workspace.dim() != 1:
+            _bad(f"workspace: uint8 [bytes] expected, got {workspace.dtype} {tuple(workspace.shape)}")
+        wn = workspace.numel()
+        wp = _dev("workspace", workspace, _U8, (wn,), dev)
+    else:
+        wn = L.bloom_op_attn_decode_kv8_workspace(cr, T, n)
+        if wn:
+            workspace = torch.empty(wn, dtype=_U8, device=dev)
+            wp = workspace.data_ptr()
+    st = L.bloom_op_attn_decode_kv8(cr, qp, pp, sp, lp, T, n, _dev("o", o, _BF16, oshape, dev), wp,
+                                    wn, fp, _raw_stream(dev))
+    if st:
+        check(st)
     return o
 
 
@@ -621,23 +645,29 @@ def op_logprobs(logits, tokens=None, top: int = 0, stream=None):
     `top` <= 32 most probable tokens: (logp like tokens or None, entropy [B],
     top_ids int32 [B][top], top_logp [B][top])."""
     dev = logits.device
-    if logits.dtype is not torch.float32 or logits.dim() != 2 or logits.stride(1) != 1:
+    if logits.dtype is not _F32 or logits.dim() != 2 or logits.stride(1) != 1:
         _bad(f"logits: float32 [B][V] with unit last stride expected, got {logits.dtype} "
              f"{tuple(logits.shape)}, strides {logits.stride()}")
     B, V = logits.shape
     if not 0 <= top <= 32:
         _bad(f"top={top}: 0 to 32 expected")
-    J, tp, logp = 0, None, None
+    J, tp, logp, lp = 0, None, None, None
     if tokens is not None:
         J = tokens.shape[1] if tokens.dim() == 2 else 1
-        tp = _dev("tokens", tokens, torch.int32, (B, J) if tokens.dim() == 2 else (B,), dev)
-    with _on(dev, stream):
-        if tokens is not None:
-            logp = torch.empty(tokens.shape, device=dev)
-        entropy = torch.empty(B, device=dev)
-        ids = torch.empty(B, top, dtype=torch.int32, device=dev)
-        lps = torch.empty(B, top, device=dev)
-        check(lib().bloom_op_logprobs(logits.data_ptr(), B, V, logits.stride(0) if B > 1 else V, tp,
-                                      J, _p(logp), _p(entropy), top, _p(ids), _p(lps),
-                                      _stream(stream)))
+        tp = _dev("tokens", tokens, _I32, (B, J) if tokens.dim() == 2 else (B,), dev)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return op_logprobs(logits, tokens, top)
+    if tokens is not None:
+        logp = torch.empty(tokens.shape, device=dev)
+        lp = logp.data_ptr()
+    entropy = torch.empty(B, device=dev)
+    ids = torch.empty((B, top), dtype=_I32, device=dev)
+    lps = torch.empty((B, top), device=dev)
+    st = lib().bloom_op_logprobs(logits.data_ptr(), B, V, logits.stride(0) if B > 1 else V, tp, J,
+                                 lp, entropy.data_ptr(), top, ids.data_ptr(), lps.data_ptr(),
+                                 _raw_stream(dev))
+    if st:
+        check(st)
     return logp, entropy, ids, lps
