@@ -90,7 +90,7 @@ __device__ __forceinline__ uint32_t ak8_transpose(uint32_t v) {
 }
 __device__ __forceinline__ float ak8_exp2(float x) {
     float r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));   // relative error 2^-22
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));   // relative error 2^-22
     return r;
 }
 __device__ __forceinline__ float ak8_finite(float m) { return m == -INFINITY ? 0.f : m; }

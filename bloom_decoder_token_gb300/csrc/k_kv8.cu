@@ -43,10 +43,9 @@ __global__ void __launch_bounds__(kKv8Threads) kv8_write_kernel(const Kv8WriteAr
     const long long wid = (long long)blockIdx.x * (kKv8Threads / 32) + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     const int kv = (int)(wid & 1);
-    long long rest = wid >> 1;
-    const int h = (int)(rest % a.n);
-    rest /= a.n;
-    const int i = (int)(rest % a.tiles), b = (int)(rest / a.tiles);
+    const uint32_t rest = (uint32_t)(wid >> 1), tile = rest / (uint32_t)a.n;
+    const int h = (int)(rest - tile * (uint32_t)a.n), b = (int)(tile / (uint32_t)a.tiles);
+    const int i = (int)(tile - (uint32_t)b * (uint32_t)a.tiles);
     if (b >= a.B) return;
     const Kv8Range row = kv8_range(a.start, a.count, b, a.T, a.max_seq, a.err, i == 0 && h == 0 && lane == 0);
     if (row.lo >= row.hi) return;
@@ -91,6 +90,7 @@ __global__ void __launch_bounds__(kKv8Threads) kv8_write_kernel(const Kv8WriteAr
         __syncwarp();
         if (s > old && old > 0.f) {
             const float shift = old / s;
+#pragma unroll 1
             for (int r = r0; r < lo - base; r += RPP) {
                 uint4 *p = reinterpret_cast<uint4 *>(codes + r * D + c0);
                 uint4 w = *p;
@@ -130,55 +130,49 @@ __global__ void __launch_bounds__(kKv8Threads) kv8_write_kernel(const Kv8WriteAr
 
 // One warp: 32 tokens of one (sequence, head), K or V, widened to bf16.  Tokens
 // that the call does not read (idle row, t >= count, beyond the cache) are 0.
+// A lane takes 8 codes of a row, so that its 16-byte store lies beside its
+// neighbours' (16 codes a lane, two 16-byte stores 32 bytes apart: 5.4 TB/s).
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kKv8Threads) kv8_read_kernel(const Kv8ReadArgs a) {
-    constexpr int LPR = D / 16, RPP = 32 / LPR, NP = 32 / RPP;
+    constexpr int LPR = D / 8, RPP = 32 / LPR, NP = 32 / RPP;
     griddep_launch();
     griddep_wait();
     const long long wid = (long long)blockIdx.x * (kKv8Threads / 32) + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     const int kv = (int)(wid & 1);
-    long long rest = wid >> 1;
-    const int h = (int)(rest % a.n);
-    rest /= a.n;
-    const int i = (int)(rest % a.tiles), b = (int)(rest / a.tiles);
+    const uint32_t rest = (uint32_t)(wid >> 1), tile = rest / (uint32_t)a.n;
+    const int h = (int)(rest - tile * (uint32_t)a.n), b = (int)(tile / (uint32_t)a.tiles);
+    const int i = (int)(tile - (uint32_t)b * (uint32_t)a.tiles);
     if (b >= a.B) return;
     const Kv8Range row = kv8_range(a.start, a.count, b, a.T, a.max_seq, a.err, i == 0 && h == 0 && lane == 0);
     const long long bh = (long long)b * a.n + h;
-    const uint8_t *codes = (kv ? a.vc : a.kc) + bh * a.max_seq * D;
+    const int r0 = lane / LPR, c0 = (lane % LPR) * 8;
+    const long long first = row.lo + i * 32;   // the tile's first slot; `here` of its slots are read
+    const int here = row.lo < 0 ? 0 : (int)max(0ll, min(32ll, row.hi - first));
+    const uint8_t *codes = (kv ? a.vc : a.kc) + (bh * a.max_seq + first + r0) * D + c0;
     const float *scale = (kv ? a.vs : a.ks) + bh * a.blocks;
-    uint16_t *dst = (kv ? a.v : a.k) + b * a.stride[kv][0] + h * a.stride[kv][2];
-    const long long ts = a.stride[kv][1];
-    const int r0 = lane / LPR, c0 = (lane % LPR) * 16;
-    uint4 w[NP];
-    float s[NP];
+    uint2 w[NP];
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
-        const long long slot = row.lo + i * 32 + p * RPP + r0;
-        w[p] = make_uint4(0u, 0u, 0u, 0u);
-        s[p] = 0.f;
-        if (row.lo >= 0 && slot < row.hi) {
-            w[p] = *reinterpret_cast<const uint4 *>(codes + slot * D + c0);
-            s[p] = scale[slot / kKv8Block];
-        }
+        w[p] = make_uint2(0u, 0u);
+        if (p * RPP + r0 < here) w[p] = *reinterpret_cast<const uint2 *>(codes + p * RPP * D);
     }
+    // a tile lies in two blocks at most: slots below `turn` in the first
+    const int blk = (int)(first / kKv8Block), turn = kKv8Block - (int)(first - (long long)blk * kKv8Block);
+    const float s0 = here > 0 ? scale[blk] : 0.f, s1 = here > turn ? scale[blk + 1] : 0.f;
+    uint16_t *dst = (kv ? a.v : a.k) + b * a.stride[kv][0] + h * a.stride[kv][2] + (i * 32 + r0) * a.stride[kv][1] + c0;
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
-        const int t = i * 32 + p * RPP + r0;
-        if (t >= a.T) continue;
-        const uint32_t *wp = &w[p].x;
-        uint4 o[2];
-        uint32_t *op = &o[0].x;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float f[4];
-            kv8_widen<E4M3>(wp[e], f);
-            op[2 * e] = pack_bf2(f[0] * s[p], f[1] * s[p]);
-            op[2 * e + 1] = pack_bf2(f[2] * s[p], f[3] * s[p]);
-        }
-        uint4 *q = reinterpret_cast<uint4 *>(dst + t * ts + c0);
-        q[0] = o[0];
-        q[1] = o[1];
+        const int r = p * RPP + r0;
+        if (i * 32 + r >= a.T) continue;
+        const float s = r < turn ? s0 : s1;
+        float f[8];
+        kv8_widen<E4M3>(w[p].x, f);
+        kv8_widen<E4M3>(w[p].y, f + 4);
+        uint4 o = make_uint4(kv8_bf16x2(f[0] * s, f[1] * s), kv8_bf16x2(f[2] * s, f[3] * s),
+                             kv8_bf16x2(f[4] * s, f[5] * s), kv8_bf16x2(f[6] * s, f[7] * s));
+        if (r >= here) o = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4 *>(dst + p * RPP * a.stride[kv][1]) = o;
     }
 }
 

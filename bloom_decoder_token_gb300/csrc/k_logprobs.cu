@@ -8,13 +8,15 @@
 // equal ones by index.
 //
 // Bound by HBM: the logits are read once.  One cluster of up to 8 CTAs per row,
-// each CTA a contiguous slice.  Each thread keeps a running maximum with its
-// index, and sums rescaled when the maximum moves (float32).  The top k need no
-// second pass over the slice: the k-th highest of the maxima of 128 groups of
-// four threads is a lower bound of the slice's k-th highest logit, and only the
-// k groups whose maximum reaches it can hold one.  Their elements (k / 128 of the
-// slice, still in L2) are looked at again, those that reach the bound are ranked
-// by counting, and the cluster's first CTA ranks the lists of all.
+// each CTA a contiguous slice, in rounds of 8192 logits.  Each thread keeps a
+// running maximum and sums rescaled when it moves (float32), the next round's
+// loads in flight meanwhile.  The top k come out of the same pass: after the
+// first round (and, for a large k and many rounds, after the 5th, 25th, 125th)
+// the k-th highest of the maxima of 128 groups of four threads is a lower bound
+// of the k-th highest logit; from then on a logit that reaches the bound becomes
+// a candidate.  The candidates are ranked by counting, and the cluster's first
+// CTA ranks the lists of all.
+#include <float.h>
 #include <math.h>
 
 #include "common.cuh"
@@ -25,9 +27,9 @@ namespace bloom {
 constexpr int kLpThreads = 512;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpMaxCluster = 8;
-constexpr int kLpGroups = kLpThreads / 4;    // of four threads: 16 neighbouring logits a step
-constexpr int kLpStep = 4 * kLpThreads;      // logits of a CTA's step
-constexpr int kLpUnroll = 4;                 // steps whose loads are in flight together
+constexpr int kLpGroups = kLpThreads / 4;    // of four threads
+constexpr int kLpUnroll = 4;                 // float4s of a thread's round
+constexpr int kLpRound = kLpUnroll * kLpThreads;   // float4s of a CTA's round
 constexpr int kLpCand = 1024;                // candidates ranked in shared memory
 constexpr float kLpFar = -1e4f;              // stands for any difference whose exponential is 0
 
@@ -48,7 +50,7 @@ __device__ __forceinline__ lp_u64 lp_max(lp_u64 a, lp_u64 b) { return a > b ? a 
 __device__ __forceinline__ float lp_diff(float a, float b) { return a == b ? 0.f : fmaxf(a - b, kLpFar); }
 __device__ __forceinline__ float lp_exp(float d) {
     float r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(d * 1.4426950408889634f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d * 1.4426950408889634f));   // relative error 2^-22
     return r;
 }
 
@@ -69,18 +71,29 @@ struct LpStat {   // maximum, sum exp(z - m), sum (z - m) exp(z - m)
     }
 };
 
+// How many of p[0, n) are above k; p 16-byte aligned, in shared memory.
+__device__ __forceinline__ int lp_above(const lp_u64 *p, int n, lp_u64 k) {
+    int above = 0;
+#pragma unroll 8
+    for (int j = 0; j + 1 < n; j += 2) {
+        const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(p + j);
+        above += (v.x > k) + (v.y > k);
+    }
+    return above + ((n & 1) && p[n - 1] > k);
+}
+
 struct LpSmem {
-    lp_u64 group[kLpGroups];
-    lp_u64 cand[kLpCand];
+    alignas(16) uint32_t group[kLpGroups];        // order-preserving keys of the groups' maxima
+    int index[kLpCand];                           // candidates
+    alignas(16) lp_u64 cand[kLpCand];
     lp_u64 list[kLpMaxTop];                       // this slice's top, highest first
-    lp_u64 lists[kLpMaxCluster][kLpMaxTop];       // first CTA: every slice's
+    alignas(16) lp_u64 lists[kLpMaxCluster * kLpMaxTop];   // first CTA: every slice's, [cluster][top]
     lp_u64 top[kLpMaxTop];
     LpStat stats[kLpMaxCluster];
     LpStat warp[kLpWarps];
     lp_u64 wmax[kLpWarps];
-    lp_u64 bound;
-    int hot[kLpMaxTop];
-    int nhot, ncand;
+    uint32_t bound[2];                            // of alternate calls of rebound()
+    int ncand;
 };
 
 __device__ __forceinline__ uint32_t lp_rank() {
@@ -99,7 +112,7 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
     const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const uint32_t rank = lp_rank(), cluster = gridDim.x;
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // waited for before the first push
-    if (tid == 0) sm.nhot = sm.ncand = 0;
+    if (tid == 0) sm.ncand = 0;
     griddep_launch();
     griddep_wait();
     const float *z = a.logits + (long long)b * a.ld;
@@ -114,29 +127,39 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
     auto end_at = [&](int i) { return i < head ? i : tail + i - head; };
 
     LpStat st = {-INFINITY, 0.f, 0.f};
-    lp_u64 best = 0;
-    auto take = [&](const float *v, int n, auto index) {   // n logits, index(i) of each ascending
-        float mx = st.m;
+    float bound = __uint_as_float(0x7fc00000u);   // NaN: no logit reaches it
+    auto offer = [&](int i) {
+        const int at = atomicAdd(&sm.ncand, 1);
+        if (at < kLpCand) sm.index[at] = i;
+    };
+    auto offer_all = [&](const float *v, int i0) {   // a round's logits that reach the bound
+        uint32_t reach = 0;
 #pragma unroll
-        for (int i = 0; i < n; ++i) mx = fmaxf(mx, v[i]);
-        if (mx > st.m) {   // rare after the first steps
-            st.shift(mx);
+        for (int j = 0; j < 4 * kLpUnroll; ++j) reach |= v[j] >= bound ? 1u << j : 0u;
+        for (; reach; reach &= reach - 1) {
+            const int j = __ffs(reach) - 1;
+            offer(at0 + 4 * (i0 + (j >> 2) * kLpThreads) + (j & 3));
+        }
+    };
+    auto take = [&](const float *v, int n) {   // into the sums; returns the maximum
+        float mx = v[0];
 #pragma unroll
-            for (int i = n - 1; i >= 0; --i)
-                if (v[i] == mx) best = lp_key(mx, index(i));
+        for (int i = 1; i < n; ++i) mx = fmaxf(mx, v[i]);
+        if (mx > st.m) st.shift(mx);
+        if (st.m == INFINITY) {
+            for (int i = 0; i < n; ++i)
+                if (v[i] == INFINITY) st.s += 1.f;
+            return mx;
         }
 #pragma unroll
         for (int i = 0; i < n; ++i) {
-            // below the maximum; kLpFar for NaN, -inf and in a row of nothing so far
-            float d = fmaxf(v[i] - st.m, kLpFar);
-            if (st.m == INFINITY) d = v[i] == INFINITY ? 0.f : kLpFar;
-            const float e = lp_exp(d);
+            const float d = fmaxf(v[i] - st.m, kLpFar), e = lp_exp(d);   // kLpFar for NaN and -inf
             st.s += e;
             st.t += e * d;
         }
+        return mx;
     };
-    for (int i0 = tid; i0 < nq; i0 += kLpUnroll * kLpThreads) {
-        float v[4 * kLpUnroll];
+    auto load = [&](int i0, float *v) {
 #pragma unroll
         for (int k = 0; k < kLpUnroll; ++k) {
             const int i = i0 + k * kLpThreads;
@@ -147,15 +170,58 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
             v[4 * k + 2] = f.z;
             v[4 * k + 3] = f.w;
         }
-        take(v, 4 * kLpUnroll, [&](int j) { return (uint32_t)(at0 + 4 * (i0 + (j >> 2) * kLpThreads) + (j & 3)); });
-    }
-    if (tid < ends) {   // a lower index than the body's, or a higher one
-        const int i = end_at(tid);
-        const float v[1] = {z[i]};
-        const lp_u64 before = best;
-        const float m0 = st.m;
-        take(v, 1, [&](int) { return (uint32_t)i; });
-        if (v[0] == m0) best = lp_max(before, lp_key(v[0], i));
+    };
+    int turn = 0;
+    auto rebound = [&]() {   // from the maxima so far; by the whole CTA
+        turn ^= 1;
+        const float g = fmaxf(fmaxf(st.m, __shfl_xor_sync(0xffffffffu, st.m, 1)),
+                              fmaxf(__shfl_xor_sync(0xffffffffu, st.m, 2), __shfl_xor_sync(0xffffffffu, st.m, 3)));
+        if ((tid & 3) == 0) sm.group[tid >> 2] = (uint32_t)(lp_key(g, 0u) >> 32);   // 0: nothing
+        if (tid == 0) sm.bound[turn] = 0u;
+        __syncthreads();
+        if (tid < kLpGroups) {
+            const uint32_t mine = sm.group[tid];
+            int above = 0, upto = 0;   // groups above this one; and equal ones too
+#pragma unroll 8
+            for (int i = 0; i < kLpGroups; i += 4) {
+                const uint4 o = *reinterpret_cast<const uint4 *>(&sm.group[i]);
+                above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+                upto += (o.x >= mine) + (o.y >= mine) + (o.z >= mine) + (o.w >= mine);
+            }
+            if (above < a.top && a.top <= upto) sm.bound[turn] = mine;
+        }
+        __syncthreads();
+        // no bound while fewer groups hold logits: all that take part
+        bound = sm.bound[turn] ? lp_logit((lp_u64)sm.bound[turn] << 32) : -FLT_MAX;
+    };
+    const int rounds = (nq + kLpRound - 1) / kLpRound;
+    const float end = tid < ends ? z[end_at(tid)] : -INFINITY;
+    {
+        int next = 0;   // the round after which the bound is found (again, where the first leaves many)
+        auto round = [&](int r, const float *v) {
+            const float mx = take(v, 4 * kLpUnroll);
+            const int i0 = r * kLpRound + tid;
+            if (a.top > 0 && r == next) {
+                const float before = bound;
+                rebound();
+                next = a.top * rounds > kLpCand / 4 ? 5 * next + 4 : rounds;
+                if (!(before == before)) {   // the first
+                    offer_all(v, i0);
+                    if (end >= bound) offer(end_at(tid));
+                    return;
+                }
+            }
+            if (mx >= bound) offer_all(v, i0);
+        };
+        float v[2][4 * kLpUnroll];
+        load(tid, v[0]);
+        if (tid < ends) take(&end, 1);
+        for (int r = 0; r < max(rounds, 1); r += 2) {
+            load((r + 1) * kLpRound + tid, v[1]);
+            round(r, v[0]);
+            load((r + 2) * kLpRound + tid, v[0]);
+            if (r + 1 < rounds) round(r + 1, v[1]);
+        }
     }
 
     // ---- sums of the slice
@@ -167,70 +233,36 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
         r.t = warp_sum(r.t);
         if (lane == 0) sm.warp[w] = r;
     }
-    if (a.top > 0) {
-        lp_u64 g = lp_max(best, __shfl_xor_sync(0xffffffffu, best, 1));
-        g = lp_max(g, __shfl_xor_sync(0xffffffffu, g, 2));
-        if ((tid & 3) == 0) sm.group[tid >> 2] = g;
-    }
+    if (a.top > 0 && tid < kLpMaxTop) sm.list[tid] = 0ull;
     __syncthreads();
     if (a.top > 0) {
-        // ---- the bound: the top-th highest of the group maxima (0: fewer groups hold logits)
-        if (tid < kLpGroups) {
-            const lp_u64 mine = sm.group[tid];
-            int above = 0;
-#pragma unroll 16
-            for (int i = 0; i < kLpGroups; ++i) above += sm.group[i] > mine;
-            if (mine && above < a.top) {
-                sm.hot[atomicAdd(&sm.nhot, 1)] = tid;
-                if (above == a.top - 1) sm.bound = mine;
-            }
-        }
-        if (tid < kLpMaxTop) sm.list[tid] = 0ull;
-        __syncthreads();
-        const int nhot = sm.nhot;
-        const lp_u64 bound = nhot < a.top ? 1ull : sm.bound;
-        // ---- the logits of those groups (and the ends) that reach it
-        auto offer = [&](float v, int i) {
-            const lp_u64 k = lp_key(v, (uint32_t)i);
-            if (k >= bound) {
-                const int at = atomicAdd(&sm.ncand, 1);
-                if (at < kLpCand) sm.cand[at] = k;
-            }
-        };
-        const int steps = (nq + kLpThreads - 1) / kLpThreads;
-        auto each_hot = [&](auto f) {   // every logit of the hot groups, once, by all threads
-            for (long long j = tid; j < (long long)nhot * 4 * steps; j += kLpThreads) {
-                const int i = sm.hot[(int)(j >> 2) % nhot] * 4 + (int)(j & 3) + (int)((j >> 2) / nhot) * kLpThreads;
-                if (i < nq) {
-                    const float4 v = __ldg(zq + i);
-                    f(v.x, at0 + 4 * i);
-                    f(v.y, at0 + 4 * i + 1);
-                    f(v.z, at0 + 4 * i + 2);
-                    f(v.w, at0 + 4 * i + 3);
-                }
-            }
-            if (tid < ends) f(z[end_at(tid)], end_at(tid));
-        };
-        each_hot(offer);
-        __syncthreads();
         const int n = sm.ncand;
         if (n <= kLpCand) {
+            for (int i = tid; i < n; i += kLpThreads) sm.cand[i] = lp_key(z[sm.index[i]], (uint32_t)sm.index[i]);
+            __syncthreads();
             for (int i = tid; i < n; i += kLpThreads) {
                 const lp_u64 k = sm.cand[i];
-                int above = 0;
-                for (int j = 0; j < n; ++j) above += sm.cand[j] > k;
+                const int above = lp_above(sm.cand, n, k);
                 if (above < a.top) sm.list[above] = k;
             }
         } else {
-            // more logits crowd into the hot groups than are ranked (large ones at
-            // regular places): the next highest, one at a time
+            // more logits reached the bounds than are ranked (equal or ascending ones):
+            // the next highest, one at a time
             lp_u64 last = ~0ull;
             for (int r = 0; r < a.top; ++r) {
                 lp_u64 next = 0;
-                each_hot([&](float v, int i) {
+                auto see = [&](float v, int i) {
                     const lp_u64 k = lp_key(v, (uint32_t)i);
                     if (k < last && k > next) next = k;
-                });
+                };
+                for (int i = tid; i < nq; i += kLpThreads) {
+                    const float4 v = __ldg(zq + i);
+                    see(v.x, at0 + 4 * i);
+                    see(v.y, at0 + 4 * i + 1);
+                    see(v.z, at0 + 4 * i + 2);
+                    see(v.w, at0 + 4 * i + 3);
+                }
+                if (tid < ends) see(end, end_at(tid));
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) next = lp_max(next, __shfl_xor_sync(0xffffffffu, next, o));
                 if (lane == 0) sm.wmax[w] = next;
@@ -248,7 +280,7 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
     // ---- to the cluster's first CTA
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // it runs
     if (tid < a.top)
-        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(lp_first(&sm.lists[rank][tid])), "l"(sm.list[tid]) : "memory");
+        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(lp_first(&sm.lists[rank * a.top + tid])), "l"(sm.list[tid]) : "memory");
     if (tid == 0) {
         LpStat r = sm.warp[0];
 #pragma unroll
@@ -279,10 +311,8 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
         __syncthreads();
         const int n = (int)cluster * a.top;
         if (tid < n) {
-            const lp_u64 k = sm.lists[tid / a.top][tid % a.top];
-            int above = 0;
-            for (int i = 0; i < (int)cluster; ++i)
-                for (int j = 0; j < a.top; ++j) above += sm.lists[i][j] > k;
+            const lp_u64 k = sm.lists[tid];
+            const int above = lp_above(sm.lists, n, k);
             if (k && above < a.top) sm.top[above] = k;
         }
         __syncthreads();
@@ -296,9 +326,15 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
 }
 
 cudaError_t launch_logprobs(const LogprobsArgs &a, cudaStream_t s) {
-    // slices of 8192 logits (one round of a CTA's loads) at least, eight of them at most
+    // Two CTAs fit an SM.  Slices of a round (8192 logits) at least, eight at most, and
+    // no more of them than fill the GPU twice: what a slice costs beside its loads
+    // (its bound, its list) is then shared by more logits (509 rows of 250880, top 1:
+    // 87 us in whole rows, 94 in halves, 111 in quarters, 157 in eighths; 32 rows,
+    // top 20, in eighths: 17 us)
     int cluster = 1;
-    while (cluster < kLpMaxCluster && a.V / (2 * cluster) >= kLpUnroll * kLpStep) cluster *= 2;
+    while (cluster < kLpMaxCluster && a.V / (2 * cluster) >= 4 * kLpRound &&
+           2ll * a.B * cluster <= 4ll * bloom_device_sms())
+        cluster *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)cluster, (unsigned)a.B);
     cfg.blockDim = dim3(kLpThreads);

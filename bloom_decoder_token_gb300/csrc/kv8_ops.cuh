@@ -17,10 +17,18 @@ namespace bloom {
 
 constexpr int kKv8Block = 32;   // slots per scale (BLOOM_KV8_BLOCK)
 
-// Four int8 codes of a word -> 4 floats.
+// Four int8 codes of a word -> 4 floats: each byte code + 128 as the last bits of
+// 2^23 + byte, less 2^23 + 128 (exact, and no conversion instruction).
 __device__ __forceinline__ void kv8_widen_s8(uint32_t w, float *f) {
+    w ^= 0x80808080u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = (float)(int)(int8_t)(w >> (8 * i));
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440u + i)) - 8388736.f;
+}
+// Two floats -> bf16x2, rounded half to even.
+__device__ __forceinline__ uint32_t kv8_bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 // Two e4m3 codes -> f16x2 (exact: 4 significant bits, exponents -9 .. 8).
 __device__ __forceinline__ uint32_t kv8_e4m3x2_f16x2(uint16_t w) {
