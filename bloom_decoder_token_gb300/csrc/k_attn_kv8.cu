@@ -48,7 +48,8 @@ namespace bloom {
 
 constexpr int kAk8Warps = 4, kAk8Threads = 32 * kAk8Warps;
 constexpr int kAk8Short = 8;      // blocks of a (row, key head) that is never cut
-constexpr int kAk8MinRun = 4;     // blocks a warp takes at least, while there are warps to spare
+constexpr int kAk8MinRun = 2;     // blocks a warp takes at least (one sequence of 2000, 32 heads: 1, 2, 4, 8
+                                  // blocks at least: 10.9, 9.6, 11.1, 14.5 us)
 constexpr int kAk8Part = 4;       // floats beside a partial's accumulator: m, M, l
 
 // ---- conversions of codes to f16 pairs
@@ -178,12 +179,17 @@ struct Ak8Maps {   // K and V codes as rows of D bytes
     CUtensorMap k, v;
 };
 
+// CTAs an SM, by registers.  One column at D = 128: two with three stages a warp rather
+// than three with two (4 x 30-33k slots, e4m3: 162 against 187 us: HBM serves 1216 streams
+// better than 1824); at D = 64 three (32 x 130..2011 slots: 23 against 25.5 us).
+constexpr int ak8_per_sm(int D, int NT, bool ONE) { return NT == 2 || (ONE && D == 128) ? 2 : 3; }
+
 // Shared memory of a CTA: stages of K and V [warps][stages], 1024-byte aligned; beside
 // each stage its queries [cols][D], positions of the block, of the row's last 32
 // slots, slopes [16], scales [2]; an mbarrier per stage.
 template <int D, bool ONE>
 struct Ak8Smem {
-    static constexpr int kStages = (ONE ? 384 : 256) / D, kStage = 2 * kKv8Block * D, kAll = kAk8Warps * kStages;
+    static constexpr int kStages = D == 128 && ONE ? 3 : 256 / D, kStage = 2 * kKv8Block * D, kAll = kAk8Warps * kStages;
     __host__ __device__ static constexpr int side(int cols) { return cols * D * 2 + 128 + 128 + 64 + 16; }
     __host__ __device__ static constexpr int bytes(int cols) { return 1024 + kAll * (kStage + side(cols) + 8); }
 };
@@ -204,7 +210,7 @@ __device__ __forceinline__ int ak8_slot(int r) {
 // Columns of a chunk: query c = t * group + i of a key head, t the token, i the query
 // head.  ONE: a single column in all (T = 1, as many key heads as query heads).
 template <int D, bool E4M3, int NT, bool ONE>
-__global__ void __launch_bounds__(kAk8Threads, NT == 1 && !ONE ? 3 : 2)
+__global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(D, NT, ONE))
     attn_kv8_kernel(const __grid_constant__ AttnKv8Args a, const __grid_constant__ Ak8Maps maps) {
     constexpr int HS = D / 64, VW = D / 32, W = 8 * NT, NE = ONE ? 1 : 2;
     using Smem = Ak8Smem<D, ONE>;
@@ -559,18 +565,54 @@ __global__ void __launch_bounds__(kAk8Threads, NT == 1 && !ONE ? 3 : 2)
     cp_async_wait_all();
 }
 
-// Joins the partial results of one (row, head), in the order of the runs.  Block x
-// is the (row, head) x where those are fewer than the runs; else the one that run
-// x began and did not end.  Warps take the partials in turn, lanes D / 32 elements.
-template <int D, int NT>
-__global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnKv8Args a, int warps, int by_head) {
-    constexpr int W = 8 * NT, E = D / 32, U = 4;
-    __shared__ float sm_o[4][D], sm_st[4][3];
+// Running joint of partial results (references m and M, sum l, accumulator o).
+template <int E>
+struct Ak8Joint {
+    float m = -INFINITY, M = -INFINITY, l = 0.f, o[E] = {};
+    // U partials at once: st (m, M, l, -) and v
+    template <int U>
+    __device__ __forceinline__ void add(const float4 (&st)[U], const float (&v)[U][E]) {
+        float mn = m, Mn = M;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            mn = fmaxf(mn, st[u].x);
+            Mn = fmaxf(Mn, st[u].y);
+        }
+        const float mf = ak8_finite(mn), Mf = ak8_finite(Mn), f = ak8_exp2(M - Mf);
+        l *= ak8_exp2(m - mf);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] *= f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            l += st[u].z * ak8_exp2(st[u].x - mf);
+            const float k = ak8_exp2(st[u].y - Mf);
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] += v[u][e] * k;
+        }
+        m = mn;
+        M = Mn;
+    }
+    // what o is multiplied by in the end
+    __device__ __forceinline__ float last() const {
+        return l == 0.f ? 0.f : ak8_exp2(ak8_finite(M) - ak8_finite(m)) / l * 0x1p-6f;
+    }
+};
+
+// Joins the partial results of one column of one (row, head), in the order of the
+// runs.  Item i is the (row, head) i where those are fewer than the runs; else the
+// one that run i began and did not end.  SPLIT: one CTA an item and column, the
+// four warps take the partials in turn; else one warp does it all.  Lanes hold D / 32
+// elements, neighbours side by side.
+template <int D, int NT, bool SPLIT>
+__global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnKv8Args a, int warps, int by_head, int items) {
+    constexpr int W = 8 * NT, E = D / 32, U = SPLIT ? 4 : 8, kStep = SPLIT ? 4 : 1;
     griddep_launch();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int id = SPLIT ? (int)blockIdx.x : (int)blockIdx.x * 4 + w;
+    const int item = id / a.part_cols, col = id - item * a.part_cols;
     const int group = a.n / a.kv, C = group * a.T, chunks = (C + W - 1) / W;
     const Ak8Rows rows{a.lens, a.B, a.max_seq, a.kv * chunks};
-    int b = by_head ? blockIdx.x / rows.heads : 0, head = 0, before = 0, total = 0;
+    int b = by_head ? min(item, items - 1) / rows.heads : 0, head = 0, before = 0, total = 0;
     for (int i = lane; i < a.B; i += 32) {
         const int n = rows.blocks(i);
         total += n;
@@ -579,93 +621,70 @@ __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnKv8Args a,
     const Ak8Runs runs(__reduce_add_sync(0xffffffffu, total) * rows.heads, warps);
     int first = 0, end = 0, blocks = 0;   // its blocks
     if (by_head) {
-        head = blockIdx.x - b * rows.heads;
-        blocks = rows.blocks(b);
+        head = item - b * rows.heads;
+        blocks = item < items ? rows.blocks(b) : 0;
         first = __reduce_add_sync(0xffffffffu, before) * rows.heads + head * blocks;
         end = first + blocks;
-    } else if (blockIdx.x + 1 < runs.R) {
+    } else if (item + 1 < runs.R) {
         Ak8Cursor c;
-        const int x1 = runs.start(blockIdx.x + 1);
+        const int x1 = runs.start(item + 1);
         c.at(rows, x1);
         b = c.b;
         head = c.head;
         first = x1 - c.blk;
         end = first + c.blocks;
         // begun by this run, and not just before the cut
-        blocks = c.blk != 0 && runs.start(blockIdx.x) <= first ? c.blocks : 0;
+        blocks = c.blk != 0 && runs.start(item) <= first ? c.blocks : 0;
     }
-    const int r0 = runs.of(first), r1 = runs.of(max(first, end - 1));   // the runs it lies in
+    const int r0 = blocks ? runs.of(first) : 0, r1 = blocks ? runs.of(end - 1) : 0;   // the runs it lies in
     const int slot0 = runs.start(r0) != first;             // run r0 began with an earlier (row, head)
     const int h = head / chunks, chunk = head - h * chunks, ncol = min(W, C - chunk * W);
     griddep_wait();                                        // the partials (lengths were final before)
-    if (blocks <= kAk8Short || r0 == r1) return;           // whole
-    for (int col = blockIdx.y; col < ncol; col += gridDim.y) {
-        // a warp's partials r0 + w, + 4, ..., U of them in flight
-        float m = -INFINITY, M = -INFINITY, l = 0.f, o[E] = {};
-        for (int rr = r0 + w; rr <= r1; rr += 4 * U) {
-            float4 st[U];
-            float v[U][E];
+    if (blocks <= kAk8Short || r0 == r1 || col >= ncol) return;   // whole
+
+    Ak8Joint<E> sum;
+    for (int rr = r0 + (SPLIT ? w : 0); rr <= r1; rr += kStep * U) {   // U partials in flight
+        float4 st[U];
+        float v[U][E];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int r = rr + 4 * u;
-                st[u] = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+        for (int u = 0; u < U; ++u) {
+            const int r = rr + kStep * u;
+            st[u] = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
 #pragma unroll
-                for (int e = 0; e < E; ++e) v[u][e] = 0.f;
-                if (r <= r1) {
-                    const float *p = a.part + ((long long)(2 * r + (r == r0 ? slot0 : 0)) * a.part_cols + col) * (D + kAk8Part);
-                    st[u] = *reinterpret_cast<const float4 *>(p + D);
+            for (int e = 0; e < E; ++e) v[u][e] = 0.f;
+            if (r <= r1) {
+                const float *p = a.part + ((long long)(2 * r + (r == r0 ? slot0 : 0)) * a.part_cols + col) * (D + kAk8Part);
+                st[u] = *reinterpret_cast<const float4 *>(p + D);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) v[u][e] = p[32 * e + lane];
-                }
+                for (int e = 0; e < E; ++e) v[u][e] = p[32 * e + lane];
             }
-            float mn = m, Mn = M;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                mn = fmaxf(mn, st[u].x);
-                Mn = fmaxf(Mn, st[u].y);
-            }
-            const float mf = ak8_finite(mn), Mf = ak8_finite(Mn), f = ak8_exp2(M - Mf);
-            l *= ak8_exp2(m - mf);
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[e] *= f;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                l += st[u].z * ak8_exp2(st[u].x - mf);
-                const float k = ak8_exp2(st[u].y - Mf);
-#pragma unroll
-                for (int e = 0; e < E; ++e) o[e] += v[u][e] * k;
-            }
-            m = mn;
-            M = Mn;
         }
-        __syncthreads();   // the previous column's values have been read
-#pragma unroll
-        for (int e = 0; e < E; ++e) sm_o[w][32 * e + lane] = o[e];
-        if (lane == 0) {
-            sm_st[w][0] = m;
-            sm_st[w][1] = M;
-            sm_st[w][2] = l;
-        }
-        __syncthreads();
-        const int d = threadIdx.x, cc = chunk * W + col;
-        if (d < D) {
-            float mm = -INFINITY, MM = -INFINITY, ll = 0.f, v = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                mm = fmaxf(mm, sm_st[i][0]);
-                MM = fmaxf(MM, sm_st[i][1]);
-            }
-            mm = ak8_finite(mm);
-            MM = ak8_finite(MM);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                ll += sm_st[i][2] * ak8_exp2(sm_st[i][0] - mm);
-                v += sm_o[i][d] * ak8_exp2(sm_st[i][1] - MM);
-            }
-            const float inv = ll == 0.f ? 0.f : ak8_exp2(MM - mm) / ll;
-            a.o[(((long long)b * a.T + cc / group) * a.n + h * group + cc % group) * D + d] = f2bf(v * 0x1p-6f * inv);
-        }
+        sum.add(st, v);
     }
+    if (SPLIT) {
+        __shared__ float sm_o[4][D];
+        __shared__ float4 sm_st[4];
+#pragma unroll
+        for (int e = 0; e < E; ++e) sm_o[w][32 * e + lane] = sum.o[e];
+        if (lane == 0) sm_st[w] = make_float4(sum.m, sum.M, sum.l, 0.f);
+        __syncthreads();
+        if (w != 0) return;
+        float4 st[4];
+        float v[4][E];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            st[u] = sm_st[u];
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[u][e] = sm_o[u][32 * e + lane];
+        }
+        sum = Ak8Joint<E>();
+        sum.add(st, v);
+    }
+    const int cc = chunk * W + col;
+    const float f = sum.last();
+    uint16_t *o = a.o + (((long long)b * a.T + cc / group) * a.n + h * group + cc % group) * D;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[32 * e + lane] = f2bf(sum.o[e] * f);
 }
 
 // CTAs per SM of a variant with its shared memory, found once per device.
@@ -697,10 +716,12 @@ static cudaError_t ak8_launch(AttnKv8Args a, int sms, cudaStream_t s) {
     const int G = (int)(runs < (long long)sms * per_sm ? runs : (long long)sms * per_sm), warps = G * kAk8Warps;
     e = launch_pdl_smem(kern, dim3(G), dim3(kAk8Threads), smem, s, a, maps);
     if (e != cudaSuccess || a.blocks <= kAk8Short) return e;   // nothing can have been cut
-    const int by_head = heads < warps, blocks = by_head ? heads : warps;
-    int y = 2 * warps / blocks;   // columns apart while that keeps the grid small
-    y = y < 1 ? 1 : y > a.part_cols ? a.part_cols : y;
-    return launch_pdl(attn_kv8_join_kernel<D, NT>, dim3(blocks, y), dim3(128), s, a, warps, by_head);
+    const int by_head = heads < warps, items = by_head ? heads : warps;
+    const int todo = items * a.part_cols;
+    // more than 16 partials an item (two rounds of one warp's loads): four warps share them
+    if (warps > 16 * items)
+        return launch_pdl(attn_kv8_join_kernel<D, NT, true>, dim3(todo), dim3(128), s, a, warps, by_head, items);
+    return launch_pdl(attn_kv8_join_kernel<D, NT, false>, dim3((todo + 3) / 4), dim3(128), s, a, warps, by_head, items);
 }
 
 bool attn_kv8_fits(int B, int n, int kv, int T, int max_seq) {
