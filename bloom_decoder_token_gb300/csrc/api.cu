@@ -1523,6 +1523,10 @@ extern "C" bloom_status bloom_op_kv8_read(const bloom_kv8 *kv, void *k, const in
     g_pdl = true;
     bloom_status st = check_kv8_io(kv, k, k_stride, v, v_stride, T, start);
     if (st || T == 0) return st;
+    const int extent[3] = {kv->batch, T, kv->n_kv};
+    for (int i = 0; i < 3; ++i)   // no two elements at one place
+        if (extent[i] > 1 && (k_stride[i] < kv->d || v_stride[i] < kv->d))
+            return fail(BLOOM_E_INVALID, "output strides below d=%d", kv->d);
     Kv8ReadArgs a;
     kv8_io_args(a, kv, k_stride, v_stride, T, start, count, flag);
     a.kc = (const uint8_t *)kv->k;

@@ -305,14 +305,16 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(D, NT, ONE))
     int ref = 0, st = 0, seg0 = x0;            // seg0: first block of the current (row, head) in this run
     uint32_t parity = 0;
     bool fresh = true;
+    float poison = 0.f;            // NaN after a wait that expired
     for (int x = x0; x < x1; ++x) {
         unsigned char *stage = ring + st * Smem::kStage;
         const int *pos = reinterpret_cast<const int *>(sides + st * side_bytes + cols * D * 2);
         // ---- the block's copies
         cp_async_wait<ST - 1>();
         const bool ok = __all_sync(0xffffffffu, tc_mbar_wait(&bar[st], parity, 0));
-        if (!ok) {   // report; a second bounded wait, so that no copy lands later; the block is skipped
+        if (!ok) {   // report; a second bounded wait, so that no copy lands later; what follows is NaN
             if (a.err) atomicOr(a.err, kErrTimeout);
+            poison = __uint_as_float(0x7fc00000u);
             tc_mbar_wait(&bar[st], parity, kTcWaitNs);
         }
         __syncwarp();
@@ -532,7 +534,7 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(D, NT, ONE))
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < NE; ++e) {
-                float sum = l[nt][e];
+                float sum = l[nt][e] + poison;
                 sum += __shfl_xor_sync(0xffffffffu, sum, 4);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 8);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 16);

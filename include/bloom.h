@@ -449,14 +449,15 @@ typedef struct {
 
 /* `flag` of the three calls below: a device int32 word, or NULL, that a kernel
  * ORs a bit of bloom_check_device into when it meets a bad value (2: a slot
- * beyond the cache; 8: a bounded wait expired, the call's output is invalid). */
+ * beyond the cache; 8: a bounded wait, of about two seconds, expired: outputs of
+ * the call are NaN). */
 
 /* Quantise new keys and values into the cache: token t of row b goes to slot
  * start[b] + t, t < count[b] (count NULL: T; clamped to 0..T).  k and v: bf16,
  * element (b, t, head, e) at b * stride[0] + t * stride[1] + head * stride[2] +
  * e, strides in elements, multiples of 8, k_stride and v_stride HOST arrays of
  * three (views of a fused QKV row, of [B][T][n][d] and of a bf16 cache's
- * [B][n][S][d] all fit); k and v 16-byte aligned.  start, count: device int32
+ * [B][n][S][d] all fit; a stride may be 0); k and v 16-byte aligned.  start, count: device int32
  * [batch]; mask: device uint8 [batch][T] or NULL.
  *  - A block's scale is the smallest power of two, 2^-126 at least, with
  *    amax <= 127 * scale (int8) or 448 * scale (e4m3) over its tokens, 0 if all
@@ -472,7 +473,7 @@ typedef struct {
  *    are dropped (flag 2).
  *  - An infinity or NaN among a block's tokens makes its scale NaN: all of the
  *    block reads as NaN until it is started afresh.
- * The values must not overlap the cache.  T = 0 does nothing. */
+ * The values must not overlap the cache.  T <= max_seq; T = 0 does nothing. */
 bloom_status bloom_op_kv8_write(const bloom_kv8 *kv, const void *k, const int64_t *k_stride,
                                 const void *v, const int64_t *v_stride, int32_t T,
                                 const int32_t *start, const int32_t *count, const uint8_t *mask,
@@ -481,7 +482,8 @@ bloom_status bloom_op_kv8_write(const bloom_kv8 *kv, const void *k, const int64_
 /* Read slots start[b] + t, t < T, back as bf16 values (rounded half to even;
  * exact for scales that bloom_op_kv8_write made) into k and v, addressed as in
  * bloom_op_kv8_write.  Tokens t >= count[b], of idle rows (start[b] < 0) and
- * beyond max_seq (flag 2) are written as 0. */
+ * beyond max_seq (flag 2) are written as 0.  The strides of dimensions of more
+ * than one element are at least d; k, v and the cache must not overlap. */
 bloom_status bloom_op_kv8_read(const bloom_kv8 *kv, void *k, const int64_t *k_stride, void *v,
                                const int64_t *v_stride, int32_t T, const int32_t *start,
                                const int32_t *count, int32_t *flag, void *stream);
@@ -497,6 +499,7 @@ bloom_status bloom_op_kv8_read(const bloom_kv8 *kv, void *k, const int64_t *k_st
  * counts as max_seq (flag 2).  o bf16 [batch][T][n_head * d].  Masked slots and
  * slots from lens on are never looked at: they may hold anything.  A block with
  * a NaN scale makes every query that sees a slot of it NaN, in that head.
+ * batch * n_kv * max_seq is below 2^31 (BLOOM_E_UNSUPPORTED otherwise, as T > 32).
  * workspace: device scratch of bloom_op_attn_decode_kv8_workspace() bytes (0:
  * NULL will do), 16-byte aligned, contents immaterial; calls that may overlap on
  * the GPU (other streams, graphs that may run at once) need one each. */

@@ -4,6 +4,8 @@ together, against the plain float64 forms (kv8_plain).
 Codes, scales and values read back must be equal to the last bit (every scale is
 a power of two, so the only rounding is the code's).  Attention's bound is
 derived in kv8_plain.attend."""
+import ctypes as C
+
 import numpy as np
 import pytest
 import torch
@@ -429,6 +431,63 @@ def test_attention_long_cache():
     for b in (0, 2):
         assert bool((np.abs(got[b] - ref[b]) <= tol[b] + 1e-30).all())
     assert (got[1] == 0).all()      # every position masked
+
+
+def test_attention_explicit_workspace():
+    g = rng(32)
+    lens = (1500, 700)
+    cache, pos, kf, vf = filled(2, 4, 1600, 64, torch.int8, lens, g)
+    q = bf((2, 2, 8, 64), g)
+    c = cache.c()
+    need = bg.lib().bloom_op_attn_decode_kv8_workspace(C.byref(c), 2, 8)
+    assert need > 0
+    ws = torch.full((need + 64,), 0xFF, dtype=torch.uint8, device=DEV)      # NaNs: contents do not matter
+    o = check_attention(cache, pos, kf, vf, q, slopes_of(8), lens, workspace=ws)
+    out = torch.full_like(o, 3.0)
+    o2 = bg.op_attn_decode_kv8(q.to(DEV), cache, pos.to(DEV), slopes_of(8).to(DEV), i32(*lens).to(DEV), o=out, workspace=ws[:need])
+    assert o2 is out and torch.equal(o, out)
+    assert (ws[need:] == 0xFF).all()
+    for bad in (ws[:need - 1], ws[1:need + 1], ws[:0], ws.cpu(), ws.view(torch.int8)):
+        with pytest.raises(bg.BloomError):
+            bg.op_attn_decode_kv8(q.to(DEV), cache, pos.to(DEV), slopes_of(8).to(DEV), i32(*lens).to(DEV), workspace=bad)
+
+
+def test_attention_many_rows():
+    """More rows than a warp scans at once, most of them idle or short, some cut."""
+    g = rng(33)
+    B, S = 2500, 600
+    lens = [0] * B
+    for i in range(0, B, 7):
+        lens[i] = (i * 37) % 601
+    cache, pos, kf, vf = filled(B, 1, S, 64, torch.float8_e4m3fn, lens, g)
+    check_attention(cache, pos, kf, vf, bf((B, 1, 2, 64), g), slopes_of(2), lens)
+
+
+def test_first_call_of_a_form_inside_a_capture():
+    """Nothing that a form sets up on its first call is forbidden in a capture."""
+    g = rng(34)
+    lens = (400, 90)
+    for T, n, kv, codes in [(3, 3, 3, torch.int8), (7, 5, 5, torch.float8_e4m3fn), (11, 4, 2, torch.int8)]:
+        cache, pos, kf, vf = filled(2, kv, 420, 128, codes, lens, g)
+        q, posd, sl, ln = bf((2, T, n, 128), g), pos.to(DEV), slopes_of(n).to(DEV), i32(*lens).to(DEV)
+        qd = q.to(DEV)
+        torch.cuda.synchronize()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            o = bg.op_attn_decode_kv8(qd, cache, posd, sl, ln)
+        gr.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, check_attention(cache, pos, kf, vf, q, slopes_of(n), lens))
+
+
+def test_write_of_one_head_to_all():
+    """Source strides of 0: one key head's values written to every head of the cache."""
+    g = rng(35)
+    k, v = bf((2, 40, 1, 64), g).to(DEV).expand(2, 40, 5, 64), bf((1, 40, 5, 64), g).to(DEV).expand(2, 40, 5, 64)
+    kv = garbage(2, 5, 64, 64, torch.int8, g)
+    m = mirror(kv)
+    write_both(kv, m, k, v, i32(0, 0))
+    check(kv, m)
 
 
 # ------------------------------------------------------ streams, graphs, a run

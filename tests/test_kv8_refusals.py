@@ -60,6 +60,10 @@ def test_write_and_read_refusals(lib):
                                    (X, neg, X, ST, 4, X), (X, ST, X, ST, -1, X), (X, ST, X, ST, 65, X)]:
         assert w(c, k, ks, v, vs, T, start, None, None, None, None) == 1
         assert r(c, k, ks, v, vs, T, start, None, None, None) == 1
+    # outputs that would lie on one another; sources may
+    for bad in [(0, 128, 64), (512, 0, 64), (512, 128, 0), (512, 32, 64)]:
+        assert r(c, X, (C.c_int64 * 3)(*bad), X, ST, 4, X, None, None, None) == 1
+        assert r(c, X, ST, X, (C.c_int64 * 3)(*bad), 4, X, None, None, None) == 1
     # nothing to do is no error, whatever the pointers
     assert w(c, None, None, None, None, 0, None, None, None, None, None) == 0
     assert r(c, None, None, None, None, 0, None, None, None, None) == 0
@@ -82,7 +86,11 @@ def test_attention_refusals(lib):
     assert f(c, X, X, X, X, 1, 0, X, X, big, None, None) == 1
     assert f(c, X, X, X, X, 0, 2, X, X, big, None, None) == 1
     assert f(c, X, X, X, X, 33, 2, X, X, big, None, None) == 2
+    huge = desc(batch=1 << 12, n_kv=16, max_seq=1 << 15)       # 2^31 slots
+    assert f(C.byref(huge), X, X, X, X, 1, 16, X, X, big, None, None) == 2
+    c = C.byref(desc(max_seq=1000))                            # rows that may be cut need a workspace
     need = lib.bloom_op_attn_decode_kv8_workspace(c, 1, 2)
+    assert need > 0
     if need:
         assert f(c, X, X, X, X, 1, 2, X, None, 0, None, None) == 1
         assert f(c, X, X, X, X, 1, 2, X, X, need - 1, None, None) == 1
