@@ -521,15 +521,15 @@ class KV8(NamedTuple):
     def c(self) -> KV8C:
         """The C descriptor (bloom_kv8), after checking types, shapes and devices."""
         k, v, ks, vs = self
-        codes, shape, dev = _KV8_CODES.get(k.dtype), k.shape, k.device
+        dt, shape, dev = k.dtype, k.shape, k.device
+        codes = _KV8_CODES.get(dt)
         if codes is None or len(shape) != 4 or not k.is_contiguous():
             _bad(f"cache codes: contiguous int8 or float8_e4m3fn [B][n][S][d] expected, got "
-                 f"{k.dtype} {tuple(shape)}, strides {k.stride()}")
+                 f"{dt} {tuple(shape)}, strides {k.stride()}")
         B, n, S, d = shape
         sc = (B, n, -(-S // KV8_BLOCK))
-        return KV8C(k.data_ptr(), _dev("v", v, k.dtype, shape, dev),
-                    _dev("k_scale", ks, _F32, sc, dev), _dev("v_scale", vs, _F32, sc, dev),
-                    codes, B, n, S, d)
+        return KV8C(k.data_ptr(), _dev("v", v, dt, shape, dev), _dev("k_scale", ks, _F32, sc, dev),
+                    _dev("v_scale", vs, _F32, sc, dev), codes, B, n, S, d)
 
 
 def _kv8_values(name: str, t, shape, device):
@@ -578,14 +578,21 @@ def op_kv8_read(kv: KV8, start, T: int, count=None, k=None, v=None, flag=None, s
     if there is not None:
         with there:
             return op_kv8_read(kv, start, T, count, k, v, flag)
-    B = c.batch
-    shape = (B, T, c.n_kv, c.d)
+    B, n, d = c.batch, c.n_kv, c.d
+    shape = (B, T, n, d)
+    ks = vs = None
+    if k is None or v is None:
+        dense = _I64x3(T * n * d, n * d, d)
     if k is None:
-        k = torch.empty(shape, dtype=_BF16, device=dev)
+        k, ks = torch.empty(shape, dtype=_BF16, device=dev), dense
+        kp = k.data_ptr()
     if v is None:
-        v = torch.empty(shape, dtype=_BF16, device=dev)
-    kp, ks = _kv8_values("k", k, shape, dev)
-    vp, vs = _kv8_values("v", v, shape, dev)
+        v, vs = torch.empty(shape, dtype=_BF16, device=dev), dense
+        vp = v.data_ptr()
+    if ks is None:
+        kp, ks = _kv8_values("k", k, shape, dev)
+    if vs is None:
+        vp, vs = _kv8_values("v", v, shape, dev)
     st = lib().bloom_op_kv8_read(
         C.byref(c), kp, ks, vp, vs, T, _dev("start", start, _I32, (B,), dev),
         _dev("count", count, _I32, (B,), dev), _dev("flag", flag, _I32, (1,), dev),

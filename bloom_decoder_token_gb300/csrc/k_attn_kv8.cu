@@ -47,7 +47,8 @@
 namespace bloom {
 
 constexpr int kAk8Warps = 4, kAk8Threads = 32 * kAk8Warps;
-constexpr int kAk8Short = 8;      // blocks of a (row, key head) that is never cut
+constexpr int kAk8Short = 4;      // blocks of a (row, key head) that is never cut (32 heads x 128: 1 sequence
+                                  // of 250, 8 blocks against 4: 12.4, 7.6 us; 32 of 128, 4 against 2: 10.9, 12.8 us)
 constexpr int kAk8MinRun = 2;     // blocks a warp takes at least (one sequence of 2000, 32 heads: 1, 2, 4, 8
                                   // blocks at least: 10.9, 9.6, 11.1, 14.5 us)
 constexpr int kAk8Part = 4;       // floats beside a partial's accumulator: m, M, l
