@@ -25,11 +25,11 @@
 //    multiplied with exact codes into float32 accumulators.  Both references
 //    move, and what was summed is rescaled, only when a score passes one by
 //    more than 2^8.
-//  * Work is cut evenly whatever the lengths: the scale blocks (32 slots) of all
-//    rows and key heads are numbered in one sequence, and each resident warp takes
-//    an equal run of it.  A (row, key head) of at most kAk8Short blocks is left
-//    whole; a longer one that falls into several runs leaves partial results,
-//    which a second kernel joins in order.
+//  * Work is cut evenly whatever the lengths: the blocks (32 slots at d = 128, 64 at
+//    64) of all rows and key heads are numbered in one sequence, and each resident
+//    warp takes an equal run of it.  A (row, key head) of at most kAk8Whole slots
+//    is left whole; a longer one that falls into several runs leaves partial
+//    results, which a second kernel joins in order.
 //  * A warp keeps its own ring of stages ahead of it, one block each: K and V by TMA
 //    (swizzled by the row's width, and the slots dealt to the fragments' rows, so
 //    that the fragment loads meet no bank twice), and by cp.async positions,
@@ -47,10 +47,12 @@
 namespace bloom {
 
 constexpr int kAk8Warps = 4, kAk8Threads = 32 * kAk8Warps;
-constexpr int kAk8Short = 4;      // blocks of a (row, key head) that is never cut (32 heads x 128: 1 sequence
-                                  // of 250, 8 blocks against 4: 12.4, 7.6 us; 32 of 128, 4 against 2: 10.9, 12.8 us)
-constexpr int kAk8MinRun = 2;     // blocks a warp takes at least (one sequence of 2000, 32 heads: 1, 2, 4, 8
-                                  // blocks at least: 10.9, 9.6, 11.1, 14.5 us)
+// Slots of a block of work: 4 KB of K and of V, one scale block at d = 128, two at 64.
+__host__ __device__ constexpr int ak8_slots(int D) { return 4096 / D; }
+constexpr int kAk8Whole = 128;    // a (row, key head) of up to so many slots is never cut (32 heads x 128: 1
+                                  // sequence of 250, 256 against 128: 12.4, 7.6 us; 32 of 128, 128 against 64: 10.9, 12.8)
+constexpr int kAk8MinRun = 64;    // slots a warp takes at least (one sequence of 2000, 32 heads x 128: 32, 64, 128,
+                                  // 256 slots at least: 10.9, 9.6, 11.1, 14.5 us)
 constexpr int kAk8Part = 4;       // floats beside a partial's accumulator: m, M, l
 
 // ---- conversions of codes to f16 pairs
@@ -98,14 +100,17 @@ __device__ __forceinline__ float ak8_exp2(float x) {
 __device__ __forceinline__ float ak8_finite(float m) { return m == -INFINITY ? 0.f : m; }
 
 // ---- where a block number lies
+template <int D>
 struct Ak8Rows {
+    static constexpr int kSlots = ak8_slots(D);
     const int *lens;
     int B, max_seq, heads;   // heads: (key head, column chunk) pairs of a row
     __device__ __forceinline__ int len(int b) const { return max(0, min(lens[b], max_seq)); }
     // blocks of one head of row b; at least one, so that every output is written
-    __device__ __forceinline__ int blocks(int b) const { return max(1, (len(b) + kKv8Block - 1) / kKv8Block); }
+    __device__ __forceinline__ int blocks(int b) const { return max(1, (len(b) + kSlots - 1) / kSlots); }
 };
-__device__ __forceinline__ int ak8_total(const Ak8Rows &r) {   // by the whole warp
+template <int D>
+__device__ __forceinline__ int ak8_total(const Ak8Rows<D> &r) {   // by the whole warp
     int t = 0;
     for (int b = threadIdx.x & 31; b < r.B; b += 32) t += r.blocks(b);
     return __reduce_add_sync(0xffffffffu, t) * r.heads;
@@ -113,7 +118,8 @@ __device__ __forceinline__ int ak8_total(const Ak8Rows &r) {   // by the whole w
 struct Ak8Cursor {   // a block: its row, head, place in that head; the row's length and blocks a head
     int b, head, blk, len, blocks;
     // block number x < total, by the whole warp
-    __device__ __forceinline__ void at(const Ak8Rows &r, int x) {
+    template <int D>
+    __device__ __forceinline__ void at(const Ak8Rows<D> &r, int x) {
         const int lane = threadIdx.x & 31;
         int before = 0;
         for (int b0 = 0;; b0 += 32) {
@@ -137,11 +143,13 @@ struct Ak8Cursor {   // a block: its row, head, place in that head; the row's le
         head = x / blocks;
         blk = x - head * blocks;
     }
-    __device__ __forceinline__ void row(const Ak8Rows &r) {
+    template <int D>
+    __device__ __forceinline__ void row(const Ak8Rows<D> &r) {
         len = b < r.B ? r.len(b) : 0;
         blocks = b < r.B ? r.blocks(b) : 1;
     }
-    __device__ __forceinline__ void next(const Ak8Rows &r) {
+    template <int D>
+    __device__ __forceinline__ void next(const Ak8Rows<D> &r) {
         if (++blk < blocks) return;
         blk = 0;
         if (++head < r.heads) return;
@@ -151,10 +159,12 @@ struct Ak8Cursor {   // a block: its row, head, place in that head; the row's le
     }
 };
 // The runs: R equal shares of `total` blocks, the first `rem` one longer.
+template <int D>
 struct Ak8Runs {
+    static constexpr int kWhole = kAk8Whole / ak8_slots(D), kMin = kAk8MinRun / ak8_slots(D);   // in blocks
     int total, R, q, rem;
     __device__ __forceinline__ Ak8Runs(int t, int warps) : total(t) {
-        R = min(warps, (t + kAk8MinRun - 1) / kAk8MinRun);
+        R = min(warps, (t + kMin - 1) / kMin);
         q = t / R;
         rem = t - q * R;
     }
@@ -164,11 +174,11 @@ struct Ak8Runs {
         return y < 0 ? x / (q + 1) : rem + y / q;
     }
     // where run k begins in earnest: a short (row, head) belongs to the run of its last block
-    __device__ __forceinline__ int cut(const Ak8Rows &r, int k, Ak8Cursor &c) const {
+    __device__ __forceinline__ int cut(const Ak8Rows<D> &r, int k, Ak8Cursor &c) const {
         int x = start(k);
         if (x >= total) return total;
         c.at(r, x);
-        if (c.blocks <= kAk8Short) {
+        if (c.blocks <= kWhole) {
             x -= c.blk;
             c.blk = 0;
         }
@@ -180,18 +190,19 @@ struct Ak8Maps {   // K and V codes as rows of D bytes
     CUtensorMap k, v;
 };
 
-// CTAs an SM, by registers.  One column at D = 128: two with three stages a warp rather
-// than three with two (4 x 30-33k slots, e4m3: 162 against 187 us: HBM serves 1216 streams
-// better than 1824); at D = 64 three (32 x 130..2011 slots: 23 against 25.5 us).
-constexpr int ak8_per_sm(int D, int NT, bool ONE) { return NT == 2 || (ONE && D == 128) ? 2 : 3; }
+// CTAs an SM, by registers.  One column: two with three stages a warp rather than three
+// with two (HBM serves 1216 streams better than 1824; e4m3, 4 x 30-33k slots, 32 x 128:
+// 162 against 187 us; 32 x 130..2011 slots, 16 x 64: 20.5 against 22.5 us).
+constexpr int ak8_per_sm(int NT, bool ONE) { return NT == 2 || ONE ? 2 : 3; }
 
 // Shared memory of a CTA: stages of K and V [warps][stages], 1024-byte aligned; beside
 // each stage its queries [cols][D], positions of the block, of the row's last 32
-// slots, slopes [16], scales [2]; an mbarrier per stage.
+// slots, slopes [16], scales [2 or 4]; an mbarrier per stage.
 template <int D, bool ONE>
 struct Ak8Smem {
-    static constexpr int kStages = D == 128 && ONE ? 3 : 256 / D, kStage = 2 * kKv8Block * D, kAll = kAk8Warps * kStages;
-    __host__ __device__ static constexpr int side(int cols) { return cols * D * 2 + 128 + 128 + 64 + 16; }
+    static constexpr int kStages = ONE ? 3 : 2, kSlots = ak8_slots(D), kStage = 2 * kSlots * D;
+    static constexpr int kAll = kAk8Warps * kStages, kPos = 4 * (kSlots + 32);   // bytes of positions
+    __host__ __device__ static constexpr int side(int cols) { return cols * D * 2 + kPos + 64 + 16; }
     __host__ __device__ static constexpr int bytes(int cols) { return 1024 + kAll * (kStage + side(cols) + 8); }
 };
 
@@ -211,9 +222,10 @@ __device__ __forceinline__ int ak8_slot(int r) {
 // Columns of a chunk: query c = t * group + i of a key head, t the token, i the query
 // head.  ONE: a single column in all (T = 1, as many key heads as query heads).
 template <int D, bool E4M3, int NT, bool ONE>
-__global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(D, NT, ONE))
+__global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(NT, ONE))
     attn_kv8_kernel(const __grid_constant__ AttnKv8Args a, const __grid_constant__ Ak8Maps maps) {
     constexpr int HS = D / 64, VW = D / 32, W = 8 * NT, NE = ONE ? 1 : 2;
+    constexpr int SL = ak8_slots(D), MT = SL / 16, NB = SL / kKv8Block;   // slots, fragments of 16, scale blocks of a block
     using Smem = Ak8Smem<D, ONE>;
     constexpr int ST = Smem::kStages;
     constexpr float kLog2e = 1.4426950408889634f, kSlack = 8.f, kLift = 6.f;   // weights up to 2^15 in f16
@@ -233,14 +245,14 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(D, NT, ONE))
     griddep_launch();   // after the wait: what the join kernel finds when it starts is final but for the partials
 
     const int group = ONE ? 1 : a.n / a.kv, C = ONE ? 1 : group * a.T, chunks = ONE ? 1 : (C + W - 1) / W;
-    const Ak8Rows rows{a.lens, a.B, a.max_seq, a.kv * chunks};
+    const Ak8Rows<D> rows{a.lens, a.B, a.max_seq, a.kv * chunks};
     if (a.err && blockIdx.x == 0)
         for (int b = threadIdx.x; b < a.B; b += kAk8Threads)
             if (a.lens[b] > a.max_seq) atomicOr(a.err, kErrSlot);
-    const Ak8Runs runs(ak8_total(rows), (int)gridDim.x * kAk8Warps);
+    const Ak8Runs<D> runs(ak8_total(rows), (int)gridDim.x * kAk8Warps);
     const int run = w * (int)gridDim.x + (int)blockIdx.x;   // runs spread over the CTAs first
     if (run >= runs.R) return;
-    Ak8Cursor cur, ahead;
+    Ak8Cursor cur = {}, ahead = {};
     const int x1 = runs.cut(rows, run + 1, ahead), x0 = runs.cut(rows, run, cur);
     if (x0 >= x1) return;
     ahead = cur;
@@ -250,16 +262,16 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(D, NT, ONE))
     auto issue = [&](int st) {
         if (xa < x1) {
             unsigned char *stage = ring + st * Smem::kStage, *side = sides + st * side_bytes;
-            int *pos = reinterpret_cast<int *>(side + cols * D * 2);   // [32], [32], slopes, scales
-            const int base = ahead.blk * kKv8Block;
+            int *pos = reinterpret_cast<int *>(side + cols * D * 2);   // [SL], [32], slopes, scales
+            const int base = ahead.blk * SL;
             const int *rowpos = a.pos + (long long)ahead.b * a.max_seq;
             if (xa == x0 || ahead.blk == 0) {   // the first block of a (row, head) in this run
                 const int h = ONE ? ahead.head : ahead.head / chunks, c0 = (ahead.head - h * chunks) * W;
                 bh = ahead.b * a.kv + h;
-                if (ahead.len - 1 - lane >= 0) ak8_async4(pos + 32 + lane, rowpos + ahead.len - 1 - lane);
-                else pos[32 + lane] = -1;
+                if (ahead.len - 1 - lane >= 0) ak8_async4(pos + SL + lane, rowpos + ahead.len - 1 - lane);
+                else pos[SL + lane] = -1;
                 const int nc = ONE ? 1 : min(W, C - c0);
-                if (a.slopes && lane < nc) ak8_async4(pos + 64 + lane, a.slopes + h * group + (c0 + lane) % group);
+                if (a.slopes && lane < nc) ak8_async4(pos + SL + 32 + lane, a.slopes + h * group + (c0 + lane) % group);
                 for (int i = lane; i < nc * (D / 8); i += 32) {
                     const int c = c0 + i / (D / 8), e = i % (D / 8) * 8;
                     cp_async16(side + (i / (D / 8) * D + e) * 2,
@@ -271,11 +283,15 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(D, NT, ONE))
                 asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(tc_smem(&bar[st])), "r"(Smem::kStage)
                              : "memory");
                 tc_tma_2d(stage, &maps.k, 0, bh * a.max_seq + base, &bar[st]);
-                tc_tma_2d(stage + kKv8Block * D, &maps.v, 0, bh * a.max_seq + base, &bar[st]);
+                tc_tma_2d(stage + SL * D, &maps.v, 0, bh * a.max_seq + base, &bar[st]);
             }
-            if (base + lane < ahead.len) ak8_async4(pos + lane, rowpos + base + lane);
-            else pos[lane] = -1;
-            if (lane < 2) ak8_async4(pos + 80 + lane, (lane ? a.vs : a.ks) + (long long)bh * a.blocks + ahead.blk);
+#pragma unroll
+            for (int i = 0; i < SL; i += 32) {
+                if (base + i + lane < ahead.len) ak8_async4(pos + i + lane, rowpos + base + i + lane);
+                else pos[i + lane] = -1;
+            }
+            if (lane < 2 * NB)   // K, V; the row's last block may have no second scale
+                ak8_async4(pos + SL + 48 + lane, (lane & 1 ? a.vs : a.ks) + (long long)bh * a.blocks + min(ahead.blk * NB + (lane >> 1), a.blocks - 1));
             ++xa;
             ahead.next(rows);
         }
@@ -326,7 +342,7 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(D, NT, ONE))
             chunk = cur.head - h * chunks;
             ncol = ONE ? 1 : min(W, C - chunk * W);
             all = cur.len - a.T + 1 + (ONE ? 0 : chunk * W / group);
-            ref = __reduce_max_sync(0xffffffffu, pos[32 + lane]);
+            ref = __reduce_max_sync(0xffffffffu, pos[SL + lane]);
             for (int k0 = cur.len - 32; k0 > 0 && ref < 0; k0 -= 32)   // pads alone at the row's end
                 ref = __reduce_max_sync(0xffffffffu, k0 - 1 - lane >= 0 ? a.pos[(long long)cur.b * a.max_seq + k0 - 1 - lane] : -1);
 #pragma unroll
@@ -372,7 +388,7 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(D, NT, ONE))
                 for (int e = 0; e < NE; ++e) {   // accumulator columns 2 t4 + e
                     const int c = nt * 8 + 2 * t4 + e, cc = chunk * W + c;
                     qs[nt][e] = __shfl_sync(0xffffffffu, inv, (2 * t4 + e) * 4);
-                    slope[nt][e] = a.slopes && c < ncol ? __int_as_float(pos[64 + c]) * kLog2e : 0.f;
+                    slope[nt][e] = a.slopes && c < ncol ? __int_as_float(pos[SL + 32 + c]) * kLog2e : 0.f;
                     lim[nt][e] = c < ncol ? cur.len - a.T + 1 + (ONE ? 0 : cc / group) : 0;
                     m[nt][e] = M[nt][e] = -INFINITY;
                     l[nt][e] = 0.f;
@@ -383,11 +399,11 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(D, NT, ONE))
                     for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.f;
             }
         }
-        const int base = cur.blk * kKv8Block;
+        const int base = cur.blk * SL;
         // ---- scores: 16 slots x columns per mt
-        float s[2][NT][4];
+        float s[MT][NT][4];
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
+        for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -407,49 +423,62 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(D, NT, ONE))
                 }
             }
         }
-        const float kscale = __int_as_float(pos[80]), vscale = __int_as_float(pos[81]);
-        // vscale = mant * 2^ev
-        const uint32_t vbits = __float_as_uint(vscale), vexp = (vbits >> 23) & 255u;
-        const float ev = vexp == 255u ? 0.f : vexp == 0u ? -126.f : (float)((int)vexp - 127);
-        const float mant = vexp == 255u ? vscale : vexp == 0u ? vscale * 0x1p126f : __uint_as_float((vbits & 0x807fffffu) | 0x3f800000u);
-        int pk[4];
-        float dp[4];
+        // V scale = mant * 2^ev
+        float kscale[NB], ev[NB], mant[NB];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < NB; ++i) {
+            kscale[i] = __int_as_float(pos[SL + 48 + 2 * i]);
+            const uint32_t vbits = (uint32_t)pos[SL + 49 + 2 * i], vexp = (vbits >> 23) & 255u;
+            const float vscale = __uint_as_float(vbits);
+            ev[i] = vexp == 255u ? 0.f : vexp == 0u ? -126.f : (float)((int)vexp - 127);
+            mant[i] = vexp == 255u ? vscale : vexp == 0u ? vscale * 0x1p126f : __uint_as_float((vbits & 0x807fffffu) | 0x3f800000u);
+        }
+        int pk[2 * MT], least = 0;
+        float dp[2 * MT];
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i) {
             pk[i] = pos[8 * i + slot_g];
+            least = min(least, pk[i]);
             dp[i] = (float)(pk[i] - ref);
         }
         // does every column see every slot of the block?
-        const bool clean = __all_sync(0xffffffffu, ok && base + kKv8Block <= all && min(min(pk[0], pk[1]), min(pk[2], pk[3])) >= 0);
+        const bool clean = __all_sync(0xffffffffu, ok && base + SL <= all && least >= 0);
         // ---- softmax, then values: D elements x columns, 16 slots per mt
         auto rest = [&](auto is_clean) {
             constexpr bool CLEAN = decltype(is_clean)::value;
-            uint32_t pb[2][NT][2];
+            uint32_t pb[MT][NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float wt[2][4];
+                float wt[MT][4], bm[NE], bM[NE];   // the block's maxima: of scores, and with the V scale
                 bool move = false;
-                float bm[NE];
 #pragma unroll
                 for (int e = 0; e < NE; ++e) {
-                    const float f = kscale * qs[nt][e];
-                    bm[e] = -INFINITY;
+                    bm[e] = bM[e] = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {   // slot 8 i + slot_g
-                        float &v = s[i >> 1][nt][2 * (i & 1) + e];
-                        v = v * f + slope[nt][e] * dp[i];
-                        if (!CLEAN && (!ok || pk[i] < 0 || base + 8 * i + slot_g >= lim[nt][e])) v = -INFINITY;
-                        bm[e] = fmaxf(bm[e], v);
+                    for (int j = 0; j < NB; ++j) {
+                        const float f = kscale[j] * qs[nt][e];
+                        float top = -INFINITY;
+#pragma unroll
+                        for (int i = 4 * j; i < 4 * j + 4; ++i) {   // slot 8 i + slot_g
+                            float &v = s[i >> 1][nt][2 * (i & 1) + e];
+                            v = v * f + slope[nt][e] * dp[i];
+                            if (!CLEAN && (!ok || pk[i] < 0 || base + 8 * i + slot_g >= lim[nt][e])) v = -INFINITY;
+                            top = fmaxf(top, v);
+                        }
+                        bm[e] = fmaxf(bm[e], top);
+                        bM[e] = fmaxf(bM[e], top + ev[j]);
                     }
-                    move |= bm[e] > m[nt][e] + kSlack || bm[e] + ev > M[nt][e] + kSlack;
+                    move |= bm[e] > m[nt][e] + kSlack || bM[e] > M[nt][e] + kSlack;
                 }
                 if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
                     for (int e = 0; e < NE; ++e) {
-                        bm[e] = fmaxf(bm[e], __shfl_xor_sync(0xffffffffu, bm[e], 4));
-                        bm[e] = fmaxf(bm[e], __shfl_xor_sync(0xffffffffu, bm[e], 8));
-                        bm[e] = fmaxf(bm[e], __shfl_xor_sync(0xffffffffu, bm[e], 16));
-                        const float mn = fmaxf(m[nt][e], bm[e]), Mn = fmaxf(M[nt][e], bm[e] + ev);
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) {
+                            bm[e] = fmaxf(bm[e], __shfl_xor_sync(0xffffffffu, bm[e], o));
+                            bM[e] = fmaxf(bM[e], __shfl_xor_sync(0xffffffffu, bM[e], o));
+                        }
+                        const float mn = fmaxf(m[nt][e], bm[e]), Mn = fmaxf(M[nt][e], bM[e]);
                         l[nt][e] *= ak8_exp2(m[nt][e] - ak8_finite(mn));
                         const float r = ak8_exp2(M[nt][e] - ak8_finite(Mn));
 #pragma unroll
@@ -463,27 +492,27 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(D, NT, ONE))
                 }
 #pragma unroll
                 for (int e = 0; e < NE; ++e) {
-                    const float mf = ak8_finite(m[nt][e]), Mf = ak8_finite(M[nt][e]) - kLift - ev;
+                    const float mf = ak8_finite(m[nt][e]), Mf = ak8_finite(M[nt][e]) - kLift;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 2 * MT; ++i) {
                         const float v = s[i >> 1][nt][2 * (i & 1) + e];
                         l[nt][e] += ak8_exp2(v - mf);
-                        const float p = ak8_exp2(v - Mf) * mant;
+                        const float p = ak8_exp2(v - (Mf - ev[i / 4])) * mant[i / 4];
                         wt[i >> 1][2 * (i & 1) + e] = !CLEAN && v == -INFINITY ? 0.f : p;
                     }
                 }
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt) {   // [slot][column] -> [column][slot] fragments
+                for (int mt = 0; mt < MT; ++mt) {   // [slot][column] -> [column][slot] fragments
                     pb[mt][nt][0] = ak8_transpose(ak8_pack_f16(wt[mt][0], ONE ? 0.f : wt[mt][1]));
                     pb[mt][nt][1] = ak8_transpose(ak8_pack_f16(wt[mt][2], ONE ? 0.f : wt[mt][3]));
                 }
             }
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
+            for (int mt = 0; mt < MT; ++mt) {
                 uint32_t v[4][VW];   // slots of rows 2 t4, 2 t4 + 1, and 8 further
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const unsigned char *p = stage + (kKv8Block + mt * 16 + 8 * (i >> 1)) * D + voff[i & 1];
+                    const unsigned char *p = stage + (SL + mt * 16 + 8 * (i >> 1)) * D + voff[i & 1];
                     if (D == 128) {
                         const uint4 r = *reinterpret_cast<const uint4 *>(p);
                         v[i][0] = r.x; v[i][1] = r.y; v[i][VW - 2] = r.z; v[i][VW - 1] = r.w;
@@ -614,14 +643,14 @@ __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnKv8Args a,
     const int id = SPLIT ? (int)blockIdx.x : (int)blockIdx.x * 4 + w;
     const int item = id / a.part_cols, col = id - item * a.part_cols;
     const int group = a.n / a.kv, C = group * a.T, chunks = (C + W - 1) / W;
-    const Ak8Rows rows{a.lens, a.B, a.max_seq, a.kv * chunks};
+    const Ak8Rows<D> rows{a.lens, a.B, a.max_seq, a.kv * chunks};
     int b = by_head ? min(item, items - 1) / rows.heads : 0, head = 0, before = 0, total = 0;
     for (int i = lane; i < a.B; i += 32) {
         const int n = rows.blocks(i);
         total += n;
         if (i < b) before += n;
     }
-    const Ak8Runs runs(__reduce_add_sync(0xffffffffu, total) * rows.heads, warps);
+    const Ak8Runs<D> runs(__reduce_add_sync(0xffffffffu, total) * rows.heads, warps);
     int first = 0, end = 0, blocks = 0;   // its blocks
     if (by_head) {
         head = item - b * rows.heads;
@@ -629,7 +658,7 @@ __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnKv8Args a,
         first = __reduce_add_sync(0xffffffffu, before) * rows.heads + head * blocks;
         end = first + blocks;
     } else if (item + 1 < runs.R) {
-        Ak8Cursor c;
+        Ak8Cursor c = {};
         const int x1 = runs.start(item + 1);
         c.at(rows, x1);
         b = c.b;
@@ -643,7 +672,7 @@ __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnKv8Args a,
     const int slot0 = runs.start(r0) != first;             // run r0 began with an earlier (row, head)
     const int h = head / chunks, chunk = head - h * chunks, ncol = min(W, C - chunk * W);
     griddep_wait();                                        // the partials (lengths were final before)
-    if (blocks <= kAk8Short || r0 == r1 || col >= ncol) return;   // whole
+    if (blocks <= Ak8Runs<D>::kWhole || r0 == r1 || col >= ncol) return;   // whole
 
     Ak8Joint<E> sum;
     for (int rr = r0 + (SPLIT ? w : 0); rr <= r1; rr += kStep * U) {   // U partials in flight
@@ -712,13 +741,14 @@ static cudaError_t ak8_launch(AttnKv8Args a, int sms, cudaStream_t s) {
     }
     Ak8Maps maps;
     const long long slots = (long long)a.B * a.kv * a.max_seq;
-    if (!make_map_rows_u8(&maps.k, a.kc, slots, D, kKv8Block) || !make_map_rows_u8(&maps.v, a.vc, slots, D, kKv8Block))
+    if (!make_map_rows_u8(&maps.k, a.kc, slots, D, ak8_slots(D)) || !make_map_rows_u8(&maps.v, a.vc, slots, D, ak8_slots(D)))
         return cudaErrorInvalidValue;
     const int heads = a.B * a.kv * chunks;
-    const long long most = (long long)heads * a.blocks, runs = (most + kAk8MinRun - 1) / kAk8MinRun;
+    const long long most = (long long)heads * ((a.max_seq + ak8_slots(D) - 1) / ak8_slots(D));
+    const long long runs = (most + Ak8Runs<D>::kMin - 1) / Ak8Runs<D>::kMin;
     const int G = (int)(runs < (long long)sms * per_sm ? runs : (long long)sms * per_sm), warps = G * kAk8Warps;
     e = launch_pdl_smem(kern, dim3(G), dim3(kAk8Threads), smem, s, a, maps);
-    if (e != cudaSuccess || a.blocks <= kAk8Short) return e;   // nothing can have been cut
+    if (e != cudaSuccess || a.max_seq <= kAk8Whole) return e;   // nothing can have been cut
     const int by_head = heads < warps, items = by_head ? heads : warps;
     const int todo = items * a.part_cols;
     // more than 16 partials an item (two rounds of one warp's loads): four warps share them
@@ -735,7 +765,7 @@ bool attn_kv8_fits(int B, int n, int kv, int T, int max_seq) {
 
 size_t attn_kv8_workspace(int n, int kv, int T, int max_seq, int d, int sms) {
     const int C = n / kv * T, W = C <= 8 ? 8 : 16;
-    if (max_seq <= kAk8Short * kKv8Block) return 0;
+    if (max_seq <= kAk8Whole) return 0;
     return (size_t)sms * kAk8MaxPerSm * kAk8Warps * 2 * (C < W ? C : W) * (d + kAk8Part) * 4;
 }
 
