@@ -18,6 +18,7 @@
 // CTA ranks the lists of all.
 #include <float.h>
 #include <math.h>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -48,11 +49,36 @@ __device__ __forceinline__ float lp_logit(lp_u64 key) {   // key > 0
 __device__ __forceinline__ lp_u64 lp_max(lp_u64 a, lp_u64 b) { return a > b ? a : b; }
 // a - b for a <= b; 0 for equal ones (infinities too), kLpFar at least (a NaN too)
 __device__ __forceinline__ float lp_diff(float a, float b) { return a == b ? 0.f : fmaxf(a - b, kLpFar); }
-__device__ __forceinline__ float lp_exp(float d) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d * 1.4426950408889634f));   // relative error 2^-22
+// Pairs of floats in one register pair, one instruction for both.
+typedef unsigned long long lp_f2;
+__device__ __forceinline__ lp_f2 lp_pack(float a, float b) {
+    lp_f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
     return r;
 }
+__device__ __forceinline__ void lp_unpack(lp_f2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ lp_f2 lp_add2(lp_f2 a, lp_f2 b) {
+    lp_f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ lp_f2 lp_mul2(lp_f2 a, lp_f2 b) {
+    lp_f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ lp_f2 lp_fma2(lp_f2 a, lp_f2 b, lp_f2 c) {
+    lp_f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float lp_ex2(float x) {   // 2^x, relative error 2^-22
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float lp_exp(float d) { return lp_ex2(d * 1.4426950408889634f); }
 
 struct LpStat {   // maximum, sum exp(z - m), sum (z - m) exp(z - m)
     float m, s, t;
@@ -151,25 +177,46 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
                 if (v[i] == INFINITY) st.s += 1.f;
             return mx;
         }
+        lp_f2 s = lp_pack(st.s, 0.f), t = lp_pack(st.t, 0.f);
+        const lp_f2 minus = lp_pack(-st.m, -st.m), log2e = lp_pack(1.4426950408889634f, 1.4426950408889634f);
 #pragma unroll
-        for (int i = 0; i < n; ++i) {
-            const float d = fmaxf(v[i] - st.m, kLpFar), e = lp_exp(d);   // kLpFar for NaN and -inf
+        for (int i = 0; i + 1 < n; i += 2) {
+            float d0, d1, x0, x1;
+            lp_unpack(lp_add2(lp_pack(v[i], v[i + 1]), minus), d0, d1);
+            const lp_f2 d = lp_pack(fmaxf(d0, kLpFar), fmaxf(d1, kLpFar));   // kLpFar for NaN and -inf
+            lp_unpack(lp_mul2(d, log2e), x0, x1);
+            const lp_f2 e = lp_pack(lp_ex2(x0), lp_ex2(x1));
+            s = lp_add2(s, e);
+            t = lp_fma2(e, d, t);
+        }
+        float s0, s1, t0, t1;
+        lp_unpack(s, s0, s1);
+        lp_unpack(t, t0, t1);
+        st.s = s0 + s1;
+        st.t = t0 + t1;
+        if (n & 1) {
+            const float d = fmaxf(v[n - 1] - st.m, kLpFar), e = lp_exp(d);
             st.s += e;
             st.t += e * d;
         }
         return mx;
     };
-    auto load = [&](int i0, float *v) {
+    auto load_if = [&](int i0, float *v, auto all) {
+        constexpr bool inside = decltype(all)::value;
 #pragma unroll
         for (int k = 0; k < kLpUnroll; ++k) {
             const int i = i0 + k * kLpThreads;
             float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-            if (i < nq) f = __ldg(zq + i);
+            if (inside || i < nq) f = __ldg(zq + i);
             v[4 * k] = f.x;
             v[4 * k + 1] = f.y;
             v[4 * k + 2] = f.z;
             v[4 * k + 3] = f.w;
         }
+    };
+    auto load = [&](int r, float *v) {   // round r
+        if ((r + 1) * kLpRound <= nq) load_if(r * kLpRound + tid, v, std::true_type{});
+        else load_if(r * kLpRound + tid, v, std::false_type{});
     };
     int turn = 0;
     auto rebound = [&]() {   // from the maxima so far; by the whole CTA
@@ -214,12 +261,12 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
             if (mx >= bound) offer_all(v, i0);
         };
         float v[2][4 * kLpUnroll];
-        load(tid, v[0]);
+        load(0, v[0]);
         if (tid < ends) take(&end, 1);
         for (int r = 0; r < max(rounds, 1); r += 2) {
-            load((r + 1) * kLpRound + tid, v[1]);
+            load(r + 1, v[1]);
             round(r, v[0]);
-            load((r + 2) * kLpRound + tid, v[0]);
+            load(r + 2, v[0]);
             if (r + 1 < rounds) round(r + 1, v[1]);
         }
     }
