@@ -99,6 +99,19 @@ __device__ __forceinline__ float ak8_exp2(float x) {
 }
 __device__ __forceinline__ float ak8_finite(float m) { return m == -INFINITY ? 0.f : m; }
 
+constexpr float kAk8Lift = 6.f;   // weights carry 2^6: up to 2^15 in f16
+
+// The output of an accumulated value, from the references and the sum: v 2^(M - m - lift) / l,
+// in two steps, for M - m may pass the range of a float's exponent; 0 where nothing was seen.
+struct Ak8Last {
+    float a, b;
+    __device__ __forceinline__ Ak8Last(float m, float M, float l) {
+        a = ak8_exp2(0.5f * (ak8_finite(M) - ak8_finite(m) - kAk8Lift));
+        b = l == 0.f ? 0.f : a / l;
+    }
+    __device__ __forceinline__ float of(float v) const { return v * a * b; }
+};
+
 // ---- where a block number lies
 template <int D>
 struct Ak8Rows {
@@ -228,7 +241,7 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(NT, ONE))
     constexpr int SL = ak8_slots(D), MT = SL / 16, NB = SL / kKv8Block;   // slots, fragments of 16, scale blocks of a block
     using Smem = Ak8Smem<D, ONE>;
     constexpr int ST = Smem::kStages;
-    constexpr float kLog2e = 1.4426950408889634f, kSlack = 8.f, kLift = 6.f;   // weights up to 2^15 in f16
+    constexpr float kLog2e = 1.4426950408889634f, kSlack = 8.f;
     extern __shared__ __align__(1024) unsigned char ak8_raw[];
     unsigned char *smem = ak8_raw + ((0u - tc_smem(ak8_raw)) & 1023u);
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
@@ -278,7 +291,9 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(NT, ONE))
                                a.q + (((long long)ahead.b * a.T + c / group) * a.n + h * group + c % group) * D + e);
                 }
             }
-            if (lane == 0) {
+            if (lane == 0 && ahead.len == 0) {   // an idle row
+                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc_smem(&bar[st])) : "memory");
+            } else if (lane == 0) {
                 // slots beyond the row's length come along; they are masked
                 asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(tc_smem(&bar[st])), "r"(Smem::kStage)
                              : "memory");
@@ -492,7 +507,7 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(NT, ONE))
                 }
 #pragma unroll
                 for (int e = 0; e < NE; ++e) {
-                    const float mf = ak8_finite(m[nt][e]), Mf = ak8_finite(M[nt][e]) - kLift;
+                    const float mf = ak8_finite(m[nt][e]), Mf = ak8_finite(M[nt][e]) - kAk8Lift;
 #pragma unroll
                     for (int i = 0; i < 2 * MT; ++i) {
                         const float v = s[i >> 1][nt][2 * (i & 1) + e];
@@ -572,7 +587,7 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(NT, ONE))
                 if (c >= ncol) continue;
                 if (whole) {
                     const int cc = chunk * W + c;
-                    const float inv = sum == 0.f ? 0.f : ak8_exp2(ak8_finite(M[nt][e]) - ak8_finite(m[nt][e])) / sum;
+                    const Ak8Last last(m[nt][e], M[nt][e], sum);
                     uint4 *o = reinterpret_cast<uint4 *>(
                         a.o + (((long long)cur.b * a.T + cc / group) * a.n + h * group + cc % group) * D + g * (D / 8));
 #pragma unroll
@@ -580,7 +595,7 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(NT, ONE))
                         uint32_t r[4];
 #pragma unroll
                         for (int u = 0; u < 4; ++u)
-                            r[u] = pack_bf2(acc[4 * i + u][nt][e] * 0x1p-6f * inv, acc[4 * i + u][nt][2 + e] * 0x1p-6f * inv);
+                            r[u] = pack_bf2(last.of(acc[4 * i + u][nt][e]), last.of(acc[4 * i + u][nt][2 + e]));
                         o[i] = make_uint4(r[0], r[1], r[2], r[3]);
                     }
                 } else {   // slot 0 of this run: its first (row, head); 1: its last
@@ -623,10 +638,6 @@ struct Ak8Joint {
         }
         m = mn;
         M = Mn;
-    }
-    // what o is multiplied by in the end
-    __device__ __forceinline__ float last() const {
-        return l == 0.f ? 0.f : ak8_exp2(ak8_finite(M) - ak8_finite(m)) / l * 0x1p-6f;
     }
 };
 
@@ -713,10 +724,10 @@ __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnKv8Args a,
         sum.add(st, v);
     }
     const int cc = chunk * W + col;
-    const float f = sum.last();
+    const Ak8Last last(sum.m, sum.M, sum.l);
     uint16_t *o = a.o + (((long long)b * a.T + cc / group) * a.n + h * group + cc % group) * D;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[32 * e + lane] = f2bf(sum.o[e] * f);
+    for (int e = 0; e < E; ++e) o[32 * e + lane] = f2bf(last.of(sum.o[e]));
 }
 
 // CTAs per SM of a variant with its shared memory, found once per device.

@@ -289,7 +289,7 @@ struct AttnKv8Args {
     float *part = nullptr;                       // workspace: attn_kv8_workspace() bytes
     int part_cols = 0;                           // set by the launch
 };
-constexpr int kAk8MaxPerSm = 4;                  // CTAs per SM that the workspace allows for
+constexpr int kAk8MaxPerSm = 3;                  // CTAs per SM that the workspace allows for
 // whether blocks and slots can be numbered in 31 bits
 bool attn_kv8_fits(int B, int n, int kv, int T, int max_seq);
 size_t attn_kv8_workspace(int n, int kv, int T, int max_seq, int d, int sms);

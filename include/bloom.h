@@ -473,7 +473,9 @@ typedef struct {
  *    are dropped (flag 2).
  *  - An infinity or NaN among a block's tokens makes its scale NaN: all of the
  *    block reads as NaN until it is started afresh.
- * The values must not overlap the cache.  T <= max_seq; T = 0 does nothing. */
+ * The values must not overlap the cache.  T <= max_seq; T = 0 does nothing.
+ * Calls that write one row, or read it, are issued in order (one stream, or
+ * streams that wait for one another). */
 bloom_status bloom_op_kv8_write(const bloom_kv8 *kv, const void *k, const int64_t *k_stride,
                                 const void *v, const int64_t *v_stride, int32_t T,
                                 const int32_t *start, const int32_t *count, const uint8_t *mask,

@@ -277,7 +277,7 @@ def check_attention(kv, pos, kf, vf, q, slopes, lens, **kw):
     ref, tol = plain.attend(plain.f64(q), kf, vf, pos.numpy(), sl, lens)
     got = plain.f64(o).reshape(ref.shape)
     assert bool(np.isfinite(got).all())
-    bad = np.abs(got - ref) > tol + 1e-30
+    bad = np.abs(got - ref) > tol + 2.0 ** -134      # half the smallest bf16 number
     assert not bool(bad.any()), (int(bad.sum()), float(np.abs(got - ref)[bad].max()), np.argwhere(bad)[:4].tolist())
     return o
 
@@ -285,6 +285,8 @@ def check_attention(kv, pos, kf, vf, q, slopes, lens, **kw):
 # (B, T, n, kv, d, S, lens, pads, holes)
 ATTN = [
     (1, 1, 16, 16, 64, 1, (1,), 0, ()),                       # one key
+    (1, 1, 1, 1, 64, 1, (1,), 0, ()),                         # a cache of one slot in all
+    (1, 2, 3, 1, 128, 2, (2,), 0, ()),
     (1, 1, 4, 4, 128, 33, (33,), 0, ()),                      # the cache ends one slot into a block
     (3, 1, 16, 16, 64, 140, (37, 0, 140), 5, (9,)),           # an idle row; pads and a hole
     (2, 1, 12, 12, 64, 100, (31, 32), 0, ()),
@@ -330,7 +332,7 @@ def test_attention_one_key_is_its_value():
 
 @codes_param
 @pytest.mark.parametrize("qs,ks,vs", [(1e4, 1.0, 1.0), (1e-4, 1e-4, 1e-30), (1e30, 1e-30, 1e30), (1e-37, 1e37, 1.0),
-                                      (0.0, 1.0, 1.0)])
+                                      (0.0, 1.0, 1.0), (1.0, 1.0, 1e-37), (1.0, 1.0, 1e37), (1e-39, 1e-39, 1e-39)])
 def test_attention_magnitudes(codes, qs, ks, vs):
     """Queries, keys and values far from 1; scores stay moderate or one key takes all."""
     g = rng(23)
@@ -429,7 +431,7 @@ def test_attention_long_cache():
     ref, tol = plain.attend(plain.f64(q), vals[0], vals[1], small.numpy(), plain.f64(slopes_of(n)), (T, T, T))
     got = plain.f64(o).reshape(ref.shape)
     for b in (0, 2):
-        assert bool((np.abs(got[b] - ref[b]) <= tol[b] + 1e-30).all())
+        assert bool((np.abs(got[b] - ref[b]) <= tol[b] + 2.0 ** -134).all())
     assert (got[1] == 0).all()      # every position masked
 
 
