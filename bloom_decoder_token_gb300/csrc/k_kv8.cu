@@ -1,10 +1,12 @@
 // Writing and reading back the 8-bit KV cache (kv8_ops.cuh has its arithmetic).
 //
 // Both kernels give one warp to one tile of up to 32 tokens of one (sequence,
-// head), K or V: 32 x d values, all of whose loads (16 per lane at d = 128 for
-// the write) are in flight at once.  Both are bound by HBM: 3 bytes a value
-// (2 + 1).  Neighbouring warps take K and V, then neighbouring heads, which lie
-// side by side in a fused QKV row.
+// head), K or V: 32 x d values, all of whose loads (16 per lane at d = 128) are
+// in flight at once.  Both are bound by HBM: 3 bytes a value (2 + 1).
+// Neighbouring warps take K and V, then neighbouring heads, which lie side by
+// side in a fused QKV row.  Measured (int8, 8 x 2048 tokens, 32 x 128, 403 MB
+// each): write 59.5 us, read-back 61.8 us = 6.8, 6.5 TB/s (a copy: 6.7); one
+// token for each of 32 rows 3.4 us, 7 us where every block's scale grows.
 #include "common.cuh"
 #include "kernels.h"
 #include "kv8_ops.cuh"

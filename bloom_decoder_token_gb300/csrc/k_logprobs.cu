@@ -15,7 +15,9 @@
 // the k-th highest of the maxima of 128 groups of four threads is a lower bound
 // of the k-th highest logit; from then on a logit that reaches the bound becomes
 // a candidate.  The candidates are ranked by counting, and the cluster's first
-// CTA ranks the lists of all.
+// CTA ranks the lists of all.  Measured (rows of 250880): 509 rows, top 1, 85 us =
+// 6.0 TB/s (top 0: 78 us); 32 rows, top 20, 17 us (top 0: 9); one row, top 5, 8 us,
+// most of it the chain of loads, bound, ranking and the cluster's barriers.
 #include <float.h>
 #include <math.h>
 #include <type_traits>
