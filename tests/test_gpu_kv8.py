@@ -435,6 +435,56 @@ def test_attention_long_cache():
     assert (got[1] == 0).all()      # every position masked
 
 
+# more work than the GPU's warps hold at once: many short rows among long ones, rows whose
+# every visible slot lies at the end, lengths at the borders of blocks
+BUSY = [
+    (24, 1, 40, 40, 128, 1600, lambda b: (1600, 129, 128, 160, 1, 0, 1599, 33)[b % 8], 0),
+    (6, 1, 112, 112, 64, 4100, lambda b: (4100, 4033, 193, 0, 2048, 3000)[b], 3900),
+    (9, 3, 64, 64, 128, 1400, lambda b: 1400 - 37 * b, 3),
+    (16, 2, 96, 32, 64, 3000, lambda b: 3000 - 150 * b, 0),
+    (8, 4, 64, 16, 128, 6000, lambda b: 6000 - 700 * b, 0),
+]
+
+
+@codes_param
+@pytest.mark.parametrize("B,T,n,kv,d,S,length,pads", BUSY)
+def test_attention_busy(codes, B, T, n, kv, d, S, length, pads):
+    g = torch.Generator(device=DEV).manual_seed(B + n + S)
+    lens = [length(b) for b in range(B)]
+    cache = bg.KV8.empty(B, kv, S, d, codes, DEV)
+    x = torch.randn(2, B, S, kv, d, generator=g, device=DEV).to(torch.bfloat16)
+    bg.op_kv8_write(cache, x[0], x[1], torch.zeros(B, dtype=torch.int32, device=DEV))
+    pos = torch.arange(S, dtype=torch.int32)[None].repeat(B, 1) - pads
+    pos = torch.where(pos < 0, torch.tensor(-1, dtype=torch.int32), pos)
+    q = torch.randn(B, T, n, d, generator=g, device=DEV).to(torch.bfloat16)
+    sl = slopes_of(n)
+    o = bg.op_attn_decode_kv8(q, cache, pos.to(DEV), sl.to(DEV), i32(*lens).to(DEV))
+    again = bg.op_attn_decode_kv8(q, cache, pos.to(DEV), sl.to(DEV), i32(*lens).to(DEV))
+    assert torch.equal(o, again)
+    # float64 on the device, all rows and heads
+    kf, vf = (c.double() * s.double().repeat_interleave(32, 2)[:, :, :S, None] for c, s in ((cache.k.float(), cache.k_scale), (cache.v.float(), cache.v_scale)))
+    qd, posd, grp = q.double(), pos.to(DEV).double(), n // kv
+    for b in range(B):
+        ln = lens[b]
+        for t in range(T):
+            upto = max(0, ln - T + t + 1) if ln > 0 else 0
+            see = posd[b, :upto] >= 0
+            got = o[b, t].double().view(n, d)
+            if not bool(see.any()):
+                assert (got == 0).all()
+                continue
+            k, v = kf[b, :, :upto][:, see].repeat_interleave(grp, 0), vf[b, :, :upto][:, see].repeat_interleave(grp, 0)
+            far = sl.to(DEV).double()[:, None] * (posd[b, :upto][see] - posd[b, :upto][see].max())
+            s = (k @ qd[b, t][:, :, None])[..., 0] / d ** 0.5 + far
+            p = torch.softmax(s, 1)
+            ref = (p[:, None] @ v)[:, 0]
+            # the bound of kv8_plain.attend
+            size = (k.abs() @ qd[b, t].abs()[:, :, None])[..., 0] / d ** 0.5 + far.abs()
+            es = (d + 16) * 2.0 ** -23 * torch.where(p > 1e-9, size, torch.zeros_like(size)).amax(1)
+            tol = 2.0 ** -8 * ref.abs() + (2.0 ** -11 + 2 * es)[:, None] * (p[:, None] @ v.abs())[:, 0]
+            assert bool(((got - ref).abs() <= tol + 2.0 ** -134).all()), (b, t, float((got - ref).abs().max()))
+
+
 def test_attention_explicit_workspace():
     g = rng(32)
     lens = (1500, 700)
