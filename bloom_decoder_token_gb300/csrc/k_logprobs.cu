@@ -253,7 +253,8 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
             if (a.top > 0 && r == next) {
                 const float before = bound;
                 rebound();
-                next = a.top * rounds > kLpCand / 4 ? 5 * next + 4 : rounds;
+                // once more after the next round while there is none (logits ruled out in bulk)
+                next = bound == -FLT_MAX ? r + 1 : a.top * rounds > kLpCand / 4 ? 5 * r + 4 : rounds;
                 if (!(before == before)) {   // the first
                     offer_all(v, i0);
                     if (end >= bound) offer(end_at(tid));

@@ -88,6 +88,23 @@ def test_large_logits_at_regular_places(period):
     check(torch.tensor(z, dtype=torch.float32), torch.tensor([[7], [7 + period], [1003], [5]], dtype=torch.int32), 32)
 
 
+@pytest.mark.parametrize("B", [2, 200])
+def test_vocabularies_ruled_out_in_bulk(B):
+    """Rows whose logits are -inf but for one range, or for every k-th token: the range begins
+    late in a slice, in its last round, or at the row's end."""
+    V = 250880
+    g = torch.Generator().manual_seed(B)
+    z = torch.full((B, V), -float("inf"))
+    for b in range(B):
+        lo = (200_000, 12_345, 250_000, 31_360 + 20_480, 0, 123_456)[b % 6]
+        n = (50_000, 20_000, 880, 9_000, 5, 1)[b % 6]
+        n = min(n, V - lo)
+        z[b, lo:lo + n] = torch.randn(n, generator=g) * 3
+    z[0, :] = -float("inf")
+    z[0, 77::1009] = torch.randn(len(range(77, V, 1009)), generator=g)
+    check(z, torch.full((B, 1), 200_001, dtype=torch.int32), 20)
+
+
 @pytest.mark.parametrize("B", [1, 3, 40, 700])
 def test_row_counts_and_strides(B):
     V = 2000
