@@ -8,12 +8,12 @@
 // equal ones by index.
 //
 // Bound by HBM: the logits are read once.  One cluster of up to 8 CTAs per row,
-// each CTA a contiguous slice, in rounds of 8192 logits.  Each thread keeps a
+// each CTA a contiguous slice, in rounds of 16 logits a thread.  Each thread keeps a
 // running maximum and sums rescaled when it moves (float32), the next round's
 // loads in flight meanwhile.  The top k come out of the same pass: after the
 // first round (and, for a large k and many rounds, after the 5th, 25th, 125th)
-// the k-th highest of the maxima of 128 groups of four threads is a lower bound
-// of the k-th highest logit; from then on a logit that reaches the bound becomes
+// the k-th highest of the maxima of its groups of four threads is a lower bound
+// of the slice's k-th highest logit; from then on a logit that reaches the bound becomes
 // a candidate.  The candidates are ranked by counting, and the cluster's first
 // CTA ranks the lists of all.  Measured (rows of 250880): 509 rows, top 1, 85 us =
 // 6.0 TB/s (top 0: 78 us); 32 rows, top 20, 17 us (top 0: 9); one row, top 5, 8 us,
@@ -27,12 +27,8 @@
 
 namespace bloom {
 
-constexpr int kLpThreads = 512;
-constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpMaxCluster = 8;
-constexpr int kLpGroups = kLpThreads / 4;    // of four threads
 constexpr int kLpUnroll = 4;                 // float4s of a thread's round
-constexpr int kLpRound = kLpUnroll * kLpThreads;   // float4s of a CTA's round
 constexpr int kLpCand = 1024;                // candidates ranked in shared memory
 constexpr float kLpFar = -1e4f;              // stands for any difference whose exponential is 0
 
@@ -110,16 +106,18 @@ __device__ __forceinline__ int lp_above(const lp_u64 *p, int n, lp_u64 k) {
     return above + ((n & 1) && p[n - 1] > k);
 }
 
+template <int THREADS>
 struct LpSmem {
-    alignas(16) uint32_t group[kLpGroups];        // order-preserving keys of the groups' maxima
+    static constexpr int kWarps = THREADS / 32, kGroups = THREADS / 4;
+    alignas(16) uint32_t group[kGroups];          // order-preserving keys of the groups' maxima
     int index[kLpCand];                           // candidates
     alignas(16) lp_u64 cand[kLpCand];
     lp_u64 list[kLpMaxTop];                       // this slice's top, highest first
     alignas(16) lp_u64 lists[kLpMaxCluster * kLpMaxTop];   // first CTA: every slice's, [cluster][top]
     lp_u64 top[kLpMaxTop];
     LpStat stats[kLpMaxCluster];
-    LpStat warp[kLpWarps];
-    lp_u64 wmax[kLpWarps];
+    LpStat warp[kWarps];
+    lp_u64 wmax[kWarps];
     uint32_t bound[2];                            // of alternate calls of rebound()
     int ncand;
 };
@@ -135,8 +133,12 @@ __device__ __forceinline__ uint32_t lp_first(const void *p) {   // address in th
     return r;
 }
 
-__global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs a) {
-    __shared__ LpSmem sm;
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) logprobs_kernel(const LogprobsArgs a) {
+    // groups of four threads; float4s of a CTA's round
+    constexpr int kWarps = THREADS / 32, kGroups = THREADS / 4, kRound = kLpUnroll * THREADS;
+    static_assert(kGroups >= kLpMaxTop && THREADS >= kLpMaxTop, "a bound and a list for every top");
+    __shared__ LpSmem<THREADS> sm;
     const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const uint32_t rank = lp_rank(), cluster = gridDim.x;
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // waited for before the first push
@@ -166,7 +168,7 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
         for (int j = 0; j < 4 * kLpUnroll; ++j) reach |= v[j] >= bound ? 1u << j : 0u;
         for (; reach; reach &= reach - 1) {
             const int j = __ffs(reach) - 1;
-            offer(at0 + 4 * (i0 + (j >> 2) * kLpThreads) + (j & 3));
+            offer(at0 + 4 * (i0 + (j >> 2) * THREADS) + (j & 3));
         }
     };
     auto take = [&](const float *v, int n) {   // into the sums; returns the maximum
@@ -207,7 +209,7 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
         constexpr bool inside = decltype(all)::value;
 #pragma unroll
         for (int k = 0; k < kLpUnroll; ++k) {
-            const int i = i0 + k * kLpThreads;
+            const int i = i0 + k * THREADS;
             float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
             if (inside || i < nq) f = __ldg(zq + i);
             v[4 * k] = f.x;
@@ -217,8 +219,8 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
         }
     };
     auto load = [&](int r, float *v) {   // round r
-        if ((r + 1) * kLpRound <= nq) load_if(r * kLpRound + tid, v, std::true_type{});
-        else load_if(r * kLpRound + tid, v, std::false_type{});
+        if ((r + 1) * kRound <= nq) load_if(r * kRound + tid, v, std::true_type{});
+        else load_if(r * kRound + tid, v, std::false_type{});
     };
     int turn = 0;
     auto rebound = [&]() {   // from the maxima so far; by the whole CTA
@@ -228,11 +230,11 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
         if ((tid & 3) == 0) sm.group[tid >> 2] = (uint32_t)(lp_key(g, 0u) >> 32);   // 0: nothing
         if (tid == 0) sm.bound[turn] = 0u;
         __syncthreads();
-        if (tid < kLpGroups) {
+        if (tid < kGroups) {
             const uint32_t mine = sm.group[tid];
             int above = 0, upto = 0;   // groups above this one; and equal ones too
 #pragma unroll 8
-            for (int i = 0; i < kLpGroups; i += 4) {
+            for (int i = 0; i < kGroups; i += 4) {
                 const uint4 o = *reinterpret_cast<const uint4 *>(&sm.group[i]);
                 above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
                 upto += (o.x >= mine) + (o.y >= mine) + (o.z >= mine) + (o.w >= mine);
@@ -243,13 +245,13 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
         // no bound while fewer groups hold logits: all that take part
         bound = sm.bound[turn] ? lp_logit((lp_u64)sm.bound[turn] << 32) : -FLT_MAX;
     };
-    const int rounds = (nq + kLpRound - 1) / kLpRound;
+    const int rounds = (nq + kRound - 1) / kRound;
     const float end = tid < ends ? z[end_at(tid)] : -INFINITY;
     {
         int next = 0;   // the round after which the bound is found (again, where the first leaves many)
         auto round = [&](int r, const float *v) {
             const float mx = take(v, 4 * kLpUnroll);
-            const int i0 = r * kLpRound + tid;
+            const int i0 = r * kRound + tid;
             if (a.top > 0 && r == next) {
                 const float before = bound;
                 rebound();
@@ -288,9 +290,9 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
     if (a.top > 0) {
         const int n = sm.ncand;
         if (n <= kLpCand) {
-            for (int i = tid; i < n; i += kLpThreads) sm.cand[i] = lp_key(z[sm.index[i]], (uint32_t)sm.index[i]);
+            for (int i = tid; i < n; i += THREADS) sm.cand[i] = lp_key(z[sm.index[i]], (uint32_t)sm.index[i]);
             __syncthreads();
-            for (int i = tid; i < n; i += kLpThreads) {
+            for (int i = tid; i < n; i += THREADS) {
                 const lp_u64 k = sm.cand[i];
                 const int above = lp_above(sm.cand, n, k);
                 if (above < a.top) sm.list[above] = k;
@@ -305,7 +307,7 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
                     const lp_u64 k = lp_key(v, (uint32_t)i);
                     if (k < last && k > next) next = k;
                 };
-                for (int i = tid; i < nq; i += kLpThreads) {
+                for (int i = tid; i < nq; i += THREADS) {
                     const float4 v = __ldg(zq + i);
                     see(v.x, at0 + 4 * i);
                     see(v.y, at0 + 4 * i + 1);
@@ -318,7 +320,7 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
                 if (lane == 0) sm.wmax[w] = next;
                 __syncthreads();
 #pragma unroll
-                for (int i = 0; i < kLpWarps; ++i) next = lp_max(next, sm.wmax[i]);
+                for (int i = 0; i < kWarps; ++i) next = lp_max(next, sm.wmax[i]);
                 if (tid == 0) sm.list[r] = next;
                 last = next;
                 __syncthreads();
@@ -334,7 +336,7 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
     if (tid == 0) {
         LpStat r = sm.warp[0];
 #pragma unroll
-        for (int i = 1; i < kLpWarps; ++i) r.join(sm.warp[i]);
+        for (int i = 1; i < kWarps; ++i) r.join(sm.warp[i]);
         const uint32_t p = lp_first(&sm.stats[rank]);
         asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(p), "f"(r.m) : "memory");
         asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(p + 4), "f"(r.s) : "memory");
@@ -349,7 +351,7 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
     const bool any = r.m > -INFINITY;
     const float ls = logf(r.s);
     if (tid == 0 && a.entropy) a.entropy[b] = any ? ls - r.t / r.s : 0.f;
-    for (int j = tid; j < a.J; j += kLpThreads) {
+    for (int j = tid; j < a.J; j += THREADS) {
         const int tok = a.tokens[(long long)b * a.J + j];
         float p = 0.f;   // no token
         if (tok < -1 || tok >= a.V) p = __uint_as_float(0x7fc00000u);
@@ -360,8 +362,8 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
         if (tid < a.top) sm.top[tid] = 0ull;
         __syncthreads();
         const int n = (int)cluster * a.top;
-        if (tid < n) {
-            const lp_u64 k = sm.lists[tid];
+        for (int i = tid; i < n; i += THREADS) {
+            const lp_u64 k = sm.lists[i];
             const int above = lp_above(sm.lists, n, k);
             if (k && above < a.top) sm.top[above] = k;
         }
@@ -375,19 +377,11 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
     }
 }
 
-cudaError_t launch_logprobs(const LogprobsArgs &a, cudaStream_t s) {
-    // Two CTAs fit an SM.  Slices of a round (8192 logits) at least, eight at most, and
-    // no more of them than fill the GPU twice: what a slice costs beside its loads
-    // (its bound, its list) is then shared by more logits (509 rows of 250880, top 1:
-    // 87 us in whole rows, 94 in halves, 111 in quarters, 157 in eighths; 32 rows,
-    // top 20, in eighths: 17 us)
-    int cluster = 1;
-    while (cluster < kLpMaxCluster && a.V / (2 * cluster) >= 4 * kLpRound &&
-           2ll * a.B * cluster <= 4ll * bloom_device_sms())
-        cluster *= 2;
+template <int THREADS>
+static cudaError_t lp_launch(const LogprobsArgs &a, int cluster, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)cluster, (unsigned)a.B);
-    cfg.blockDim = dim3(kLpThreads);
+    cfg.blockDim = dim3(THREADS);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -398,7 +392,26 @@ cudaError_t launch_logprobs(const LogprobsArgs &a, cudaStream_t s) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, logprobs_kernel, a);
+    return cudaLaunchKernelEx(&cfg, logprobs_kernel<THREADS>, a);
+}
+
+cudaError_t launch_logprobs(const LogprobsArgs &a, cudaStream_t s) {
+    // Many short rows: CTAs of 128 threads, eight of which fit an SM, hide one another's
+    // phases (512 against 128 threads, top 5: 5000 rows of 2000 103, 27 us; 512 of 8000 13.9,
+    // 9.3; 2000 of 30000 66, 52; but 300 of 16000 8.9, 10.7; 500 of 30000 21, 24; 64 of 12000,
+    // top 20, 7.0, 12.4)
+    const int sms = bloom_device_sms();
+    if (a.V <= 2048 || (a.V < 65536 && a.B > (a.V <= 8192 ? 2 : 4) * sms)) return lp_launch<128>(a, 1, s);
+    // Two CTAs of 512 fit an SM.  Slices of a round (8192 logits) at least, eight at most,
+    // and no more of them than fill the GPU twice: what a slice costs beside its loads
+    // (its bound, its list) is then shared by more logits (509 rows of 250880, top 1:
+    // 87 us in whole rows, 94 in halves, 111 in quarters, 157 in eighths; 32 rows,
+    // top 20, in eighths: 17 us)
+    int cluster = 1;
+    while (cluster < kLpMaxCluster && a.V / (2 * cluster) >= 4 * kLpUnroll * 512 &&
+           2ll * a.B * cluster <= 4ll * sms)
+        cluster *= 2;
+    return lp_launch<512>(a, cluster, s);
 }
 
 }  // namespace bloom

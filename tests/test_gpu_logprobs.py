@@ -105,9 +105,9 @@ def test_vocabularies_ruled_out_in_bulk(B):
     check(z, torch.full((B, 1), 200_001, dtype=torch.int32), 20)
 
 
+@pytest.mark.parametrize("V", [2000, 2049, 7001])
 @pytest.mark.parametrize("B", [1, 3, 40, 700])
-def test_row_counts_and_strides(B):
-    V = 2000
+def test_row_counts_and_strides(B, V):
     g = torch.Generator().manual_seed(B)
     buf = torch.randn(B, V + 13, generator=g)
     d = buf.to(DEV)
