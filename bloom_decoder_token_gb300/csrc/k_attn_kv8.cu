@@ -648,15 +648,15 @@ struct Ak8Joint {
 
 // Joins the partial results of one column of one (row, head), in the order of the
 // runs.  Item i is the (row, head) i where those are fewer than the runs; else the
-// one that run i began and did not end.  SPLIT: one CTA an item and column, the
-// four warps take the partials in turn; else one warp does it all.  Lanes hold D / 32
-// elements, neighbours side by side.
-template <int D, int NT, bool SPLIT>
-__global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnKv8Args a, int warps, int by_head, int items) {
-    constexpr int W = 8 * NT, E = D / 32, U = SPLIT ? 4 : 8, kStep = SPLIT ? 4 : 1;
+// one that run i began and did not end.  NW > 1: one CTA an item and column, its NW
+// warps take the partials in turn; NW = 1: one warp does it all, four to a CTA.  Lanes
+// hold D / 32 elements, neighbours side by side.
+template <int D, int NT, int NW>
+__global__ void __launch_bounds__(NW == 1 ? 128 : 32 * NW) attn_kv8_join_kernel(const AttnKv8Args a, int warps, int by_head, int items) {
+    constexpr int W = 8 * NT, E = D / 32, U = NW == 1 ? 8 : 4;
     griddep_launch();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int id = SPLIT ? (int)blockIdx.x : (int)blockIdx.x * 4 + w;
+    const int id = NW > 1 ? (int)blockIdx.x : (int)blockIdx.x * 4 + w;
     const int item = id / a.part_cols, col = id - item * a.part_cols;
     const int group = a.n / a.kv, C = group * a.T, chunks = (C + W - 1) / W;
     const Ak8Rows<D> rows{a.lens, a.B, a.max_seq, a.kv * chunks};
@@ -691,12 +691,12 @@ __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnKv8Args a,
     if (blocks <= Ak8Runs<D>::kWhole || r0 == r1 || col >= ncol) return;   // whole
 
     Ak8Joint<E> sum;
-    for (int rr = r0 + (SPLIT ? w : 0); rr <= r1; rr += kStep * U) {   // U partials in flight
+    for (int rr = r0 + (NW > 1 ? w : 0); rr <= r1; rr += NW * U) {   // U partials in flight
         float4 st[U];
         float v[U][E];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int r = rr + kStep * u;
+            const int r = rr + NW * u;
             st[u] = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
 #pragma unroll
             for (int e = 0; e < E; ++e) v[u][e] = 0.f;
@@ -709,24 +709,26 @@ __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnKv8Args a,
         }
         sum.add(st, v);
     }
-    if (SPLIT) {
-        __shared__ float sm_o[4][D];
-        __shared__ float4 sm_st[4];
+    if (NW > 1) {
+        __shared__ float sm_o[NW][D];
+        __shared__ float4 sm_st[NW];
 #pragma unroll
         for (int e = 0; e < E; ++e) sm_o[w][32 * e + lane] = sum.o[e];
         if (lane == 0) sm_st[w] = make_float4(sum.m, sum.M, sum.l, 0.f);
         __syncthreads();
         if (w != 0) return;
-        float4 st[4];
-        float v[4][E];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            st[u] = sm_st[u];
-#pragma unroll
-            for (int e = 0; e < E; ++e) v[u][e] = sm_o[u][32 * e + lane];
-        }
         sum = Ak8Joint<E>();
-        sum.add(st, v);
+        for (int i = 0; i < NW; i += 4) {
+            float4 st[4];
+            float v[4][E];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                st[u] = sm_st[i + u];
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[u][e] = sm_o[i + u][32 * e + lane];
+            }
+            sum.add(st, v);
+        }
     }
     const int cc = chunk * W + col;
     const Ak8Last last(sum.m, sum.M, sum.l);
@@ -767,10 +769,14 @@ static cudaError_t ak8_launch(AttnKv8Args a, int sms, cudaStream_t s) {
     if (e != cudaSuccess || a.max_seq <= kAk8Whole) return e;   // nothing can have been cut
     const int by_head = heads < warps, items = by_head ? heads : warps;
     const int todo = items * a.part_cols;
-    // more than 16 partials an item (two rounds of one warp's loads): four warps share them
+    // many partials an item: four warps share them (from 16 on: two rounds of one warp's
+    // loads), or sixteen (one key head of 131000 slots, 1216 partials: 57 us with four, 35 with
+    // sixteen; four keep room beside the main kernel's CTAs)
+    if (warps > 64 * items)
+        return launch_pdl(attn_kv8_join_kernel<D, NT, 16>, dim3(todo), dim3(512), s, a, warps, by_head, items);
     if (warps > 16 * items)
-        return launch_pdl(attn_kv8_join_kernel<D, NT, true>, dim3(todo), dim3(128), s, a, warps, by_head, items);
-    return launch_pdl(attn_kv8_join_kernel<D, NT, false>, dim3((todo + 3) / 4), dim3(128), s, a, warps, by_head, items);
+        return launch_pdl(attn_kv8_join_kernel<D, NT, 4>, dim3(todo), dim3(128), s, a, warps, by_head, items);
+    return launch_pdl(attn_kv8_join_kernel<D, NT, 1>, dim3((todo + 3) / 4), dim3(128), s, a, warps, by_head, items);
 }
 
 bool attn_kv8_fits(int B, int n, int kv, int T, int max_seq) {

@@ -301,6 +301,8 @@ ATTN = [
     (33, 1, 4, 4, 64, 140, tuple(range(33)), 0, ()),
     (40, 1, 25, 5, 64, 95, tuple((7 * i) % 96 for i in range(40)), 1, ()),
     (1, 1, 2, 2, 64, 9000, (8987,), 11, (8000,)),             # few heads, long: the most splitting
+    (1, 1, 1, 1, 128, 40000, (39990,), 3, ()),                # one head: partials by the hundred
+    (1, 4, 5, 1, 64, 30000, (29999,), 0, (29998,)),
     (300, 1, 1, 1, 64, 64, tuple((i * 13) % 65 for i in range(300)), 0, ()),
 ]
 
