@@ -54,8 +54,11 @@ namespace bloom {
 constexpr int kAk8Warps = 4, kAk8Threads = 32 * kAk8Warps;
 // Slots of a block of work: 4 KB of K and of V, one scale block at d = 128, two at 64.
 __host__ __device__ constexpr int ak8_slots(int D) { return 4096 / D; }
-constexpr int kAk8Whole = 128;    // a (row, key head) of up to so many slots is never cut (32 heads x 128: 1
-                                  // sequence of 250, 256 against 128: 12.4, 7.6 us; 32 of 128, 128 against 64: 10.9, 12.8)
+// A (row, key head) of up to so many slots is never cut, and rows of at most so many need no
+// join: a launch, a workspace and about 5 us of the host less a call.  On the GPU (32 x 128,
+// 128 against 192): 1 row of 160 7.5, 8.3 us; 8 rows 8.4, 10.1; 32 rows 14.2, 12.5.  256
+// would cost more: 1 row of 250 11.3 against 7.3 us, 8 rows 13.9 against 8.4.
+constexpr int kAk8Whole = 192;
 constexpr int kAk8MinRun = 64;    // slots a warp takes at least (one sequence of 2000, 32 heads x 128: 32, 64, 128,
                                   // 256 slots at least: 10.9, 9.6, 11.1, 14.5 us)
 constexpr int kAk8Part = 4;       // floats beside a partial's accumulator: m, M, l
