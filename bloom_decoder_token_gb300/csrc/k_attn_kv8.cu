@@ -13,18 +13,28 @@
 //  * The products run on mma.sync m16n8k16 with the keys (for V: the elements d)
 //    as the 16-row operand and the queries of one key head as the 8 columns: 8
 //    queries cost what one costs, and a code costs half a conversion to f16
-//    (exact for both code types) and, in V, half a byte permutation that pairs
+//    (exact for both code types; V's codes in the forms with several columns: to
+//    bf16, one and a half) and, in V, half a byte permutation that pairs
 //    two keys.  tcgen05 would want the codes in f16 in shared memory first.
 //  * q is multiplied by a power of two that brings its largest element to
-//    [2^14, 2^15), where bf16 -> f16 is exact over 2^-28 of that element; the
-//    scores are float32 sums of exact products.
+//    [2^14, 2^15), where bf16 -> f16 is exact from 2^-28 of that element on
+//    (smaller ones are off by 2^-39 of it at most); the scores are float32 sums
+//    of exact products.
 //  * The softmax is one pass: running maxima and sums in float32, in powers of
 //    two.  The weight of V_k carries the block's V scale: exp2(s_k + log2 scale -
-//    M) with a reference M of its own, so that scales far apart cost nothing,
-//    rounded to f16 (relative 2^-11; the bf16 result rounds at 2^-8) and
-//    multiplied with exact codes into float32 accumulators.  Both references
+//    M) with a reference M of its own, the largest such sum.  Both references
 //    move, and what was summed is rescaled, only when a score passes one by
 //    more than 2^8.
+//  * The weights, multiplied with exact codes into float32 accumulators, keep 16
+//    bits at least and a float's range: a key of zeros, or a block that is large in
+//    other channels only, may lie any number of binades above the keys that make an
+//    output.  Several columns: two bf16 parts (8 + 8 bits, from 2^-126 of the
+//    reference on), a product each.  One column: the other seven columns of the same
+//    product are free, so the weight goes in as f16 parts (11 + 11 bits) in one of
+//    four column pairs by its size, 28 binades each (from 2^-104 of the reference
+//    on, fewer bits to 2^-114, then 0).  Weights of one f16 part, 2^-31 of the
+//    reference at least, lost such outputs; they took 36 against 40 us for 16 rows x 4
+//    tokens over 1025..4090 slots, 32 heads on 8, and the same time in the one-column form.
 //  * Work is cut evenly whatever the lengths: the blocks (32 slots at d = 128, 64 at
 //    64) of all rows and key heads are numbered in one sequence, and each resident
 //    warp takes an equal run of it.  A (row, key head) of at most kAk8Whole slots
@@ -82,11 +92,38 @@ __device__ __forceinline__ void ak8_widen(uint32_t w, uint32_t &lo, uint32_t &hi
 }
 template <bool E4M3>
 __device__ __forceinline__ uint32_t ak8_bias(uint32_t w) { return E4M3 ? w : w ^ 0x80808080u; }
+// The same to bf16 pairs, exact too (a NaN code stays NaN); int8 codes come without the bias.
+__device__ __forceinline__ uint32_t ak8_s8x2_bf16(uint32_t w, uint32_t sel) {
+    // 0x4300 | byte is 128 + its low seven bits where the sign bit is taken out; less 128 or, negative, 256
+    const uint32_t t = __byte_perm(w, 0x43434343u, sel);
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(t & 0xff7fff7fu), "r"(t & 0xff80ff80u));
+    return r;
+}
+template <bool E4M3>
+__device__ __forceinline__ void ak8_widen_bf16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    if (E4M3) {
+        float f[4];
+        kv8_widen_e4m3(w, f);
+        lo = __byte_perm(__float_as_uint(f[0]), __float_as_uint(f[1]), 0x7632);
+        hi = __byte_perm(__float_as_uint(f[2]), __float_as_uint(f[3]), 0x7632);
+    } else {
+        lo = ak8_s8x2_bf16(w, 0x4140);
+        hi = ak8_s8x2_bf16(w, 0x4342);
+    }
+}
 
 __device__ __forceinline__ void ak8_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
     asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ak8_mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -107,7 +144,11 @@ __device__ __forceinline__ float ak8_exp2(float x) {
 }
 __device__ __forceinline__ float ak8_finite(float m) { return m == -INFINITY ? 0.f : m; }
 
-constexpr float kAk8Lift = 6.f;   // weights carry 2^6: up to 2^15 in f16
+constexpr float kAk8Lift = 6.f;   // weights carry 2^6: up to 2^15
+// The one-column form's f16 weights: column pair j takes those from 2^(-20 - 28 j) to 2^(8 - 28 j)
+// of the reference (the last pair all smaller ones), times 2^(28 j), as two parts: eleven bits,
+// and what is left of the weight times 2^11.
+constexpr float kAk8Band = 28.f, kAk8Low = -20.f;
 
 // The output of an accumulated value, from the references and the sum: v 2^(M - m - lift) / l,
 // in two steps, for M - m may pass the range of a float's exponent; 0 where nothing was seen.
@@ -338,6 +379,10 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(NT, ONE))
         voff[1] = vb * D + ((g >> 1) ^ (vb >> 1)) * 16 + (g & 1) * 8;
     }
 
+    // ONE: the weights of this lane's column pair, in binades below the reference, and their factor
+    const float band_lo = t4 == 3 ? -INFINITY : kAk8Low - kAk8Band * t4, band_hi = t4 == 0 ? INFINITY : kAk8Low - kAk8Band * (t4 - 1);
+    const float band_up = ak8_exp2(kAk8Lift + kAk8Band * t4), band_down = ak8_exp2(-kAk8Band * t4);
+
     uint32_t qf[NT][D / 16][2];
     float qs[NT][NE], slope[NT][NE], m[NT][NE], M[NT][NE], l[NT][NE], acc[D / 16][NT][4];
     int lim[NT][NE];               // slots that a column sees
@@ -376,9 +421,10 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(NT, ONE))
 #pragma unroll
                 for (int s = 0; s < HS; ++s) {
                     raw[s][0] = raw[s][1] = make_uint4(0u, 0u, 0u, 0u);
-                    if (nt * 8 + g < ncol) {
+                    const int col = ONE ? 0 : nt * 8 + g;   // ONE: the query in every column
+                    if (col < ncol) {
                         const uint4 *q = reinterpret_cast<const uint4 *>(
-                            sides + st * side_bytes + ((nt * 8 + g) * D + 64 * s + 16 * t4) * 2);
+                            sides + st * side_bytes + (col * D + 64 * s + 16 * t4) * 2);
                         raw[s][0] = q[0];
                         raw[s][1] = q[1];
                     }
@@ -409,7 +455,7 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(NT, ONE))
                     }
 #pragma unroll
                 for (int e = 0; e < NE; ++e) {   // accumulator columns 2 t4 + e
-                    const int c = nt * 8 + 2 * t4 + e, cc = chunk * W + c;
+                    const int c = ONE ? 0 : nt * 8 + 2 * t4 + e, cc = chunk * W + c;
                     qs[nt][e] = __shfl_sync(0xffffffffu, inv, (2 * t4 + e) * 4);
                     slope[nt][e] = a.slopes && c < ncol ? __int_as_float(pos[SL + 32 + c]) * kLog2e : 0.f;
                     lim[nt][e] = c < ncol ? cur.len - a.T + 1 + (ONE ? 0 : cc / group) : 0;
@@ -455,6 +501,7 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(NT, ONE))
             const float vscale = __uint_as_float(vbits);
             ev[i] = vexp == 255u ? 0.f : vexp == 0u ? -126.f : (float)((int)vexp - 127);
             mant[i] = vexp == 255u ? vscale : vexp == 0u ? vscale * 0x1p126f : __uint_as_float((vbits & 0x807fffffu) | 0x3f800000u);
+            if (ONE) mant[i] *= band_up;
         }
         int pk[2 * MT], least = 0;
         float dp[2 * MT];
@@ -469,7 +516,7 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(NT, ONE))
         // ---- softmax, then values: D elements x columns, 16 slots per mt
         auto rest = [&](auto is_clean) {
             constexpr bool CLEAN = decltype(is_clean)::value;
-            uint32_t pb[MT][NT][2];
+            uint32_t pb[MT][NT][2], pl[MT][ONE ? 1 : NT][2];   // the weights' first and second parts (ONE: both in pb)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float wt[MT][4], bm[NE], bM[NE];   // the block's maxima: of scores, and with the V scale
@@ -508,6 +555,10 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(NT, ONE))
                         for (int i = 0; i < D / 16; ++i) {
                             acc[i][nt][e] *= r;
                             acc[i][nt][2 + e] *= r;
+                            if (ONE) {
+                                acc[i][nt][1] *= r;
+                                acc[i][nt][3] *= r;
+                            }
                         }
                         m[nt][e] = mn;
                         M[nt][e] = Mn;
@@ -515,20 +566,30 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(NT, ONE))
                 }
 #pragma unroll
                 for (int e = 0; e < NE; ++e) {
-                    const float mf = ak8_finite(m[nt][e]), Mf = ak8_finite(M[nt][e]) - kAk8Lift;
+                    const float mf = ak8_finite(m[nt][e]), Mf = ak8_finite(M[nt][e]) - (ONE ? 0.f : kAk8Lift);
 #pragma unroll
                     for (int i = 0; i < 2 * MT; ++i) {
                         const float v = s[i >> 1][nt][2 * (i & 1) + e];
                         l[nt][e] += ak8_exp2(v - mf);
-                        const float p = ak8_exp2(v - (Mf - ev[i / 4])) * mant[i / 4];
-                        wt[i >> 1][2 * (i & 1) + e] = !CLEAN && v == -INFINITY ? 0.f : p;
+                        const float x = v - (Mf - ev[i / 4]), p = ak8_exp2(x) * mant[i / 4];
+                        const bool none = ONE ? x < band_lo || x >= band_hi : false;
+                        wt[i >> 1][2 * (i & 1) + e] = none || (!CLEAN && v == -INFINITY) ? 0.f : p;
                     }
                 }
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {   // [slot][column] -> [column][slot] fragments
-                    pb[mt][nt][0] = ak8_transpose(ak8_pack_f16(wt[mt][0], ONE ? 0.f : wt[mt][1]));
-                    pb[mt][nt][1] = ak8_transpose(ak8_pack_f16(wt[mt][2], ONE ? 0.f : wt[mt][3]));
-                }
+                for (int mt = 0; mt < MT; ++mt)   // [slot][column] -> [column][slot] fragments
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float w0 = wt[mt][2 * i], w1 = ONE ? 0.f : wt[mt][2 * i + 1];
+                        if (ONE) {   // columns 2 t4 and 2 t4 + 1: the first eleven bits, the rest
+                            const float h = __uint_as_float(__float_as_uint(w0) & 0xffffe000u);
+                            pb[mt][nt][i] = ak8_transpose(ak8_pack_f16(h, (w0 - h) * 2048.f));
+                        } else {     // the first eight bits, the rest
+                            const uint32_t u0 = __float_as_uint(w0), u1 = __float_as_uint(w1);
+                            pb[mt][nt][i] = ak8_transpose(__byte_perm(u0, u1, 0x7632));
+                            pl[mt][nt][i] = ak8_transpose(kv8_bf16x2(w0 - __uint_as_float(u0 & 0xffff0000u), w1 - __uint_as_float(u1 & 0xffff0000u)));
+                        }
+                    }
             }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
@@ -548,8 +609,10 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(NT, ONE))
 #pragma unroll
                         for (int u = 0; u < VW; ++u) v[i][u] = 0;
                     }
+                    if (ONE) {
 #pragma unroll
-                    for (int u = 0; u < VW; ++u) v[i][u] = ak8_bias<E4M3>(v[i][u]);
+                        for (int u = 0; u < VW; ++u) v[i][u] = ak8_bias<E4M3>(v[i][u]);
+                    }
                 }
 #pragma unroll
                 for (int u = 0; u < VW; ++u) {
@@ -557,11 +620,21 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(NT, ONE))
                     for (int hh = 0; hh < 2; ++hh) {   // elements 4 u + 2 hh, + 1 of two slots, side by side
                         const uint32_t sel = hh ? 0x7362u : 0x5140u;
                         uint32_t a0, a1, a2, a3;
-                        ak8_widen<E4M3>(__byte_perm(v[0][u], v[1][u], sel), a0, a1);
-                        ak8_widen<E4M3>(__byte_perm(v[2][u], v[3][u], sel), a2, a3);
+                        const uint32_t va2 = __byte_perm(v[0][u], v[1][u], sel), vb2 = __byte_perm(v[2][u], v[3][u], sel);
+                        if (ONE) {
+                            ak8_widen<E4M3>(va2, a0, a1);
+                            ak8_widen<E4M3>(vb2, a2, a3);
+                            ak8_mma(acc[2 * u + hh][0], a0, a1, a2, a3, pb[mt][0][0], pb[mt][0][1]);
+                        } else {
+                            ak8_widen_bf16<E4M3>(va2, a0, a1);
+                            ak8_widen_bf16<E4M3>(vb2, a2, a3);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            ak8_mma(acc[2 * u + hh][nt], a0, a1, a2, a3, pb[mt][nt][0], pb[mt][nt][1]);
+                            for (int nt = 0; nt < NT; ++nt)
+                                ak8_mma_bf16(acc[2 * u + hh][nt], a0, a1, a2, a3, pb[mt][nt][0], pb[mt][nt][1]);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                ak8_mma_bf16(acc[2 * u + hh][nt], a0, a1, a2, a3, pl[mt][nt][0], pl[mt][nt][1]);
+                        }
                     }
                 }
             }
@@ -583,6 +656,17 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(NT, ONE))
         // ---- the end of a (row, head), or of the run
         fresh = true;
         const bool whole = ends && x - cur.blk >= seg0;
+        if (ONE) {   // the parts of all column pairs together
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    float v = (acc[i][0][e] + acc[i][0][e + 1] * 0x1p-11f) * band_down;
+                    v += __shfl_xor_sync(0xffffffffu, v, 1);
+                    v += __shfl_xor_sync(0xffffffffu, v, 2);
+                    acc[i][0][e] = v;
+                }
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

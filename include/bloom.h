@@ -502,6 +502,10 @@ bloom_status bloom_op_kv8_read(const bloom_kv8 *kv, void *k, const int64_t *k_st
  * counts as max_seq (flag 2).  o bf16 [batch][T][n_head * d].  Masked slots and
  * slots from lens on are never looked at: they may hold anything.  A block with
  * a NaN scale makes every query that sees a slot of it NaN, in that head.
+ * Scores, sums and outputs are float32 until the one rounding to bf16; a softmax
+ * weight keeps 16 bits.  Its product with the V scale of its block counts down to
+ * 2^-104 of the largest such product of the query (fewer bits, then 0, from there
+ * on); elements of q below 2^-28 of the query's largest are off by up to 2^-39 of it.
  * batch * n_kv * max_seq is below 2^31 (BLOOM_E_UNSUPPORTED otherwise, as T > 32).
  * workspace: device scratch of bloom_op_attn_decode_kv8_workspace() bytes (0:
  * NULL will do), 16-byte aligned, contents immaterial; calls that may overlap on
