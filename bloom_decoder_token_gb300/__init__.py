@@ -114,6 +114,7 @@ _SIGS = {
     "bloom_op_kv8_read": (I32, [P, P, P, P, P, I32, P, P, P, P]),
     "bloom_op_attn_decode_kv8": (I32, [P, P, P, P, P, I32, I32, P, P, C.c_size_t, P, P]),
     "bloom_op_attn_decode_kv8_workspace": (C.c_size_t, [P, I32, I32]),
+    "bloom_op_attn_decode_kv8_wait_us": (I32, [I32]),
     "bloom_op_lmhead_argmax_noalloc": (I32, [P, P, I32, I32, I32, P, P, P]),
 }
 EXPORTS = tuple(_SIGS)

@@ -1557,6 +1557,14 @@ extern "C" size_t bloom_op_attn_decode_kv8_workspace(const bloom_kv8 *kv, int32_
     return attn_kv8_workspace(n_head, kv->n_kv, T, kv->max_seq, kv->d, device_sms());
 }
 
+static thread_local int32_t g_kv8_wait_us = 0;
+
+extern "C" bloom_status bloom_op_attn_decode_kv8_wait_us(int32_t wait_us) {
+    if (wait_us < 0) return fail(BLOOM_E_INVALID, "wait_us=%d", wait_us);
+    g_kv8_wait_us = wait_us;
+    return BLOOM_OK;
+}
+
 extern "C" bloom_status bloom_op_attn_decode_kv8(const bloom_kv8 *kv, const void *q,
                                                  const int32_t *pos, const float *slopes,
                                                  const int32_t *lens, int32_t T, int32_t n_head,
@@ -1589,6 +1597,7 @@ extern "C" bloom_status bloom_op_attn_decode_kv8(const bloom_kv8 *kv, const void
     a.scale = (float)(1.0 / sqrt((double)kv->d));
     a.o = (uint16_t *)o;
     a.err = flag;
+    a.wait_ns = (unsigned long long)g_kv8_wait_us * 1000ull;
     a.part = (float *)workspace;
     CK(launch_attn_kv8(a, kv->d, kv->codes == BLOOM_KV8_E4M3, device_sms(), (cudaStream_t)stream));
     return BLOOM_OK;

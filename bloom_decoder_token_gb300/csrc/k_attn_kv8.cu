@@ -272,6 +272,22 @@ __device__ __forceinline__ void ak8_async4(const void *dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc_smem(dst)), "l"(src) : "memory");
 }
 
+// Wait for the phase `parity` of `bar`: tc_mbar_wait, or, where the caller set a bound,
+// without its try_wait, which may itself sleep for longer than a bound of microseconds.
+__device__ __forceinline__ bool ak8_wait(uint64_t *bar, uint32_t parity, unsigned long long limit_ns) {
+    if (limit_ns == 0) return tc_mbar_wait(bar, parity);
+    const unsigned long long t0 = tc_now_ns();
+    for (;;) {
+        uint32_t done;
+        asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+                     : "=r"(done)
+                     : "r"(tc_smem(bar)), "r"(parity)
+                     : "memory");
+        if (done) return true;
+        if (tc_now_ns() - t0 > limit_ns) return false;
+    }
+}
+
 // The slot (of 8) that row r of a fragment takes.  With 16-byte pieces c of a row at
 // c ^ slot % 8 (D = 128) or c ^ slot / 2 % 4 (D = 64), the eight lanes of a K access
 // (rows 2 i and 2 i + 1, four pieces each) and those of a V access (rows 0, 2, 4, 6
@@ -390,17 +406,48 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(NT, ONE))
     int ref = 0, st = 0, seg0 = x0;            // seg0: first block of the current (row, head) in this run
     uint32_t parity = 0;
     bool fresh = true;
-    float poison = 0.f;            // NaN after a wait that expired
+
+    // A wait for block x expired: report it, wait (with a bound again) for the copies in
+    // flight, so that none lands later, and give up the rest of the run: NaN for every
+    // (row, head) that it has blocks of.
+    auto give_up = [&](int x) {
+        if (a.err && lane == 0) atomicOr(a.err, kErrTimeout);
+        for (int y = x; y < xa; ++y) {
+            tc_mbar_wait(&bar[st], parity, kTcWaitNs);
+            if (++st == ST) {
+                st = 0;
+                parity ^= 1u;
+            }
+        }
+        for (;;) {
+            if (fresh) seg0 = x;
+            const int hd = ONE ? cur.head : cur.head / chunks, c0 = (cur.head - hd * chunks) * W, nc = ONE ? 1 : min(W, C - c0);
+            const int last = min(cur.blocks - 1, cur.blk + (x1 - 1 - x));   // of its blocks in this run
+            x += last + 1 - cur.blk;
+            cur.blk = last;
+            if (last + 1 == cur.blocks && x - 1 - last >= seg0) {
+                for (int i = lane; i < nc * (D / 8); i += 32) {
+                    const int cc = c0 + i / (D / 8);
+                    reinterpret_cast<uint4 *>(a.o + (((long long)cur.b * a.T + cc / group) * a.n + hd * group + cc % group) * D)[i % (D / 8)] =
+                        make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+                }
+            } else if (lane < nc) {   // a partial result whose sum is NaN
+                float *p = a.part + ((long long)(2 * run + (seg0 == x0 ? 0 : 1)) * cols + lane) * (D + kAk8Part);
+                *reinterpret_cast<float4 *>(p + D) = make_float4(-INFINITY, -INFINITY, __uint_as_float(0x7fc00000u), 0.f);
+            }
+            if (x >= x1) break;
+            cur.next(rows);
+            fresh = true;
+        }
+    };
     for (int x = x0; x < x1; ++x) {
         unsigned char *stage = ring + st * Smem::kStage;
         const int *pos = reinterpret_cast<const int *>(sides + st * side_bytes + cols * D * 2);
         // ---- the block's copies
         cp_async_wait<ST - 1>();
-        const bool ok = __all_sync(0xffffffffu, tc_mbar_wait(&bar[st], parity, 0));
-        if (!ok) {   // report; a second bounded wait, so that no copy lands later; what follows is NaN
-            if (a.err) atomicOr(a.err, kErrTimeout);
-            poison = __uint_as_float(0x7fc00000u);
-            tc_mbar_wait(&bar[st], parity, kTcWaitNs);
+        if (!__all_sync(0xffffffffu, ak8_wait(&bar[st], parity, a.wait_ns))) {
+            give_up(x);
+            break;
         }
         __syncwarp();
         if (fresh) {
@@ -512,7 +559,7 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(NT, ONE))
             dp[i] = (float)(pk[i] - ref);
         }
         // does every column see every slot of the block?
-        const bool clean = __all_sync(0xffffffffu, ok && base + SL <= all && least >= 0);
+        const bool clean = __all_sync(0xffffffffu, base + SL <= all && least >= 0);
         // ---- softmax, then values: D elements x columns, 16 slots per mt
         auto rest = [&](auto is_clean) {
             constexpr bool CLEAN = decltype(is_clean)::value;
@@ -532,7 +579,7 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(NT, ONE))
                         for (int i = 4 * j; i < 4 * j + 4; ++i) {   // slot 8 i + slot_g
                             float &v = s[i >> 1][nt][2 * (i & 1) + e];
                             v = v * f + slope[nt][e] * dp[i];
-                            if (!CLEAN && (!ok || pk[i] < 0 || base + 8 * i + slot_g >= lim[nt][e])) v = -INFINITY;
+                            if (!CLEAN && (pk[i] < 0 || base + 8 * i + slot_g >= lim[nt][e])) v = -INFINITY;
                             top = fmaxf(top, v);
                         }
                         bm[e] = fmaxf(bm[e], top);
@@ -605,7 +652,7 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(NT, ONE))
                         v[i][0] = r.x; v[i][1] = r.y;
                     }
                     // slots that take no part may hold e4m3 NaNs: their codes count as 0
-                    if (E4M3 && !CLEAN && (!ok || pos[mt * 16 + 8 * (i >> 1) + (i & 1 ? vb : va)] < 0)) {
+                    if (E4M3 && !CLEAN && pos[mt * 16 + 8 * (i >> 1) + (i & 1 ? vb : va)] < 0) {
 #pragma unroll
                         for (int u = 0; u < VW; ++u) v[i][u] = 0;
                     }
@@ -671,7 +718,7 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(NT, ONE))
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < NE; ++e) {
-                float sum = l[nt][e] + poison;
+                float sum = l[nt][e];
                 sum += __shfl_xor_sync(0xffffffffu, sum, 4);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 8);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 16);

@@ -286,6 +286,7 @@ struct AttnKv8Args {
     float scale = 0.f;                           // 1 / sqrt(d)
     uint16_t *o = nullptr;                       // [B][T][n][d]
     int *err = nullptr;
+    unsigned long long wait_ns = 0;              // bound of its waits (0: about 2 s)
     float *part = nullptr;                       // workspace: attn_kv8_workspace() bytes
     int part_cols = 0;                           // set by the launch
 };

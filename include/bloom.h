@@ -449,8 +449,8 @@ typedef struct {
 
 /* `flag` of the three calls below: a device int32 word, or NULL, that a kernel
  * ORs a bit of bloom_check_device into when it meets a bad value (2: a slot
- * beyond the cache; 8: a bounded wait, of about two seconds, expired: outputs of
- * the call are NaN). */
+ * beyond the cache; 8: a bounded wait of the attention expired: the outputs that
+ * depend on what it waited for are NaN, the others right). */
 
 /* Quantise new keys and values into the cache: token t of row b goes to slot
  * start[b] + t, t < count[b] (count NULL: T; clamped to 0..T).  k and v: bf16,
@@ -517,6 +517,13 @@ bloom_status bloom_op_attn_decode_kv8(const bloom_kv8 *kv, const void *q, const 
 
 /* Bytes of that scratch; 0 also for arguments that the call refuses. */
 size_t bloom_op_attn_decode_kv8_workspace(const bloom_kv8 *kv, int32_t T, int32_t n_head);
+
+/* Bound of every wait of this thread's later bloom_op_attn_decode_kv8 calls, in
+ * microseconds (0, the default: about two seconds).  A warp whose wait expires
+ * stops there: it waits for its own copies in flight (at most three, about two
+ * seconds each), sets flag 8, writes NaN for what is left of its work and ends.
+ * BLOOM_E_INVALID below 0. */
+bloom_status bloom_op_attn_decode_kv8_wait_us(int32_t wait_us);
 
 /* Tied LM head with fused argmax: logits[m][v] = x[m] . E[v]; out_tokens[m] =
  * lowest index of the row maximum of the float32 logits; out_logits may be
