@@ -90,11 +90,15 @@ __global__ void __launch_bounds__(kKv8Threads) kv8_write_kernel(const Kv8WriteAr
         const float old = *scale;
         s = old > s || old != old ? old : s;   // NaN, once there, stays
         __syncwarp();
-        if (s > old && old > 0.f) {
+        if (s > old) {
             const float shift = old / s;
 #pragma unroll 1
             for (int r = r0; r < lo - base; r += RPP) {
                 uint4 *p = reinterpret_cast<uint4 *>(codes + r * D + c0);
+                if (old == 0.f) {   // whatever the codes, they stood for 0
+                    *p = make_uint4(0u, 0u, 0u, 0u);
+                    continue;
+                }
                 uint4 w = *p;
                 uint32_t *wp = &w.x;
 #pragma unroll
