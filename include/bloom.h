@@ -468,9 +468,12 @@ typedef struct {
  *    starts afresh, whatever it held.  So a cache need not be cleared, provided
  *    each row is first written from a slot that is a multiple of 32.
  *  - mask 0 (a pad slot): the token is stored as zeros and not looked at.
- *  - start[b] < 0: row b is idle and left as it is, as are all slots that the
- *    call does not name (but for that second rounding).  Tokens beyond max_seq
- *    are dropped (flag 2).
+ *  - start[b] < 0: row b is idle and left as it is, as are all blocks that the
+ *    call writes no slot of.  Slots of a written block from the row's end (start[b] +
+ *    count[b]) on keep their codes, but not their values: they count as free, and the
+ *    block's scale may change without them.  A row that goes back writes again from
+ *    there on.  Tokens beyond max_seq are dropped; flag 2 for those and for a row whose
+ *    start lies beyond max_seq.
  *  - An infinity or NaN among a block's tokens makes its scale NaN: all of the
  *    block reads as NaN until it is started afresh.
  * The values must not overlap the cache.  T <= max_seq; T = 0 does nothing.

@@ -1,5 +1,5 @@
 """Writes into blocks that hold something already: codes under a scale of 0 stand for 0
-and stay 0 when the scale grows."""
+and stay 0 when the scale grows; what the header says of slots behind the write."""
 import pytest
 import torch
 
@@ -44,3 +44,19 @@ def test_codes_under_a_scale_of_zero_stay_zero(codes, d, at):
     # row 1's held codes and everything behind the written slot are as they were
     assert torch.equal(kv.k.view(torch.uint8)[1, :, :at], before[1, :, :at])
     assert torch.equal(kv.k.view(torch.uint8)[:, :, at + 1:], before[:, :, at + 1:])
+
+
+@codes_param
+def test_slots_behind_the_write_keep_their_codes_only(codes):
+    """A filled block overwritten in its middle with larger values: the slots before keep their
+    values (rounded again), those behind their codes, which the block's new scale now covers."""
+    kv = bg.KV8.empty(1, 1, 32, 64, codes, DEV)
+    x = torch.full((1, 32, 1, 64), 1.0, dtype=torch.bfloat16, device=DEV)
+    bg.op_kv8_write(kv, x, x, i32(0))
+    old = kv.k_scale.item()
+    behind = kv.k.clone().view(torch.uint8)[:, :, 6:]
+    bg.op_kv8_write(kv, x[:, :3] * 16, x[:, :3] * 16, i32(3))
+    assert kv.k_scale.item() == 16 * old
+    k, _ = bg.op_kv8_read(kv, i32(0), 32)
+    assert (k[0, :3] == 1).all() and (k[0, 3:6] == 16).all() and (k[0, 6:] == 16).all()
+    assert torch.equal(kv.k.view(torch.uint8)[:, :, 6:], behind)
