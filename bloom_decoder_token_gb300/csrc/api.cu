@@ -1516,6 +1516,22 @@ extern "C" bloom_status bloom_op_kv8_write(const bloom_kv8 *kv, const void *k,
     return BLOOM_OK;
 }
 
+// Whether the strides nest: each dimension of more than one element steps past all that
+// the dimensions of smaller strides span, so that no two elements lie at one place.
+static bool strides_nest(const int64_t *stride, const int *extent, int d) {
+    int order[3] = {0, 1, 2};
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2 - i; ++j)
+            if (stride[order[j]] > stride[order[j + 1]]) std::swap(order[j], order[j + 1]);
+    __int128 span = d;   // past 64 bits for the largest strides
+    for (int i : order) {
+        if (extent[i] < 2) continue;
+        if (stride[i] < span) return false;
+        span += (__int128)stride[i] * (extent[i] - 1);
+    }
+    return true;
+}
+
 extern "C" bloom_status bloom_op_kv8_read(const bloom_kv8 *kv, void *k, const int64_t *k_stride,
                                           void *v, const int64_t *v_stride, int32_t T,
                                           const int32_t *start, const int32_t *count, int32_t *flag,
@@ -1524,9 +1540,8 @@ extern "C" bloom_status bloom_op_kv8_read(const bloom_kv8 *kv, void *k, const in
     bloom_status st = check_kv8_io(kv, k, k_stride, v, v_stride, T, start);
     if (st || T == 0) return st;
     const int extent[3] = {kv->batch, T, kv->n_kv};
-    for (int i = 0; i < 3; ++i)   // no two elements at one place
-        if (extent[i] > 1 && (k_stride[i] < kv->d || v_stride[i] < kv->d))
-            return fail(BLOOM_E_INVALID, "output strides below d=%d", kv->d);
+    if (!strides_nest(k_stride, extent, kv->d) || !strides_nest(v_stride, extent, kv->d))
+        return fail(BLOOM_E_INVALID, "output strides that do not nest (d=%d): elements share places", kv->d);
     Kv8ReadArgs a;
     kv8_io_args(a, kv, k_stride, v_stride, T, start, count, flag);
     a.kc = (const uint8_t *)kv->k;

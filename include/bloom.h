@@ -487,8 +487,9 @@ bloom_status bloom_op_kv8_write(const bloom_kv8 *kv, const void *k, const int64_
 /* Read slots start[b] + t, t < T, back as bf16 values (rounded half to even;
  * exact for scales that bloom_op_kv8_write made) into k and v, addressed as in
  * bloom_op_kv8_write.  Tokens t >= count[b], of idle rows (start[b] < 0) and
- * beyond max_seq (flag 2) are written as 0.  The strides of dimensions of more
- * than one element are at least d; k, v and the cache must not overlap.
+ * beyond max_seq (flag 2) are written as 0.  The strides of the dimensions of
+ * more than one element nest (BLOOM_E_INVALID otherwise): the smallest is at least d,
+ * each next one at least what the smaller ones span; k, v and the cache must not overlap.
  * T <= max_seq; T = 0 does nothing. */
 bloom_status bloom_op_kv8_read(const bloom_kv8 *kv, void *k, const int64_t *k_stride, void *v,
                                const int64_t *v_stride, int32_t T, const int32_t *start,
