@@ -119,6 +119,7 @@ struct LpSmem {
     LpStat warp[kWarps];
     lp_u64 wmax[kWarps];
     uint32_t bound[2];                            // of alternate calls of rebound()
+    lp_u64 key_bound;
     int ncand;
 };
 
@@ -243,7 +244,9 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(const LogprobsArgs a)
         }
         __syncthreads();
         // no bound while fewer groups hold logits: all that take part
-        bound = sm.bound[turn] ? lp_logit((lp_u64)sm.bound[turn] << 32) : -FLT_MAX;
+        const uint32_t found = sm.bound[turn];
+        bound = found ? lp_logit((lp_u64)found << 32) : -FLT_MAX;
+        return found != 0u;
     };
     const int rounds = (nq + kRound - 1) / kRound;
     const float end = tid < ends ? z[end_at(tid)] : -INFINITY;
@@ -254,16 +257,15 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(const LogprobsArgs a)
             const int i0 = r * kRound + tid;
             if (a.top > 0 && r == next) {
                 const float before = bound;
-                rebound();
                 // once more after the next round while there is none (logits ruled out in bulk)
-                next = bound == -FLT_MAX ? r + 1 : a.top * rounds > kLpCand / 4 ? 5 * r + 4 : rounds;
+                next = !rebound() ? r + 1 : a.top * rounds > kLpCand / 4 ? 5 * r + 4 : rounds;
                 if (!(before == before)) {   // the first
                     offer_all(v, i0);
                     if (end >= bound) offer(end_at(tid));
                     return;
                 }
             }
-            if (mx >= bound) offer_all(v, i0);
+            if (mx >= bound && *(volatile int *)&sm.ncand <= kLpCand) offer_all(v, i0);   // more are not ranked
         };
         float v[2][4 * kLpUnroll];
         load(0, v[0]);
@@ -288,7 +290,43 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(const LogprobsArgs a)
     if (a.top > 0 && tid < kLpMaxTop) sm.list[tid] = 0ull;
     __syncthreads();
     if (a.top > 0) {
-        const int n = sm.ncand;
+        int n = sm.ncand;
+        auto each = [&](auto see) {   // the slice's logits and their indexes
+            for (int i = tid; i < nq; i += THREADS) {
+                const float4 v = __ldg(zq + i);
+                see(v.x, at0 + 4 * i);
+                see(v.y, at0 + 4 * i + 1);
+                see(v.z, at0 + 4 * i + 2);
+                see(v.w, at0 + 4 * i + 3);
+            }
+            if (tid < ends) see(end, end_at(tid));
+        };
+        if (n > kLpCand) {
+            // More logits reached the bounds than are ranked (equal ones, a finite value for
+            // ruled-out tokens, ascending ones).  No two (logit, index) keys are equal: the
+            // k-th highest of the groups' highest keys leaves few however many logits are
+            // equal, for two more passes over the slice (32 rows of 250880, all but three one
+            // value, top 20: 38 us; a pass for each alternative: 175).
+            lp_u64 best = 0;
+            each([&](float v, int i) { best = lp_max(best, lp_key(v, (uint32_t)i)); });
+            best = lp_max(best, __shfl_xor_sync(0xffffffffu, best, 1));
+            best = lp_max(best, __shfl_xor_sync(0xffffffffu, best, 2));
+            if ((tid & 3) == 0) sm.cand[tid >> 2] = best;
+            if (tid == 0) sm.key_bound = 0ull;
+            __syncthreads();
+            if (tid < kGroups) {
+                const lp_u64 mine = sm.cand[tid];
+                if (mine && lp_above(sm.cand, kGroups, mine) == a.top - 1) sm.key_bound = mine;
+            }
+            if (tid == 0) sm.ncand = 0;
+            __syncthreads();
+            const lp_u64 kb = lp_max(sm.key_bound, 1ull);   // 0, fewer groups than top: all that take part
+            each([&](float v, int i) {
+                if (lp_key(v, (uint32_t)i) >= kb) offer(i);
+            });
+            __syncthreads();
+            n = sm.ncand;
+        }
         if (n <= kLpCand) {
             for (int i = tid; i < n; i += THREADS) sm.cand[i] = lp_key(z[sm.index[i]], (uint32_t)sm.index[i]);
             __syncthreads();
@@ -298,23 +336,14 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(const LogprobsArgs a)
                 if (above < a.top) sm.list[above] = k;
             }
         } else {
-            // more logits reached the bounds than are ranked (equal or ascending ones):
-            // the next highest, one at a time
+            // still more (a few groups hold them all): the next highest, one at a time
             lp_u64 last = ~0ull;
             for (int r = 0; r < a.top; ++r) {
                 lp_u64 next = 0;
-                auto see = [&](float v, int i) {
+                each([&](float v, int i) {
                     const lp_u64 k = lp_key(v, (uint32_t)i);
                     if (k < last && k > next) next = k;
-                };
-                for (int i = tid; i < nq; i += THREADS) {
-                    const float4 v = __ldg(zq + i);
-                    see(v.x, at0 + 4 * i);
-                    see(v.y, at0 + 4 * i + 1);
-                    see(v.z, at0 + 4 * i + 2);
-                    see(v.w, at0 + 4 * i + 3);
-                }
-                if (tid < ends) see(end, end_at(tid));
+                });
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) next = lp_max(next, __shfl_xor_sync(0xffffffffu, next, o));
                 if (lane == 0) sm.wmax[w] = next;
