@@ -428,9 +428,13 @@ cudaError_t launch_logprobs(const LogprobsArgs &a, cudaStream_t s) {
     // Many short rows: CTAs of 128 threads, eight of which fit an SM, hide one another's
     // phases (512 against 128 threads, top 5: 5000 rows of 2000 103, 27 us; 512 of 8000 13.9,
     // 9.3; 2000 of 30000 66, 52; but 300 of 16000 8.9, 10.7; 500 of 30000 21, 24; 64 of 12000,
-    // top 20, 7.0, 12.4)
+    // top 20, 7.0, 12.4).  The bound of 32 groups is low for a top near 32: normal logits
+    // then give hundreds of candidates, or more than are ranked (512 against 128 threads, 700 rows of
+    // 16000, top 20, 24, 32: 28, 28, 28 against 34, 44, 120 us; 2000 of 6000: 50, 52, 52
+    // against 28, 32, 100; but top 32 of 2000 rows of 3000: 50 against 40; of 1000 of 4096: 30, 40)
     const int sms = bloom_device_sms();
-    if (a.V <= 2048 || (a.V < 65536 && a.B > (a.V <= 8192 ? 2 : 4) * sms)) return lp_launch<128>(a, 1, s);
+    const bool many = a.V < 65536 && a.B > (a.V <= 8192 ? 2 : 4) * sms;
+    if (a.V <= 2048 || (many && (a.V <= 4096 || a.top <= 24))) return lp_launch<128>(a, 1, s);
     // Two CTAs of 512 fit an SM.  Slices of a round (8192 logits) at least, eight at most,
     // and no more of them than fill the GPU twice: what a slice costs beside its loads
     // (its bound, its list) is then shared by more logits (509 rows of 250880, top 1:

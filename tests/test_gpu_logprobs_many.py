@@ -116,3 +116,13 @@ def test_finite_values_cost_little_more():
             z[:, 7:300:97] = 1.0
             us.append(gpu_us(z, 20, flush))
         assert max(us) < 4 * us[0], (B, V, us)
+
+
+def test_the_most_alternatives_cost_little_more():
+    """top 32 against top 16 for many short rows: within four times (3 to 22 times as long with
+    CTAs of 128 threads for both)."""
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device=DEV)
+    for B, V in [(512, 8000), (700, 16000), (700, 50000), (700, 65000)]:
+        z = normal(B, V, V)
+        few, all32 = gpu_us(z, 16, flush), gpu_us(z, 32, flush)
+        assert all32 < 4 * few, (B, V, few, all32)
