@@ -458,8 +458,13 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(NT, ONE))
             ncol = ONE ? 1 : min(W, C - chunk * W);
             all = cur.len - a.T + 1 + (ONE ? 0 : chunk * W / group);
             ref = __reduce_max_sync(0xffffffffu, pos[SL + lane]);
-            for (int k0 = cur.len - 32; k0 > 0 && ref < 0; k0 -= 32)   // pads alone at the row's end
-                ref = __reduce_max_sync(0xffffffffu, k0 - 1 - lane >= 0 ? a.pos[(long long)cur.b * a.max_seq + k0 - 1 - lane] : -1);
+            for (int k0 = cur.len - 33 - lane; ref < 0 && k0 + lane >= 0; k0 -= 512) {   // pads alone at the row's end
+                int best = -1;
+#pragma unroll
+                for (int u = 0; u < 16; ++u)   // as many loads in flight
+                    if (k0 - 32 * u >= 0) best = max(best, a.pos[(long long)cur.b * a.max_seq + k0 - 32 * u]);
+                ref = __reduce_max_sync(0xffffffffu, best);
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 // B fragments: column g, elements 64 s + 16 t4 + 4 u + (0, 1 | 2, 3)
