@@ -33,7 +33,7 @@
 //    product are free, so the weight goes in as f16 parts (11 + 11 bits) in one of
 //    four column pairs by its size, 28 binades each (from 2^-104 of the reference
 //    on, fewer bits to 2^-114, then 0).  Weights of one f16 part, 2^-31 of the
-//    reference at least, lost such outputs; they took 36 against 40 us for 16 rows x 4
+//    reference at least, lost such outputs; they took 29 against 34 us for 16 rows x 4
 //    tokens over 1025..4090 slots, 32 heads on 8, and the same time in the one-column form.
 //  * Work is cut evenly whatever the lengths: the blocks (32 slots at d = 128, 64 at
 //    64) of all rows and key heads are numbered in one sequence, and each resident
@@ -46,9 +46,10 @@
 //    scales and, at the first block of a (row, key head), its queries.  Warps
 //    never wait for one another.
 // Measured (codes' bytes over time, join included): 4 rows of 30-33k slots, 32 x 128,
-// e4m3, 164 us = 6.4 TB/s; 32 rows of 130..2011, int8, 55 us = 5.2 TB/s; 16 rows x 4
-// tokens over 1025..4090 slots, 32 heads on 8, 29 us; one row of 2000, 9.4 us; one of 41
-// slots, 16 x 64, 4.9 us.  What short jobs lose is about 5 us from launch to the first
+// e4m3, 168 us = 6.2 TB/s; 32 rows of 130..2011, int8, 54 us = 5.3 TB/s; 16 rows x 4
+// tokens over 1025..4090 slots, 32 heads on 8, 34 us, bound by the latency of eight
+// warps' instructions an SM; one row of 2000, 9.6 us; one of 41
+// slots, 16 x 64, 4.8 us.  What short jobs lose is about 5 us from launch to the first
 // block's data and 3 us for the join.
 #include <atomic>
 #include <math.h>
@@ -64,10 +65,11 @@ namespace bloom {
 constexpr int kAk8Warps = 4, kAk8Threads = 32 * kAk8Warps;
 // Slots of a block of work: 4 KB of K and of V, one scale block at d = 128, two at 64.
 __host__ __device__ constexpr int ak8_slots(int D) { return 4096 / D; }
-// A (row, key head) of up to so many slots is never cut, and rows of at most so many need no
+// A (row, key head) of up to so many slots is never cut, and caches of at most so many need no
 // join: a launch, a workspace and about 5 us of the host less a call.  On the GPU (32 x 128,
-// 128 against 192): 1 row of 160 7.5, 8.3 us; 8 rows 8.4, 10.1; 32 rows 14.2, 12.5.  256
-// would cost more: 1 row of 250 11.3 against 7.3 us, 8 rows 13.9 against 8.4.
+// int8, 160 slots, 128 against 192), a cache of 160: 1 row 8.0, 8.8 us; 8 rows 8.8, 10.7; 32 rows
+// 14.9, 13.2; a cache of 2048, where the join runs all the same: 7.7, 9.7; 8.7, 11.2; 14.9,
+// 13.9.  256 would cost more: 1 row of 250 11.3 against 7.3 us, 8 rows 13.9 against 8.4.
 constexpr int kAk8Whole = 192;
 constexpr int kAk8MinRun = 64;    // slots a warp takes at least (one sequence of 2000, 32 heads x 128: 32, 64, 128,
                                   // 256 slots at least: 10.9, 9.6, 11.1, 14.5 us)
