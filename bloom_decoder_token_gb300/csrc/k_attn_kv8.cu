@@ -13,8 +13,8 @@
 //  * The products run on mma.sync m16n8k16 with the keys (for V: the elements d)
 //    as the 16-row operand and the queries of one key head as the 8 columns: 8
 //    queries cost what one costs, and a code costs half a conversion to f16
-//    (exact for both code types; V's codes in the forms with several columns: to
-//    bf16, one and a half) and, in V, half a byte permutation that pairs
+//    (int8: one; exact for both code types; V's codes in the forms with several
+//    columns: two instructions to bf16) and, in V, half a byte permutation that pairs
 //    two keys.  tcgen05 would want the codes in f16 in shared memory first.
 //  * q is multiplied by a power of two that brings its largest element to
 //    [2^14, 2^15), where bf16 -> f16 is exact from 2^-28 of that element on
