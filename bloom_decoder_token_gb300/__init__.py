@@ -72,6 +72,10 @@ class KVC(C.Structure):
                 ("host_buf", P), ("host_bytes", C.c_size_t), ("offload_from", I32)]
 
 
+class W4C(C.Structure):
+    _fields_ = [("tiles", P), ("n", I32), ("k", I32), ("group", I32)]
+
+
 class KV8C(C.Structure):
     _fields_ = [("k", P), ("v", P), ("k_scale", P), ("v_scale", P), ("codes", I32),
                 ("batch", I32), ("n_kv", I32), ("max_seq", I32), ("d", I32)]
@@ -115,6 +119,11 @@ _SIGS = {
     "bloom_op_attn_decode_kv8": (I32, [P, P, P, P, P, I32, I32, P, P, C.c_size_t, P, P]),
     "bloom_op_attn_decode_kv8_workspace": (C.c_size_t, [P, I32, I32]),
     "bloom_op_attn_decode_kv8_wait_us": (I32, [I32]),
+    "bloom_w4_bytes": (C.c_size_t, [I32, I32, I32]),
+    "bloom_op_w4_quantize": (I32, [P, C.c_int64, P, P]),
+    "bloom_op_w4_read": (I32, [P, P, C.c_int64, P]),
+    "bloom_op_linear_w4": (I32, [P, P, C.c_int64, I32, P, I32, P, C.c_int64, I32, P, P]),
+    "bloom_op_linear_w4_wait_ns": (I32, [I32]),
     "bloom_op_lmhead_argmax_noalloc": (I32, [P, P, I32, I32, I32, P, P, P]),
 }
 EXPORTS = tuple(_SIGS)
@@ -679,3 +688,114 @@ def op_logprobs(logits, tokens=None, top: int = 0, stream=None):
     if st:
         check(st)
     return logp, entropy, ids, lps
+
+
+def _w4_bytes(n: int, k: int, group: int) -> int:
+    # sizes past 32 bits would wrap in the call
+    size = lib().bloom_w4_bytes(n, k, group) if max(n, k, group) < 2 ** 31 else 0
+    if size == 0:
+        _bad(f"n={n}, k={k}, group={group}: k a multiple of 8, groups of 32, 64 or 128 expected")
+    return size
+
+
+class W4(NamedTuple):
+    """4-bit weights [n][k] with group scales: value = code * scale, codes -7 .. 7, a
+    bf16 scale for every `group` (32, 64 or 128) neighbouring weights of a row.  tiles:
+    uint8 [bloom_w4_bytes(n, k, group)], in the order that the linear layer reads them."""
+    tiles: torch.Tensor
+    n: int
+    k: int
+    group: int
+
+    @classmethod
+    def empty(cls, n: int, k: int, group: int = 64, device="cuda"):
+        """Room for [n][k] weights (k a multiple of 8), not initialised."""
+        size = _w4_bytes(n, k, group)
+        return cls(torch.empty(size, dtype=_U8, device=device), n, k, group)
+
+    def c(self) -> W4C:
+        """The C descriptor (bloom_w4), after checking type, size and layout."""
+        t, n, k, group = self
+        size = _w4_bytes(n, k, group)
+        return W4C(_dev("tiles", t, _U8, (size,), t.device), n, k, group)
+
+
+def _rows(name: str, t, dtype, shape, device):
+    """(address, row stride) of a [rows][columns] tensor whose columns lie together."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device or t.stride(1) != 1:
+        _expected(name, t, dtype, shape, device, "unit last stride,")
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]   # one row: its stride means nothing
+
+
+def op_w4_quantize(w, group: int = 64, out: Optional[W4] = None, stream=None) -> W4:
+    """bf16 weights w [n][k] (rows may be strided, k a multiple of 8) in 4 bits: into
+    `out`, or new tiles."""
+    dev = w.device
+    if w.dim() != 2:
+        _bad(f"w: [n][k] expected, got {tuple(w.shape)}")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return op_w4_quantize(w, group, out)
+    n, k = w.shape
+    wp, ld = _rows("w", w, _BF16, (n, k), dev)
+    if out is None:
+        out = W4.empty(n, k, group, dev)
+    elif (out.n, out.k, out.tiles.device) != (n, k, dev):
+        _bad(f"out: weights {(n, k)} on {dev} expected, got {(out.n, out.k)} on {out.tiles.device}")
+    st = lib().bloom_op_w4_quantize(wp, ld, C.byref(out.c()), _raw_stream(dev))
+    if st:
+        check(st)
+    return out
+
+
+def op_w4_read(w4: W4, out=None, stream=None):
+    """The weights back as bf16 [n][k] (rows of `out` may be strided): for prompts, which
+    run on op_gemm, or to look at what the codes stand for."""
+    dev = w4.tiles.device
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return op_w4_read(w4, out)
+    c = w4.c()
+    if out is None:
+        out = torch.empty((c.n, c.k), dtype=_BF16, device=dev)
+    wp, ld = _rows("out", out, _BF16, (c.n, c.k), dev)
+    st = lib().bloom_op_w4_read(C.byref(c), wp, ld, _raw_stream(dev))
+    if st:
+        check(st)
+    return out
+
+
+def op_linear_w4(x, w4: W4, bias=None, epilogue=EPI_STORE, y=None, dtype=torch.bfloat16, flag=None,
+                 stream=None):
+    """Linear layer of a decode step over 4-bit weights: x bf16 [M][k], bias bf16 [n];
+    y bf16 or float32 [M][n], given (required for EPI_RESID, which adds to it) or new, of
+    `dtype`.  Rows of x and y may be strided.  flag int32 [1] that errors are recorded in."""
+    dev = x.device
+    if x.dim() != 2:
+        _bad(f"x: [M][k] expected, got {tuple(x.shape)}")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return op_linear_w4(x, w4, bias, epilogue, y, dtype, flag)
+    c = w4.c()
+    if w4.tiles.device != dev:
+        _bad(f"weights on {w4.tiles.device}, x on {dev}")
+    M = x.shape[0]
+    xp, ldx = _rows("x", x, _BF16, (M, c.k), dev)
+    if M > 1 << 20:
+        _bad(f"M={M}: at most {1 << 20} tokens")
+    if y is None:
+        if epilogue == EPI_RESID:
+            _bad("y: EPI_RESID adds to it")
+        if dtype is not _BF16 and dtype is not _F32:
+            _bad(f"dtype={dtype}: bfloat16 or float32 expected")
+        y = torch.empty((M, c.n), dtype=dtype, device=dev)
+    f32 = y.dtype is _F32
+    yp, ldy = _rows("y", y, _F32 if f32 else _BF16, (M, c.n), dev)
+    st = lib().bloom_op_linear_w4(C.byref(c), xp, ldx, M, _dev("bias", bias, _BF16, (c.n,), dev), epilogue, yp,
+                                  ldy, f32, _dev("flag", flag, _I32, (1,), dev), _raw_stream(dev))
+    if st:
+        check(st)
+    return y

@@ -15,6 +15,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "kernels.h"
+#include "w4_ops.cuh"
 
 using namespace bloom;
 
@@ -1638,6 +1639,98 @@ extern "C" bloom_status bloom_decode_step_sampled(bloom_model *m, bloom_kv *kv,
     a.active = kv_ptrs(m, kv).active;
     a.out = out_tokens;
     CK(launch_sample(a, (cudaStream_t)stream));
+    return BLOOM_OK;
+}
+
+// ---- 4-bit weights
+static bool w4_sizes(int32_t n, int32_t k, int32_t group) {
+    return n >= 1 && k >= 8 && k % 8 == 0 && (group == 32 || group == 64 || group == 128) &&
+           n <= (1 << 30) && k <= (1 << 24);
+}
+static bloom_status check_w4(const bloom_w4 *w) {
+    if (!w || !w->tiles) return fail(BLOOM_E_INVALID, "null argument");
+    if (w->group != 32 && w->group != 64 && w->group != 128)
+        return fail(BLOOM_E_UNSUPPORTED, "group=%d: 32, 64 or 128", w->group);
+    if (!w4_sizes(w->n, w->k, w->group))
+        return fail(w->k > 0 && w->k % 8 ? BLOOM_E_UNSUPPORTED : BLOOM_E_INVALID,
+                    "n=%d k=%d (k a multiple of 8)", w->n, w->k);
+    if (!aligned16(w->tiles)) return fail(BLOOM_E_INVALID, "tiles must be 16-byte aligned");
+    return BLOOM_OK;
+}
+extern "C" size_t bloom_w4_bytes(int32_t n, int32_t k, int32_t group) {
+    if (!w4_sizes(n, k, group)) return 0;
+    return (size_t)((n + kW4Rows - 1) / kW4Rows) * ((k + kW4Cols - 1) / kW4Cols) * w4_tile_bytes(group);
+}
+static bloom_status w4_io(W4Args &a, const bloom_w4 *w4, const void *w, int64_t ld) {
+    bloom_status st = check_w4(w4);
+    if (st) return st;
+    if (!w) return fail(BLOOM_E_INVALID, "null argument");
+    if (!aligned16(w) || ld < w4->k || ld % 8)
+        return fail(BLOOM_E_INVALID, "w: 16-byte aligned, ld=%lld >= k=%d and a multiple of 8", (long long)ld, w4->k);
+    a.tiles = (unsigned char *)w4->tiles;
+    a.w = (uint16_t *)const_cast<void *>(w);
+    a.ld = ld;
+    a.N = w4->n;
+    a.K = w4->k;
+    a.group = w4->group;
+    return BLOOM_OK;
+}
+extern "C" bloom_status bloom_op_w4_quantize(const void *w, int64_t ld, const bloom_w4 *out, void *stream) {
+    g_pdl = true;
+    W4Args a;
+    bloom_status st = w4_io(a, out, w, ld);
+    if (st) return st;
+    CK(launch_w4_quantize(a, (cudaStream_t)stream));
+    return BLOOM_OK;
+}
+extern "C" bloom_status bloom_op_w4_read(const bloom_w4 *in, void *w, int64_t ld, void *stream) {
+    g_pdl = true;
+    W4Args a;
+    bloom_status st = w4_io(a, in, w, ld);
+    if (st) return st;
+    CK(launch_w4_read(a, (cudaStream_t)stream));
+    return BLOOM_OK;
+}
+
+static thread_local int32_t g_linear_w4_wait_ns = 0;
+
+extern "C" bloom_status bloom_op_linear_w4_wait_ns(int32_t wait_ns) {
+    if (wait_ns < 0) return fail(BLOOM_E_INVALID, "wait_ns=%d", wait_ns);
+    g_linear_w4_wait_ns = wait_ns;
+    return BLOOM_OK;
+}
+extern "C" bloom_status bloom_op_linear_w4(const bloom_w4 *w, const void *x, int64_t ldx, int32_t M,
+                                           const void *bias, int32_t epilogue, void *y, int64_t ldy,
+                                           int32_t y_f32, int32_t *flag, void *stream) {
+    g_pdl = true;
+    bloom_status st = check_w4(w);
+    if (st) return st;
+    if (M < 0 || M > (1 << 20)) return fail(BLOOM_E_INVALID, "M=%d", M);
+    if (epilogue < BLOOM_EPI_STORE || epilogue > BLOOM_EPI_RESID)
+        return fail(BLOOM_E_INVALID, "epilogue %d", epilogue);
+    if (M == 0) return BLOOM_OK;
+    if (!x || !y) return fail(BLOOM_E_INVALID, "null argument");
+    if (!aligned16(x) || ldx < w->k || ldx % 8)
+        return fail(BLOOM_E_INVALID, "x: 16-byte aligned, ldx=%lld >= k=%d and a multiple of 8", (long long)ldx, w->k);
+    if (ldy < w->n) return fail(BLOOM_E_INVALID, "ldy=%lld < n=%d", (long long)ldy, w->n);
+    if (((uintptr_t)y & (y_f32 ? 3u : 1u)) || ((uintptr_t)bias & 1u) || ((uintptr_t)flag & 3u))
+        return fail(BLOOM_E_INVALID, "y, bias and flag must be aligned to their elements");
+    LinearW4Args a;
+    a.tiles = (const unsigned char *)w->tiles;
+    a.bias = (const uint16_t *)bias;
+    a.x = (const uint16_t *)x;
+    a.ldx = ldx;
+    a.ldy = ldy;
+    a.M = M;
+    a.N = w->n;
+    a.K = w->k;
+    a.group = w->group;
+    a.epi = epilogue;
+    a.y = y;
+    a.f32 = y_f32 != 0;
+    a.err = flag;
+    a.wait_ns = (unsigned long long)g_linear_w4_wait_ns;
+    CK(launch_linear_w4(a, device_sms(), (cudaStream_t)stream));
     return BLOOM_OK;
 }
 

@@ -274,22 +274,6 @@ __device__ __forceinline__ void ak8_async4(const void *dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc_smem(dst)), "l"(src) : "memory");
 }
 
-// Wait for the phase `parity` of `bar`: tc_mbar_wait, or, where the caller set a bound,
-// without its try_wait, which may itself sleep for longer than a bound of microseconds.
-__device__ __forceinline__ bool ak8_wait(uint64_t *bar, uint32_t parity, unsigned long long limit_ns) {
-    if (limit_ns == 0) return tc_mbar_wait(bar, parity);
-    const unsigned long long t0 = tc_now_ns();
-    for (;;) {
-        uint32_t done;
-        asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-                     : "=r"(done)
-                     : "r"(tc_smem(bar)), "r"(parity)
-                     : "memory");
-        if (done) return true;
-        if (tc_now_ns() - t0 > limit_ns) return false;
-    }
-}
-
 // The slot (of 8) that row r of a fragment takes.  With 16-byte pieces c of a row at
 // c ^ slot % 8 (D = 128) or c ^ slot / 2 % 4 (D = 64), the eight lanes of a K access
 // (rows 2 i and 2 i + 1, four pieces each) and those of a V access (rows 0, 2, 4, 6
@@ -447,7 +431,7 @@ __global__ void __launch_bounds__(kAk8Threads, ak8_per_sm(NT, ONE))
         const int *pos = reinterpret_cast<const int *>(sides + st * side_bytes + cols * D * 2);
         // ---- the block's copies
         cp_async_wait<ST - 1>();
-        if (!__all_sync(0xffffffffu, ak8_wait(&bar[st], parity, a.wait_ns))) {
+        if (!__all_sync(0xffffffffu, tc_mbar_wait_within(&bar[st], parity, a.wait_ns))) {
             give_up(x);
             break;
         }

@@ -296,6 +296,37 @@ bool attn_kv8_fits(int B, int n, int kv, int T, int max_seq);
 size_t attn_kv8_workspace(int n, int kv, int T, int max_seq, int d, int sms);
 cudaError_t launch_attn_kv8(const AttnKv8Args &a, int d, int e4m3, int sms, cudaStream_t s);
 
+// 4-bit weights with group scales (w4_ops.cuh): quantising bf16 [N][K] (rows ld apart)
+// into tiles, and reading them back.
+struct W4Args {
+    unsigned char *tiles = nullptr;
+    uint16_t *w = nullptr;             // bf16; read-only when quantising
+    long long ld = 0;
+    int N = 0, K = 0, group = 0;
+};
+cudaError_t launch_w4_quantize(const W4Args &a, cudaStream_t s);
+cudaError_t launch_w4_read(const W4Args &a, cudaStream_t s);
+
+// The linear layer over them (k_linear_w4.cu).
+struct LinearW4Args {
+    const unsigned char *tiles = nullptr;
+    const uint16_t *bias = nullptr;    // bf16 [N] or null
+    const uint16_t *x = nullptr;       // bf16 [M][K], rows ldx apart
+    long long ldx = 0, ldy = 0;
+    int M = 0, N = 0, K = 0, group = 0;
+    int epi = EPI_STORE;               // STORE / GELU / RESID
+    void *y = nullptr;                 // bf16 or (f32) float [M][N], rows ldy apart
+    int f32 = 0;
+    int *err = nullptr;
+    unsigned long long wait_ns = 0;    // bound of its waits (0: about 2 s)
+    // set by the launch
+    int row_tiles = 0, k_tiles = 0;
+    int cluster = 1, passes = 1;       // CTAs that share rows of tiles; times each takes them
+    int k_warps = 0, row_warps = 0;    // warps side by side on a row of tiles; rows at a time
+    int chunk = 0;                     // rows of tiles between two joints of a cluster's sums
+};
+cudaError_t launch_linear_w4(LinearW4Args a, int sms, cudaStream_t s);
+
 struct AttnPrefillArgs {
     const uint16_t *q = nullptr;     // [B*T][n][d], prompt i's tokens at rows i*T ..
     const uint16_t *k = nullptr;     // [rows][n][max_seq][d] (the cache)

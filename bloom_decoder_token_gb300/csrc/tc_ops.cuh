@@ -50,6 +50,21 @@ __device__ __forceinline__ bool tc_mbar_wait(uint64_t *bar, uint32_t parity,
         if ((i & 15u) == 0 && tc_now_ns() - t0 > limit) return false;
     }
 }
+// Wait for the phase `parity` of `bar`: tc_mbar_wait, or, where the caller set a bound,
+// without its try_wait, which may itself sleep for longer than a bound of microseconds.
+__device__ __forceinline__ bool tc_mbar_wait_within(uint64_t *bar, uint32_t parity, unsigned long long limit_ns) {
+    if (limit_ns == 0) return tc_mbar_wait(bar, parity);
+    const unsigned long long t0 = tc_now_ns();
+    for (;;) {
+        uint32_t done;
+        asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+                     : "=r"(done)
+                     : "r"(tc_smem(bar)), "r"(parity)
+                     : "memory");
+        if (done) return true;
+        if (tc_now_ns() - t0 > limit_ns) return false;
+    }
+}
 __device__ __forceinline__ void tc_tma_2d(void *dst, const CUtensorMap *map, int c0, int c1,
                                           uint64_t *bar) {
     asm volatile(

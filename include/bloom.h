@@ -529,6 +529,53 @@ size_t bloom_op_attn_decode_kv8_workspace(const bloom_kv8 *kv, int32_t T, int32_
  * BLOOM_E_INVALID below 0. */
 bloom_status bloom_op_attn_decode_kv8_wait_us(int32_t wait_us);
 
+/* ------------------------------------------------------------------------
+ * 4-bit weights with group scales: value = code * scale, codes -7 .. 7, one
+ * bf16 scale for every `group` neighbouring weights of a row of [n][k].  4.25
+ * bits a weight at groups of 64 for a decode step to read.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    void *tiles;           /* bloom_w4_bytes() bytes, 16-byte aligned, device: tiles of 16 rows x
+                              256 columns, in the order that the linear layer reads them */
+    int32_t n, k;          /* rows (outputs) and columns (inputs); k % 8 == 0 */
+    int32_t group;         /* 32, 64 or 128 */
+} bloom_w4;
+
+/* Bytes of the tiles of [n][k] weights; 0 on bad sizes. */
+size_t bloom_w4_bytes(int32_t n, int32_t k, int32_t group);
+
+/* Quantise bf16 weights [n][k] (row i at w + i * ld elements; ld >= k, ld % 8 ==
+ * 0; w 16-byte aligned, device): a group's scale is its largest magnitude / 7
+ * rounded to bf16, its codes value / scale rounded half to even, at most 7 in
+ * magnitude.  A group of zeros, or whose scale rounds to 0, has codes 0; one
+ * with an infinity or NaN has scale NaN.  The last group of a row may be short.
+ * w must not overlap the tiles. */
+bloom_status bloom_op_w4_quantize(const void *w, int64_t ld, const bloom_w4 *out, void *stream);
+
+/* Read the weights back: code * scale rounded to bf16, [n][k] at w (rows ld
+ * apart, as above).  For prompts: widen a matrix once, then bloom_op_gemm. */
+bloom_status bloom_op_w4_read(const bloom_w4 *in, void *w, int64_t ld, void *stream);
+
+/* The linear layer of a decode step over 4-bit weights: y[m][i] = epilogue(sum_k
+ * W[i][k] x[m][k] + bias[i]), W = code * scale, sums in float32.  x: bf16 [M][k],
+ * rows ldx apart (ldx >= k, ldx % 8 == 0; 16-byte aligned); bias: bf16 [n] or
+ * NULL; y: bf16 (y_f32 = 0) or float (1) [M][n], rows ldy >= n apart, aligned to
+ * its elements; epilogue as bloom_op_linear (BLOOM_EPI_RESID adds to y in
+ * place).  Any M >= 0; the weights are read once for every 32 tokens.  An
+ * activation smaller than 2^-14 of the largest of its token's 256 columns
+ * (256 i .. 256 i + 255) is taken to within 2^-22 of that one; others exactly.
+ * A token with an infinity or NaN among its activations has NaN outputs.  y
+ * must not overlap x, the tiles or the bias.
+ * `flag`: as for the 8-bit cache; bit 8: a bounded wait expired, the outputs
+ * that depend on it are NaN. */
+bloom_status bloom_op_linear_w4(const bloom_w4 *w, const void *x, int64_t ldx, int32_t M,
+                                const void *bias, int32_t epilogue, void *y, int64_t ldy,
+                                int32_t y_f32, int32_t *flag, void *stream);
+
+/* Bound of the waits of this thread's calls of bloom_op_linear_w4 from now on, in
+ * nanoseconds; 0 (the default): about two seconds. */
+bloom_status bloom_op_linear_w4_wait_ns(int32_t wait_ns);
+
 /* Tied LM head with fused argmax: logits[m][v] = x[m] . E[v]; out_tokens[m] =
  * lowest index of the row maximum of the float32 logits; out_logits may be
  * NULL.  x bf16 [M][K], E bf16 [V][K]. */

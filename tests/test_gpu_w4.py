@@ -1,0 +1,254 @@
+"""4-bit weights on the GPU: quantising, reading back and the linear layer against plain
+float64 forms, over sizes, groups, token counts, strides, epilogues and odd values."""
+import pytest
+import torch
+
+import bloom_decoder_token_gb300 as bg
+import w4_plain as plain
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+def weights(n, k, seed=0, std=0.02):
+    g = torch.Generator(device=DEV).manual_seed(seed + 7919 * n + k)
+    w = torch.randn(n, k, generator=g, device=DEV) * std
+    w[:, 5::61] *= 4.0
+    return w.to(torch.bfloat16)
+
+
+def acts(M, k, seed=0):
+    g = torch.Generator(device=DEV).manual_seed(seed + 31 * M + k)
+    x = torch.randn(M, k, generator=g, device=DEV)
+    x[:, 7::113] *= 30.0
+    return x.to(torch.bfloat16)
+
+
+def check(y, want, far):
+    eps = torch.finfo(y.dtype).eps / 2
+    off = (y.double() - want).abs()
+    assert (off <= want.abs() * eps + far * (1 + eps)).all(), (off - want.abs() * eps - far).max()
+
+
+# ------------------------------------------------------------ quantise, read back
+@pytest.mark.parametrize("n,k", [(1, 8), (16, 256), (17, 264), (5, 72), (100, 1000), (33, 4096), (1000, 520)])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_quantize_and_read(n, k, group):
+    w = weights(n, k)
+    got = bg.op_w4_read(bg.op_w4_quantize(w, group))
+    # the values to the bit: codes and scales as in exact arithmetic, their product rounded once
+    assert torch.equal(got.double(), plain.bf16_of(plain.values(w, group)))
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_every_bf16_magnitude(group):
+    """Groups whose largest weight takes every positive finite bf16 value, the others spread below it, ties among
+    them: multiples of an eighth of it."""
+    top = torch.arange(1, 0x7F80, dtype=torch.int32, device=DEV).to(torch.int16).view(torch.bfloat16)
+    part = (torch.arange(group, device=DEV) % 17 - 8).float() / 8
+    w = (top.float()[:, None] * part).to(torch.bfloat16)
+    w[:, 8] = top
+    got = bg.op_w4_read(bg.op_w4_quantize(w, group))
+    assert torch.equal(got.double(), plain.bf16_of(plain.values(w, group)))
+
+
+def test_ties_go_to_the_even_code():
+    w = torch.zeros(2, 32, device=DEV)
+    w[0, :8] = torch.tensor([7.0, 0.5, 1.5, 2.5, -0.5, -1.5, -2.5, 6.5])
+    w[1, :8] = w[0, :8] * 2.0 ** -100
+    want = torch.tensor([7.0, 0.0, 2.0, 2.0, 0.0, -2.0, -2.0, 6.0], device=DEV)
+    got = bg.op_w4_read(bg.op_w4_quantize(w.to(torch.bfloat16), 32))
+    assert torch.equal(got[0, :8].float(), want) and torch.equal(got[1, :8].float(), want * 2.0 ** -100)
+
+
+def test_zero_nan_and_infinite_groups():
+    w = weights(4, 192).float()
+    w[0, :64] = 0.0
+    w[1, 70] = float("inf")
+    w[2, 10] = float("nan")
+    w[3, 64:128] = 2.0 ** -133          # the scale rounds to 0
+    w = w.to(torch.bfloat16)
+    got = bg.op_w4_read(bg.op_w4_quantize(w, 64))
+    want = plain.bf16_of(plain.values(w, 64))
+    assert torch.isnan(got[1, 64:128]).all() and torch.isnan(got[2, :64]).all()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(got.double().nan_to_num(0.0), want.nan_to_num(0.0))
+    assert (got[3, 64:128] == 0).all()
+
+
+def test_strided_rows_and_reuse():
+    wide = weights(50, 512)
+    w = wide[:, 128:392]                # 264 columns, rows 512 apart, 16-byte aligned
+    w4 = bg.op_w4_quantize(w, 64)
+    again = bg.op_w4_quantize(w.contiguous(), 64, out=bg.W4(torch.full_like(w4.tiles, 255), 50, 264, 64))
+    assert torch.equal(again.tiles, w4.tiles)        # every byte is written
+    out = torch.full((50, 512), 3.0, dtype=torch.bfloat16, device=DEV)
+    bg.op_w4_read(w4, out[:, 64:328])
+    assert torch.equal(out[:, 64:328], bg.op_w4_read(w4))
+    assert (out[:, :64] == 3).all() and (out[:, 328:] == 3).all()
+
+
+# ------------------------------------------------------------ the linear layer
+SHAPES = [  # tokens in one to eight column tiles and several blocks; one to eight CTAs a cluster, passes, chunks
+    (1, 1, 8), (1, 16, 256), (1, 4096, 1024), (2, 100, 264), (3, 1000, 4096), (4, 17, 4104), (5, 333, 1000),
+    (7, 2100, 8200), (8, 64, 16384), (9, 48, 520), (16, 1003, 4096), (13, 40, 12296), (17, 129, 2048), (31, 500, 2056),
+    (32, 4096, 1024), (24, 64, 16392), (33, 100, 776), (64, 257, 2304), (65, 33, 264), (200, 40, 512),
+    (2, 33, 33000), (12, 20, 40968), (20, 24, 20000), (1, 90000, 4360), (20, 12000, 2112), (10, 20000, 4608),
+    (1, 40000, 64),
+]
+
+
+@pytest.mark.parametrize("M,n,k", SHAPES)
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_linear(M, n, k, group):
+    w, x = weights(n, k), acts(M, k)
+    w4 = bg.op_w4_quantize(w, group)
+    want, far = plain.linear(x, plain.values(w, group))
+    y = bg.op_linear_w4(x, w4, dtype=torch.float32)
+    check(y, want, far)
+    z = bg.op_linear_w4(x, w4)
+    assert torch.equal(z, y.to(torch.bfloat16))          # the same sums, rounded
+    assert torch.equal(y, bg.op_linear_w4(x, w4, dtype=torch.float32))
+
+
+@pytest.mark.parametrize("M,n,k", [(1, 100, 264), (6, 500, 4104), (16, 33, 1024), (40, 70, 2304)])
+@pytest.mark.parametrize("f32", [False, True], ids=["bf16", "f32"])
+@pytest.mark.parametrize("epilogue", [0, 1, 2], ids=["store", "gelu", "resid"])
+@pytest.mark.parametrize("bias", [False, True], ids=["plain", "bias"])
+def test_epilogues(M, n, k, f32, epilogue, bias):
+    g = torch.Generator(device=DEV).manual_seed(M)
+    w, x = weights(n, k, 1), acts(M, k, 1)
+    b = torch.randn(n, generator=g, device=DEV).to(torch.bfloat16) if bias else None
+    y0 = torch.randn(M, n, generator=g, device=DEV).to(torch.float32 if f32 else torch.bfloat16)
+    y = y0.clone() if epilogue == 2 else None
+    got = bg.op_linear_w4(x, bg.op_w4_quantize(w, 64), b, epilogue, y, dtype=y0.dtype)
+    assert got.dtype == y0.dtype and (y is None or got is y)
+    check(got, *plain.linear(x, plain.values(w, 64), b, epilogue, y0))
+
+
+def test_strided_activations_and_outputs():
+    M, n, k = 5, 70, 520
+    w, wide = weights(n, k), acts(M, 1024)
+    x = wide[:, 8:528]
+    out = torch.full((M, 200), 3.0, device=DEV)
+    w4 = bg.op_w4_quantize(w, 32)
+    got = bg.op_linear_w4(x, w4, y=out[:, 50:120])
+    assert torch.equal(got, bg.op_linear_w4(x.contiguous(), w4, dtype=torch.float32))
+    assert (out[:, :50] == 3).all() and (out[:, 120:] == 3).all()
+
+
+def test_rows_of_activations_are_their_own():
+    """A token's outputs do not depend on the tokens beside it, up to the tiles that the count picks."""
+    w4, x = bg.op_w4_quantize(weights(200, 4608), 64), acts(32, 4608)
+    for M, step in ((4, 1), (8, 5), (16, 9), (32, 17)):
+        a = bg.op_linear_w4(x[:M], w4, dtype=torch.float32)
+        for m in range(step, M + 1):
+            assert torch.equal(bg.op_linear_w4(x[:m], w4, dtype=torch.float32), a[:m])
+
+
+def test_activations_of_far_apart_sizes():
+    """Outliers 2^13 above the others lose nothing; one that is larger still costs what the tolerance says."""
+    M, n, k = 6, 64, 1024
+    w, x = weights(n, k), acts(M, k).float()
+    x[:, 3::256] *= 2.0 ** 9
+    x[1] *= 2.0 ** -60
+    x[2] *= 2.0 ** 60
+    x[3, 256:512] *= 2.0 ** -40
+    x[4, 9] = 2.0 ** 40
+    x[5] = 0.0
+    x = x.to(torch.bfloat16)
+    w4 = bg.op_w4_quantize(w, 64)
+    check(bg.op_linear_w4(x, w4, dtype=torch.float32), *plain.linear(x, plain.values(w, 64)))
+
+
+def test_small_activations_beside_large_ones_of_zero_weight():
+    """What a large activation hides is off by 2^-22 of it at most, also where its own weight is 0."""
+    n, k = 16, 256
+    w = torch.zeros(n, k, device=DEV)
+    w[:, 100:132] = 7.0 * 0.01
+    x = torch.full((1, k), 1.0, device=DEV)
+    x[0, 0] = 2.0 ** 13
+    x = x.to(torch.bfloat16)
+    w = w.to(torch.bfloat16)
+    got = bg.op_linear_w4(x, bg.op_w4_quantize(w, 32), dtype=torch.float32)
+    want = x.double() @ plain.values(w, 32).t()
+    assert ((got.double() - want).abs() <= want.abs() * 2.0 ** -20).all()
+
+
+def test_nan_and_infinities():
+    w, x = weights(40, 600), acts(9, 600)
+    clean = bg.op_linear_w4(x, bg.op_w4_quantize(w, 64), dtype=torch.float32)
+    x2 = x.clone()
+    x2[3, 599] = float("nan")
+    x2[5, 0] = float("inf")
+    got = bg.op_linear_w4(x2, bg.op_w4_quantize(w, 64), dtype=torch.float32)
+    bad = torch.tensor([3, 5], device=DEV)
+    assert torch.isnan(got[bad]).all()
+    ok = [i for i in range(9) if i not in (3, 5)]
+    assert torch.equal(got[ok], clean[ok])
+    w[7, 70] = float("nan")             # a weight of one row
+    got = bg.op_linear_w4(x, bg.op_w4_quantize(w, 64), dtype=torch.float32)
+    assert torch.isnan(got[:, 7]).all()
+    got[:, 7] = clean[:, 7]
+    assert torch.equal(got, clean)
+
+
+def test_no_tokens():
+    w4 = bg.op_w4_quantize(weights(40, 64), 32)
+    assert bg.op_linear_w4(torch.empty(0, 64, dtype=torch.bfloat16, device=DEV), w4).shape == (0, 40)
+
+
+@pytest.mark.parametrize("M,n,k", [(3, 40000, 4608), (1, 40000, 2048), (12, 9000, 33000), (32, 20000, 4096)])
+def test_expired_waits(M, n, k):
+    """Waits bounded by a few nanoseconds: the call ends, flag 8 says so, whole outputs are NaN or as ever.  (With
+    many tokens the copies may land while the activations are converted, and no wait runs out.)"""
+    w4, x = bg.op_w4_quantize(weights(n, k), 64), acts(M, k)
+    flag = torch.zeros(1, dtype=torch.int32, device=DEV)
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device=DEV)
+    want = bg.op_linear_w4(x, w4, flag=flag)
+    assert flag.item() == 0
+    lost = 0
+    try:
+        assert bg.lib().bloom_op_linear_w4_wait_ns(20) == 0
+        for _ in range(10):
+            flush.zero_()
+            flag.zero_()
+            got = bg.op_linear_w4(x, w4, flag=flag)
+            torch.cuda.synchronize()
+            nan = torch.isnan(got)
+            assert flag.item() == (8 if nan.any() else 0)
+            assert torch.equal(torch.where(nan, want, got), want)
+            lost += int(nan.any())
+    finally:
+        assert bg.lib().bloom_op_linear_w4_wait_ns(0) == 0
+    assert lost > 0 or M > 4
+    flag.zero_()
+    assert torch.equal(bg.op_linear_w4(x, w4, flag=flag), want) and flag.item() == 0
+
+
+def test_streams_and_graphs():
+    """Two streams at once on the same weights, and a captured call replayed with new activations."""
+    w4, x, x2 = bg.op_w4_quantize(weights(3000, 8200), 128), acts(4, 8200), acts(4, 8200, 9)
+    want, want2 = bg.op_linear_w4(x, w4), bg.op_linear_w4(x2, w4)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = []
+    for _ in range(20):
+        outs.append((bg.op_linear_w4(x, w4, stream=s1), bg.op_linear_w4(x2, w4, stream=s2)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, want) and torch.equal(b, want2) for a, b in outs)
+    buf, y = x.clone(), torch.empty_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        bg.op_linear_w4(buf, w4, y=y)
+    for src, res in ((x, want), (x2, want2), (x, want)):
+        buf.copy_(src)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, res)
