@@ -3,15 +3,15 @@
 //
 // At so few tokens the time is the time to read the weights once, 4.25 bits each at
 // groups of 64, and the arithmetic has to stay out of the way of 46 codes a clock and SM:
-//  * The codes go into mma.sync m16n8k32 as e4m3 numbers, which they are but for two
-//    masks and a turn a word (w4_ops.cuh): 3 instructions for 8 codes, where f16 took
-//    9.  Measured here (2070 MHz, one SM): m16n8k32 of e4m3 1.2 clocks, m16n8k16 of f16
-//    2.1, so the same product costs 3.6 times less; its sums keep 24 bits.
-//  * An activation is two e4m3 numbers in neighbouring columns: x = hi + lo / 16, after a
-//    power of two that brings the largest of the token's 256 values to [2^7, 2^8).  bf16 has 8
-//    significant bits, an e4m3 4: nothing is lost down to 2^-14 of that largest value;
-//    smaller ones are off by 2^-22 of it at most.  So four tokens fill the eight columns.
-//    A token with an infinity or NaN gives NaN.
+//  * The products run on mma.sync m16n8k16 with 16 rows of weights as one operand and 8
+//    tokens as the other.  The codes are f16 numbers but for a turn and a mask a pair
+//    (w4_ops.cuh): 7 instructions for 8 codes, exact.  (e4m3 numbers and m16n8k32 would take 3,
+//    but that instruction is made of two f16 ones and conversions here: 5.1 clocks an SM
+//    against 2.5, and bf16 activations need two e4m3 columns.  12288 x 4096, one token:
+//    11.1 us with them.)
+//  * An activation goes in as f16 after a power of two that brings the largest of the
+//    token's 256 values to [2^14, 2^15): exact down to 2^-31 of that largest value; smaller
+//    ones are off by 2^-39 of it at most.  Sums are float32.
 //  * A group's products are summed apart, then times the scale into the float32 sums.
 //  * A warp owns 256 columns, whose activations stay in its registers, and goes down the
 //    matrix: tile after tile of 16 rows, by bulk copies into a ring of its own.  The
@@ -29,34 +29,34 @@
 
 namespace bloom {
 
+constexpr int kLw4Unit = 2;                      // tiles of a step: 32 rows
 constexpr int kLw4Partial = 16384;               // bytes of a buffer of sums that wait for the cluster
-constexpr int kLw4Stride = 24;                   // floats of a token's 16 rows in a warp's sums: no bank twice
-constexpr int lw4_warps(int NT) { return NT == 8 ? 8 : 16; }
+constexpr int kLw4Stride = 20;                   // floats of a token's 16 rows in a warp's sums: no bank twice
+constexpr int kLw4MaxCluster = 8;
+constexpr int lw4_warps(int NT) { return NT == 4 ? 8 : 16; }
+constexpr int lw4_stages(int NT) { return NT == 1 ? 4 : NT == 2 ? 3 : 6; }
 
 template <int NT, int G>
 struct Lw4Smem {
-    static constexpr int kWarps = lw4_warps(NT), kStages = 64 / kWarps, kTile = w4_tile_bytes(G);
-    static constexpr int kSums = kWarps * 4 * NT * kLw4Stride * 4;   // one of the two buffers
+    static constexpr int kWarps = lw4_warps(NT), kStages = lw4_stages(NT), kTile = w4_tile_bytes(G);
+    static constexpr int kSum = 8 * NT * kLw4Stride;                         // floats of a warp's tile
+    static constexpr int kSums = kWarps * kLw4Unit * kSum;                   // of one of the two buffers
     static constexpr int kRing = kWarps * kStages * kTile;
-    static constexpr int kBytes = kRing + 2 * kSums + 2 * kLw4Partial + kWarps * kStages * 8;
+    static constexpr int kBytes = kRing + 8 * kSums + 2 * kLw4Partial + kWarps * kStages * 8;
+    static_assert(kBytes <= 227 * 1024, "shared memory of an SM");
 };
 
 __device__ __forceinline__ void lw4_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
     asm(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint16_t lw4_e4m3x2(float lo, float hi) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+__device__ __forceinline__ uint32_t lw4_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
-}
-__device__ __forceinline__ void lw4_widen(uint16_t v, float &lo, float &hi) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(v));
-    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}\n" : "=f"(lo), "=f"(hi) : "r"(h));
 }
 __device__ __forceinline__ void lw4_bulk(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(tc_smem(dst)),
@@ -67,37 +67,53 @@ __device__ __forceinline__ void lw4_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+__device__ __forceinline__ float4 lw4_peer(const float *p, int rank) {   // the same place in a rank's shared memory
+    uint32_t there;
+    float4 f;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(tc_smem(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w) : "r"(there) : "memory");
+    return f;
+}
+__device__ __forceinline__ void lw4_add(float4 &a, float4 b) {
+    a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+}
 
-__device__ __forceinline__ void lw4_store(const LinearW4Args &a, int m, int row, float v) {
-    if (row >= a.N) return;
-    if (a.bias) v += bf2f(a.bias[row]);
-    if (a.epi == EPI_GELU) v = gelu_tanh(v);
+// Rows row .. row + 3 of token m.
+__device__ __forceinline__ void lw4_store(const LinearW4Args &a, int m, int row, float4 v4) {
+    const float v[4] = {v4.x, v4.y, v4.z, v4.w};
     const long long at = m * a.ldy + row;
-    if (a.f32) {
-        float *y = static_cast<float *>(a.y) + at;
-        *y = a.epi == EPI_RESID ? *y + v : v;
-    } else {
-        uint16_t *y = static_cast<uint16_t *>(a.y) + at;
-        *y = f2bf(a.epi == EPI_RESID ? bf2f(*y) + v : v);
+    float o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        o[e] = v[e];
+        if (row + e >= a.N) continue;
+        if (a.bias) o[e] += bf2f(a.bias[row + e]);
+        if (a.epi == EPI_GELU) o[e] = gelu_tanh(o[e]);
+        if (a.epi == EPI_RESID) o[e] += a.f32 ? static_cast<float *>(a.y)[at + e] : bf2f(static_cast<uint16_t *>(a.y)[at + e]);
+    }
+    if (a.wide && row + 3 < a.N) {
+        if (a.f32) *reinterpret_cast<float4 *>(static_cast<float *>(a.y) + at) = make_float4(o[0], o[1], o[2], o[3]);
+        else *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.y) + at) = make_uint2(pack_bf2(o[0], o[1]), pack_bf2(o[2], o[3]));
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (row + e >= a.N) continue;
+        if (a.f32) static_cast<float *>(a.y)[at + e] = o[e];
+        else static_cast<uint16_t *>(a.y)[at + e] = f2bf(o[e]);
     }
 }
 
-// Where a warp is: its rows of tiles in chunks (whose sums wait for the cluster
-// together), the passes over the columns within a chunk, the steps within a pass.
-struct Lw4Place {
-    int cb, pass, rb;
-};
-
-// NT: column tiles, four tokens each.
+// NT: column tiles, eight tokens each.
 template <int NT, int G>
 __global__ void __launch_bounds__(32 * lw4_warps(NT), 1) linear_w4_kernel(const LinearW4Args a) {
     using Smem = Lw4Smem<NT, G>;
-    constexpr int NW = Smem::kWarps, ST = Smem::kStages, TB = Smem::kTile, THREADS = 32 * NW;
+    constexpr int NW = Smem::kWarps, ST = Smem::kStages, TB = Smem::kTile, THREADS = 32 * NW, UT = kLw4Unit;
     extern __shared__ __align__(128) unsigned char lw4_smem[];
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, q = lane & 3;
     unsigned char *ring = lw4_smem + w * ST * TB;
-    float *sums = reinterpret_cast<float *>(lw4_smem + Smem::kRing);              // [2][NW][4 NT][kLw4Stride]
-    float *part = sums + 2 * (Smem::kSums / 4);                                   // [2][rows of tiles][tokens][16]
+    float *sums = reinterpret_cast<float *>(lw4_smem + Smem::kRing);              // [2][NW][UT][8 NT][kLw4Stride]
+    float *part = sums + 2 * Smem::kSums;                                         // [2][tiles][8 NT][16]
     uint64_t *bar = reinterpret_cast<uint64_t *>(part + 2 * (kLw4Partial / 4)) + w * ST;
     if (lane == 0) {
         for (int i = 0; i < ST; ++i) tc_mbar_init(&bar[i], 1);
@@ -107,103 +123,104 @@ __global__ void __launch_bounds__(32 * lw4_warps(NT), 1) linear_w4_kernel(const 
     griddep_wait();
     griddep_launch();
 
+    // The cluster's tiles of rows, [r0, r0 + n), in RW runs of `run`, one for each KW warps
+    // side by side; a warp's own: len from `row` on.
     const int P = a.cluster, cl = (int)blockIdx.x / P, rank = (int)blockIdx.x - cl * P, clusters = (int)gridDim.x / P;
-    const int rb0 = (int)((long long)a.row_tiles * cl / clusters), rb1 = (int)((long long)a.row_tiles * (cl + 1) / clusters);
-    const int m0 = (int)blockIdx.y * 4 * NT, Mt = min(a.M - m0, 4 * NT);
+    const int r0 = (int)((long long)a.row_tiles * cl / clusters), n = (int)((long long)a.row_tiles * (cl + 1) / clusters) - r0;
     const int KW = a.k_warps, RW = a.row_warps, slot = w / KW, kw = w - slot * KW;
+    const int run = (n + RW - 1) / RW, row = r0 + slot * run, len = slot < RW ? max(0, min(run, n - slot * run)) : 0;
+    const int m0 = (int)blockIdx.y * 8 * NT, Mt = min(a.M - m0, 8 * NT);
     const bool direct = P == 1 && a.passes == 1;
+    auto kt_of = [&](int pass) { return (pass * P + rank) * KW + kw; };   // the column tile
 
-    // the place's column tile, and whether this warp has work there
-    auto kt_of = [&](int pass) { return (pass * P + rank) * KW + kw; };
-    auto has = [&](const Lw4Place &at) {
-        return slot < RW && at.rb + slot < min(at.cb + a.chunk, rb1) && kt_of(at.pass) < a.k_tiles;
-    };
-    auto next = [&](Lw4Place &at) {
-        at.rb += RW;
-        if (at.rb < min(at.cb + a.chunk, rb1)) return;
-        at.rb = at.cb;
-        if (++at.pass < a.passes) return;
-        at.pass = 0;
-        at.cb += a.chunk;
-        at.rb = at.cb;
-    };
-    Lw4Place ahead = {rb0, 0, rb0};
-    int issued = 0;
+    // The warp's stream: for every chunk of its rows, in every pass, the chunk's tiles.
+    int ahead = 0, ahead_pass = -1, left = 0;   // chunk's first tile; tiles left in it
+    const unsigned char *src = nullptr;
     auto issue = [&](int st) {
-        while (ahead.cb < rb1 && !has(ahead)) next(ahead);
-        if (ahead.cb >= rb1) return;
+        while (left == 0) {
+            if (++ahead_pass == a.passes) {
+                ahead_pass = 0;
+                ahead += a.chunk;
+            }
+            if (ahead >= len) {                 // the end
+                ahead_pass = -1;
+                return false;
+            }
+            const int kt = kt_of(ahead_pass);
+            if (kt >= a.k_tiles) continue;
+            left = min(a.chunk, len - ahead);
+            src = a.tiles + ((long long)kt * a.row_tiles + row + ahead) * TB;
+        }
         if (lane == 0) {
             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(tc_smem(&bar[st])), "r"(TB) : "memory");
-            lw4_bulk(ring + st * TB, a.tiles + ((long long)(ahead.rb + slot) * a.k_tiles + kt_of(ahead.pass)) * TB, TB, &bar[st]);
+            lw4_bulk(ring + st * TB, src, TB, &bar[st]);
         }
-        ++issued;
-        next(ahead);
+        src += TB;
+        --left;
+        return true;
     };
-    for (int i = 0; i < ST; ++i) issue(i);
+    int flying = 0;
+    for (int i = 0; i < ST; ++i) flying += issue(i);
 
-    uint32_t b[NT][8][2];   // activations: column g (token g / 2, part g % 2), elements 32 j + 8 q + (0..3 | 4..7)
-    float inv[NT];          // 2^-up of token q of the tile
+    uint32_t b[NT][8][4];   // activations: token g of the tile, elements 32 j + 8 q + (0, 1 | 2, 3 | 4, 5 | 6, 7)
+    float inv[NT][2];       // 2^-up of tokens 2 q and 2 q + 1 of the tile
     auto load_x = [&](int kt) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int token = 4 * nt + (g >> 1), piece = g & 1;   // both parts of half the elements; the rest by the neighbour
-            const uint16_t *x = a.x + (m0 + token) * a.ldx + kt * kW4Cols + 8 * q + 4 * piece;
-            uint2 raw[8];
+            const int token = 8 * nt + g;
+            const uint16_t *x = a.x + (m0 + token) * a.ldx + kt * kW4Cols + 8 * q;
             uint32_t m2 = 0;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                raw[j] = make_uint2(0u, 0u);
-                if (token < Mt && kt * kW4Cols + 32 * j + 8 * q < a.K) raw[j] = __ldg(reinterpret_cast<const uint2 *>(x + 32 * j));
-                m2 = __vmaxu2(m2, raw[j].x & 0x7fff7fffu);
-                m2 = __vmaxu2(m2, raw[j].y & 0x7fff7fffu);
+                uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+                if (token < Mt && kt * kW4Cols + 32 * j + 8 * q < a.K) raw = ld_act(x + 32 * j);
+                b[nt][j][0] = raw.x; b[nt][j][1] = raw.y; b[nt][j][2] = raw.z; b[nt][j][3] = raw.w;
             }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) m2 = __vmaxu2(m2, b[nt][j][e] & 0x7fff7fffu);
             uint32_t amax = max(m2 & 0xffffu, m2 >> 16);
             amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 4));
-            // 2^up brings the largest element to [2^7, 2^8)
-            const int up = min(120, 7 + 127 - (int)(amax >> 7));
+            // 2^up brings the largest element to [2^14, 2^15); an infinity or NaN makes the token NaN
+            const int up = min(120, 14 + 127 - (int)(amax >> 7));
             const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
-            inv[nt] = __shfl_sync(0xffffffffu, __uint_as_float((uint32_t)(127 - up) << 23), 8 * q);
+            const float back = amax >= 0x7f80u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(127 - up) << 23);
+            inv[nt][0] = __shfl_sync(0xffffffffu, back, 8 * q);
+            inv[nt][1] = __shfl_sync(0xffffffffu, back, 8 * q + 4);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float f[4] = {bf_lo(raw[j].x) * mul, bf_hi(raw[j].x) * mul, bf_lo(raw[j].y) * mul, bf_hi(raw[j].y) * mul};
-                const uint16_t h0 = lw4_e4m3x2(f[0], f[1]), h1 = lw4_e4m3x2(f[2], f[3]);
-                float r[4];
-                lw4_widen(h0, r[0], r[1]);
-                lw4_widen(h1, r[2], r[3]);
-                const uint16_t l0 = lw4_e4m3x2((f[0] - r[0]) * 16.f, (f[1] - r[1]) * 16.f);
-                const uint16_t l1 = lw4_e4m3x2((f[2] - r[2]) * 16.f, (f[3] - r[3]) * 16.f);
-                uint32_t hi = (uint32_t)h0 | (uint32_t)h1 << 16, lo = (uint32_t)l0 | (uint32_t)l1 << 16;
-                if (amax >= 0x7f80u) hi = lo = 0x7f7f7f7fu;   // NaN
-                // piece 0 (elements 0..3) keeps its hi and gets the neighbour's, piece 1 the lo's
-                const uint32_t other = __shfl_xor_sync(0xffffffffu, piece ? hi : lo, 4);
-                b[nt][j][0] = piece ? other : hi;
-                b[nt][j][1] = piece ? lo : other;
-            }
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) b[nt][j][e] = lw4_f16x2(bf_lo(b[nt][j][e]) * mul, bf_hi(b[nt][j][e]) * mul);
         }
     };
 
-    int st = 0, used = 0, turn = 0, fill = 0;   // turn: buffer of sums; fill: of partial sums
+    int st = 0, turn = 0, fill = 0;   // turn: buffer of the warps' sums; fill: of those that wait for the cluster
     uint32_t parity = 0;
-    bool lost = false;                          // a wait expired
-    for (int cb = rb0; cb < rb1; cb += a.chunk, fill ^= 1) {
-        const int ce = min(cb + a.chunk, rb1);
+    bool lost = false;                // a wait expired
+    for (int c0 = 0; c0 < run; c0 += a.chunk, fill ^= 1) {
+        const int c1 = min(c0 + a.chunk, run);
         float *mine = part + fill * (kLw4Partial / 4);
         for (int pass = 0; pass < a.passes; ++pass) {
             const int kt = kt_of(pass);
-            if (slot < RW && kt < a.k_tiles && (a.passes > 1 || cb == rb0)) load_x(kt);
-            const int nk = min(KW, a.k_tiles - (pass * P + rank) * KW);   // warps with columns, of those that share rows
-            for (int rb = cb; rb < ce; rb += RW, turn ^= 1) {
-                float *sum = sums + turn * (Smem::kSums / 4);
-                if (has(Lw4Place{cb, pass, rb})) {
+            const int own = kt < a.k_tiles ? min(c1, len) : 0;   // this warp's tiles of the chunk end here
+            if (own > 0 && (a.passes > 1 || c0 == 0)) load_x(kt);
+            const int nk = min(KW, a.k_tiles - (pass * P + rank) * KW);   // warps side by side that have columns
+            for (int t0 = c0; t0 < c1; t0 += UT, turn ^= 1) {
+                float *sum = sums + turn * Smem::kSums;
+                float *to = sum + w * (UT * Smem::kSum) + 2 * q * kLw4Stride + g;
+#pragma unroll 1
+                for (int t = t0; t < min(t0 + UT, own); ++t, to += Smem::kSum) {
                     if (!lost && !__all_sync(0xffffffffu, tc_mbar_wait_within(&bar[st], parity, a.wait_ns))) {
                         lost = true;
                         if (a.err && lane == 0) atomicOr(a.err, kErrTimeout);
                     }
-                    float acc[NT][2];
+                    float acc[NT][4];   // row g, tokens 2 q and 2 q + 1; row g + 8
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = lost ? __uint_as_float(0x7fc00000u) : 0.f;
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[nt][e] = lost ? __uint_as_float(0x7fc00000u) : 0.f;
                     if (!lost) {
                         const unsigned char *tile = ring + st * TB;
                         uint4 v[4];
@@ -220,45 +237,48 @@ __global__ void __launch_bounds__(32 * lw4_warps(NT), 1) linear_w4_kernel(const 
 #pragma unroll
                             for (int j = gr * (G / 32); j < (gr + 1) * (G / 32); ++j) {
                                 const uint32_t w0 = (&v[j / 2].x)[2 * (j & 1)], w1 = (&v[j / 2].x)[2 * (j & 1) + 1];
-                                const uint32_t a0 = w4_low(w0), a1 = w4_low(w1), a2 = w4_high(w0), a3 = w4_high(w1);
 #pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) lw4_mma(c[nt], a0, a1, a2, a3, b[nt][j][0], b[nt][j][1]);
+                                for (int h = 0; h < 2; ++h) {
+                                    const uint32_t a0 = w4_pair(w0, 2 * h), a1 = w4_pair(w1, 2 * h);
+                                    const uint32_t a2 = w4_pair(w0, 2 * h + 1), a3 = w4_pair(w1, 2 * h + 1);
+#pragma unroll
+                                    for (int nt = 0; nt < NT; ++nt) lw4_mma(c[nt], a0, a1, a2, a3, b[nt][j][2 * h], b[nt][j][2 * h + 1]);
+                                }
                             }
                             const float s0 = bf_lo(sc), s1 = bf_hi(sc);
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                acc[nt][0] += s0 * (c[nt][0] + c[nt][1] * 0.0625f);
-                                acc[nt][1] += s1 * (c[nt][2] + c[nt][3] * 0.0625f);
-                            }
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) acc[nt][e] += (e < 2 ? s0 : s1) * c[nt][e];
                         }
                         __syncwarp();   // the tile has been read
-                        ++used;
-                        issue(st);
+                        if (!issue(st)) --flying;
                         if (++st == ST) {
                             st = 0;
                             parity ^= 1u;
                         }
                     }
-                    float *to = sum + w * (4 * NT * kLw4Stride) + q * kLw4Stride + g;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {   // the codes' 2^-9 back, then the activations' power of two
-                        to[4 * nt * kLw4Stride] = acc[nt][0] * 512.f * inv[nt];
-                        to[4 * nt * kLw4Stride + 8] = acc[nt][1] * 512.f * inv[nt];
-                    }
+                    for (int nt = 0; nt < NT; ++nt)   // the codes' 2^-16 back, then the activations' power of two
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            to[(8 * nt + (e & 1)) * kLw4Stride + 8 * (e >> 1)] = acc[nt][e] * 0x1p16f * inv[nt][e & 1];
                 }
                 __syncthreads();
-                // the warps' sums; each step other warps begin
-                const int rows = min(RW, ce - rb);
-                for (int i = (tid - 32 * (rb - cb)) & (THREADS - 1); i < rows * Mt * 16; i += THREADS) {
-                    const int r = i & 15, mt = i >> 4, s = mt / Mt, m = mt - s * Mt;
-                    const float *from = sum + s * KW * (4 * NT * kLw4Stride) + m * kLw4Stride + r;
-                    float v = 0.f;
-                    for (int k = 0; k < nk; ++k) v += from[k * (4 * NT * kLw4Stride)];
+                // the warps' sums, four rows a thread; each step other warps begin
+                for (int i = (tid - 64 * (t0 / UT)) & (THREADS - 1); i < RW * UT * Mt * 4; i += THREADS) {
+                    const int r = 4 * (i & 3), um = i >> 2, u = um / Mt, m = um - u * Mt, s = u / UT, t = t0 + u - s * UT;
+                    if (t >= min(c1, n - s * run)) continue;
+                    const float *from = sum + (s * KW * UT + u - s * UT) * Smem::kSum + m * kLw4Stride + r;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                    for (int k = 0; k < nk; ++k) lw4_add(v, *reinterpret_cast<const float4 *>(from + k * (UT * Smem::kSum)));
                     if (direct) {
-                        lw4_store(a, m0 + m, (rb + s) * kW4Rows + r, v);
+                        lw4_store(a, m0 + m, (r0 + s * run + t) * kW4Rows + r, v);
                     } else {
-                        float *p = mine + ((rb - cb + s) * 4 * NT + m) * 16 + r;
-                        *p = pass == 0 ? v : *p + v;
+                        float4 *p = reinterpret_cast<float4 *>(mine + ((s * a.chunk + t - c0) * 8 * NT + m) * 16 + r);
+                        if (pass > 0) lw4_add(v, *p);
+                        *p = v;
                     }
                 }
             }
@@ -267,24 +287,22 @@ __global__ void __launch_bounds__(32 * lw4_warps(NT), 1) linear_w4_kernel(const 
         // the ranks' sums.  A buffer is written again after the next one's barrier, which
         // every rank reaches when it has read this one.
         lw4_cluster_sync();
-        for (int i = rank * THREADS + tid; i < (ce - cb) * Mt * 16; i += P * THREADS) {
-            const int r = i & 15, mt = i >> 4, s = mt / Mt, m = mt - s * Mt;
-            const uint32_t at = tc_smem(mine + (s * 4 * NT + m) * 16 + r);
-            float v = 0.f;
-#pragma unroll 8
-            for (int k = 0; k < P; ++k) {
-                uint32_t there;
-                float f;
-                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(k));
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(there) : "memory");
-                v += f;
-            }
-            lw4_store(a, m0 + m, (cb + s) * kW4Rows + r, v);
+        for (int i = rank * THREADS + tid; i < RW * (c1 - c0) * Mt * 4; i += P * THREADS) {
+            const int r = 4 * (i & 3), um = i >> 2, u = um / Mt, m = um - u * Mt, s = u / (c1 - c0), t = c0 + u - s * (c1 - c0);
+            if (t >= n - s * run) continue;
+            const float *p = mine + ((s * a.chunk + t - c0) * 8 * NT + m) * 16 + r;
+            float4 f[kLw4MaxCluster], v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kLw4MaxCluster; ++k) f[k] = k < P ? lw4_peer(p, k) : v;
+#pragma unroll
+            for (int k = 0; k < kLw4MaxCluster; ++k)
+                if (k < P) lw4_add(v, f[k]);
+            lw4_store(a, m0 + m, (r0 + s * run + t) * kW4Rows + r, v);
         }
     }
     if (!direct) lw4_cluster_sync();   // a rank's shared memory lives until all have read it
     // copies in flight behind an expired wait land before the CTA ends
-    for (; lost && used < issued; ++used) {
+    for (; lost && flying > 0; --flying) {
         tc_mbar_wait(&bar[st], parity, kTcWaitNs);
         if (++st == ST) {
             st = 0;
@@ -296,21 +314,15 @@ __global__ void __launch_bounds__(32 * lw4_warps(NT), 1) linear_w4_kernel(const 
 template <int NT, int G>
 static cudaError_t lw4_launch(LinearW4Args a, int sms, cudaStream_t s) {
     using Smem = Lw4Smem<NT, G>;
-    constexpr int kDevices = 64, kMaxCluster = 8, NW = Smem::kWarps;
-    static std::atomic<int> known[kDevices][kMaxCluster + 1];   // clusters that are resident at once
+    constexpr int kDevices = 64, NW = Smem::kWarps;
+    static std::atomic<int> known[kDevices][kLw4MaxCluster + 1];   // clusters that are resident at once
     const auto kern = linear_w4_kernel<NT, G>;
-    const int per = (a.k_tiles + NW - 1) / NW;
-    a.cluster = per < kMaxCluster ? per : kMaxCluster;
-    a.passes = (a.k_tiles + a.cluster * NW - 1) / (a.cluster * NW);
-    a.k_warps = (a.k_tiles + a.cluster * a.passes - 1) / (a.cluster * a.passes);
-
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(32 * NW);
     cfg.dynamicSmemBytes = Smem::kBytes;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)a.cluster;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -319,38 +331,56 @@ static cudaError_t lw4_launch(LinearW4Args a, int sms, cudaStream_t s) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    int clusters = dev < kDevices ? known[dev][a.cluster].load(std::memory_order_relaxed) : 0;
-    if (clusters == 0) {
+    if (dev >= kDevices) return cudaErrorInvalidDevice;
+    if (known[dev][1].load(std::memory_order_acquire) == 0) {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::kBytes);
         if (e != cudaSuccess) return e;
-        clusters = sms / a.cluster;
-        if (a.cluster > 1) {   // fewer where the SMs of a GPC are no multiple of the cluster
-            int most = 0;
-            cfg.gridDim = dim3((unsigned)(sms / a.cluster * a.cluster));
-            cfg.numAttrs = 1;
-            e = cudaOccupancyMaxActiveClusters(&most, kern, &cfg);
-            if (e != cudaSuccess) return e;
-            if (most > 0 && most < clusters) clusters = most;
+        for (int P = kLw4MaxCluster; P >= 1; --P) {   // fewer than sms / P where a GPC's SMs are no multiple of P
+            int most = sms / P;
+            if (P > 1) {
+                attr[0].val.clusterDim.x = (unsigned)P;
+                cfg.gridDim = dim3((unsigned)(sms / P * P));
+                cfg.numAttrs = 1;
+                e = cudaOccupancyMaxActiveClusters(&most, kern, &cfg);
+                if (e != cudaSuccess) return e;
+            }
+            known[dev][P].store(most < 1 ? 1 : most < sms / P ? most : sms / P, std::memory_order_release);
         }
-        if (clusters < 1) clusters = 1;
-        if (dev < kDevices) known[dev][a.cluster].store(clusters, std::memory_order_relaxed);
     }
+    // The cluster that keeps most warps busy; of equals the smallest.  One pass if eight CTAs' warps
+    // hold the columns.
+    long long best = -1;
+    for (int P = 1; P <= kLw4MaxCluster; ++P) {
+        const int passes = (a.k_tiles + P * NW - 1) / (P * NW), kw = (a.k_tiles + P * passes - 1) / (P * passes);
+        if (passes > 1 && P < kLw4MaxCluster) continue;
+        const long long busy = (long long)known[dev][P].load(std::memory_order_relaxed) * (NW / kw) * a.k_tiles / passes;
+        if (busy <= best) continue;
+        best = busy;
+        a.cluster = P;
+        a.passes = passes;
+        a.k_warps = kw;
+    }
+    int clusters = known[dev][a.cluster].load(std::memory_order_relaxed);
     if (clusters > a.row_tiles) clusters = a.row_tiles;
     const int rows = (a.row_tiles + clusters - 1) / clusters;   // of tiles, at most, of a cluster
+    const bool direct = a.cluster == 1 && a.passes == 1;
+    const int fit = kLw4Partial / (8 * NT * 16 * 4);
     a.row_warps = NW / a.k_warps < rows ? NW / a.k_warps : rows;
-    const int fit = kLw4Partial / (4 * NT * 16 * 4);
-    a.chunk = a.cluster == 1 && a.passes == 1 ? rows : (fit < a.row_warps ? a.row_warps : fit / a.row_warps * a.row_warps);
-    cfg.gridDim = dim3((unsigned)(clusters * a.cluster), (unsigned)((a.M + 4 * NT - 1) / (4 * NT)));
+    if (!direct && a.row_warps * kLw4Unit > fit) a.row_warps = fit / kLw4Unit;
+    const int run = (rows + a.row_warps - 1) / a.row_warps;
+    a.chunk = direct ? run : fit / a.row_warps / kLw4Unit * kLw4Unit;
+    a.wide = a.ldy % 4 == 0 && ((uintptr_t)a.y & (a.f32 ? 15u : 7u)) == 0;
+    attr[0].val.clusterDim.x = (unsigned)a.cluster;
+    cfg.gridDim = dim3((unsigned)(clusters * a.cluster), (unsigned)((a.M + 8 * NT - 1) / (8 * NT)));
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 template <int G>
 static cudaError_t lw4_launch_tokens(const LinearW4Args &a, int sms, cudaStream_t s) {
-    if (a.M <= 4) return lw4_launch<1, G>(a, sms, s);
-    if (a.M <= 8) return lw4_launch<2, G>(a, sms, s);
-    if (a.M <= 16) return lw4_launch<4, G>(a, sms, s);
-    return lw4_launch<8, G>(a, sms, s);
+    if (a.M <= 8) return lw4_launch<1, G>(a, sms, s);
+    if (a.M <= 16) return lw4_launch<2, G>(a, sms, s);
+    return lw4_launch<4, G>(a, sms, s);
 }
 
 cudaError_t launch_linear_w4(LinearW4Args a, int sms, cudaStream_t s) {

@@ -19,13 +19,14 @@ namespace bloom {
 
 constexpr int kW4Threads = 128;
 
-// Columns 8 q + b (low) and 8 q + 4 + b (high) of a word from eight codes.
+// A word from its eight codes, for w4_pair().
 __device__ __forceinline__ uint32_t w4_word(const int (&c)[8]) {
     uint32_t w = 0;
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        w |= (uint32_t)abs(c[b]) << (8 * b) | (uint32_t)abs(c[4 + b]) << (8 * b + 4);
-        w |= (c[b] < 0 ? 1u : 0u) << (8 * b + 7) | (c[4 + b] < 0 ? 1u : 0u) << ((8 * b + 11) & 31);
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t half = (uint32_t)abs(c[e]) << 8 | (c[e] < 0 ? 0x8000u : 0u);
+        const uint32_t both = half << (16 * (e & 1));
+        w |= e < 6 ? __funnelshift_r(both, both, 4 * (e >> 1)) : __funnelshift_l(both, both, 4);
     }
     return w;
 }
@@ -54,7 +55,7 @@ __global__ void __launch_bounds__(kW4Threads) w4_quantize_kernel(const W4Args a)
     const int ktiles = (a.K + kW4Cols - 1) / kW4Cols, row_tiles = (a.N + kW4Rows - 1) / kW4Rows;
     if (tile >= (long long)ktiles * row_tiles) return;
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const int rt = (int)(tile / ktiles), k0 = (int)(tile - (long long)rt * ktiles) * kW4Cols;
+    const int kt = (int)(tile / row_tiles), rt = (int)(tile - (long long)kt * row_tiles), k0 = kt * kW4Cols;
     const int row[2] = {rt * kW4Rows + g, rt * kW4Rows + g + 8};
     unsigned char *out = a.tiles + tile * w4_tile_bytes(G);
 #pragma unroll
@@ -107,11 +108,11 @@ __global__ void __launch_bounds__(kW4Threads) w4_quantize_kernel(const W4Args a)
     }
 }
 
-// Code b of the eight of a word.
-__device__ __forceinline__ float w4_code(uint32_t w, int b) {
-    const uint32_t byte = ((b < 4 ? w : __funnelshift_r(w, w, 4)) >> (8 * (b & 3))) & 0x87u;
-    const float m = (float)(byte & 7u);
-    return byte & 0x80u ? -m : m;
+// Code e of the eight of a word.
+__device__ __forceinline__ float w4_code(uint32_t w, int e) {
+    const uint32_t half = w4_pair(w, e >> 1) >> (16 * (e & 1));
+    const float m = (float)(half >> 8 & 7u);
+    return half & 0x8000u ? -m : m;
 }
 
 template <int G>
@@ -122,7 +123,7 @@ __global__ void __launch_bounds__(kW4Threads) w4_read_kernel(const W4Args a) {
     const int ktiles = (a.K + kW4Cols - 1) / kW4Cols, row_tiles = (a.N + kW4Rows - 1) / kW4Rows;
     if (tile >= (long long)ktiles * row_tiles) return;
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const int rt = (int)(tile / ktiles), k0 = (int)(tile - (long long)rt * ktiles) * kW4Cols;
+    const int kt = (int)(tile / row_tiles), rt = (int)(tile - (long long)kt * row_tiles), k0 = kt * kW4Cols;
     const unsigned char *in = a.tiles + tile * w4_tile_bytes(G);
     uint4 v[4];
     uint32_t s[kW4Cols / G];

@@ -323,7 +323,8 @@ struct LinearW4Args {
     int row_tiles = 0, k_tiles = 0;
     int cluster = 1, passes = 1;       // CTAs that share rows of tiles; times each takes them
     int k_warps = 0, row_warps = 0;    // warps side by side on a row of tiles; rows at a time
-    int chunk = 0;                     // rows of tiles between two joints of a cluster's sums
+    int chunk = 0;                     // tiles of a warp between two joints of a cluster's sums
+    int wide = 0;                      // y takes four neighbouring rows at once
 };
 cudaError_t launch_linear_w4(LinearW4Args a, int sms, cudaStream_t s);
 

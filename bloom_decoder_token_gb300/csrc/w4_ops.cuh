@@ -5,15 +5,18 @@
 // 128) neighbouring weights of a row.  The matrix [N][K] lies in tiles of 16 rows x
 // 256 columns, [ceil(N / 16)][ceil(K / 256)], zeros beyond N and K, so that a warp
 // streams whole tiles with one bulk copy each and finds its fragments of mma.sync
-// m16n8k32 in place:
+// m16n8k16 in place:
 //  * codes, 2048 bytes: lane (g, q) = 4 g + q holds rows g and g + 8, of every 32
 //    columns j the eight 8 q .. 8 q + 7: 16-byte piece i (at i * 512 + lane * 16) =
 //    words (row g, j = 2 i), (row g + 8, 2 i), (row g, 2 i + 1), (row g + 8, 2 i + 1);
 //  * scales, 32 bytes a group: rows g and g + 8 side by side, for g = 0 .. 7.
-// Byte b of a word holds columns 8 q + b and 8 q + 4 + b as sign and magnitude, laid so
-// that the word itself and the word turned right by 4 bits, masked with 0x87 in
-// every byte, are four e4m3 numbers each: the magnitude (0 .. 7) in the last three bits
-// of an e4m3 is a subnormal, magnitude * 2^-9.  Eight codes cost three instructions.
+// A word's pair i is columns 8 q + 2 i and 8 q + 2 i + 1, each as sign and magnitude, laid
+// so that the word, shifted (w4_pair) and masked with 0x87008700, is the two codes as f16
+// numbers: with the magnitude (0 .. 7) in bits 8 to 10, the last two bits of its place in
+// the fraction and the last of the exponent, an f16 is magnitude * 2^-16.  Eight codes cost
+// seven instructions, and nothing has to be subtracted.  (In the last three bits, as
+// subnormals of 2^-24, they cost the tensor cores' sums seven bits: products are
+// aligned by exponent.)
 #pragma once
 
 #include <stdint.h>
@@ -23,10 +26,12 @@
 namespace bloom {
 
 constexpr int kW4Rows = 16, kW4Cols = 256;
-constexpr uint32_t kW4Mask = 0x87878787u;
 __host__ __device__ constexpr int w4_tile_bytes(int group) { return 2048 + 8192 / group; }
 
-__device__ __forceinline__ uint32_t w4_low(uint32_t w) { return w & kW4Mask; }
-__device__ __forceinline__ uint32_t w4_high(uint32_t w) { return __funnelshift_r(w, w, 4) & kW4Mask; }
+// Codes 2 i and 2 i + 1 of a word, times 2^-16, as f16x2.  Shifts to the left can run on
+// another pipe than the masks; the last pair takes a turn, for one sign bit is left at the other end.
+__device__ __forceinline__ uint32_t w4_pair(uint32_t w, int i) {
+    return (i < 3 ? w << (4 * i) : __funnelshift_r(w, w, 4)) & 0x87008700u;
+}
 
 }  // namespace bloom

@@ -153,7 +153,7 @@ def test_rows_of_activations_are_their_own():
 
 
 def test_activations_of_far_apart_sizes():
-    """Outliers 2^13 above the others lose nothing; one that is larger still costs what the tolerance says."""
+    """Outliers far above the others lose nothing; one that is larger still costs what the tolerance says."""
     M, n, k = 6, 64, 1024
     w, x = weights(n, k), acts(M, k).float()
     x[:, 3::256] *= 2.0 ** 9
@@ -168,7 +168,7 @@ def test_activations_of_far_apart_sizes():
 
 
 def test_small_activations_beside_large_ones_of_zero_weight():
-    """What a large activation hides is off by 2^-22 of it at most, also where its own weight is 0."""
+    """A large activation whose own weight is 0 hides nothing of the others."""
     n, k = 16, 256
     w = torch.zeros(n, k, device=DEV)
     w[:, 100:132] = 7.0 * 0.01

@@ -40,15 +40,15 @@ def linear(x, wide, bias=None, epilogue=0, y=None):
 
     The tolerance, before the output's own rounding: a float32 sum of products in chains
     of at most 64 additions (8 of a tensor core's sums a group, 8 groups a warp, 16 warps, 8 ranks, passes), each
-    off by 2^-23 of the sum of magnitudes at most; activations below 2^-14 of the largest
-    of their 256 columns, off by 2^-22 of it; the GeLU's slope is below 1.13, its own
+    off by 2^-23 of the sum of magnitudes at most; activations below 2^-31 of the largest
+    of their 256 columns, off by 2^-39 of it; the GeLU's slope is below 1.13, its own
     arithmetic off by 2^-20 of its result or 2^-22 of its argument at most."""
     x = x.double()
     k = x.shape[1]
     v = x @ wide.t()
     far = x.abs() @ wide.abs().t() * (64 * 2.0 ** -23)
     for a in range(0, k, 256):
-        far += x[:, a: a + 256].abs().amax(1, keepdim=True) * wide[:, a: a + 256].abs().sum(1) * 2.0 ** -22
+        far += x[:, a: a + 256].abs().amax(1, keepdim=True) * wide[:, a: a + 256].abs().sum(1) * 2.0 ** -39
     if bias is not None:
         v = v + bias.double()
         far += v.abs() * 2.0 ** -23
