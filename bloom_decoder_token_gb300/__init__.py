@@ -113,6 +113,7 @@ _SIGS = {
     "bloom_op_attn_decode": (I32, [P, P, P, P, P, I32, I32, I32, I32, I32, I32, P, P]),
     "bloom_op_lmhead_argmax": (I32, [P, P, I32, I32, I32, P, P, P]),
     "bloom_op_sample": (I32, [P, I32, I32, C.c_int64, P, P, P, P, P]),
+    "bloom_op_sample_filtered": (I32, [P, I32, I32, C.c_int64, P, P, P, P, P, I32, P, P]),
     "bloom_op_logprobs": (I32, [P, I32, I32, C.c_int64, P, I32, P, P, I32, P, P, P]),
     "bloom_op_kv8_write": (I32, [P, P, P, P, P, I32, P, P, P, P, P]),
     "bloom_op_kv8_read": (I32, [P, P, P, P, P, I32, P, P, P, P]),
@@ -654,6 +655,38 @@ def op_attn_decode_kv8(q, kv: KV8, pos, slopes, lens, o=None, workspace=None, fl
     if st:
         check(st)
     return o
+
+
+def op_sample_filtered(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out=None,
+                       stream=None):
+    """Tokens of float32 logits [B][V] (rows may be strided) drawn at uniform numbers u
+    (float32 [B], or [B][J] for J draws a row) with per-row temperature, top_p, min_p
+    (float32 [B]) and top_k (int32 [B]), None for none: int32, shaped like u."""
+    dev = logits.device
+    if logits.dtype is not _F32 or logits.dim() != 2 or logits.stride(1) != 1:
+        _bad(f"logits: float32 [B][V] with unit last stride expected, got {logits.dtype} "
+             f"{tuple(logits.shape)}, strides {logits.stride()}")
+    B, V = logits.shape
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return op_sample_filtered(logits, u, temperature, top_k, top_p, min_p, out)
+    J = u.shape[1] if u.dim() == 2 else 1
+    shape = (B, J) if u.dim() == 2 else (B,)
+    up, row = _dev("u", u, _F32, shape, dev), (B,)
+    if out is None:
+        out = torch.empty(shape, dtype=_I32, device=dev)
+        op = out.data_ptr()
+    else:
+        op = _dev("out", out, _I32, shape, dev)
+    st = lib().bloom_op_sample_filtered(
+        logits.data_ptr(), B, V, logits.stride(0) if B > 1 else V,
+        _dev("temperature", temperature, _F32, row, dev), _dev("top_k", top_k, _I32, row, dev),
+        _dev("top_p", top_p, _F32, row, dev), _dev("min_p", min_p, _F32, row, dev), up, J, op,
+        _raw_stream(dev))
+    if st:
+        check(st)
+    return out
 
 
 def op_logprobs(logits, tokens=None, top: int = 0, stream=None):

@@ -1419,6 +1419,35 @@ extern "C" bloom_status bloom_op_sample(const float *logits, int32_t B, int32_t 
     return BLOOM_OK;
 }
 
+extern "C" bloom_status bloom_op_sample_filtered(const float *logits, int32_t B, int32_t V, int64_t ld,
+                                                 const float *temperature, const int32_t *top_k,
+                                                 const float *top_p, const float *min_p,
+                                                 const float *u, int32_t J, int32_t *out_tokens,
+                                                 void *stream) {
+    g_pdl = true;
+    if (B < 0 || B > 65535 || V < 1 || ld < V || J < 0)
+        return fail(BLOOM_E_INVALID, "B=%d V=%d ld=%lld J=%d", B, V, (long long)ld, J);
+    if (B == 0 || J == 0) return BLOOM_OK;
+    if (!logits || !u || !out_tokens) return fail(BLOOM_E_INVALID, "null argument");
+    if (((uintptr_t)logits | (uintptr_t)temperature | (uintptr_t)top_k | (uintptr_t)top_p |
+         (uintptr_t)min_p | (uintptr_t)u | (uintptr_t)out_tokens) & 3u)
+        return fail(BLOOM_E_INVALID, "pointers must be aligned to their elements");
+    SampleFilteredArgs a;
+    a.logits = logits;
+    a.ld = ld;
+    a.B = B;
+    a.V = V;
+    a.J = J;
+    a.temperature = temperature;
+    a.top_k = top_k;
+    a.top_p = top_p;
+    a.min_p = min_p;
+    a.u = u;
+    a.out = out_tokens;
+    CK(launch_sample_filtered(a, (cudaStream_t)stream));
+    return BLOOM_OK;
+}
+
 extern "C" bloom_status bloom_op_logprobs(const float *logits, int32_t B, int32_t V, int64_t ld,
                                           const int32_t *tokens, int32_t J, float *logp,
                                           float *entropy, int32_t top, int32_t *top_ids,

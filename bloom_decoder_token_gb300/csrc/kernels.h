@@ -233,6 +233,22 @@ struct SampleArgs {
 };
 cudaError_t launch_sample(const SampleArgs &a, cudaStream_t s);
 
+// Sampling with temperature, top-k, top-p and min-p (k_sample_filtered.cu): arrays as
+// bloom_op_sample_filtered describes them.
+struct SampleFilteredArgs {
+    const float *logits = nullptr;
+    long long ld = 0;
+    int B = 0, V = 0, J = 0;
+    const float *temperature = nullptr;   // [B] or null, as the next three
+    const int32_t *top_k = nullptr;
+    const float *top_p = nullptr;
+    const float *min_p = nullptr;
+    const float *u = nullptr;             // [B][J]
+    int32_t *out = nullptr;               // [B][J]
+    int cached = 0;                       // set by the launch: slices stay in shared memory
+};
+cudaError_t launch_sample_filtered(SampleFilteredArgs a, cudaStream_t s);
+
 // Log probabilities of given tokens, entropy and the top alternatives of B rows of
 // float32 logits (k_logprobs.cu); arrays as bloom_op_logprobs describes them.
 struct LogprobsArgs {

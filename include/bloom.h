@@ -411,6 +411,28 @@ bloom_status bloom_op_sample(const float *logits, int32_t B, int32_t V, int64_t 
                              const float *temperature, const float *top_p, const float *u,
                              int32_t *out_tokens, void *stream);
 
+/* Sampling with temperature, top-k, top-p and min-p of B rows of float32 logits (row
+ * b at logits + b * ld, ld >= V), J draws a row.  temperature, top_p, min_p (float) and
+ * top_k (int32): device arrays [B], or NULL for none (temperature 1); u: device
+ * float [B][J]; out_tokens: device int32 [B][J].  Row b: p proportional to
+ * exp((z - max z) / temperature); in the order of bloom_op_sample (probability,
+ * highest first, equal logits by index) the kept tokens are the first top_k, of
+ * those the shortest prefix that holds top_p of their mass, and of those the
+ * ones with p >= min_p * max p.  Each draw takes the token where the kept mass,
+ * summed in vocabulary order, first exceeds u times the whole of it.
+ * temperature <= 0 or NaN, or top_p <= 0: the most probable token.  Off: top_k <= 0,
+ * top_p >= 1 or NaN, min_p <= 0 or NaN; min_p >= 1 keeps the tokens of the largest
+ * logit.  u < 0 or NaN counts as 0, u >= 1 takes the last kept token with mass.
+ * NaN and -inf logits take no part, nor do logits 40 or more binades of mass below the
+ * maximum; +inf logits share the whole mass.  Masses are 2^-40 fixed point, summed in
+ * 64-bit integers: the result does not depend on the order of summation.  A row
+ * where nothing takes part gives -1.  BLOOM_E_INVALID for null or misaligned
+ * pointers, B outside 0..65535, V < 1, ld < V, J < 0 (B = 0 or J = 0 does nothing). */
+bloom_status bloom_op_sample_filtered(const float *logits, int32_t B, int32_t V, int64_t ld,
+                                      const float *temperature, const int32_t *top_k,
+                                      const float *top_p, const float *min_p, const float *u,
+                                      int32_t J, int32_t *out_tokens, void *stream);
+
 /* Log probabilities of given tokens, with entropy and top alternatives, of B rows
  * of float32 logits (row b at logits + b * ld, ld >= V; device), natural
  * logarithms of softmax(logits):
