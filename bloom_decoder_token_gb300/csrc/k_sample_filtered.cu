@@ -16,18 +16,19 @@
 //
 // Bound by the logits' first read; then by the passes over them in shared memory or
 // L2.  One cluster of up to 8 CTAs a row, each a slice of the vocabulary:
-//  1. the maximum and minimum;
-//  2. (top-k or top-p) a histogram of counts over the exponent, in 2048 bins, and the whole
-//     mass.  A bin's tokens have masses within its edges', so the counts alone bound
-//     where the cut's mass is reached to a band of bins.  (A histogram of masses needs 64-bit
-//     atomics for every token.)
-//  3. the exact mass above the band, and the band's tokens to the first CTA, which finds
-//     the cut among them by radix over their keys.  A band of more tokens than fit
-//     there is divided by another histogram, of masses over its range of keys, until it fits
-//     or is a single logit.
-//     Top-k and then top-p: one list serves both where it holds all of the top k.
-//  4. the kept mass of 64 segments of each slice; the segment of a draw is walked to
-//     the token.
+//  1. the maximum and minimum, and every thread's own maximum;
+//  2. where few tokens can be kept, these come to the first CTA, which ranks them and does the
+//     rest: of the top 256, those that reach the k-th of a slice's 512 thread maxima; the maximum's
+//     ties; what reaches min-p;
+//  3. else (top-p, or a larger k) a histogram of counts over the exponent, in 2048 bins, and
+//     the whole mass.  A bin's tokens have masses within its edges', so the counts alone
+//     bound where the cut's mass is reached to a band of bins.  (A histogram of masses needs
+//     64-bit atomics for every token.)  If all down to the band are few: 2.
+//  4. the exact mass above the band, by segments of the slices, and the band's tokens to
+//     the first CTA, which finds the cut among them by radix over their keys.  A band of more
+//     tokens than fit there is divided by another histogram, of masses over its range of
+//     keys, until it fits or is a single logit.
+//  5. the kept mass by segments; the segment of a draw is walked to the token.
 #include <atomic>
 #include <math.h>
 #include <stdint.h>
@@ -43,8 +44,11 @@ constexpr int kSfMaxCluster = 8;
 constexpr int kSfThreads = 512;
 constexpr int kSfWarps = kSfThreads / 32;
 constexpr int kSfBins = 2048;
-constexpr int kSfList = 4096;                  // tokens of a band that the first CTA looks through
-constexpr int kSfSegments = 64;                // of a slice
+constexpr int kSfList = 4096;                  // tokens that a CTA lists
+constexpr int kSfRank = 1024;                  // that the first CTA ranks
+constexpr int kSfBound = 256;                  // a top-k up to which thread maxima give a bound
+constexpr int kSfDigits = 1024;
+constexpr int kSfSegments = 64;                // of a slice; before them its ragged head, after them its tail
 constexpr float kSfUnit = 1099511627776.f;     // 2^40
 constexpr float kSfFar = 40.f;                 // binades below the maximum from which on a mass is 0
 // Bounds of a bin's masses allow for the rounding of exponents (40 * 2^-23) and exponentials.  (The
@@ -53,15 +57,18 @@ constexpr float kSfSlack = 1.f / 65536.f;
 
 // Slots of the values that the ranks tell one another.  A slot is written again only after a
 // barrier that follows its reading.
-enum { kSfRange, kSfAbove, kSfFound, kSfLeft, kSfWhole, kSfBand, kSfHeld, kSfMass, kSfTies, kSfSlots };
+enum { kSfRange, kSfBoundKey, kSfCount, kSfAbove, kSfFound, kSfLeft, kSfWhole, kSfBand, kSfHeld, kSfMass, kSfTies, kSfSlots };
 
-struct alignas(16) SfSmem {   // the cached slice follows, in float4s
-    sf_u64 list[kSfList];                      // first CTA: key << 32 | ~index
-    uint32_t hist[kSfBins];                    // this CTA's counts
+struct alignas(16) SfSmem {                    // the cached slice follows, in float4s
+    sf_u64 list[kSfList];                      // key << 32 | ~index; first CTA: of all ranks
+    union {
+        uint32_t hist[kSfBins];                // this CTA's counts
+        sf_u64 digit[kSfDigits];               // first CTA, looking through the list
+    };
     uint32_t counts[kSfBins];                  // the cluster's
-    sf_u64 digit[256];
-    sf_u64 seg_mass[kSfSegments];
-    uint32_t seg_ties[kSfSegments];
+    sf_u64 seg_mass[kSfSegments + 2];
+    uint32_t seg_ties[kSfSegments + 2];
+    alignas(16) uint32_t own_max[kSfThreads];
     sf_u64 scan[2][kSfWarps];
     uint32_t scan_n[kSfWarps];
     sf_u64 part[kSfWarps][3];
@@ -85,6 +92,16 @@ __device__ __forceinline__ uint32_t sf_at(const void *p, uint32_t rank) {
 __device__ __forceinline__ void sf_put(void *p, uint32_t rank, sf_u64 v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(sf_at(p, rank)), "l"(v) : "memory");
 }
+__device__ __forceinline__ sf_u64 sf_get(const void *p, uint32_t rank) {
+    sf_u64 v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(sf_at(p, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t sf_get32(const void *p, uint32_t rank) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(sf_at(p, rank)) : "memory");
+    return v;
+}
 
 // ---- a row's exponents and masses
 __device__ __forceinline__ uint32_t sf_key(float z) { return ordered_key(z + 0.f); }   // -0 as +0
@@ -96,54 +113,53 @@ __device__ __forceinline__ bool sf_takes_part(float z) { return z > -INFINITY; }
 struct SfRow {
     float top;         // the maximum
     float c, c_low;    // log2(e) / t, in two floats
-    // (top - z) c in two floats; at least kSfFar where no mass is left
-    __device__ __forceinline__ float exponent(float z, float &low) const {
-        low = 0.f;
-        if (z == top) return 0.f;
-        const float d = top - z, w = d - top;
-        const float e = (top - (d - w)) - (z + w);     // what d lost
-        if (d == INFINITY) return kSfFar;              // an infinite maximum, or too far
-        const float x = d * c;
-        low = fmaf(d, c, -x) + fmaf(d, c_low, e * c);
-        return x;
-    }
-    __device__ __forceinline__ sf_u64 mass(float z) const {
-        float low;
-        const float x = exponent(z, low);
-        if (!(x < kSfFar)) return 0ull;
+    // For logits that take part: (top - z) c; an infinite maximum's own is 0, others' are past kSfFar.
+    __device__ __forceinline__ float exponent(float z) const { return fmaxf(top - z, 0.f) * c; }
+    __device__ __forceinline__ sf_u64 mass(float z, float &x) const {
+        const float d = fmaxf(top - z, 0.f);
+        x = d * c;
+        // what the product, c and the difference (where |top| >= |z|) lost
+        const float low = fmaf(d, c_low, fmaf((top - d) - z, c, fmaf(d, c, -x)));
         float y;
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(-x));
-        y = fmaf(y * -0.6931471805599453f, low, y);
-        return (sf_u64)(y * kSfUnit);
+        if (d > 0.f) y = fmaf(y * -0.6931471805599453f, low, y);
+        // to 2^-40: from 2^-9 on in steps of 2^-31, which a float has there
+        const bool near = y >= 0x1p-9f;
+        const uint32_t m = __float2uint_rz(y * (near ? 0x1p31f : kSfUnit));
+        return x < kSfFar ? (near ? (sf_u64)m << 9 : (sf_u64)m) : 0ull;
+    }
+    __device__ __forceinline__ sf_u64 mass(float z) const {
+        float x;
+        return mass(z, x);
     }
 };
 
-// How the tokens are dealt to bins: by exponent, or by key from `high` down.
+// How the tokens are dealt to bins: by exponent (rounded to the nearest of per_binade a
+// binade), or by key from `high` down.
 struct SfBins {
     bool keys;
     float per_binade;
     uint32_t high, low;
     int shift;
-    // the bin; -1: above all bins, kSfBins: below them
+    __device__ __forceinline__ int near(float x) const {   // x < kSfFar
+        return __float_as_int(fmaf(x, per_binade, 8388608.f)) & (kSfBins - 1);
+    }
+    // the bin of a logit that takes part; -1: above all bins, kSfBins: below them
     __device__ __forceinline__ int of(const SfRow &row, float z) const {
         if (keys) {
             const uint32_t k = sf_key(z);
             return k > high ? -1 : k < low ? kSfBins : (int)((high - k) >> shift);
         }
-        float low_part;
-        const float x = row.exponent(z, low_part);
-        return x < kSfFar ? min(kSfBins - 1, (int)(x * per_binade)) : kSfBins;
+        const float x = row.exponent(z);
+        return x < kSfFar ? near(x) : kSfBins;
     }
     // bounds of the masses in bin i, by exponent
     __device__ __forceinline__ sf_u64 most(int i) const {
-        return up((sf_u64)((per_binade > 0.f ? exp2f(-(float)i / per_binade) : 1.f) * kSfUnit));   // 0: one exponent
+        const sf_u64 m = (sf_u64)((per_binade > 0.f ? exp2f(-fmaxf((float)i - 0.5f, 0.f) / per_binade) : 1.f) * kSfUnit);
+        return m + (sf_u64)((float)m * kSfSlack) + 2ull;
     }
     __device__ __forceinline__ sf_u64 least(int i) const {
-        if (i == kSfBins - 1) return 0ull;
-        return down((sf_u64)((per_binade > 0.f ? exp2f(-(float)(i + 1) / per_binade) : 1.f) * kSfUnit));
-    }
-    static __device__ __forceinline__ sf_u64 up(sf_u64 m) { return m + (sf_u64)((float)m * kSfSlack) + 2ull; }
-    static __device__ __forceinline__ sf_u64 down(sf_u64 m) {
+        const sf_u64 m = (sf_u64)((per_binade > 0.f ? exp2f(-((float)i + 0.5f) / per_binade) : 1.f) * kSfUnit);
         const sf_u64 less = (sf_u64)((float)m * kSfSlack) + 2ull;
         return m > less ? m - less : 0ull;
     }
@@ -162,6 +178,22 @@ __device__ __forceinline__ sf_u64 sf_warp_scan(sf_u64 v) {   // inclusive
     }
     return v;
 }
+// Exclusive scan over the block in thread order; `total` of all.
+__device__ __forceinline__ sf_u64 sf_block_scan(SfSmem &sm, sf_u64 v, sf_u64 &total) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const sf_u64 in = sf_warp_scan(v);
+    __syncthreads();
+    if (lane == 31) sm.scan[0][w] = in;
+    __syncthreads();
+    sf_u64 before = 0ull;
+    total = 0ull;
+#pragma unroll
+    for (int i = 0; i < kSfWarps; ++i) {
+        if (i < w) before += sm.scan[0][i];
+        total += sm.scan[0][i];
+    }
+    return before + in - v;
+}
 
 // A cut: kept are keys above `key`, and the first `ties` tokens by index that have it.
 struct SfCut {
@@ -176,81 +208,181 @@ struct SfCut {
     }
 };
 
-// In the first CTA's list (n tokens): the key at which the weights of the highest keys,
-// one a token or its mass, reach `target`, and what of the target is left for its ties.
-__device__ __forceinline__ uint32_t sf_select(SfSmem &sm, const SfRow &row, int n, bool by_mass, sf_u64 &target) {
-    const int tid = threadIdx.x, lane = tid & 31;
-    uint32_t found = 0;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) sm.digit[tid] = 0ull;
+// In the first CTA's list (n tokens, keys from `least` to `most`): the key at which the weights of the
+// highest keys, one a token or its mass, reach `target`, and what of the target is left for its ties.
+__device__ __forceinline__ uint32_t sf_select(SfSmem &sm, const SfRow &row, int n, uint32_t most, uint32_t least,
+                                              bool by_mass, sf_u64 &target) {
+    constexpr int kBits = 10, PT = kSfDigits / kSfThreads;
+    const int tid = threadIdx.x;
+    uint32_t found = 0;   // of most - key, the bits above `shift`
+    for (int shift = max(0, 32 - __clz((int)(most - least)) - kBits);; shift = max(0, shift - kBits)) {
+        __syncthreads();
+        for (int i = tid; i < kSfDigits; i += kSfThreads) sm.digit[i] = 0ull;
         __syncthreads();
         for (int i = tid; i < n; i += kSfThreads) {
-            const uint32_t k = (uint32_t)(sm.list[i] >> 32);
-            if (shift < 24 && (k >> (shift + 8)) != found >> (shift + 8)) continue;
-            atomicAdd(&sm.digit[k >> shift & 255u], by_mass ? row.mass(sf_unkey(k)) : 1ull);
+            const uint32_t k = (uint32_t)(sm.list[i] >> 32), far = (most - k) >> shift;
+            if (far >= found && far - found < kSfDigits) atomicAdd(&sm.digit[far - found], by_mass ? row.mass(sf_unkey(k)) : 1ull);
         }
         __syncthreads();
-        if (tid < 32) {   // digits from 255 down, eight a lane
-            sf_u64 own = 0ull;
+        sf_u64 own[PT], sum = 0ull, total;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) own += sm.digit[255 - 8 * lane - e];
-            const sf_u64 upto = sf_warp_scan(own);
-            const unsigned reach = __ballot_sync(0xffffffffu, upto >= target);
-            const int src = reach ? __ffs(reach) - 1 : 31;
-            if (lane == src) {
-                sf_u64 run = upto - own;
-                int e = 0;
-                for (; e < 7 && run + sm.digit[255 - 8 * lane - e] < target; ++e) run += sm.digit[255 - 8 * lane - e];
-                sm.found[0] = (sf_u64)(255 - 8 * lane - e);
+        for (int e = 0; e < PT; ++e) sum += own[e] = sm.digit[tid * PT + e];
+        sf_u64 run = sf_block_scan(sm, sum, total);
+#pragma unroll
+        for (int e = 0; e < PT; ++e) {
+            if (run < target && run + own[e] >= target) {
+                sm.found[0] = (sf_u64)(tid * PT + e);
                 sm.found[1] = target - run;
             }
+            run += own[e];
         }
         __syncthreads();
-        found |= (uint32_t)sm.found[0] << shift;
+        found += (uint32_t)sm.found[0];
         target = sm.found[1];
-        __syncthreads();
+        if (shift == 0) return most - found;
+        found <<= min(shift, kBits);
     }
-    return found;
 }
 
-__global__ void __launch_bounds__(kSfThreads) sample_filtered_kernel(const SampleFilteredArgs a) {
+// The first CTA's end of a row whose kept tokens are all listed (n of them, at most kSfRank): ranks
+// them, cuts, and draws.  k: top-k or 0; part: of the listed tokens' mass after top-k that is kept, or
+// target: the mass itself; floor: least key kept.
+__device__ __forceinline__ void sf_finish(SfSmem &sm, const SfRow &row, const SampleFilteredArgs &a, int b, int n, int k,
+                                          float part, sf_u64 target, uint32_t floor) {
+    constexpr int PT = kSfRank / kSfThreads;
+    const int tid = threadIdx.x;
+    sf_u64 *sorted = sm.list + kSfRank, *mass = sorted + kSfRank;   // highest first
+    if (tid == 0 && (n & 1)) sm.list[n] = 0ull;
+    __syncthreads();
+    for (int i = tid; i < n; i += kSfThreads) {
+        const sf_u64 mine = sm.list[i];
+        int above = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; j += 2) {
+            const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(&sm.list[j]);
+            above += (v.x > mine) + (v.y > mine);
+        }
+        sorted[above] = mine;
+        mass[above] = row.mass(sf_unkey((uint32_t)(mine >> 32)));
+    }
+    __syncthreads();
+    const int upto = k > 0 ? min(n, k) : n;
+    sf_u64 own[PT], sum = 0ull, total;
+#pragma unroll
+    for (int e = 0; e < PT; ++e) {
+        const int i = tid * PT + e;
+        sum += own[e] = i < upto ? mass[i] : 0ull;
+    }
+    sf_u64 run = sf_block_scan(sm, sum, total);
+    if (part < 1.f) {
+        if (tid == 0) {
+            const double want = ceil((double)part * (double)total);
+            sm.found[0] = want < 1.0 ? 1ull : min((sf_u64)want, total);
+        }
+        __syncthreads();
+        target = sm.found[0];
+    }
+    // of the tokens up to top-k: those before which the target is not reached, down to the floor
+    uint32_t kept = 0;
+#pragma unroll
+    for (int e = 0; e < PT; ++e) {
+        const int i = tid * PT + e;
+        if (i < upto && run < target && (uint32_t)(sorted[i] >> 32) >= floor) ++kept;
+        run += own[e];
+    }
+    sf_u64 m;
+    sf_block_scan(sm, kept, m);
+    m = m ? m : 1ull;
+    sum = 0ull;
+#pragma unroll
+    for (int e = 0; e < PT; ++e) sum += tid * PT + e < (int)m ? own[e] : 0ull;
+    sf_block_scan(sm, sum, total);
+    // the kept tokens' places in vocabulary order: the mass before each
+    sf_u64 from[PT], at[PT];
+#pragma unroll
+    for (int e = 0; e < PT; ++e) {
+        const int i = tid + e * kSfThreads;
+        from[e] = 0ull;
+        at[e] = 0ull;
+        if (i < (int)m) {
+            const uint32_t mine = (uint32_t)sorted[i];   // ~index
+            for (int j = 0; j < (int)m; ++j) from[e] += (uint32_t)sorted[j] > mine ? mass[j] : 0ull;
+            at[e] = from[e] + mass[i];
+        }
+    }
+    sf_u64 *pos = sm.digit;
+    for (int j0 = 0; j0 < a.J; j0 += kSfDigits) {
+        __syncthreads();
+        const int nj = min(a.J - j0, kSfDigits);
+        for (int j = tid; j < nj; j += kSfThreads) {
+            const float u = a.u[(long long)b * a.J + j0 + j];
+            pos[j] = min(u > 0.f ? (sf_u64)((double)u * (double)total) : 0ull, total - 1ull);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < PT; ++e) {
+            if (at[e] == from[e]) continue;
+            for (int j = 0; j < nj; ++j)
+                if (from[e] <= pos[j] && pos[j] < at[e]) a.out[(long long)b * a.J + j0 + j] = (int)~(uint32_t)sorted[tid + e * kSfThreads];
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const SampleFilteredArgs a) {
     extern __shared__ __align__(16) unsigned char sf_raw[];
     SfSmem &sm = *reinterpret_cast<SfSmem *>(sf_raw);
     griddep_launch();
-    griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int b = blockIdx.y, CS = (int)gridDim.x;
     uint32_t rank;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    if (tid == 0) sm.nlist = 0u;
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // every CTA runs: waited for before the first store to another
+    griddep_wait();
     const float *z = a.logits + (long long)b * a.ld;
 
-    // this CTA's slice: whole float4s [at0, at0 + 4 nq) of the row's aligned body, and beside
-    // them the row's ragged head (first CTA) and tail (last): indexes [s0, s1)
+    // this CTA's slice: whole float4s [at0, at0 + 4 nq) of the row's aligned body in segments of sq, and
+    // beside them the row's ragged head (first CTA) and tail (last): indexes [s0, s1)
     const int head = min(a.V, (int)((0u - (uint32_t)(uintptr_t)z >> 2) & 3u));
     const int quads = (a.V - head) >> 2, per = (quads + CS - 1) / CS;
     const int q0 = min(quads, (int)rank * per), nq = min(quads, q0 + per) - q0, at0 = head + 4 * q0;
     const int s0 = rank == 0 ? 0 : at0, s1 = (int)rank == CS - 1 ? a.V : at0 + 4 * nq;
+    const int sq = max(32, (nq + 32 * kSfSegments - 1) / (32 * kSfSegments) * 32);
+    const float4 *there = reinterpret_cast<const float4 *>(z + at0);
     float4 *cache = reinterpret_cast<float4 *>(sf_raw + sizeof(SfSmem));
-    const float4 *body = a.cached ? cache : reinterpret_cast<const float4 *>(z + at0);
-    const int ends = (at0 - s0) + (s1 - at0 - 4 * nq);   // at most six
-    auto end_at = [&](int i) { return i < at0 - s0 ? s0 + i : at0 + 4 * nq + i - (at0 - s0); };
-    auto each = [&](auto see) {   // every logit of the slice, in no order
-        for (int i = tid; i < nq; i += 4 * kSfThreads) {
-            float4 v[4];
+    const float4 *body = a.cached ? cache : there;
+    // Every logit of the slice: warps take segments in turn (0: the head, then kSfSegments of the body,
+    // then the tail), lanes float4s of them; done(segment) after each, by the whole warp.
+    auto each = [&](auto see, auto done) {
+        for (int s = w; s < kSfSegments; s += kSfWarps) {
+            const int i1 = min(nq, (s + 1) * sq);
+            if (s * sq < i1) {
+                for (int i = s * sq + lane; i < i1; i += 4 * 32) {
+                    float4 v[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                v[k] = i + k * kSfThreads < nq ? body[i + k * kSfThreads] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                    for (int k = 0; k < 4; ++k)
+                        v[k] = i + 32 * k < i1 ? body[i + 32 * k] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int at = at0 + 4 * (i + k * kSfThreads);
-                see(v[k].x, at);
-                see(v[k].y, at + 1);
-                see(v[k].z, at + 2);
-                see(v[k].w, at + 3);
+                    for (int k = 0; k < 4; ++k) {
+                        const int at = at0 + 4 * (i + 32 * k);
+                        see(v[k].x, at);
+                        see(v[k].y, at + 1);
+                        see(v[k].z, at + 2);
+                        see(v[k].w, at + 3);
+                    }
+                }
+                __syncwarp();
             }
+            done(s + 1);
         }
-        if (tid < ends) see(z[end_at(tid)], end_at(tid));
+        if (w < 2) {
+            const int i0 = w ? at0 + 4 * nq : s0, i1 = w ? s1 : at0;
+            if (i0 + lane < i1) see(z[i0 + lane], i0 + lane);
+            __syncwarp();
+            done(w ? kSfSegments + 1 : 0);
+        }
     };
+    auto no_segment = [](int) {};
     // a value of every rank, in all of them after the next sf_sync()
     auto publish = [&](int slot, sf_u64 v) {
         if (tid < CS) sf_put(&sm.xch[slot][rank], (uint32_t)tid, v);
@@ -279,24 +411,65 @@ __global__ void __launch_bounds__(kSfThreads) sample_filtered_kernel(const Sampl
     };
 
     // ---- 1. maximum and minimum, as keys (0: nothing takes part)
-    if (tid == 0) sm.nlist = 0u;
-    sf_sync();   // every CTA runs, its counter is 0
     uint32_t kmax = 0u, kmin = ~0u;
-    if (a.cached)
-        for (int i = tid; i < nq; i += kSfThreads) cache[i] = reinterpret_cast<const float4 *>(z + at0)[i];   // a thread reads back its own below
     {
         float mx = -INFINITY, mn = INFINITY;
-        each([&](float v, int) {
+        auto see = [&](float v) {
             mx = fmaxf(mx, v);
             mn = fminf(mn, v > -INFINITY ? v : INFINITY);
-        });
+        };
+        for (int i = tid; i < nq; i += 6 * kSfThreads) {
+            float4 v[6];
+#pragma unroll
+            for (int k = 0; k < 6; ++k)
+                v[k] = i + k * kSfThreads < nq ? __ldg(there + i + k * kSfThreads) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+#pragma unroll
+            for (int k = 0; k < 6; ++k) {
+                if (a.cached && i + k * kSfThreads < nq) cache[i + k * kSfThreads] = v[k];
+                see(v[k].x);
+                see(v[k].y);
+                see(v[k].z);
+                see(v[k].w);
+            }
+        }
+        if (tid < at0 - s0) see(z[s0 + tid]);
+        else if (tid < at0 - s0 + s1 - at0 - 4 * nq) see(z[at0 + 4 * nq + tid - (at0 - s0)]);
         if (mx > -INFINITY) {
             kmax = sf_key(mx);
             kmin = sf_key(mn);
         }
     }
+    sm.own_max[tid] = kmax;
     block_range(kmax, kmin);
+
+    // ---- the row's settings
+    float t = a.temperature ? a.temperature[b] : 1.f;
+    int k = a.top_k ? max(a.top_k[b], 0) : 0;
+    const float p = a.top_p ? a.top_p[b] : 1.f, mp = a.min_p ? a.min_p[b] : 0.f;
+    const bool nucleus = p < 1.f && p > 0.f;   // NaN: off
+    if (!(t > 0.f)) {
+        t = 1.f;
+        k = 1;
+    }
+    if (p <= 0.f) k = 1;
+    // 2. the k-th of this slice's thread maxima: at least k tokens reach it
+    if (k > 1 && k <= kSfBound) {
+        const uint32_t mine = sm.own_max[tid];
+        int above = 0, upto = 0;
+#pragma unroll 8
+        for (int i = 0; i < kSfThreads; i += 4) {
+            const uint4 o = *reinterpret_cast<const uint4 *>(&sm.own_max[i]);
+            above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+            upto += (o.x >= mine) + (o.y >= mine) + (o.z >= mine) + (o.w >= mine);
+        }
+        if (tid == 0) sm.bin[0] = 0;
+        __syncthreads();
+        if (mine && above < k && k <= upto) sm.bin[0] = (int)mine;   // equal ones write the same
+        __syncthreads();
+    }
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     publish(kSfRange, (sf_u64)kmax << 32 | kmin);
+    if (k > 1 && k <= kSfBound) publish(kSfBoundKey, (uint32_t)sm.bin[0]);
     sf_sync();
     for (int r = 0; r < CS; ++r) {
         kmax = max(kmax, (uint32_t)(sm.xch[kSfRange][r] >> 32));
@@ -305,20 +478,8 @@ __global__ void __launch_bounds__(kSfThreads) sample_filtered_kernel(const Sampl
     if (kmax == 0u) {
         if (rank == 0)
             for (int j = tid; j < a.J; j += kSfThreads) a.out[(long long)b * a.J + j] = -1;
-        sf_sync();   // no rank leaves while another's stores to it are under way
         return;
     }
-
-    // ---- the row's settings
-    float t = a.temperature ? a.temperature[b] : 1.f;
-    int k = a.top_k ? a.top_k[b] : 0;
-    const float p = a.top_p ? a.top_p[b] : 1.f, mp = a.min_p ? a.min_p[b] : 0.f;
-    const bool nucleus = p < 1.f && p > 0.f;   // NaN: off
-    if (!(t > 0.f)) {
-        t = 1.f;
-        k = 1;
-    }
-    if (p <= 0.f) k = 1;
     SfRow row;
     row.top = sf_unkey(kmax);
     const bool floored = mp > 0.f && mp < 1.f && row.top < INFINITY;
@@ -330,20 +491,73 @@ __global__ void __launch_bounds__(kSfThreads) sample_filtered_kernel(const Sampl
     row.c = (float)sm.real[0];
     row.c_low = (float)(sm.real[0] - (double)row.c);
     SfCut cut = {0u, ~0u};
-    if (mp > 0.f) {   // the least logit with exp((z - top) / t) >= min_p
-        float least = row.top;
-        if (floored) least = fminf(__double2float_ru(sm.real[1]), row.top);
-        cut.tighten(sf_key(least), ~0u);
-    }
+    if (mp > 0.f)   // the least logit with exp((z - top) / t) >= min_p
+        cut.tighten(sf_key(floored ? fminf(__double2float_ru(sm.real[1]), row.top) : row.top), ~0u);
+    const uint32_t floor_key = cut.key;
     if (k == 1) cut.tighten(kmax, 1u);
 
-    // ---- 2., 3. the cuts of top-k and top-p
+    // Lists the tokens from key `least` on in every CTA; their number in all.
+    auto collect = [&](uint32_t least) {
+        const float from = sf_unkey(least);
+        each([&](float v, int at) {
+            if (v >= from) {
+                const uint32_t n = atomicAdd(&sm.nlist, 1u);
+                if (n < kSfList) sm.list[n] = (sf_u64)sf_key(v) << 32 | (uint32_t)~at;
+            }
+        }, no_segment);
+        __syncthreads();
+        publish(kSfCount, sm.nlist);
+        sf_sync();
+        uint32_t all = 0;
+        for (int r = 0; r < CS; ++r) all += (uint32_t)min(sm.xch[kSfCount][r], 1ull << 28);
+        return all;
+    };
+    // The first CTA: the other ranks' lists behind its own.
+    auto gather = [&]() {
+        uint32_t at = min(sm.nlist, (uint32_t)kSfList);
+        for (int r = 1; r < CS; ++r) {
+            const uint32_t n = min((uint32_t)sm.xch[kSfCount][r], kSfList - at);
+            for (uint32_t i = tid; i < n; i += kSfThreads) sm.list[at + i] = sf_get(&sm.list[i], (uint32_t)r);
+            at += n;
+        }
+        __syncthreads();
+        return (int)at;
+    };
+    // All that can be kept is listed, `n` in all: the first CTA ends the row.
+    auto finish = [&](float part, sf_u64 target) {
+        if (rank == 0) {
+            const int n = min(gather(), kSfRank);
+            sf_finish(sm, row, a, b, n, k, part, target, max(floor_key, 1u));
+        }
+        sf_sync();   // the lists have been read
+    };
+
+    // ---- 2. few tokens
+    {
+        uint32_t least = 0u;
+        if (a.V <= kSfRank) least = kmin;
+        else if (k == 1) least = kmax;
+        else if (k > 1 && k <= kSfBound)
+            for (int r = 0; r < CS; ++r) least = max(least, (uint32_t)sm.xch[kSfBoundKey][r]);
+        if (!nucleus) least = max(least, floor_key);   // else the mass of what lies below counts
+        if (least) {
+            const uint32_t n = collect(least);
+            if (n <= kSfRank) {
+                finish(nucleus ? p : 1.f, ~0ull);
+                return;
+            }
+            __syncthreads();
+            if (tid == 0) sm.nlist = 0u;
+            sf_sync();   // the counts have been read
+        }
+    }
+
+    // ---- 3., 4. the cuts of top-k and top-p
+    bool ready = false;   // the segments' masses are those of the cut
     if (k != 1 && (k > 1 || nucleus)) {
-        float far_low;
-        const float far = fminf(row.exponent(sf_unkey(kmin), far_low), kSfFar);
-        SfBins bins = {false, far > 0.f ? 0.9999f * kSfBins / far : 0.f, 0u, 0u, 0};
-        const bool all = a.V <= kSfList;       // the list holds the row: no histogram
-        if (all) bins.per_binade = 0.f;
+        const float far = fminf(row.exponent(sf_unkey(kmin)), kSfFar);
+        SfBins bins = {false, far > 0.f ? (kSfBins - 1) / far : 0.f, 0u, 0u, 0};
+        if (!(bins.per_binade < 1e30f)) bins.per_binade = 0.f;   // logits that differ by next to nothing
         // the cluster's counts of `bins`; by exponent with the whole mass, by keys with the bins'
         // masses, in the place of the list
         sf_u64 *mass_own = sm.list, *mass_all = sm.list + kSfBins;
@@ -354,33 +568,35 @@ __global__ void __launch_bounds__(kSfThreads) sample_filtered_kernel(const Sampl
             }
             __syncthreads();
             sf_u64 own = 0ull;
-            each([&](float v, int) {
-                if (!sf_takes_part(v)) return;
-                const int i = bins.of(row, v);
-                if (whole) own += row.mass(v);
-                if (i < 0 || i >= kSfBins) return;
-                atomicAdd(&sm.hist[i], 1u);
-                if (bins.keys) atomicAdd(&mass_own[i], row.mass(v));
-            });
-            if (whole) publish(kSfWhole, block_sum(own));
+            if (whole) {
+                each([&](float v, int) {
+                    float x;
+                    const sf_u64 m = row.mass(v, x);
+                    if (sf_takes_part(v) && x < kSfFar) {
+                        own += m;
+                        atomicAdd(&sm.hist[bins.near(x)], 1u);
+                    }
+                }, no_segment);
+                publish(kSfWhole, block_sum(own));
+            } else {
+                each([&](float v, int) {
+                    if (!sf_takes_part(v)) return;
+                    const int i = bins.of(row, v);
+                    if (i < 0 || i >= kSfBins) return;
+                    atomicAdd(&sm.hist[i], 1u);
+                    if (bins.keys) atomicAdd(&mass_own[i], row.mass(v));
+                }, no_segment);
+            }
             sf_sync();
             const int share = kSfBins / CS;    // this rank adds up its share of the bins for all
             for (int i = (int)rank * share + tid; i < ((int)rank + 1) * share; i += kSfThreads) {
                 uint32_t n = 0;
-                for (int r = 0; r < CS; ++r) {
-                    uint32_t x;
-                    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(sf_at(&sm.hist[i], (uint32_t)r)) : "memory");
-                    n += x;
-                }
+                for (int r = 0; r < CS; ++r) n += sf_get32(&sm.hist[i], (uint32_t)r);
                 for (int r = 0; r < CS; ++r)
                     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(sf_at(&sm.counts[i], (uint32_t)r)), "r"(n) : "memory");
                 if (!bins.keys) continue;
                 sf_u64 m = 0ull;
-                for (int r = 0; r < CS; ++r) {
-                    sf_u64 x;
-                    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(x) : "r"(sf_at(&mass_own[i], (uint32_t)r)) : "memory");
-                    m += x;
-                }
+                for (int r = 0; r < CS; ++r) m += sf_get(&mass_own[i], (uint32_t)r);
                 for (int r = 0; r < CS; ++r) sf_put(&mass_all[i], (uint32_t)r, m);
             }
             sf_sync();
@@ -388,6 +604,17 @@ __global__ void __launch_bounds__(kSfThreads) sample_filtered_kernel(const Sampl
                 *whole = 0ull;
                 for (int r = 0; r < CS; ++r) *whole += sm.xch[kSfWhole][r];
             }
+        };
+        auto sum_all = [&]() {
+            sf_u64 own = 0ull;
+            each([&](float v, int) {
+                if (sf_takes_part(v)) own += row.mass(v);
+            }, no_segment);
+            publish(kSfWhole, block_sum(own));
+            sf_sync();
+            own = 0ull;
+            for (int r = 0; r < CS; ++r) own += sm.xch[kSfWhole][r];
+            return own;
         };
         // The bins [lo, hi] in which the weights from the top, `base` above all bins, reach
         // `target`; tokens before lo and up to hi.  False: they do not.
@@ -449,12 +676,25 @@ __global__ void __launch_bounds__(kSfThreads) sample_filtered_kernel(const Sampl
             upto = (uint32_t)sm.bin[3];
             return lo < kSfBins;
         };
+        // The least key whose bin is at most i, by the warp, five bits a step (0: all are below it).
+        auto least_key = [&](int i) {
+            uint32_t key = kmin;   // its bin is more than i, if any of the row's is
+            if (bins.of(row, sf_unkey(kmin)) <= i) return kmin;
+            uint32_t span = kmax - kmin;   // kmax's bin is 0 or, by keys, above: at most i
+            while (span > 1) {             // bin(key) > i >= bin(key + span)
+                const uint32_t step = span / 32 + (span % 32 ? 1 : 0);
+                const uint32_t mine = (uint32_t)min((sf_u64)span, (sf_u64)step * (uint32_t)(lane + 1));
+                const unsigned in = __ballot_sync(0xffffffffu, bins.of(row, sf_unkey(key + mine)) <= i);
+                const uint32_t first = step * (uint32_t)(__ffs(in) - 1);   // the last lane's is in
+                span = min(span - first, step);
+                key += first;
+            }
+            return key + 1;
+        };
         bool divided = false;
-        int listed = 0;          // tokens in the first CTA's list: all from the top on
-        uint32_t list_from = 0;  // number of tokens above the list
-        sf_u64 above = 0ull;     // their mass
+        bool low_set = false;
         // The cut where the weights reach `target`; by_mass: a mass, else a count.  `held`: the
-        // mass that the cut keeps, where want_held.
+        // mass that the cut keeps, where want_held.  2: the row has been ended.
         auto find = [&](bool by_mass, sf_u64 target, bool want_held, SfCut &result, sf_u64 &held) {
             const SfBins coarse = bins;
             int lo = 0, hi = kSfBins - 1;
@@ -463,121 +703,135 @@ __global__ void __launch_bounds__(kSfThreads) sample_filtered_kernel(const Sampl
                 count(nullptr);
                 divided = false;
             }
-            if (!all && !bracket(by_mass, 0ull, target, lo, hi, before, upto)) return false;
-            if (!by_mass && upto <= kSfList) {   // all of the top k
-                lo = 0;
-                before = 0;
+            if (!bracket(by_mass, 0ull, target, lo, hi, before, upto)) return 0;
+            if (upto <= kSfRank) {   // few after all
+                if (w == 0) {
+                    const uint32_t key = least_key(hi);
+                    if (lane == 0) sm.found[2] = key;
+                }
+                __syncthreads();
+                collect((uint32_t)sm.found[2]);
+                finish(by_mass ? 1.f : nucleus ? p : 1.f, by_mass ? target : ~0ull);
+                return 2;
             }
             // by keys a band is one bin, 2^-10 of the last band's keys at most: three divisions reach a single one
             for (int division = 0; division < 8; ++division) {
                 const bool fits = upto - before <= kSfList;
-                sf_u64 own = 0ull;
+                if (w < 2) {   // logits above the band, and from its end on
+                    uint32_t key = ~0u;        // none
+                    if (w) key = least_key(hi);
+                    else if (lo > 0) key = least_key(lo - 1);
+                    else if (bins.keys && bins.high < kmax) key = bins.high + 1u;
+                    if (lane == 0) sm.found[2 + w] = key;
+                }
+                __syncthreads();
+                const float over = (uint32_t)sm.found[2] == ~0u ? __uint_as_float(0x7fc00000u) : sf_unkey((uint32_t)sm.found[2]);
+                const float from = sf_unkey((uint32_t)sm.found[3]);
+                sf_u64 own = 0ull, seg = 0ull;
                 uint32_t most = 0u, least = ~0u;
+                const bool weigh = by_mass || want_held;
                 each([&](float v, int at) {
-                    if (!sf_takes_part(v)) return;
-                    const int i = bins.of(row, v);
-                    if (i < lo) {
-                        if (by_mass || want_held) own += row.mass(v);
-                    } else if (i <= hi) {
+                    if (v >= over) {
+                        if (weigh) seg += row.mass(v);
+                    } else if (v >= from) {
                         const uint32_t key = sf_key(v);
                         most = max(most, key);
                         least = min(least, key);
                         if (fits) {
-                            uint32_t n;
-                            asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(n) : "r"(sf_at(&sm.nlist, 0u)), "r"(1u) : "memory");
-                            if (n < kSfList) sf_put(&sm.list[n], 0u, (sf_u64)key << 32 | (uint32_t)~at);
+                            const uint32_t n = atomicAdd(&sm.nlist, 1u);
+                            if (n < kSfList) sm.list[n] = (sf_u64)key << 32 | (uint32_t)~at;
                         }
                     }
+                }, [&](int s) {
+                    seg = sf_warp_sum(seg);
+                    if (lane == 0) sm.seg_mass[s] = seg;
+                    own += lane == 0 ? seg : 0ull;
+                    seg = 0ull;
                 });
                 block_range(most, least);
                 publish(kSfBand, (sf_u64)most << 32 | least);
                 publish(kSfAbove, block_sum(own));
+                publish(kSfCount, sm.nlist);
                 sf_sync();
-                above = 0ull;
+                sf_u64 above = 0ull;
                 for (int r = 0; r < CS; ++r) {
                     above += sm.xch[kSfAbove][r];
                     most = max(most, (uint32_t)(sm.xch[kSfBand][r] >> 32));
                     least = min(least, (uint32_t)sm.xch[kSfBand][r]);
                 }
+                if (most < least) return 0;    // the band is empty
                 sf_u64 left = target - (by_mass ? above : (sf_u64)before);
-                if (fits || most == least) {
-                    if (fits) {
-                        if (rank == 0) {
-                            listed = (int)min(sm.nlist, (uint32_t)kSfList);
-                            __syncthreads();
-                            if (tid == 0) sm.nlist = 0u;
-                            const bool short_of = !by_mass && (sf_u64)listed < left;   // fewer take part: no cut
-                            if (short_of) left = (sf_u64)listed;
-                            const uint32_t key = sf_select(sm, row, listed, by_mass, left);
-                            publish(kSfFound, (sf_u64)key << 32 | (short_of ? 1u : 0u));
-                            publish(kSfLeft, left);
-                        }
-                        sf_sync();
-                        result.key = (uint32_t)(sm.xch[kSfFound][0] >> 32);
-                        left = sm.xch[kSfLeft][0];
-                        if ((uint32_t)sm.xch[kSfFound][0]) return false;
-                        list_from = before;
-                    } else {
-                        result.key = most;
-                        sf_sync();
-                        list_from = ~0u;
-                    }
-                    const sf_u64 each_mass = row.mass(sf_unkey(result.key));
-                    if (by_mass) left = each_mass ? (left + each_mass - 1ull) / each_mass : 1ull;
-                    result.ties = (uint32_t)min(left, (sf_u64)0xffffffffull);
-                    if (want_held) {
-                        held = above + left * each_mass;
-                        if (fits) {
-                            if (rank == 0) {
-                                sf_u64 m = 0ull;
-                                for (int i = tid; i < listed; i += kSfThreads) {
-                                    const uint32_t key = (uint32_t)(sm.list[i] >> 32);
-                                    if (key > result.key) m += row.mass(sf_unkey(key));
-                                }
-                                publish(kSfHeld, block_sum(m));
-                            }
-                            sf_sync();
-                            held += sm.xch[kSfHeld][0];
-                        }
-                    }
-                    bins = coarse;
-                    return true;
+                if (!fits && most != least) {  // divide the band by keys
+                    int shift = 0;
+                    while ((most - least) >> shift >= kSfBins) ++shift;
+                    bins = SfBins{true, 0.f, most, least, shift};
+                    divided = true;
+                    const uint32_t top = before;
+                    sf_sync();                 // what was published has been read
+                    count(nullptr);
+                    if (!bracket(by_mass, by_mass ? above : (sf_u64)before, target, lo, hi, before, upto)) return 0;
+                    before += top;
+                    upto += top;
+                    continue;
                 }
-                // divide the band by keys
-                int shift = 0;
-                while ((most - least) >> shift >= kSfBins) ++shift;
-                bins = SfBins{true, 0.f, most, least, shift};
-                divided = true;
-                const uint32_t top = before;
-                sf_sync();   // what was published has been read
-                count(nullptr);
-                if (!bracket(by_mass, by_mass ? above : (sf_u64)before, target, lo, hi, before, upto)) return false;
-                before += top;
-                upto += top;
+                uint32_t own_listed = sm.nlist;
+                if (fits) {
+                    if (rank == 0) {
+                        const int n = gather();
+                        const uint32_t key = sf_select(sm, row, n, most, least, by_mass, left);
+                        publish(kSfFound, key);
+                        publish(kSfLeft, left);
+                        sf_u64 m = 0ull;
+                        if (want_held)
+                            for (int i = tid; i < n; i += kSfThreads) {
+                                const uint32_t one = (uint32_t)(sm.list[i] >> 32);
+                                if (one > key) m += row.mass(sf_unkey(one));
+                            }
+                        publish(kSfHeld, block_sum(m));
+                    }
+                    sf_sync();
+                    result.key = (uint32_t)sm.xch[kSfFound][0];
+                    left = sm.xch[kSfLeft][0];
+                } else {
+                    result.key = most;
+                }
+                const sf_u64 each_mass = row.mass(sf_unkey(result.key));
+                if (by_mass) left = each_mass ? (left + each_mass - 1ull) / each_mass : 1ull;
+                result.ties = (uint32_t)min(left, 0xffffffffull);
+                if (want_held) held = above + (fits ? sm.xch[kSfHeld][0] : 0ull) + left * each_mass;
+                // the segments' masses: what of the band is kept, from this rank's own list (the first
+                // CTA's has the others' behind it)
+                low_set = fits && weigh;
+                if (low_set) {
+                    if (tid < kSfSegments + 2) sm.seg_ties[tid] = 0u;
+                    __syncthreads();
+                    own_listed = min(own_listed, (uint32_t)kSfList);
+                    for (uint32_t i = tid; i < own_listed; i += kSfThreads) {
+                        const uint32_t key = (uint32_t)(sm.list[i] >> 32);
+                        const int at = (int)~(uint32_t)sm.list[i];
+                        const int s = at < at0 ? 0 : at >= at0 + 4 * nq ? kSfSegments + 1 : 1 + (at - at0) / 4 / sq;
+                        if (key > result.key) atomicAdd(&sm.seg_mass[s], row.mass(sf_unkey(key)));
+                        else if (key == result.key) atomicAdd(&sm.seg_ties[s], 1u);
+                    }
+                }
+                __syncthreads();
+                if (tid == 0) sm.nlist = 0u;
+                bins = coarse;
+                sf_sync();   // what was published has been read, and the lists
+                return 1;
             }
-            return false;
+            return 0;
         };
 
-        auto sum_all = [&]() {
-            sf_u64 own = 0ull;
-            each([&](float v, int) {
-                if (sf_takes_part(v)) own += row.mass(v);
-            });
-            publish(kSfWhole, block_sum(own));
-            sf_sync();
-            own = 0ull;
-            for (int r = 0; r < CS; ++r) own += sm.xch[kSfWhole][r];
-            return own;
-        };
         sf_u64 whole = 0ull;
-        if (!all) count(nucleus && k <= 1 ? &whole : nullptr);
-        else if (nucleus && k <= 1) whole = sum_all();
-        bool have_list = false;
+        count(nucleus && k <= 1 ? &whole : nullptr);
         if (k > 1) {
-            SfCut by_k;
-            if (find(false, (sf_u64)k, nucleus, by_k, whole)) {
+            SfCut by_k = {0u, ~0u};
+            const int r = find(false, (sf_u64)k, nucleus, by_k, whole);
+            if (r == 2) return;
+            if (r == 1) {
                 cut.tighten(by_k.key, by_k.ties);
-                have_list = list_from == 0u;
+                ready = low_set && cut.key == by_k.key && cut.ties == by_k.ties;
             } else if (nucleus) {   // all take part
                 whole = sum_all();
             }
@@ -591,67 +845,50 @@ __global__ void __launch_bounds__(kSfThreads) sample_filtered_kernel(const Sampl
             __syncthreads();
             const sf_u64 target = sm.found[2];
             SfCut by_p = {0u, ~0u};
-            if (have_list) {   // the top k are listed
-                if (rank == 0) {
-                    sf_u64 left = target;
-                    const uint32_t key = sf_select(sm, row, listed, true, left);
-                    const sf_u64 m = row.mass(sf_unkey(key));
-                    publish(kSfFound, (sf_u64)key << 32 | (uint32_t)(m ? (left + m - 1ull) / m : 1ull));
-                }
-                sf_sync();
-                by_p.key = (uint32_t)(sm.xch[kSfFound][0] >> 32);
-                by_p.ties = (uint32_t)sm.xch[kSfFound][0];
+            sf_u64 held;
+            const int r = find(true, target, false, by_p, held);
+            if (r == 2) return;
+            if (r == 1) {
                 cut.tighten(by_p.key, by_p.ties);
-            } else {
-                sf_u64 held;
-                sf_sync();   // after a search for the top k: what it published has been read
-                if (find(true, target, false, by_p, held)) cut.tighten(by_p.key, by_p.ties);
+                ready = low_set && cut.key == by_p.key && cut.ties == by_p.ties;
             }
         }
     }
 
-    // ---- 4. kept mass by segments of the slice
-    const int len = s1 - s0, sl = ((len + kSfSegments - 1) / kSfSegments + 31) / 32 * 32;
-    const float *flat = reinterpret_cast<const float *>(body);
-    auto logit = [&](int i) { return i >= at0 && i < at0 + 4 * nq ? flat[i - at0] : z[i]; };
-    for (int s = w; s < kSfSegments; s += kSfWarps) {
-        const int i1 = min(s1, s0 + (s + 1) * sl);
-        sf_u64 m = 0ull;
+    // ---- 5. kept mass by segments of the slice
+    const float cut_at = cut.key ? sf_unkey(cut.key) : -INFINITY;
+    if (!ready) {
+        sf_u64 seg = 0ull;
         uint32_t ties = 0;
-        for (int i = s0 + s * sl + lane; i < i1; i += 4 * 32) {
-            float v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = i + 32 * e < i1 ? logit(i + 32 * e) : -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (!sf_takes_part(v[e])) continue;
-                const uint32_t key = sf_key(v[e]);
-                if (key > cut.key) m += row.mass(v[e]);
-                else if (key == cut.key) ++ties;
+        each([&](float v, int) {
+            if (v > cut_at) seg += row.mass(v);
+            ties += v == cut_at ? 1u : 0u;
+        }, [&](int s) {
+            seg = sf_warp_sum(seg);
+            ties = __reduce_add_sync(0xffffffffu, ties);
+            if (lane == 0) {
+                sm.seg_mass[s] = seg;
+                sm.seg_ties[s] = ties;
             }
-        }
-        m = sf_warp_sum(m);
-        ties = __reduce_add_sync(0xffffffffu, ties);
-        if (lane == 0) {
-            sm.seg_mass[s] = m;
-            sm.seg_ties[s] = ties;
-        }
+            seg = 0ull;
+            ties = 0;
+        });
     }
     __syncthreads();
-    static_assert(kSfSegments == 64, "two segments a lane");
-    const sf_u64 tie_mass = row.mass(sf_unkey(cut.key));
-    sf_u64 own_mass = 0ull, own_ties = 0ull;
-    if (w == 0) {
-        own_mass = sf_warp_sum(sm.seg_mass[lane] + sm.seg_mass[lane + 32]);
-        own_ties = sf_warp_sum((sf_u64)sm.seg_ties[lane] + sm.seg_ties[lane + 32]);
-        if (lane == 0) {
-            sm.found[2] = own_mass;
-            sm.found[3] = own_ties;
-        }
+    const sf_u64 tie_mass = cut.key ? row.mass(cut_at) : 0ull;
+    // every warp: the head's, the segments' and the tail's, three a lane
+    static_assert(kSfSegments + 2 <= 3 * 32, "three places a lane");
+    sf_u64 sm3[3], st3[3], mass_sum = 0ull, tie_sum = 0ull;
+#pragma unroll
+    for (int e = 0; e < 3; ++e) {
+        const int s = 3 * lane + e;
+        sm3[e] = s < kSfSegments + 2 ? sm.seg_mass[s] : 0ull;
+        st3[e] = s < kSfSegments + 2 && cut.key ? sm.seg_ties[s] : 0ull;
+        mass_sum += sm3[e];
+        tie_sum += st3[e];
     }
-    __syncthreads();
-    publish(kSfMass, sm.found[2]);
-    publish(kSfTies, sm.found[3]);
+    publish(kSfMass, sf_warp_sum(mass_sum));
+    publish(kSfTies, sf_warp_sum(tie_sum));
     sf_sync();
     sf_u64 start = 0ull, kept = 0ull, ties_before = 0ull, seen = 0ull;
     for (int r = 0; r < CS; ++r) {
@@ -663,43 +900,58 @@ __global__ void __launch_bounds__(kSfThreads) sample_filtered_kernel(const Sampl
         kept += sm.xch[kSfMass][r] + min(n, left) * tie_mass;
         seen += n;
     }
+    auto logit = [&](int i) { return i >= at0 && i < at0 + 4 * nq ? reinterpret_cast<const float *>(body)[i - at0] : z[i]; };
     // a warp a draw
     for (int j = w; j < a.J; j += kSfWarps) {
-        const long long at = (long long)b * a.J + j;
-        const float u = a.u[at];
+        const long long out = (long long)b * a.J + j;
+        const float u = a.u[out];
         sf_u64 pos = u > 0.f ? (sf_u64)((double)u * (double)kept) : 0ull;
         if (pos >= kept) pos = kept - 1ull;
-        // segments 2 lane and 2 lane + 1: ties, then masses before them
-        const sf_u64 t0 = sm.seg_ties[2 * lane], t1 = sm.seg_ties[2 * lane + 1];
-        const sf_u64 tb = ties_before + sf_warp_scan(t0 + t1) - t0 - t1;
-        auto of = [&](sf_u64 n, sf_u64 before) { return before < cut.ties ? min(n, (sf_u64)cut.ties - before) : 0ull; };
-        const sf_u64 m0 = sm.seg_mass[2 * lane] + of(t0, tb) * tie_mass, m1 = sm.seg_mass[2 * lane + 1] + of(t1, tb + t0) * tie_mass;
-        const sf_u64 upto = start + sf_warp_scan(m0 + m1), from = upto - m0 - m1;
-        const unsigned mine = __ballot_sync(0xffffffffu, from <= pos && pos < upto);
-        if (!mine) continue;   // another rank's
-        const int src = __ffs(mine) - 1;
-        const int second = __shfl_sync(0xffffffffu, (int)(pos >= from + m0), src);
-        sf_u64 run = __shfl_sync(0xffffffffu, second ? from + m0 : from, src);
-        sf_u64 tied = __shfl_sync(0xffffffffu, second ? tb + t0 : tb, src);
-        const int s = 2 * src + second, i1 = min(s1, s0 + (s + 1) * sl);
-        for (int i0 = s0 + s * sl; i0 < i1; i0 += 32) {
-            const float v = i0 + lane < i1 ? logit(i0 + lane) : -INFINITY;
-            const uint32_t key = sf_takes_part(v) ? sf_key(v) : 0u;
-            const unsigned ties = __ballot_sync(0xffffffffu, key != 0u && key == cut.key);
+        // the place whose mass the draw falls into, with the ties and the mass before it
+        sf_u64 tb = ties_before + sf_warp_scan(tie_sum) - tie_sum, own = 0ull, m3[3], t3[3];
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+            t3[e] = tb;
+            m3[e] = sm3[e] + (tb < cut.ties ? min(st3[e], (sf_u64)cut.ties - tb) : 0ull) * tie_mass;
+            own += m3[e];
+            tb += st3[e];
+        }
+        sf_u64 run = start + sf_warp_scan(own) - own;
+        int mine = -1;
+        sf_u64 at_mass = 0ull, at_ties = 0ull;
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+            if (run <= pos && pos < run + m3[e]) {
+                mine = 3 * lane + e;
+                at_mass = run;
+                at_ties = t3[e];
+            }
+            run += m3[e];
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, mine >= 0);
+        if (!hit) continue;   // another rank's
+        const int src = __ffs(hit) - 1, s = __shfl_sync(0xffffffffu, mine, src);
+        run = __shfl_sync(0xffffffffu, at_mass, src);
+        sf_u64 tied = __shfl_sync(0xffffffffu, at_ties, src);
+        const int i0 = s == 0 ? s0 : at0 + 4 * min(nq, (s - 1) * sq);
+        const int i1 = s == 0 ? at0 : s == kSfSegments + 1 ? s1 : at0 + 4 * min(nq, s * sq);
+        for (int i = s == kSfSegments + 1 ? at0 + 4 * nq : i0; i < i1; i += 32) {
+            const float v = i + lane < i1 ? logit(i + lane) : -INFINITY;
+            const bool tie = cut.key && v == cut_at;
+            const unsigned ties = __ballot_sync(0xffffffffu, tie);
             sf_u64 m = 0ull;
-            if (key > cut.key) m = row.mass(v);
-            else if (key != 0u && key == cut.key && tied + __popc(ties & ((1u << lane) - 1u)) < cut.ties) m = tie_mass;
+            if (v > cut_at) m = row.mass(v);
+            else if (tie && tied + __popc(ties & ((1u << lane) - 1u)) < cut.ties) m = tie_mass;
             const sf_u64 sum = run + sf_warp_scan(m);
             const unsigned past = __ballot_sync(0xffffffffu, m != 0ull && sum > pos);
             if (past) {
-                if (lane == __ffs(past) - 1) a.out[at] = i0 + lane;
+                if (lane == __ffs(past) - 1) a.out[out] = i + lane;
                 break;
             }
             run = __shfl_sync(0xffffffffu, sum, 31);
             tied += __popc(ties);
         }
     }
-    sf_sync();   // no rank leaves while another's stores to it are under way
 }
 
 cudaError_t launch_sample_filtered(SampleFilteredArgs a, cudaStream_t s) {
