@@ -18,8 +18,8 @@
 // L2.  One cluster of up to 8 CTAs a row, each a slice of the vocabulary:
 //  1. the maximum and minimum, and every thread's own maximum;
 //  2. where few tokens can be kept, these come to the first CTA, which ranks them and does the
-//     rest: of the top 256, those that reach the k-th of a slice's 512 thread maxima; the maximum's
-//     ties; what reaches min-p;
+//     rest: of the top 192, those that reach a bound from the maxima of groups of threads; the
+//     maximum's ties;
 //  3. else (top-p, or a larger k) a histogram of counts over the exponent, in 2048 bins, and
 //     the whole mass.  A bin's tokens have masses within its edges', so the counts alone
 //     bound where the cut's mass is reached to a band of bins.  (A histogram of masses needs
@@ -45,8 +45,9 @@ constexpr int kSfThreads = 512;
 constexpr int kSfWarps = kSfThreads / 32;
 constexpr int kSfBins = 2048;
 constexpr int kSfList = 4096;                  // tokens that a CTA lists
-constexpr int kSfRank = 1024;                  // that the first CTA ranks
-constexpr int kSfBound = 256;                  // a top-k up to which thread maxima give a bound
+constexpr int kSfRank = kSfThreads;            // that the first CTA ranks, one a thread
+constexpr int kSfBound = 192;                  // a top-k up to which maxima of groups of threads give a bound
+constexpr int kSfMarks = 8;                    // of a rank's maxima: every ceil(k / 8)-th
 constexpr int kSfDigits = 1024;
 constexpr int kSfSegments = 64;                // of a slice; before them its ragged head, after them its tail
 constexpr float kSfUnit = 1099511627776.f;     // 2^40
@@ -57,7 +58,7 @@ constexpr float kSfSlack = 1.f / 65536.f;
 
 // Slots of the values that the ranks tell one another.  A slot is written again only after a
 // barrier that follows its reading.
-enum { kSfRange, kSfBoundKey, kSfCount, kSfAbove, kSfFound, kSfLeft, kSfWhole, kSfBand, kSfHeld, kSfMass, kSfTies, kSfSlots };
+enum { kSfRange, kSfCount, kSfBandMass, kSfAbove, kSfFound, kSfLeft, kSfWhole, kSfBand, kSfHeld, kSfMass, kSfTies, kSfSlots };
 
 struct alignas(16) SfSmem {                    // the cached slice follows, in float4s
     sf_u64 list[kSfList];                      // key << 32 | ~index; first CTA: of all ranks
@@ -68,7 +69,8 @@ struct alignas(16) SfSmem {                    // the cached slice follows, in f
     uint32_t counts[kSfBins];                  // the cluster's
     sf_u64 seg_mass[kSfSegments + 2];
     uint32_t seg_ties[kSfSegments + 2];
-    alignas(16) uint32_t own_max[kSfThreads];
+    alignas(16) uint32_t own_max[kSfThreads / 2];
+    uint32_t marks[kSfMaxCluster * kSfMarks];
     sf_u64 scan[2][kSfWarps];
     uint32_t scan_n[kSfWarps];
     sf_u64 part[kSfWarps][3];
@@ -115,22 +117,30 @@ struct SfRow {
     float c, c_low;    // log2(e) / t, in two floats
     // For logits that take part: (top - z) c; an infinite maximum's own is 0, others' are past kSfFar.
     __device__ __forceinline__ float exponent(float z) const { return fmaxf(top - z, 0.f) * c; }
-    __device__ __forceinline__ sf_u64 mass(float z, float &x) const {
+    // The mass as n * f, f 512 or 1: from 2^-9 on in steps of 2^-31, which a float has there, below in
+    // steps of 2^-40.  Adding n * f is one instruction.
+    __device__ __forceinline__ uint32_t mass(float z, float &x, uint32_t &f) const {
         const float d = fmaxf(top - z, 0.f);
         x = d * c;
-        // what the product, c and the difference (where |top| >= |z|) lost
-        const float low = fmaf(d, c_low, fmaf((top - d) - z, c, fmaf(d, c, -x)));
+        const float low = fmaf(d, c_low, fmaf(d, c, -x));   // what the product and c lost
         float y;
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(-x));
-        if (d > 0.f) y = fmaf(y * -0.6931471805599453f, low, y);
-        // to 2^-40: from 2^-9 on in steps of 2^-31, which a float has there
+        y = fmaf(y * -0.6931471805599453f, low, y);
         const bool near = y >= 0x1p-9f;
-        const uint32_t m = __float2uint_rz(y * (near ? 0x1p31f : kSfUnit));
-        return x < kSfFar ? (near ? (sf_u64)m << 9 : (sf_u64)m) : 0ull;
+        f = near ? 512u : 1u;
+        return __float2uint_rz(y * (near ? 0x1p31f : kSfUnit));   // 0 from kSfFar on
     }
     __device__ __forceinline__ sf_u64 mass(float z) const {
         float x;
-        return mass(z, x);
+        uint32_t f;
+        const uint32_t n = mass(z, x, f);
+        return (sf_u64)n * f;
+    }
+    __device__ __forceinline__ void add(sf_u64 &sum, float z) const {
+        float x;
+        uint32_t f;
+        const uint32_t n = mass(z, x, f);
+        sum += (sf_u64)n * f;
     }
 };
 
@@ -157,6 +167,9 @@ struct SfBins {
     __device__ __forceinline__ sf_u64 most(int i) const {
         const sf_u64 m = (sf_u64)((per_binade > 0.f ? exp2f(-fmaxf((float)i - 0.5f, 0.f) / per_binade) : 1.f) * kSfUnit);
         return m + (sf_u64)((float)m * kSfSlack) + 2ull;
+    }
+    __device__ __forceinline__ sf_u64 middle(int i) const {
+        return (sf_u64)((per_binade > 0.f ? exp2f(-(float)i / per_binade) : 1.f) * kSfUnit);
     }
     __device__ __forceinline__ sf_u64 least(int i) const {
         const sf_u64 m = (sf_u64)((per_binade > 0.f ? exp2f(-((float)i + 0.5f) / per_binade) : 1.f) * kSfUnit);
@@ -439,7 +452,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
             kmin = sf_key(mn);
         }
     }
-    sm.own_max[tid] = kmax;
+    const uint32_t thread_max = kmax;
     block_range(kmax, kmin);
 
     // ---- the row's settings
@@ -452,24 +465,38 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
         k = 1;
     }
     if (p <= 0.f) k = 1;
-    // 2. the k-th of this slice's thread maxima: at least k tokens reach it
-    if (k > 1 && k <= kSfBound) {
-        const uint32_t mine = sm.own_max[tid];
-        int above = 0, upto = 0;
-#pragma unroll 8
-        for (int i = 0; i < kSfThreads; i += 4) {
-            const uint4 o = *reinterpret_cast<const uint4 *>(&sm.own_max[i]);
-            above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
-            upto += (o.x >= mine) + (o.y >= mine) + (o.z >= mine) + (o.w >= mine);
+    // 2. Of the maxima of groups of threads every step-th largest goes to all ranks, `step` of them
+    // reaching the first mark, 2 step the second, ...: the eighth largest of all ranks' marks is
+    // reached by 8 step >= k tokens.
+    const bool bounded = k > 1 && k <= kSfBound;
+    const int step = (k + kSfMarks - 1) / kSfMarks;
+    if (bounded) {
+        const int wide = k <= 64 ? 4 : 2, groups = kSfThreads / wide;
+        uint32_t g = max(thread_max, __shfl_xor_sync(0xffffffffu, thread_max, 1));
+        if (wide == 4) g = max(g, __shfl_xor_sync(0xffffffffu, g, 2));
+        if (tid % wide == 0) sm.own_max[tid / wide] = g;
+        if (tid < kSfMaxCluster * kSfMarks) sm.marks[tid] = 0u;
+        __syncthreads();
+        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        sf_sync();                               // every rank's marks are empty
+        if (tid < groups) {
+            const uint32_t mine = sm.own_max[tid];
+            int above = 0, upto = 0;
+#pragma unroll 4
+            for (int i = 0; i < groups; i += 4) {
+                const uint4 o = *reinterpret_cast<const uint4 *>(&sm.own_max[i]);
+                above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+                upto += (o.x >= mine) + (o.y >= mine) + (o.z >= mine) + (o.w >= mine);
+            }
+            // marks that fall on this value; equal ones write the same
+            for (int i = above / step; mine && i < kSfMarks && (i + 1) * step <= upto; ++i)
+                for (int r = 0; r < CS; ++r)
+                    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(sf_at(&sm.marks[rank * kSfMarks + i], (uint32_t)r)), "r"(mine) : "memory");
         }
-        if (tid == 0) sm.bin[0] = 0;
-        __syncthreads();
-        if (mine && above < k && k <= upto) sm.bin[0] = (int)mine;   // equal ones write the same
-        __syncthreads();
+    } else {
+        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     }
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     publish(kSfRange, (sf_u64)kmax << 32 | kmin);
-    if (k > 1 && k <= kSfBound) publish(kSfBoundKey, (uint32_t)sm.bin[0]);
     sf_sync();
     for (int r = 0; r < CS; ++r) {
         kmax = max(kmax, (uint32_t)(sm.xch[kSfRange][r] >> 32));
@@ -479,6 +506,23 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
         if (rank == 0)
             for (int j = tid; j < a.J; j += kSfThreads) a.out[(long long)b * a.J + j] = -1;
         return;
+    }
+    uint32_t bound = 0u;                         // 0: none
+    if (bounded) {
+        if (tid == 0) sm.found[0] = 0ull;
+        __syncthreads();
+        if (tid < kSfMaxCluster * kSfMarks) {
+            const uint32_t mine = sm.marks[tid];
+            int above = 0, upto = 0;
+#pragma unroll 8
+            for (int i = 0; i < kSfMaxCluster * kSfMarks; ++i) {
+                above += sm.marks[i] > mine;
+                upto += sm.marks[i] >= mine;
+            }
+            if (mine && above < kSfMarks && kSfMarks <= upto) sm.found[0] = mine;
+        }
+        __syncthreads();
+        bound = (uint32_t)sm.found[0];
     }
     SfRow row;
     row.top = sf_unkey(kmax);
@@ -534,12 +578,9 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
 
     // ---- 2. few tokens
     {
-        uint32_t least = 0u;
-        if (a.V <= kSfRank) least = kmin;
-        else if (k == 1) least = kmax;
-        else if (k > 1 && k <= kSfBound)
-            for (int r = 0; r < CS; ++r) least = max(least, (uint32_t)sm.xch[kSfBoundKey][r]);
-        if (!nucleus) least = max(least, floor_key);   // else the mass of what lies below counts
+        uint32_t least = k == 1 ? kmax : bound;
+        if (least == 0u && k != 1 && (k > 1 || nucleus) && a.V <= kSfRank) least = kmin;
+        if (least && !nucleus) least = max(least, floor_key);   // with top-p the mass of what lies below counts
         if (least) {
             const uint32_t n = collect(least);
             if (n <= kSfRank) {
@@ -571,9 +612,10 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
             if (whole) {
                 each([&](float v, int) {
                     float x;
-                    const sf_u64 m = row.mass(v, x);
+                    uint32_t f;
+                    const uint32_t n = row.mass(v, x, f);
                     if (sf_takes_part(v) && x < kSfFar) {
-                        own += m;
+                        own += (sf_u64)n * f;
                         atomicAdd(&sm.hist[bins.near(x)], 1u);
                     }
                 }, no_segment);
@@ -608,7 +650,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
         auto sum_all = [&]() {
             sf_u64 own = 0ull;
             each([&](float v, int) {
-                if (sf_takes_part(v)) own += row.mass(v);
+                if (sf_takes_part(v)) row.add(own, v);
             }, no_segment);
             publish(kSfWhole, block_sum(own));
             sf_sync();
@@ -618,7 +660,8 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
         };
         // The bins [lo, hi] in which the weights from the top, `base` above all bins, reach
         // `target`; tokens before lo and up to hi.  False: they do not.
-        auto bracket = [&](bool by_mass, sf_u64 base, sf_u64 target, int &lo, int &hi, uint32_t &before, uint32_t &upto) {
+        // Estimated: by the masses of the bins' middles, and a bin on either side.
+        auto bracket = [&](bool by_mass, bool estimated, sf_u64 base, sf_u64 target, int &lo, int &hi, uint32_t &before, uint32_t &upto) {
             constexpr int PT = kSfBins / kSfThreads;
             uint32_t c[PT], n = 0;
             sf_u64 u[PT], l[PT], su = 0ull, sl = 0ull;
@@ -629,6 +672,9 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
                 u[e] = l[e] = c[e];
                 if (by_mass && bins.keys) {
                     u[e] = l[e] = mass_all[i];
+                } else if (by_mass && estimated) {
+                    if (c[e]) u[e] *= bins.middle(i);
+                    l[e] = u[e];
                 } else if (by_mass && c[e]) {
                     u[e] *= bins.most(i);
                     l[e] *= bins.least(i);
@@ -674,6 +720,10 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
             hi = min(sm.bin[1], kSfBins - 1);
             before = (uint32_t)sm.bin[2];
             upto = (uint32_t)sm.bin[3];
+            if (estimated && by_mass && lo < kSfBins) {
+                if (lo > 0) before -= sm.counts[--lo];
+                if (hi < kSfBins - 1) upto += sm.counts[++hi];
+            }
             return lo < kSfBins;
         };
         // The least key whose bin is at most i, by the warp, five bits a step (0: all are below it).
@@ -703,8 +753,10 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
                 count(nullptr);
                 divided = false;
             }
-            if (!bracket(by_mass, 0ull, target, lo, hi, before, upto)) return 0;
-            if (upto <= kSfRank) {   // few after all
+            // the estimate's band has far fewer tokens; whether the cut lies there is seen from the exact masses
+            bool guess = by_mass && bracket(true, true, 0ull, target, lo, hi, before, upto) && upto > kSfRank;
+            if (!guess && !bracket(by_mass, false, 0ull, target, lo, hi, before, upto)) return 0;
+            if (!guess && upto <= kSfRank) {   // few after all
                 if (w == 0) {
                     const uint32_t key = least_key(hi);
                     if (lane == 0) sm.found[2] = key;
@@ -715,7 +767,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
                 return 2;
             }
             // by keys a band is one bin, 2^-10 of the last band's keys at most: three divisions reach a single one
-            for (int division = 0; division < 8; ++division) {
+            for (int round = 0; round < 8; ++round) {
                 const bool fits = upto - before <= kSfList;
                 if (w < 2) {   // logits above the band, and from its end on
                     uint32_t key = ~0u;        // none
@@ -727,16 +779,17 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
                 __syncthreads();
                 const float over = (uint32_t)sm.found[2] == ~0u ? __uint_as_float(0x7fc00000u) : sf_unkey((uint32_t)sm.found[2]);
                 const float from = sf_unkey((uint32_t)sm.found[3]);
-                sf_u64 own = 0ull, seg = 0ull;
+                sf_u64 own = 0ull, seg = 0ull, in_band = 0ull;
                 uint32_t most = 0u, least = ~0u;
                 const bool weigh = by_mass || want_held;
                 each([&](float v, int at) {
                     if (v >= over) {
-                        if (weigh) seg += row.mass(v);
+                        if (weigh) row.add(seg, v);
                     } else if (v >= from) {
                         const uint32_t key = sf_key(v);
                         most = max(most, key);
                         least = min(least, key);
+                        if (guess) row.add(in_band, v);
                         if (fits) {
                             const uint32_t n = atomicAdd(&sm.nlist, 1u);
                             if (n < kSfList) sm.list[n] = (sf_u64)key << 32 | (uint32_t)~at;
@@ -751,14 +804,26 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
                 block_range(most, least);
                 publish(kSfBand, (sf_u64)most << 32 | least);
                 publish(kSfAbove, block_sum(own));
+                if (guess) publish(kSfBandMass, block_sum(in_band));
                 publish(kSfCount, sm.nlist);
                 sf_sync();
                 sf_u64 above = 0ull;
+                in_band = 0ull;
                 for (int r = 0; r < CS; ++r) {
                     above += sm.xch[kSfAbove][r];
+                    if (guess) in_band += sm.xch[kSfBandMass][r];
                     most = max(most, (uint32_t)(sm.xch[kSfBand][r] >> 32));
                     least = min(least, (uint32_t)sm.xch[kSfBand][r]);
                 }
+                if (guess && !(above < target && target <= above + in_band)) {
+                    guess = false;
+                    __syncthreads();
+                    if (tid == 0) sm.nlist = 0u;
+                    sf_sync();                 // what was published has been read
+                    if (!bracket(true, false, 0ull, target, lo, hi, before, upto)) return 0;
+                    continue;
+                }
+                guess = false;
                 if (most < least) return 0;    // the band is empty
                 sf_u64 left = target - (by_mass ? above : (sf_u64)before);
                 if (!fits && most != least) {  // divide the band by keys
@@ -769,7 +834,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
                     const uint32_t top = before;
                     sf_sync();                 // what was published has been read
                     count(nullptr);
-                    if (!bracket(by_mass, by_mass ? above : (sf_u64)before, target, lo, hi, before, upto)) return 0;
+                    if (!bracket(by_mass, false, by_mass ? above : (sf_u64)before, target, lo, hi, before, upto)) return 0;
                     before += top;
                     upto += top;
                     continue;
@@ -861,7 +926,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
         sf_u64 seg = 0ull;
         uint32_t ties = 0;
         each([&](float v, int) {
-            if (v > cut_at) seg += row.mass(v);
+            if (v > cut_at) row.add(seg, v);
             ties += v == cut_at ? 1u : 0u;
         }, [&](int s) {
             seg = sf_warp_sum(seg);

@@ -1,9 +1,10 @@
 """Plain float64 form of sampling with temperature, top-k, top-p and min-p."""
 import numpy as np
 
-# How far a mass may be off, relative to the whole: an exponential within 2^-22 of its value, its exponent within
-# 2^-22 binades, the fixed point's last place of a token (2^-40 of the largest) for 2^18 tokens at most.
-NEAR = 2.0 ** -20
+# How far a mass may be off, relative to the whole: an exponential within 2^-22 of its value, its exponent by the
+# rounding of a difference (2^-24 of at most 18 binades, where the mass lies in 2^18 tokens), the fixed point's last place of
+# a token (2^-40 of the largest) for 2^18 tokens at most: 2^-22 + 0.7 * 18 * 2^-24 + 2^-22.
+NEAR = 2.0 ** -19
 
 
 def kept_of(z, t, k, p, mp):
