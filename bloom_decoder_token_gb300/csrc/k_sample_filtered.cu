@@ -49,6 +49,7 @@ constexpr int kSfRank = kSfThreads;            // that the first CTA ranks, one 
 constexpr int kSfBound = 192;                  // a top-k up to which maxima of groups of threads give a bound
 constexpr int kSfMarks = 8;                    // of a rank's maxima: every ceil(k / 8)-th
 constexpr int kSfDigits = 1024;
+constexpr int kSfBatch = 8;                    // logits of a lane at a time
 constexpr int kSfSegments = 64;                // of a slice; before them its ragged head, after them its tail
 constexpr float kSfUnit = 1099511627776.f;     // 2^40
 constexpr float kSfFar = 40.f;                 // binades below the maximum from which on a mass is 0
@@ -82,9 +83,11 @@ struct alignas(16) SfSmem {                    // the cached slice follows, in f
 };
 
 // ---- cluster
+__device__ __forceinline__ void sf_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void sf_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void sf_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    sf_arrive();
+    sf_wait();
 }
 __device__ __forceinline__ uint32_t sf_at(const void *p, uint32_t rank) {
     uint32_t r;
@@ -168,8 +171,8 @@ struct SfBins {
         const sf_u64 m = (sf_u64)((per_binade > 0.f ? exp2f(-fmaxf((float)i - 0.5f, 0.f) / per_binade) : 1.f) * kSfUnit);
         return m + (sf_u64)((float)m * kSfSlack) + 2ull;
     }
-    __device__ __forceinline__ sf_u64 middle(int i) const {
-        return (sf_u64)((per_binade > 0.f ? exp2f(-(float)i / per_binade) : 1.f) * kSfUnit);
+    __device__ __forceinline__ float middle(int i) const {
+        return (per_binade > 0.f ? exp2f(-(float)i / per_binade) : 1.f) * kSfUnit;
     }
     __device__ __forceinline__ sf_u64 least(int i) const {
         const sf_u64 m = (sf_u64)((per_binade > 0.f ? exp2f(-((float)i + 0.5f) / per_binade) : 1.f) * kSfUnit);
@@ -365,35 +368,52 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
     float4 *cache = reinterpret_cast<float4 *>(sf_raw + sizeof(SfSmem));
     const float4 *body = a.cached ? cache : there;
     // Every logit of the slice: warps take segments in turn (0: the head, then kSfSegments of the body,
-    // then the tail), lanes float4s of them; done(segment) after each, by the whole warp.
+    // then the tail), lanes kSfBatch logits at a time (value e at index at + (e & 3) + 128 (e >> 2); -inf beyond
+    // the end); done(segment) after each.  Both are called by whole warps.
     auto each = [&](auto see, auto done) {
         for (int s = w; s < kSfSegments; s += kSfWarps) {
             const int i1 = min(nq, (s + 1) * sq);
-            if (s * sq < i1) {
-                for (int i = s * sq + lane; i < i1; i += 4 * 32) {
-                    float4 v[4];
+            for (int i = s * sq; i < i1; i += 8 * kSfBatch) {
+                float v[kSfBatch];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        v[k] = i + 32 * k < i1 ? body[i + 32 * k] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int at = at0 + 4 * (i + 32 * k);
-                        see(v[k].x, at);
-                        see(v[k].y, at + 1);
-                        see(v[k].z, at + 2);
-                        see(v[k].w, at + 3);
-                    }
+                for (int k = 0; k < kSfBatch / 4; ++k) {
+                    const int at = i + lane + 32 * k;
+                    const float4 f = at < i1 ? body[at] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                    v[4 * k] = f.x;
+                    v[4 * k + 1] = f.y;
+                    v[4 * k + 2] = f.z;
+                    v[4 * k + 3] = f.w;
                 }
-                __syncwarp();
+                see(v, at0 + 4 * (i + lane));
             }
             done(s + 1);
         }
         if (w < 2) {
-            const int i0 = w ? at0 + 4 * nq : s0, i1 = w ? s1 : at0;
-            if (i0 + lane < i1) see(z[i0 + lane], i0 + lane);
-            __syncwarp();
+            const int i0 = (w ? at0 + 4 * nq : s0) + lane, i1 = w ? s1 : at0;
+            float v[kSfBatch];
+#pragma unroll
+            for (int e = 0; e < kSfBatch; ++e) v[e] = -INFINITY;
+            if (i0 < i1) v[0] = z[i0];
+            see(v, i0);
             done(w ? kSfSegments + 1 : 0);
         }
+    };
+    auto index_of = [](int at, int e) { return at + (e & 3) + 128 * (e >> 2); };
+    // the masses of those that reach `from`, into `sum`; nothing where none of the warp's does
+    auto add_from = [&](const SfRow &row, const float (&v)[kSfBatch], float from, bool above_only, sf_u64 &sum) {
+#pragma unroll
+        for (int e = 0; e < kSfBatch; ++e) {
+            float x;
+            uint32_t f;
+            const uint32_t n = row.mass(v[e], x, f);
+            sum += (sf_u64)((above_only ? v[e] > from : v[e] >= from) ? n : 0u) * f;
+        }
+    };
+    auto any_from = [&](const float (&v)[kSfBatch], float from) {
+        float m = v[0];
+#pragma unroll
+        for (int e = 1; e < kSfBatch; ++e) m = fmaxf(m, v[e]);
+        return __any_sync(0xffffffffu, m >= from);
     };
     auto no_segment = [](int) {};
     // a value of every rank, in all of them after the next sf_sync()
@@ -497,7 +517,15 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
         asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     }
     publish(kSfRange, (sf_u64)kmax << 32 | kmin);
-    sf_sync();
+    sf_arrive();
+    const bool floored = mp > 0.f && mp < 1.f;
+    if (tid == 0) {   // in 64 bits, by one thread: few of an SM's units have them
+        sm.real[0] = fmin(1.4426950408889634 / (double)t, 3e38);
+        if (floored) sm.real[1] = (double)t * log((double)mp);
+    }
+    __syncwarp();
+    sf_wait();
+    __syncthreads();   // the settings, written after that thread's arrival
     for (int r = 0; r < CS; ++r) {
         kmax = max(kmax, (uint32_t)(sm.xch[kSfRange][r] >> 32));
         kmin = min(kmin, (uint32_t)sm.xch[kSfRange][r]);
@@ -526,28 +554,25 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
     }
     SfRow row;
     row.top = sf_unkey(kmax);
-    const bool floored = mp > 0.f && mp < 1.f && row.top < INFINITY;
-    if (tid == 0) {   // in 64 bits, by one thread: few of an SM's units have them
-        sm.real[0] = fmin(1.4426950408889634 / (double)t, 3e38);
-        if (floored) sm.real[1] = (double)row.top + (double)t * log((double)mp);
-    }
-    __syncthreads();
     row.c = (float)sm.real[0];
     row.c_low = (float)(sm.real[0] - (double)row.c);
     SfCut cut = {0u, ~0u};
     if (mp > 0.f)   // the least logit with exp((z - top) / t) >= min_p
-        cut.tighten(sf_key(floored ? fminf(__double2float_ru(sm.real[1]), row.top) : row.top), ~0u);
+        cut.tighten(sf_key(floored && row.top < INFINITY ? fminf(__double2float_ru((double)row.top + sm.real[1]), row.top) : row.top), ~0u);
     const uint32_t floor_key = cut.key;
     if (k == 1) cut.tighten(kmax, 1u);
 
     // Lists the tokens from key `least` on in every CTA; their number in all.
     auto collect = [&](uint32_t least) {
         const float from = sf_unkey(least);
-        each([&](float v, int at) {
-            if (v >= from) {
-                const uint32_t n = atomicAdd(&sm.nlist, 1u);
-                if (n < kSfList) sm.list[n] = (sf_u64)sf_key(v) << 32 | (uint32_t)~at;
-            }
+        each([&](const float (&v)[kSfBatch], int at) {
+            if (!any_from(v, from)) return;
+#pragma unroll
+            for (int e = 0; e < kSfBatch; ++e)
+                if (v[e] >= from) {
+                    const uint32_t n = atomicAdd(&sm.nlist, 1u);
+                    if (n < kSfList) sm.list[n] = (sf_u64)sf_key(v[e]) << 32 | (uint32_t)~index_of(at, e);
+                }
         }, no_segment);
         __syncthreads();
         publish(kSfCount, sm.nlist);
@@ -558,11 +583,23 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
     };
     // The first CTA: the other ranks' lists behind its own.
     auto gather = [&]() {
-        uint32_t at = min(sm.nlist, (uint32_t)kSfList);
-        for (int r = 1; r < CS; ++r) {
-            const uint32_t n = min((uint32_t)sm.xch[kSfCount][r], kSfList - at);
-            for (uint32_t i = tid; i < n; i += kSfThreads) sm.list[at + i] = sf_get(&sm.list[i], (uint32_t)r);
-            at += n;
+        uint32_t end[kSfMaxCluster], at = min(sm.nlist, (uint32_t)kSfList);
+        const uint32_t own = at;
+#pragma unroll
+        for (int r = 0; r < kSfMaxCluster; ++r) {
+            if (r > 0 && r < CS) at += min((uint32_t)sm.xch[kSfCount][r], kSfList - at);
+            end[r] = at;
+        }
+        for (uint32_t i = own + tid; i < at; i += kSfThreads) {
+            int r = 0;
+            uint32_t begin = 0;
+#pragma unroll
+            for (int q = 0; q + 1 < kSfMaxCluster; ++q)
+                if (i >= end[q]) {
+                    r = q + 1;
+                    begin = end[q];
+                }
+            sm.list[i] = sf_get(&sm.list[i - begin], (uint32_t)r);
         }
         __syncthreads();
         return (int)at;
@@ -602,44 +639,70 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
         // the cluster's counts of `bins`; by exponent with the whole mass, by keys with the bins'
         // masses, in the place of the list
         sf_u64 *mass_own = sm.list, *mass_all = sm.list + kSfBins;
+        // by exponent there: what the masses of 2^-9 and more differ from their bins' middles, in 2^-20 of
+        // them.  Few tokens hold most of the mass; the many others' differences cancel.
+        int *rest_own = reinterpret_cast<int *>(mass_own), *rest_all = reinterpret_cast<int *>(mass_all);
         auto count = [&](sf_u64 *whole) {
             for (int i = tid; i < kSfBins; i += kSfThreads) {
                 sm.hist[i] = 0u;
                 if (bins.keys) mass_own[i] = 0ull;
+                else rest_own[i] = 0;
             }
             __syncthreads();
             sf_u64 own = 0ull;
             if (whole) {
-                each([&](float v, int) {
-                    float x;
-                    uint32_t f;
-                    const uint32_t n = row.mass(v, x, f);
-                    if (sf_takes_part(v) && x < kSfFar) {
-                        own += (sf_u64)n * f;
-                        atomicAdd(&sm.hist[bins.near(x)], 1u);
+                const float binades = bins.per_binade > 0.f ? 1.f / bins.per_binade : 0.f;
+                each([&](const float (&v)[kSfBatch], int) {
+#pragma unroll
+                    for (int e = 0; e < kSfBatch; ++e) {
+                        float x;
+                        uint32_t f;
+                        const uint32_t n = row.mass(v[e], x, f);
+                        const bool on = sf_takes_part(v[e]) && x < kSfFar;
+                        const int i = bins.near(x);
+                        own += (sf_u64)(on ? n : 0u) * f;
+                        if (on) {
+                            atomicAdd(&sm.hist[i], 1u);
+                            if (f > 1u) atomicAdd(&rest_own[i], (int)(((float)i * binades - x) * (0.6931471805599453f * 1048576.f)));
+                        }
                     }
                 }, no_segment);
                 publish(kSfWhole, block_sum(own));
             } else {
-                each([&](float v, int) {
-                    if (!sf_takes_part(v)) return;
-                    const int i = bins.of(row, v);
-                    if (i < 0 || i >= kSfBins) return;
-                    atomicAdd(&sm.hist[i], 1u);
-                    if (bins.keys) atomicAdd(&mass_own[i], row.mass(v));
+                each([&](const float (&v)[kSfBatch], int) {
+#pragma unroll
+                    for (int e = 0; e < kSfBatch; ++e) {
+                        if (!sf_takes_part(v[e])) continue;
+                        const int i = bins.of(row, v[e]);
+                        if (i < 0 || i >= kSfBins) continue;
+                        atomicAdd(&sm.hist[i], 1u);
+                        if (bins.keys) atomicAdd(&mass_own[i], row.mass(v[e]));
+                    }
                 }, no_segment);
             }
             sf_sync();
             const int share = kSfBins / CS;    // this rank adds up its share of the bins for all
             for (int i = (int)rank * share + tid; i < ((int)rank + 1) * share; i += kSfThreads) {
-                uint32_t n = 0;
-                for (int r = 0; r < CS; ++r) n += sf_get32(&sm.hist[i], (uint32_t)r);
-                for (int r = 0; r < CS; ++r)
+                uint32_t n = 0, c[kSfMaxCluster];
+                int rest = 0, d[kSfMaxCluster];
+                sf_u64 m = 0ull, x[kSfMaxCluster];
+#pragma unroll
+                for (int r = 0; r < kSfMaxCluster; ++r) {
+                    c[r] = r < CS ? sf_get32(&sm.hist[i], (uint32_t)r) : 0u;
+                    d[r] = r < CS && !bins.keys ? (int)sf_get32(&rest_own[i], (uint32_t)r) : 0;
+                    x[r] = r < CS && bins.keys ? sf_get(&mass_own[i], (uint32_t)r) : 0ull;
+                }
+#pragma unroll
+                for (int r = 0; r < kSfMaxCluster; ++r) {
+                    n += c[r];
+                    rest += d[r];
+                    m += x[r];
+                }
+                for (int r = 0; r < CS; ++r) {
                     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(sf_at(&sm.counts[i], (uint32_t)r)), "r"(n) : "memory");
-                if (!bins.keys) continue;
-                sf_u64 m = 0ull;
-                for (int r = 0; r < CS; ++r) m += sf_get(&mass_own[i], (uint32_t)r);
-                for (int r = 0; r < CS; ++r) sf_put(&mass_all[i], (uint32_t)r, m);
+                    if (bins.keys) sf_put(&mass_all[i], (uint32_t)r, m);
+                    else asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(sf_at(&rest_all[i], (uint32_t)r)), "r"(rest) : "memory");
+                }
             }
             sf_sync();
             if (whole) {
@@ -649,9 +712,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
         };
         auto sum_all = [&]() {
             sf_u64 own = 0ull;
-            each([&](float v, int) {
-                if (sf_takes_part(v)) row.add(own, v);
-            }, no_segment);
+            each([&](const float (&v)[kSfBatch], int) { add_from(row, v, -INFINITY, true, own); }, no_segment);
             publish(kSfWhole, block_sum(own));
             sf_sync();
             own = 0ull;
@@ -673,7 +734,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
                 if (by_mass && bins.keys) {
                     u[e] = l[e] = mass_all[i];
                 } else if (by_mass && estimated) {
-                    if (c[e]) u[e] *= bins.middle(i);
+                    if (c[e]) u[e] = (sf_u64)(((float)c[e] + (float)rest_all[i] * 0x1p-20f) * bins.middle(i));
                     l[e] = u[e];
                 } else if (by_mass && c[e]) {
                     u[e] *= bins.most(i);
@@ -754,7 +815,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
                 divided = false;
             }
             // the estimate's band has far fewer tokens; whether the cut lies there is seen from the exact masses
-            bool guess = by_mass && bracket(true, true, 0ull, target, lo, hi, before, upto) && upto > kSfRank;
+            bool guess = by_mass && k <= 1 && bracket(true, true, 0ull, target, lo, hi, before, upto) && upto > kSfRank;
             if (!guess && !bracket(by_mass, false, 0ull, target, lo, hi, before, upto)) return 0;
             if (!guess && upto <= kSfRank) {   // few after all
                 if (w == 0) {
@@ -782,17 +843,23 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
                 sf_u64 own = 0ull, seg = 0ull, in_band = 0ull;
                 uint32_t most = 0u, least = ~0u;
                 const bool weigh = by_mass || want_held;
-                each([&](float v, int at) {
-                    if (v >= over) {
-                        if (weigh) row.add(seg, v);
-                    } else if (v >= from) {
-                        const uint32_t key = sf_key(v);
+                each([&](const float (&v)[kSfBatch], int at) {
+                    if (!any_from(v, from)) return;
+                    if (weigh) add_from(row, v, over, false, seg);
+                    uint32_t band = 0;
+#pragma unroll
+                    for (int e = 0; e < kSfBatch; ++e) band |= v[e] >= from && !(v[e] >= over) ? 1u << e : 0u;
+                    if (!__any_sync(0xffffffffu, band != 0u)) return;
+#pragma unroll
+                    for (int e = 0; e < kSfBatch; ++e) {
+                        if (!(band >> e & 1u)) continue;
+                        const uint32_t key = sf_key(v[e]);
                         most = max(most, key);
                         least = min(least, key);
-                        if (guess) row.add(in_band, v);
+                        if (guess) row.add(in_band, v[e]);
                         if (fits) {
                             const uint32_t n = atomicAdd(&sm.nlist, 1u);
-                            if (n < kSfList) sm.list[n] = (sf_u64)key << 32 | (uint32_t)~at;
+                            if (n < kSfList) sm.list[n] = (sf_u64)key << 32 | (uint32_t)~index_of(at, e);
                         }
                     }
                 }, [&](int s) {
@@ -925,9 +992,11 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
     if (!ready) {
         sf_u64 seg = 0ull;
         uint32_t ties = 0;
-        each([&](float v, int) {
-            if (v > cut_at) row.add(seg, v);
-            ties += v == cut_at ? 1u : 0u;
+        each([&](const float (&v)[kSfBatch], int) {
+            if (!any_from(v, cut_at)) return;
+            add_from(row, v, cut_at, true, seg);
+#pragma unroll
+            for (int e = 0; e < kSfBatch; ++e) ties += v[e] == cut_at ? 1u : 0u;
         }, [&](int s) {
             seg = sf_warp_sum(seg);
             ties = __reduce_add_sync(0xffffffffu, ties);
