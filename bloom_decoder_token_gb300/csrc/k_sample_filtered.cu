@@ -14,8 +14,7 @@
 // exponent (max z - z) log2(e) / t is carried in two floats, or the rounding of 1 / t would
 // shift all far tokens the same way.
 //
-// Bound by the logits' first read; then by the passes over them in shared memory or
-// L2.  One cluster of up to 8 CTAs a row, each a slice of the vocabulary:
+// Bound by the logits' first read; then by the instructions of the passes over them in L2.  One cluster of up to 8 CTAs a row, each a slice of the vocabulary:
 //  1. the maximum and minimum, and every thread's own maximum;
 //  2. where few tokens can be kept, these come to the first CTA, which ranks them and does the
 //     rest: of the top 192, those that reach a bound from the maxima of groups of threads; the
@@ -61,7 +60,7 @@ constexpr float kSfSlack = 1.f / 65536.f;
 // barrier that follows its reading.
 enum { kSfRange, kSfCount, kSfBandMass, kSfAbove, kSfFound, kSfLeft, kSfWhole, kSfBand, kSfHeld, kSfMass, kSfTies, kSfSlots };
 
-struct alignas(16) SfSmem {                    // the cached slice follows, in float4s
+struct alignas(16) SfSmem {
     sf_u64 list[kSfList];                      // key << 32 | ~index; first CTA: of all ranks
     union {
         uint32_t hist[kSfBins];                // this CTA's counts
@@ -113,17 +112,17 @@ __device__ __forceinline__ uint32_t sf_key(float z) { return ordered_key(z + 0.f
 __device__ __forceinline__ float sf_unkey(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
-__device__ __forceinline__ bool sf_takes_part(float z) { return z > -INFINITY; }   // nor NaN
 
 struct SfRow {
     float top;         // the maximum
     float c, c_low;    // log2(e) / t, in two floats
-    // For logits that take part: (top - z) c; an infinite maximum's own is 0, others' are past kSfFar.
-    __device__ __forceinline__ float exponent(float z) const { return fmaxf(top - z, 0.f) * c; }
+    // The maximum is finite (rows with infinite ones have a way of their own).  Of -inf and NaN logits the
+    // exponent is infinite or NaN, and the mass 0.
+    __device__ __forceinline__ float exponent(float z) const { return (top - z) * c; }
     // The mass as n * f, f 512 or 1: from 2^-9 on in steps of 2^-31, which a float has there, below in
     // steps of 2^-40.  Adding n * f is one instruction.
     __device__ __forceinline__ uint32_t mass(float z, float &x, uint32_t &f) const {
-        const float d = fmaxf(top - z, 0.f);
+        const float d = top - z;
         x = d * c;
         const float low = fmaf(d, c_low, fmaf(d, c, -x));   // what the product and c lost
         float y;
@@ -364,26 +363,35 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
     const int q0 = min(quads, (int)rank * per), nq = min(quads, q0 + per) - q0, at0 = head + 4 * q0;
     const int s0 = rank == 0 ? 0 : at0, s1 = (int)rank == CS - 1 ? a.V : at0 + 4 * nq;
     const int sq = max(32, (nq + 32 * kSfSegments - 1) / (32 * kSfSegments) * 32);
-    const float4 *there = reinterpret_cast<const float4 *>(z + at0);
-    float4 *cache = reinterpret_cast<float4 *>(sf_raw + sizeof(SfSmem));
-    const float4 *body = a.cached ? cache : there;
+    const float4 *body = reinterpret_cast<const float4 *>(z + at0);
     // Every logit of the slice: warps take segments in turn (0: the head, then kSfSegments of the body,
     // then the tail), lanes kSfBatch logits at a time (value e at index at + (e & 3) + 128 (e >> 2); -inf beyond
     // the end); done(segment) after each.  Both are called by whole warps.
     auto each = [&](auto see, auto done) {
+        constexpr int Q = kSfBatch / 4;
+        float4 f[Q];   // the next batch, on its way
+        auto load = [&](int s, int i) {
+            const int i1 = min(nq, (s + 1) * sq);
+#pragma unroll
+            for (int k = 0; k < Q; ++k) {
+                const int at = i + lane + 32 * k;
+                f[k] = at < i1 ? body[at] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            }
+        };
+        load(w, w * sq);
         for (int s = w; s < kSfSegments; s += kSfWarps) {
             const int i1 = min(nq, (s + 1) * sq);
-            for (int i = s * sq; i < i1; i += 8 * kSfBatch) {
+            for (int i = s * sq; i < i1; i += 32 * Q) {
                 float v[kSfBatch];
 #pragma unroll
-                for (int k = 0; k < kSfBatch / 4; ++k) {
-                    const int at = i + lane + 32 * k;
-                    const float4 f = at < i1 ? body[at] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-                    v[4 * k] = f.x;
-                    v[4 * k + 1] = f.y;
-                    v[4 * k + 2] = f.z;
-                    v[4 * k + 3] = f.w;
+                for (int k = 0; k < Q; ++k) {
+                    v[4 * k] = f[k].x;
+                    v[4 * k + 1] = f[k].y;
+                    v[4 * k + 2] = f[k].z;
+                    v[4 * k + 3] = f[k].w;
                 }
+                if (i + 32 * Q < i1) load(s, i + 32 * Q);
+                else if (s + kSfWarps < kSfSegments) load(s + kSfWarps, (s + kSfWarps) * sq);
                 see(v, at0 + 4 * (i + lane));
             }
             done(s + 1);
@@ -455,10 +463,9 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
             float4 v[6];
 #pragma unroll
             for (int k = 0; k < 6; ++k)
-                v[k] = i + k * kSfThreads < nq ? __ldg(there + i + k * kSfThreads) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                v[k] = i + k * kSfThreads < nq ? __ldg(body + i + k * kSfThreads) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
 #pragma unroll
             for (int k = 0; k < 6; ++k) {
-                if (a.cached && i + k * kSfThreads < nq) cache[i + k * kSfThreads] = v[k];
                 see(v[k].x);
                 see(v[k].y);
                 see(v[k].z);
@@ -613,8 +620,25 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
         sf_sync();   // the lists have been read
     };
 
+    // An infinite maximum: its tokens share the mass, all else has none.
+    const bool infinite = row.top == INFINITY;
+    if (infinite) {
+        sf_u64 n = 0ull;
+        each([&](const float (&v)[kSfBatch], int) {
+#pragma unroll
+            for (int e = 0; e < kSfBatch; ++e) n += v[e] == INFINITY ? 1u : 0u;
+        }, no_segment);
+        publish(kSfWhole, block_sum(n));
+        sf_sync();
+        n = 0ull;
+        for (int r = 0; r < CS; ++r) n += sm.xch[kSfWhole][r];
+        if (k > 0) n = min(n, (sf_u64)k);
+        if (nucleus && k != 1) n = max(1ull, min(n, (sf_u64)ceil((double)p * (double)n)));
+        cut.tighten(kmax, (uint32_t)n);
+    }
+
     // ---- 2. few tokens
-    {
+    if (!infinite) {
         uint32_t least = k == 1 ? kmax : bound;
         if (least == 0u && k != 1 && (k > 1 || nucleus) && a.V <= kSfRank) least = kmin;
         if (least && !nucleus) least = max(least, floor_key);   // with top-p the mass of what lies below counts
@@ -632,7 +656,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
 
     // ---- 3., 4. the cuts of top-k and top-p
     bool ready = false;   // the segments' masses are those of the cut
-    if (k != 1 && (k > 1 || nucleus)) {
+    if (!infinite && k != 1 && (k > 1 || nucleus)) {
         const float far = fminf(row.exponent(sf_unkey(kmin)), kSfFar);
         SfBins bins = {false, far > 0.f ? (kSfBins - 1) / far : 0.f, 0u, 0u, 0};
         if (!(bins.per_binade < 1e30f)) bins.per_binade = 0.f;   // logits that differ by next to nothing
@@ -658,10 +682,9 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
                         float x;
                         uint32_t f;
                         const uint32_t n = row.mass(v[e], x, f);
-                        const bool on = sf_takes_part(v[e]) && x < kSfFar;
                         const int i = bins.near(x);
-                        own += (sf_u64)(on ? n : 0u) * f;
-                        if (on) {
+                        own += (sf_u64)n * f;
+                        if (x < kSfFar) {
                             atomicAdd(&sm.hist[i], 1u);
                             if (f > 1u) atomicAdd(&rest_own[i], (int)(((float)i * binades - x) * (0.6931471805599453f * 1048576.f)));
                         }
@@ -672,7 +695,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
                 each([&](const float (&v)[kSfBatch], int) {
 #pragma unroll
                     for (int e = 0; e < kSfBatch; ++e) {
-                        if (!sf_takes_part(v[e])) continue;
+                        if (!(v[e] > -INFINITY)) continue;   // nor NaN
                         const int i = bins.of(row, v[e]);
                         if (i < 0 || i >= kSfBins) continue;
                         atomicAdd(&sm.hist[i], 1u);
@@ -1009,7 +1032,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
         });
     }
     __syncthreads();
-    const sf_u64 tie_mass = cut.key ? row.mass(cut_at) : 0ull;
+    const sf_u64 tie_mass = infinite ? 1ull << 40 : cut.key ? row.mass(cut_at) : 0ull;
     // every warp: the head's, the segments' and the tail's, three a lane
     static_assert(kSfSegments + 2 <= 3 * 32, "three places a lane");
     sf_u64 sm3[3], st3[3], mass_sum = 0ull, tie_sum = 0ull;
@@ -1034,7 +1057,6 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
         kept += sm.xch[kSfMass][r] + min(n, left) * tie_mass;
         seen += n;
     }
-    auto logit = [&](int i) { return i >= at0 && i < at0 + 4 * nq ? reinterpret_cast<const float *>(body)[i - at0] : z[i]; };
     // a warp a draw
     for (int j = w; j < a.J; j += kSfWarps) {
         const long long out = (long long)b * a.J + j;
@@ -1070,7 +1092,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
         const int i0 = s == 0 ? s0 : at0 + 4 * min(nq, (s - 1) * sq);
         const int i1 = s == 0 ? at0 : s == kSfSegments + 1 ? s1 : at0 + 4 * min(nq, s * sq);
         for (int i = s == kSfSegments + 1 ? at0 + 4 * nq : i0; i < i1; i += 32) {
-            const float v = i + lane < i1 ? logit(i + lane) : -INFINITY;
+            const float v = i + lane < i1 ? z[i + lane] : -INFINITY;
             const bool tie = cut.key && v == cut_at;
             const unsigned ties = __ballot_sync(0xffffffffu, tie);
             sf_u64 m = 0ull;
@@ -1088,27 +1110,32 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
     }
 }
 
-cudaError_t launch_sample_filtered(SampleFilteredArgs a, cudaStream_t s) {
-    constexpr int kDevices = 64, kMost = 220 * 1024;
+cudaError_t launch_sample_filtered(const SampleFilteredArgs &a, cudaStream_t s) {
+    constexpr int kDevices = 64;
     static std::atomic<bool> ready[kDevices];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= kDevices) return cudaErrorInvalidDevice;
     if (!ready[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(sample_filtered_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+        e = cudaFuncSetAttribute(sample_filtered_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SfSmem));
         if (e != cudaSuccess) return e;
         ready[dev].store(true, std::memory_order_release);
     }
     const int sms = bloom_device_sms();
+    // One resident wave of two CTAs an SM, each of 8192 logits at least: what a CTA costs beside its
+    // passes is then least (top-p 0.95, clusters of 1, 2, 4, 8: 4 rows of 250880 175, 104, 66, 44 us;
+    // 64 rows 185, 107, 86, 107; 300 rows of 32000 66, 93, 151, 250).  Many long rows: so many CTAs
+    // a row that what the resident ones read stays in L2 from one pass to the next (509 rows of
+    // 250880: 582, 519, 517, 692).
     int cluster = 1;
-    while (cluster < kSfMaxCluster && a.V / (2 * cluster) >= 4096 && (long long)a.B * cluster < 4ll * sms) cluster *= 2;
-    const size_t slice = ((size_t)(a.V / 4 + cluster - 1) / cluster + 1) * 16;
-    a.cached = sizeof(SfSmem) + slice <= 100 * 1024 || ((long long)a.B * cluster <= sms && sizeof(SfSmem) + slice <= kMost);
+    while (cluster < kSfMaxCluster && a.V / (2 * cluster) >= 8192 &&
+           (2ll * a.B * cluster <= 2ll * sms || (cluster < 4 && 2ll * sms / cluster * a.V * 4 > (100ll << 20))))
+        cluster *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)cluster, (unsigned)a.B);
     cfg.blockDim = dim3(kSfThreads);
-    cfg.dynamicSmemBytes = sizeof(SfSmem) + (a.cached ? slice : 0);
+    cfg.dynamicSmemBytes = sizeof(SfSmem);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

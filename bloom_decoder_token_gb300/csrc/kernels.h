@@ -245,9 +245,8 @@ struct SampleFilteredArgs {
     const float *min_p = nullptr;
     const float *u = nullptr;             // [B][J]
     int32_t *out = nullptr;               // [B][J]
-    int cached = 0;                       // set by the launch: slices stay in shared memory
 };
-cudaError_t launch_sample_filtered(SampleFilteredArgs a, cudaStream_t s);
+cudaError_t launch_sample_filtered(const SampleFilteredArgs &a, cudaStream_t s);
 
 // Log probabilities of given tokens, entropy and the top alternatives of B rows of
 // float32 logits (k_logprobs.cu); arrays as bloom_op_logprobs describes them.
