@@ -39,12 +39,10 @@ namespace bloom {
 
 typedef unsigned long long sf_u64;
 
-constexpr int kSfMaxCluster = 8;
-constexpr int kSfThreads = 512;
-constexpr int kSfWarps = kSfThreads / 32;
+constexpr int kSfMaxCluster = 16;
 constexpr int kSfBins = 2048;
 constexpr int kSfList = 4096;                  // tokens that a CTA lists
-constexpr int kSfRank = kSfThreads;            // that the first CTA ranks, one a thread
+constexpr int kSfRank = 512;                   // that the first CTA ranks
 constexpr int kSfBound = 192;                  // a top-k up to which maxima of groups of threads give a bound
 constexpr int kSfMarks = 8;                    // of a rank's maxima: every ceil(k / 8)-th
 constexpr int kSfDigits = 1024;
@@ -60,7 +58,9 @@ constexpr float kSfSlack = 1.f / 65536.f;
 // barrier that follows its reading.
 enum { kSfRange, kSfCount, kSfBandMass, kSfAbove, kSfFound, kSfLeft, kSfWhole, kSfBand, kSfHeld, kSfMass, kSfTies, kSfSlots };
 
+template <int THREADS>
 struct alignas(16) SfSmem {
+    static constexpr int kWarps = THREADS / 32;
     sf_u64 list[kSfList];                      // key << 32 | ~index; first CTA: of all ranks
     union {
         uint32_t hist[kSfBins];                // this CTA's counts
@@ -69,11 +69,11 @@ struct alignas(16) SfSmem {
     uint32_t counts[kSfBins];                  // the cluster's
     sf_u64 seg_mass[kSfSegments + 2];
     uint32_t seg_ties[kSfSegments + 2];
-    alignas(16) uint32_t own_max[kSfThreads / 2];
+    alignas(16) uint32_t own_max[THREADS / 2];
     uint32_t marks[kSfMaxCluster * kSfMarks];
-    sf_u64 scan[2][kSfWarps];
-    uint32_t scan_n[kSfWarps];
-    sf_u64 part[kSfWarps][3];
+    sf_u64 scan[2][kWarps];
+    uint32_t scan_n[kWarps];
+    sf_u64 part[kWarps][3];
     sf_u64 xch[kSfSlots][kSfMaxCluster];       // a value of every rank
     sf_u64 found[4];
     double real[2];
@@ -194,7 +194,8 @@ __device__ __forceinline__ sf_u64 sf_warp_scan(sf_u64 v) {   // inclusive
     return v;
 }
 // Exclusive scan over the block in thread order; `total` of all.
-__device__ __forceinline__ sf_u64 sf_block_scan(SfSmem &sm, sf_u64 v, sf_u64 &total) {
+template <int THREADS>
+__device__ __forceinline__ sf_u64 sf_block_scan(SfSmem<THREADS> &sm, sf_u64 v, sf_u64 &total) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const sf_u64 in = sf_warp_scan(v);
     __syncthreads();
@@ -203,7 +204,7 @@ __device__ __forceinline__ sf_u64 sf_block_scan(SfSmem &sm, sf_u64 v, sf_u64 &to
     sf_u64 before = 0ull;
     total = 0ull;
 #pragma unroll
-    for (int i = 0; i < kSfWarps; ++i) {
+    for (int i = 0; i < SfSmem<THREADS>::kWarps; ++i) {
         if (i < w) before += sm.scan[0][i];
         total += sm.scan[0][i];
     }
@@ -225,16 +226,17 @@ struct SfCut {
 
 // In the first CTA's list (n tokens, keys from `least` to `most`): the key at which the weights of the
 // highest keys, one a token or its mass, reach `target`, and what of the target is left for its ties.
-__device__ __forceinline__ uint32_t sf_select(SfSmem &sm, const SfRow &row, int n, uint32_t most, uint32_t least,
+template <int THREADS>
+__device__ __forceinline__ uint32_t sf_select(SfSmem<THREADS> &sm, const SfRow &row, int n, uint32_t most, uint32_t least,
                                               bool by_mass, sf_u64 &target) {
-    constexpr int kBits = 10, PT = kSfDigits / kSfThreads;
+    constexpr int kBits = 10, PT = kSfDigits / THREADS;
     const int tid = threadIdx.x;
     uint32_t found = 0;   // of most - key, the bits above `shift`
     for (int shift = max(0, 32 - __clz((int)(most - least)) - kBits);; shift = max(0, shift - kBits)) {
         __syncthreads();
-        for (int i = tid; i < kSfDigits; i += kSfThreads) sm.digit[i] = 0ull;
+        for (int i = tid; i < kSfDigits; i += THREADS) sm.digit[i] = 0ull;
         __syncthreads();
-        for (int i = tid; i < n; i += kSfThreads) {
+        for (int i = tid; i < n; i += THREADS) {
             const uint32_t k = (uint32_t)(sm.list[i] >> 32), far = (most - k) >> shift;
             if (far >= found && far - found < kSfDigits) atomicAdd(&sm.digit[far - found], by_mass ? row.mass(sf_unkey(k)) : 1ull);
         }
@@ -262,14 +264,15 @@ __device__ __forceinline__ uint32_t sf_select(SfSmem &sm, const SfRow &row, int 
 // The first CTA's end of a row whose kept tokens are all listed (n of them, at most kSfRank): ranks
 // them, cuts, and draws.  k: top-k or 0; part: of the listed tokens' mass after top-k that is kept, or
 // target: the mass itself; floor: least key kept.
-__device__ __forceinline__ void sf_finish(SfSmem &sm, const SfRow &row, const SampleFilteredArgs &a, int b, int n, int k,
+template <int THREADS>
+__device__ __forceinline__ void sf_finish(SfSmem<THREADS> &sm, const SfRow &row, const SampleFilteredArgs &a, int b, int n, int k,
                                           float part, sf_u64 target, uint32_t floor) {
-    constexpr int PT = kSfRank / kSfThreads;
+    constexpr int PT = kSfRank / THREADS;
     const int tid = threadIdx.x;
     sf_u64 *sorted = sm.list + kSfRank, *mass = sorted + kSfRank;   // highest first
     if (tid == 0 && (n & 1)) sm.list[n] = 0ull;
     __syncthreads();
-    for (int i = tid; i < n; i += kSfThreads) {
+    for (int i = tid; i < n; i += THREADS) {
         const sf_u64 mine = sm.list[i];
         int above = 0;
 #pragma unroll 4
@@ -316,7 +319,7 @@ __device__ __forceinline__ void sf_finish(SfSmem &sm, const SfRow &row, const Sa
     sf_u64 from[PT], at[PT];
 #pragma unroll
     for (int e = 0; e < PT; ++e) {
-        const int i = tid + e * kSfThreads;
+        const int i = tid + e * THREADS;
         from[e] = 0ull;
         at[e] = 0ull;
         if (i < (int)m) {
@@ -329,7 +332,7 @@ __device__ __forceinline__ void sf_finish(SfSmem &sm, const SfRow &row, const Sa
     for (int j0 = 0; j0 < a.J; j0 += kSfDigits) {
         __syncthreads();
         const int nj = min(a.J - j0, kSfDigits);
-        for (int j = tid; j < nj; j += kSfThreads) {
+        for (int j = tid; j < nj; j += THREADS) {
             const float u = a.u[(long long)b * a.J + j0 + j];
             pos[j] = min(u > 0.f ? (sf_u64)((double)u * (double)total) : 0ull, total - 1ull);
         }
@@ -338,14 +341,16 @@ __device__ __forceinline__ void sf_finish(SfSmem &sm, const SfRow &row, const Sa
         for (int e = 0; e < PT; ++e) {
             if (at[e] == from[e]) continue;
             for (int j = 0; j < nj; ++j)
-                if (from[e] <= pos[j] && pos[j] < at[e]) a.out[(long long)b * a.J + j0 + j] = (int)~(uint32_t)sorted[tid + e * kSfThreads];
+                if (from[e] <= pos[j] && pos[j] < at[e]) a.out[(long long)b * a.J + j0 + j] = (int)~(uint32_t)sorted[tid + e * THREADS];
         }
     }
 }
 
-__global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const SampleFilteredArgs a) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kernel(const SampleFilteredArgs a) {
+    constexpr int WARPS = THREADS / 32;
     extern __shared__ __align__(16) unsigned char sf_raw[];
-    SfSmem &sm = *reinterpret_cast<SfSmem *>(sf_raw);
+    SfSmem<THREADS> &sm = *reinterpret_cast<SfSmem<THREADS> *>(sf_raw);
     griddep_launch();
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int b = blockIdx.y, CS = (int)gridDim.x;
@@ -379,7 +384,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
             }
         };
         load(w, w * sq);
-        for (int s = w; s < kSfSegments; s += kSfWarps) {
+        for (int s = w; s < kSfSegments; s += WARPS) {
             const int i1 = min(nq, (s + 1) * sq);
             for (int i = s * sq; i < i1; i += 32 * Q) {
                 float v[kSfBatch];
@@ -391,7 +396,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
                     v[4 * k + 3] = f[k].w;
                 }
                 if (i + 32 * Q < i1) load(s, i + 32 * Q);
-                else if (s + kSfWarps < kSfSegments) load(s + kSfWarps, (s + kSfWarps) * sq);
+                else if (s + WARPS < kSfSegments) load(s + WARPS, (s + WARPS) * sq);
                 see(v, at0 + 4 * (i + lane));
             }
             done(s + 1);
@@ -409,12 +414,15 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
     auto index_of = [](int at, int e) { return at + (e & 3) + 128 * (e >> 2); };
     // the masses of those that reach `from`, into `sum`; nothing where none of the warp's does
     auto add_from = [&](const SfRow &row, const float (&v)[kSfBatch], float from, bool above_only, sf_u64 &sum) {
+        const bool few = from > -INFINITY;   // else all
 #pragma unroll
         for (int e = 0; e < kSfBatch; ++e) {
+            const bool on = above_only ? v[e] > from : v[e] >= from;
+            if (few && !__any_sync(0xffffffffu, on)) continue;
             float x;
             uint32_t f;
             const uint32_t n = row.mass(v[e], x, f);
-            sum += (sf_u64)((above_only ? v[e] > from : v[e] >= from) ? n : 0u) * f;
+            sum += (sf_u64)(on ? n : 0u) * f;
         }
     };
     auto any_from = [&](const float (&v)[kSfBatch], float from) {
@@ -435,7 +443,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
         __syncthreads();
         v = 0ull;
 #pragma unroll
-        for (int i = 0; i < kSfWarps; ++i) v += sm.part[i][0];
+        for (int i = 0; i < WARPS; ++i) v += sm.part[i][0];
         return v;
     };
     auto block_range = [&](uint32_t &most, uint32_t &least) {
@@ -445,7 +453,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
         if (lane == 0) sm.part[w][1] = (sf_u64)most << 32 | least;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kSfWarps; ++i) {
+        for (int i = 0; i < WARPS; ++i) {
             most = max(most, (uint32_t)(sm.part[i][1] >> 32));
             least = min(least, (uint32_t)sm.part[i][1]);
         }
@@ -459,11 +467,11 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
             mx = fmaxf(mx, v);
             mn = fminf(mn, v > -INFINITY ? v : INFINITY);
         };
-        for (int i = tid; i < nq; i += 6 * kSfThreads) {
+        for (int i = tid; i < nq; i += 6 * THREADS) {
             float4 v[6];
 #pragma unroll
             for (int k = 0; k < 6; ++k)
-                v[k] = i + k * kSfThreads < nq ? __ldg(body + i + k * kSfThreads) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                v[k] = i + k * THREADS < nq ? __ldg(body + i + k * THREADS) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
 #pragma unroll
             for (int k = 0; k < 6; ++k) {
                 see(v[k].x);
@@ -498,7 +506,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
     const bool bounded = k > 1 && k <= kSfBound;
     const int step = (k + kSfMarks - 1) / kSfMarks;
     if (bounded) {
-        const int wide = k <= 64 ? 4 : 2, groups = kSfThreads / wide;
+        const int wide = k <= 64 ? 4 : 2, groups = THREADS / wide;
         uint32_t g = max(thread_max, __shfl_xor_sync(0xffffffffu, thread_max, 1));
         if (wide == 4) g = max(g, __shfl_xor_sync(0xffffffffu, g, 2));
         if (tid % wide == 0) sm.own_max[tid / wide] = g;
@@ -539,7 +547,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
     }
     if (kmax == 0u) {
         if (rank == 0)
-            for (int j = tid; j < a.J; j += kSfThreads) a.out[(long long)b * a.J + j] = -1;
+            for (int j = tid; j < a.J; j += THREADS) a.out[(long long)b * a.J + j] = -1;
         return;
     }
     uint32_t bound = 0u;                         // 0: none
@@ -597,7 +605,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
             if (r > 0 && r < CS) at += min((uint32_t)sm.xch[kSfCount][r], kSfList - at);
             end[r] = at;
         }
-        for (uint32_t i = own + tid; i < at; i += kSfThreads) {
+        for (uint32_t i = own + tid; i < at; i += THREADS) {
             int r = 0;
             uint32_t begin = 0;
 #pragma unroll
@@ -667,7 +675,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
         // them.  Few tokens hold most of the mass; the many others' differences cancel.
         int *rest_own = reinterpret_cast<int *>(mass_own), *rest_all = reinterpret_cast<int *>(mass_all);
         auto count = [&](sf_u64 *whole) {
-            for (int i = tid; i < kSfBins; i += kSfThreads) {
+            for (int i = tid; i < kSfBins; i += THREADS) {
                 sm.hist[i] = 0u;
                 if (bins.keys) mass_own[i] = 0ull;
                 else rest_own[i] = 0;
@@ -705,7 +713,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
             }
             sf_sync();
             const int share = kSfBins / CS;    // this rank adds up its share of the bins for all
-            for (int i = (int)rank * share + tid; i < ((int)rank + 1) * share; i += kSfThreads) {
+            for (int i = (int)rank * share + tid; i < ((int)rank + 1) * share; i += THREADS) {
                 uint32_t n = 0, c[kSfMaxCluster];
                 int rest = 0, d[kSfMaxCluster];
                 sf_u64 m = 0ull, x[kSfMaxCluster];
@@ -746,7 +754,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
         // `target`; tokens before lo and up to hi.  False: they do not.
         // Estimated: by the masses of the bins' middles, and a bin on either side.
         auto bracket = [&](bool by_mass, bool estimated, sf_u64 base, sf_u64 target, int &lo, int &hi, uint32_t &before, uint32_t &upto) {
-            constexpr int PT = kSfBins / kSfThreads;
+            constexpr int PT = kSfBins / THREADS;
             uint32_t c[PT], n = 0;
             sf_u64 u[PT], l[PT], su = 0ull, sl = 0ull;
 #pragma unroll
@@ -798,7 +806,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
                 ru += u[e];
                 rl += l[e];
             }
-            if (tid == kSfThreads - 1 && rl < target) sm.bin[3] = (int)rn;   // to the last bin
+            if (tid == THREADS - 1 && rl < target) sm.bin[3] = (int)rn;   // to the last bin
             __syncthreads();
             lo = sm.bin[0];
             hi = min(sm.bin[1], kSfBins - 1);
@@ -938,7 +946,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
                         publish(kSfLeft, left);
                         sf_u64 m = 0ull;
                         if (want_held)
-                            for (int i = tid; i < n; i += kSfThreads) {
+                            for (int i = tid; i < n; i += THREADS) {
                                 const uint32_t one = (uint32_t)(sm.list[i] >> 32);
                                 if (one > key) m += row.mass(sf_unkey(one));
                             }
@@ -961,7 +969,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
                     if (tid < kSfSegments + 2) sm.seg_ties[tid] = 0u;
                     __syncthreads();
                     own_listed = min(own_listed, (uint32_t)kSfList);
-                    for (uint32_t i = tid; i < own_listed; i += kSfThreads) {
+                    for (uint32_t i = tid; i < own_listed; i += THREADS) {
                         const uint32_t key = (uint32_t)(sm.list[i] >> 32);
                         const int at = (int)~(uint32_t)sm.list[i];
                         const int s = at < at0 ? 0 : at >= at0 + 4 * nq ? kSfSegments + 1 : 1 + (at - at0) / 4 / sq;
@@ -1058,7 +1066,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
         seen += n;
     }
     // a warp a draw
-    for (int j = w; j < a.J; j += kSfWarps) {
+    for (int j = w; j < a.J; j += WARPS) {
         const long long out = (long long)b * a.J + j;
         const float u = a.u[out];
         sf_u64 pos = u > 0.f ? (sf_u64)((double)u * (double)kept) : 0ull;
@@ -1110,32 +1118,25 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Sa
     }
 }
 
-cudaError_t launch_sample_filtered(const SampleFilteredArgs &a, cudaStream_t s) {
+template <int THREADS>
+static cudaError_t sf_launch(const SampleFilteredArgs &a, int cluster, cudaStream_t s) {
     constexpr int kDevices = 64;
     static std::atomic<bool> ready[kDevices];
+    const auto kern = sample_filtered_kernel<THREADS>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= kDevices) return cudaErrorInvalidDevice;
     if (!ready[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(sample_filtered_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SfSmem));
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SfSmem<THREADS>));
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
         ready[dev].store(true, std::memory_order_release);
     }
-    const int sms = bloom_device_sms();
-    // One resident wave of two CTAs an SM, each of 8192 logits at least: what a CTA costs beside its
-    // passes is then least (top-p 0.95, clusters of 1, 2, 4, 8: 4 rows of 250880 175, 104, 66, 44 us;
-    // 64 rows 185, 107, 86, 107; 300 rows of 32000 66, 93, 151, 250).  Many long rows: so many CTAs
-    // a row that what the resident ones read stays in L2 from one pass to the next (509 rows of
-    // 250880: 582, 519, 517, 692).
-    int cluster = 1;
-    while (cluster < kSfMaxCluster && a.V / (2 * cluster) >= 8192 &&
-           (2ll * a.B * cluster <= 2ll * sms || (cluster < 4 && 2ll * sms / cluster * a.V * 4 > (100ll << 20))))
-        cluster *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)cluster, (unsigned)a.B);
-    cfg.blockDim = dim3(kSfThreads);
-    cfg.dynamicSmemBytes = sizeof(SfSmem);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = sizeof(SfSmem<THREADS>);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1146,7 +1147,21 @@ cudaError_t launch_sample_filtered(const SampleFilteredArgs &a, cudaStream_t s) 
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, sample_filtered_kernel, a);
+    return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+cudaError_t launch_sample_filtered(const SampleFilteredArgs &a, cudaStream_t s) {
+    const int sms = bloom_device_sms();
+    // CTAs of 512 threads, two an SM, in one resident wave, each of 4096 logits at least; clusters of 16
+    // for a few rows (top-p 0.95, clusters of 2, 4, 8, 16: 4 rows of 250880 87, 54, 37, 31 us; 16 rows
+    // 95, 57, 48, 64; 64 rows 117, 78, 97, 174; 300 rows of 32000, from 1 on: 62, 84, 146, 251).
+    // More rows than that: CTAs of 256 threads, four an SM, hide one another's phases; long rows on
+    // two CTAs (509 rows of 250880, clusters of 1, 2, 4, 8: 511, 443, 451, 504 us; of 512 threads
+    // 491, 463, 499, 664; 2000 rows of 8000: 228 against 266).
+    if (a.B > 2 * sms) return sf_launch<256>(a, a.V >= 65536 ? 2 : 1, s);
+    int cluster = 1;
+    while (a.V / (2 * cluster) >= 4096 && (cluster < 8 ? a.B * cluster <= sms : cluster < kSfMaxCluster && 32 * a.B <= sms)) cluster *= 2;
+    return sf_launch<512>(a, cluster, s);
 }
 
 }  // namespace bloom
