@@ -123,7 +123,8 @@ _SIGS = {
     "bloom_w4_bytes": (C.c_size_t, [I32, I32, I32]),
     "bloom_op_w4_quantize": (I32, [P, C.c_int64, P, P]),
     "bloom_op_w4_read": (I32, [P, P, C.c_int64, P]),
-    "bloom_op_linear_w4": (I32, [P, P, C.c_int64, I32, P, I32, P, C.c_int64, I32, P, P]),
+    "bloom_op_linear_w4": (I32, [P, P, C.c_int64, I32, P, I32, P, C.c_int64, I32, P, C.c_size_t, P, P]),
+    "bloom_op_linear_w4_workspace": (C.c_size_t, [P, I32]),
     "bloom_op_linear_w4_wait_ns": (I32, [I32]),
     "bloom_op_lmhead_argmax_noalloc": (I32, [P, P, I32, I32, I32, P, P, P]),
 }
@@ -800,18 +801,19 @@ def op_w4_read(w4: W4, out=None, stream=None):
     return out
 
 
-def op_linear_w4(x, w4: W4, bias=None, epilogue=EPI_STORE, y=None, dtype=torch.bfloat16, flag=None,
-                 stream=None):
+def op_linear_w4(x, w4: W4, bias=None, epilogue=EPI_STORE, y=None, dtype=torch.bfloat16, workspace=None,
+                 flag=None, stream=None):
     """Linear layer of a decode step over 4-bit weights: x bf16 [M][k], bias bf16 [n];
     y bf16 or float32 [M][n], given (required for EPI_RESID, which adds to it) or new, of
-    `dtype`.  Rows of x and y may be strided.  flag int32 [1] that errors are recorded in."""
+    `dtype`.  Rows of x and y may be strided.  workspace: uint8, bloom_op_linear_w4_workspace()
+    bytes, None to allocate it.  flag int32 [1] that errors are recorded in."""
     dev = x.device
     if x.dim() != 2:
         _bad(f"x: [M][k] expected, got {tuple(x.shape)}")
     there = _elsewhere(dev, stream)
     if there is not None:
         with there:
-            return op_linear_w4(x, w4, bias, epilogue, y, dtype, flag)
+            return op_linear_w4(x, w4, bias, epilogue, y, dtype, workspace, flag)
     c = w4.c()
     if w4.tiles.device != dev:
         _bad(f"weights on {w4.tiles.device}, x on {dev}")
@@ -827,8 +829,19 @@ def op_linear_w4(x, w4: W4, bias=None, epilogue=EPI_STORE, y=None, dtype=torch.b
         y = torch.empty((M, c.n), dtype=dtype, device=dev)
     f32 = y.dtype is _F32
     yp, ldy = _rows("y", y, _F32 if f32 else _BF16, (M, c.n), dev)
-    st = lib().bloom_op_linear_w4(C.byref(c), xp, ldx, M, _dev("bias", bias, _BF16, (c.n,), dev), epilogue, yp,
-                                  ldy, f32, _dev("flag", flag, _I32, (1,), dev), _raw_stream(dev))
+    L, cr = lib(), C.byref(c)
+    wp, wn = None, 0
+    if workspace is not None:
+        if workspace.dtype is not _U8 or workspace.dim() != 1:
+            _bad(f"workspace: uint8 [bytes] expected, got {workspace.dtype} {tuple(workspace.shape)}")
+        wn = workspace.numel()
+        wp = _dev("workspace", workspace, _U8, (wn,), dev)
+    elif M > 8:
+        wn = L.bloom_op_linear_w4_workspace(cr, M)
+        workspace = torch.empty(wn, dtype=_U8, device=dev)
+        wp = workspace.data_ptr()
+    st = L.bloom_op_linear_w4(cr, xp, ldx, M, _dev("bias", bias, _BF16, (c.n,), dev), epilogue, yp, ldy, f32, wp, wn,
+                              _dev("flag", flag, _I32, (1,), dev), _raw_stream(dev))
     if st:
         check(st)
     return y

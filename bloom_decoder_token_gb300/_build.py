@@ -16,7 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libbloom.so")
 SOURCES = ["api.cu", "k_linear.cu", "k_norm.cu", "k_attn.cu", "k_attn_tc.cu", "noalloc.cu", "k_gemm.cu", "k_gemv_tc.cu", "k_sample.cu",
-           "k_kv8.cu", "k_attn_kv8.cu", "k_logprobs.cu", "k_w4.cu", "k_linear_w4.cu",
+           "k_kv8.cu", "k_attn_kv8.cu", "k_logprobs.cu", "k_w4.cu", "k_linear_w4.cu", "k_linear_w4_tc.cu",
            "k_sample_filtered.cu"]
 HEADERS = ["common.cuh", "kernels.h", "tile_ops.cuh", "attn_ops.cuh", "norm_ops.cuh", "tc_ops.cuh",
            "kv8_ops.cuh", "w4_ops.cuh"]

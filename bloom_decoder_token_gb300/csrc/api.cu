@@ -1723,6 +1723,11 @@ extern "C" bloom_status bloom_op_w4_read(const bloom_w4 *in, void *w, int64_t ld
 
 static thread_local int32_t g_linear_w4_wait_ns = 0;
 
+extern "C" size_t bloom_op_linear_w4_workspace(const bloom_w4 *w, int32_t M) {
+    if (check_w4(w) || M < 0 || M > (1 << 20)) return 0;
+    return M <= kLw4MaxM ? 0 : linear_w4_tc_workspace(M, w->k);
+}
+
 extern "C" bloom_status bloom_op_linear_w4_wait_ns(int32_t wait_ns) {
     if (wait_ns < 0) return fail(BLOOM_E_INVALID, "wait_ns=%d", wait_ns);
     g_linear_w4_wait_ns = wait_ns;
@@ -1730,7 +1735,8 @@ extern "C" bloom_status bloom_op_linear_w4_wait_ns(int32_t wait_ns) {
 }
 extern "C" bloom_status bloom_op_linear_w4(const bloom_w4 *w, const void *x, int64_t ldx, int32_t M,
                                            const void *bias, int32_t epilogue, void *y, int64_t ldy,
-                                           int32_t y_f32, int32_t *flag, void *stream) {
+                                           int32_t y_f32, void *workspace, size_t workspace_bytes,
+                                           int32_t *flag, void *stream) {
     g_pdl = true;
     bloom_status st = check_w4(w);
     if (st) return st;
@@ -1759,7 +1765,14 @@ extern "C" bloom_status bloom_op_linear_w4(const bloom_w4 *w, const void *x, int
     a.f32 = y_f32 != 0;
     a.err = flag;
     a.wait_ns = (unsigned long long)g_linear_w4_wait_ns;
-    CK(launch_linear_w4(a, device_sms(), (cudaStream_t)stream));
+    if (M <= kLw4MaxM) {
+        CK(launch_linear_w4(a, device_sms(), (cudaStream_t)stream));
+        return BLOOM_OK;
+    }
+    const size_t need = linear_w4_tc_workspace(M, w->k);
+    if (!workspace || workspace_bytes < need || !aligned16(workspace))
+        return fail(BLOOM_E_INVALID, "workspace: %zu bytes of %zu, 16-byte aligned", workspace_bytes, need);
+    CK(launch_linear_w4_tc(a, workspace, device_sms(), (cudaStream_t)stream));
     return BLOOM_OK;
 }
 

@@ -1,0 +1,440 @@
+// Linear layer over 4-bit weights for more tokens than k_linear_w4.cu takes, on the
+// 5th-generation tensor cores: y[m][n] = epilogue(sum_k code[n][k] scale[n][k / group] x[m][k] +
+// bias[n]).
+//
+// mma.sync has 957 multiply-adds a clock and SM here, so from about 10 tokens on it, and
+// not the weights, would be what the time is made of (32 tokens, 16384 x 4096: 31 us with it, 5.4
+// for the weights).  tcgen05.mma has 8192:
+//  * W is the 128-row A operand, taken from TMEM: the tiles come by bulk copies, and warps
+//    turn a word of eight codes into f16 pairs (w4_ops.cuh, 7 instructions) that tcgen05.st of
+//    16x256b shape stores as they lie, for its registers are dealt to rows and columns as
+//    those of an mma.sync fragment.
+//  * The tokens are the N operand: f16 after a power of two for each token, in the order and
+//    swizzle of the shared-memory operand, so that a block of 256 columns is one bulk copy.
+//    A small kernel before this one lays them out (done here, the conversion would
+//    be repeated by every tile of rows: 100 instructions for a tile's 240).
+//  * A group's products make an accumulator of their own, in one of two TMEM buffers; four
+//    warps, a thread a row, add it times the row's scale to float32 sums in registers.
+//  * Few tiles of rows: the columns are split over a cluster, whose sums meet through
+//    distributed shared memory, in rank order.
+// Weights are loaded before the wait for the kernel before: that is the one that lays out
+// the tokens, and it starts its successors only after its own wait, when all work before it is done.
+#include <atomic>
+#include <math.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "tc_ops.cuh"
+#include "w4_ops.cuh"
+
+namespace bloom {
+
+constexpr int kLtRows = 128, kLtTiles = kLtRows / kW4Rows;
+constexpr int kLtThreads = 320;      // producer, MMA issuer, 4 scaling warps, 4 widening warps
+constexpr int kLtMaxSplits = 8;
+constexpr int kLtSteps = kW4Cols / 16;
+
+template <int NT, int G>
+struct LtCfg {
+    static constexpr int kTile = w4_tile_bytes(G), kX = NT * kW4Cols * 2, kW = (kLtTiles * kTile + 1023) / 1024 * 1024;
+    static constexpr int kStage = kX + kW, kPerSm = NT == 64 ? 1 : 2;
+    static constexpr int kStages = (kPerSm == 1 ? 216 : 104) * 1024 / kStage;
+    static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
+    static constexpr uint32_t kD = 128;   // TMEM columns: two A buffers of 128 columns of weights each, then two of sums
+    static_assert(kD + 2 * NT <= 256, "TMEM");
+    static_assert((NT / 4 + kLtMaxSplits) * kLtRows * 16 <= kStages * kStage, "room for the cluster's sums");
+};
+
+// Where a token's elements lie in a block of 256 columns: four boxes of 64 columns, rows of 128
+// bytes (a token each), 16-byte pieces swizzled by the row.  A product of 16 columns takes, as the weights'
+// fragments have it, place 4 q + i of product 2 j + o from column 32 j + 8 q + 4 o + i.
+__global__ void __launch_bounds__(256) w4_tokens_kernel(const uint16_t *x, long long ldx, int M, int K, int NT, int k_tiles,
+                                                        unsigned char *image, float *inv) {
+    __shared__ uint32_t red[8];
+    griddep_wait();
+    griddep_launch();
+    const int n = blockIdx.x, m = blockIdx.y * NT + n, tid = threadIdx.x;
+    const uint16_t *row = x + (long long)m * ldx;
+    uint32_t m2 = 0;
+    if (m < M)
+        for (int k = 8 * tid; k < K; k += 8 * 256) {
+            const uint4 v = ld_act(row + k);
+            m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+        }
+    uint32_t amax = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
+    if ((tid & 31) == 0) red[tid >> 5] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = max(amax, red[i]);
+    // 2^up brings the largest element to [2^14, 2^15); an infinity or NaN makes the token NaN
+    const int up = min(120, 14 + 127 - (int)(amax >> 7));
+    const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
+    if (tid == 0)
+        inv[m] = amax >= 0x7f80u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(127 - up) << 23);
+    image += (size_t)blockIdx.y * k_tiles * NT * 512;
+    for (int p = tid; p < k_tiles * 32; p += 256) {   // 16-byte pieces: block p / 32, box, piece
+        const int box = p / 8, c = p & 7;
+        const int k = 64 * box + 32 * (c >> 2) + 16 * (c & 1) + 4 * ((c >> 1) & 1);
+        uint32_t o[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint2 v = make_uint2(0u, 0u);
+            if (m < M && k + 8 * h < K) v = __ldg(reinterpret_cast<const uint2 *>(row + k + 8 * h));
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[2 * h]) : "f"(bf_hi(v.x) * mul), "f"(bf_lo(v.x) * mul));
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[2 * h + 1]) : "f"(bf_hi(v.y) * mul), "f"(bf_lo(v.y) * mul));
+        }
+        *reinterpret_cast<uint4 *>(image + ((size_t)(box / 4) * 4 + box % 4) * NT * 128 + n * 128 + ((c ^ (n & 7)) << 4)) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+__device__ __forceinline__ void lt_bulk(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(tc_smem(dst)),
+                 "l"(src), "r"(bytes), "r"(tc_smem(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void lt_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc_smem(bar)) : "memory");
+}
+__device__ __forceinline__ void lt_cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// 16 rows x 64 32-bit columns; registers as fragments of 16 x 8: lane (g, q) holds of rows g and g + 8
+// columns 2 q and 2 q + 1.
+__device__ __forceinline__ void lt_store_a(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+        "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+        "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+        "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void lt_store(const LinearW4Args &a, int m, int n, float bias, float v) {
+    v += bias;
+    if (a.epi == EPI_GELU) v = gelu_tanh(v);
+    const long long at = m * a.ldy + n;
+    if (a.f32) {
+        float *y = static_cast<float *>(a.y) + at;
+        *y = a.epi == EPI_RESID ? *y + v : v;
+    } else {
+        uint16_t *y = static_cast<uint16_t *>(a.y) + at;
+        *y = f2bf(a.epi == EPI_RESID ? bf2f(*y) + v : v);
+    }
+}
+
+template <int NT, int G>
+__global__ void __launch_bounds__(kLtThreads, LtCfg<NT, G>::kPerSm) linear_w4_tc_kernel(const LinearW4Args a) {
+    using C = LtCfg<NT, G>;
+    constexpr int TB = C::kTile, ST = C::kStages, SG = kW4Cols / G, GS = G / 16;   // groups of a block, products of a group
+    extern __shared__ unsigned char lt_raw[];
+    unsigned char *smem = lt_raw + ((0u - tc_smem(lt_raw)) & 1023u);
+    __shared__ uint64_t full[ST], empty[ST], a_full[2], a_empty[2], d_full[2], d_empty[2], done;
+    __shared__ uint32_t tmem_base;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tile = blockIdx.x, split = blockIdx.y, S = (int)gridDim.y, m0 = (int)blockIdx.z * NT;
+    const int kb0 = (int)((long long)a.k_tiles * split / S), my_kb = (int)((long long)a.k_tiles * (split + 1) / S) - kb0;
+    const int here = min(kLtTiles, a.row_tiles - tile * kLtTiles);   // tiles of rows that there are
+
+    if (tid == 0) {
+        for (int s = 0; s < ST; ++s) {
+            tc_mbar_init(&full[s], 1);
+            tc_mbar_init(&empty[s], 4 + 4 + 1);   // widening warps, scaling warps, the products' commit
+        }
+        for (int b = 0; b < 2; ++b) {
+            tc_mbar_init(&a_full[b], 4);
+            tc_mbar_init(&a_empty[b], 1);
+            tc_mbar_init(&d_full[b], 1);
+            tc_mbar_init(&d_empty[b], 4);
+        }
+        tc_mbar_init(&done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;" ::"r"(tc_smem(&tmem_base)));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = tmem_base;
+    griddep_launch();
+
+    const int quarter = warp & 3;
+    const uint32_t tquarter = tmem + ((uint32_t)(quarter * 32) << 16);
+    float acc[NT];                   // scaling warps: this thread's row
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[i] = 0.f;
+    bool ok = true;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---- copies: the weights of the first stages before the wait for the tokens
+            const uint32_t bytes = (uint32_t)(here * TB);
+            const unsigned char *wsrc = a.tiles + ((long long)kb0 * a.row_tiles + tile * kLtTiles) * TB;
+            const unsigned char *xsrc = a.image + ((size_t)blockIdx.z * a.k_tiles + kb0) * C::kX;
+            auto weights = [&](int i, int s) {
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(tc_smem(&full[s])), "r"(bytes + C::kX) : "memory");
+                lt_bulk(smem + (size_t)s * C::kStage + C::kX, wsrc + (long long)i * a.row_tiles * TB, bytes, &full[s]);
+            };
+            auto tokens = [&](int i, int s) { lt_bulk(smem + (size_t)s * C::kStage, xsrc + (size_t)i * C::kX, C::kX, &full[s]); };
+            const int pre = min(my_kb, ST);
+            for (int i = 0; i < pre; ++i) weights(i, i);
+            griddep_wait();
+            for (int i = 0; i < pre; ++i) tokens(i, i);
+            int issued = pre;
+            for (int i = pre; i < my_kb && ok; ++i) {
+                const int s = i % ST;
+                ok = tc_mbar_wait_within(&empty[s], (uint32_t)((i / ST & 1) ^ 1), a.wait_ns);
+                if (!ok) break;
+                weights(i, s);
+                tokens(i, s);
+                ++issued;
+            }
+            for (int j = 0; j < ST && j < issued; ++j) {   // no copy lands after the CTA has ended
+                const int i = issued - 1 - j;
+                ok &= tc_mbar_wait(&full[i % ST], (uint32_t)(i / ST & 1), kTcWaitNs);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ---- products
+            constexpr uint32_t idesc = tc_idesc(kLtRows, NT, true);
+            int d = 0;
+            for (int i = 0; i < my_kb && ok; ++i) {
+                const int s = i % ST;
+                ok = tc_mbar_wait_within(&full[s], (uint32_t)(i / ST & 1), a.wait_ns);
+                const uint32_t sx = tc_smem(smem + (size_t)s * C::kStage);
+                for (int hb = 0; hb < 2 && ok; ++hb) {
+                    const int h = 2 * i + hb;
+                    ok = tc_mbar_wait_within(&a_full[h & 1], (uint32_t)(h >> 1 & 1), a.wait_ns);
+                    if (!ok) break;
+#pragma unroll
+                    for (int gr = 0; gr < SG / 2; ++gr, ++d) {
+                        if (d >= 2) ok = ok && tc_mbar_wait_within(&d_empty[d & 1], (uint32_t)(((d >> 1) - 1) & 1), a.wait_ns);
+                        if (!ok) break;
+                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll
+                        for (int k = 0; k < GS; ++k) {
+                            const int step = gr * GS + k, at = hb * (kLtSteps / 2) + step;
+                            tc_mma_tmem_a(tmem + C::kD + (uint32_t)((d & 1) * NT), tmem + (uint32_t)((h & 1) * 64 + 8 * step),
+                                          tc_desc(sx + (uint32_t)(at / 4 * NT * 128)) + (uint64_t)(2 * (at % 4)), idesc, k > 0 ? 1u : 0u);
+                        }
+                        tc_commit(&d_full[d & 1]);
+                    }
+                    if (ok) tc_commit(&a_empty[h & 1]);
+                }
+                if (ok) tc_commit(&empty[s]);
+            }
+            tc_commit(&done);        // all have finished before TMEM is freed, on every path
+            ok &= tc_mbar_wait(&done, 0, kTcWaitNs);
+        }
+    } else if (warp < 6) {
+        // ---- sums: a thread a row
+        const int r = quarter * 32 + lane, rr = r & 15;
+        for (int i = 0; i < my_kb && ok; ++i) {
+            const int s = i % ST;
+            ok = __all_sync(0xffffffffu, tc_mbar_wait_within(&full[s], (uint32_t)(i / ST & 1), a.wait_ns));
+            if (!ok) break;
+            const unsigned char *sc = smem + (size_t)s * C::kStage + C::kX + (r >> 4) * TB + 2048 + (rr & 7) * 4 + (rr >> 3) * 2;
+            float scale[SG];
+#pragma unroll
+            for (int gr = 0; gr < SG; ++gr) scale[gr] = bf2f(*reinterpret_cast<const uint16_t *>(sc + gr * 32));
+            __syncwarp();
+            if (lane == 0) lt_arrive(&empty[s]);
+#pragma unroll
+            for (int gr = 0; gr < SG; ++gr) {
+                const int d = i * SG + gr;
+                ok = ok && __all_sync(0xffffffffu, tc_mbar_wait_within(&d_full[d & 1], (uint32_t)(d >> 1 & 1), a.wait_ns));
+                if (!ok) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll
+                for (int c = 0; c < NT; c += 16) {
+                    float v[16];
+                    tc_ld16(tquarter + C::kD + (uint32_t)((d & 1) * NT + c), v);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) acc[c + j] = fmaf(scale[gr], v[j], acc[c + j]);
+                }
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) lt_arrive(&d_empty[d & 1]);
+            }
+        }
+        if (!ok) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i) acc[i] = __uint_as_float(0x7fc00000u);
+        }
+    } else {
+        // ---- codes to f16 in TMEM, 128 columns at a time: two tiles of rows a warp
+        for (int i = 0; i < my_kb && ok; ++i) {
+            const int s = i % ST;
+            ok = __all_sync(0xffffffffu, tc_mbar_wait_within(&full[s], (uint32_t)(i / ST & 1), a.wait_ns));
+            if (!ok) break;
+            const unsigned char *tiles = smem + (size_t)s * C::kStage + C::kX + 2 * quarter * TB + lane * 16;
+#pragma unroll
+            for (int hb = 0; hb < 2; ++hb) {
+                const int h = 2 * i + hb;
+                uint4 v[2][2];
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) v[t][c] = *reinterpret_cast<const uint4 *>(tiles + t * TB + (2 * hb + c) * 512);
+                if (h >= 2) ok = ok && __all_sync(0xffffffffu, tc_mbar_wait_within(&a_empty[h & 1], (uint32_t)(((h >> 1) - 1) & 1), a.wait_ns));
+                if (!ok) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    uint32_t r[32];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t w0 = (&v[t][j >> 1].x)[2 * (j & 1)], w1 = (&v[t][j >> 1].x)[2 * (j & 1) + 1];
+#pragma unroll
+                        for (int o = 0; o < 2; ++o) {
+                            r[8 * j + 4 * o] = w4_pair(w0, 2 * o);
+                            r[8 * j + 4 * o + 1] = w4_pair(w0, 2 * o + 1);
+                            r[8 * j + 4 * o + 2] = w4_pair(w1, 2 * o);
+                            r[8 * j + 4 * o + 3] = w4_pair(w1, 2 * o + 1);
+                        }
+                    }
+                    lt_store_a(tquarter + ((uint32_t)(16 * t) << 16) + (uint32_t)((h & 1) * 64), r);
+                }
+                tc_wait_st();
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) lt_arrive(&a_full[h & 1]);
+            }
+            if (!ok) break;
+            if (lane == 0) lt_arrive(&empty[s]);
+        }
+    }
+    if (!ok && a.err) atomicOr(a.err, kErrTimeout);
+    __syncwarp();
+
+    // ---- the codes' 2^-16 back, the activations' power of two, and the epilogue
+    const bool sums = warp >= 2 && warp < 6;
+    const int r = quarter * 32 + lane, n = tile * kLtRows + r, mmax = min(a.M - m0, NT);
+    griddep_wait();                  // the tokens' powers, y
+    float bias = 0.f;
+    if (sums) {
+        if (a.bias && n < a.N) bias = bf2f(a.bias[n]);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) acc[i] = acc[i] * 0x1p16f * a.inv[m0 + i];
+    }
+    if (S == 1) {
+        if (sums && n < a.N) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+                if (i < mmax) lt_store(a, m0 + i, n, bias, acc[i]);
+        }
+    } else {
+        // Four tokens at a time to the rank that finishes them, into its ring: [split][row][its groups]
+        const int groups = (mmax + 3) / 4, each = (groups + S - 1) / S;
+        float4 *recv = reinterpret_cast<float4 *>(smem);
+        lt_cluster_sync();           // every rank's ring is idle
+        if (sums) {
+#pragma unroll
+            for (int q = 0; q < NT / 4; ++q) {
+                if (q >= groups) break;
+                uint32_t there;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                             : "=r"(there)
+                             : "r"(tc_smem(recv + (split * kLtRows + r) * each + q / S)), "r"(q % S));
+                asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(there), "f"(acc[4 * q]), "f"(acc[4 * q + 1]),
+                             "f"(acc[4 * q + 2]), "f"(acc[4 * q + 3])
+                             : "memory");
+            }
+        }
+        lt_cluster_sync();
+        if (sums && n < a.N) {
+            for (int l = 0; l < each; ++l) {
+                const int q = l * S + split;
+                if (q >= groups) break;
+                float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int p = 0; p < S; ++p) {
+                    const float4 v = recv[(p * kLtRows + r) * each + l];
+                    t.x += v.x;
+                    t.y += v.y;
+                    t.z += v.z;
+                    t.w += v.w;
+                }
+                const float f[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (4 * q + j < mmax) lt_store(a, m0 + 4 * q + j, n, bias, f[j]);
+            }
+        }
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    if (warp == 0) {
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(tmem));
+    }
+}
+
+static int lt_tokens(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
+
+size_t linear_w4_tc_workspace(int M, int K) {
+    const int NT = lt_tokens(M), blocks = (M + NT - 1) / NT, k_tiles = (K + kW4Cols - 1) / kW4Cols;
+    return (size_t)blocks * NT * ((size_t)k_tiles * kW4Cols * 2 + 4);
+}
+
+template <int NT, int G>
+static cudaError_t lt_launch(LinearW4Args a, void *workspace, int sms, cudaStream_t s) {
+    using C = LtCfg<NT, G>;
+    constexpr int kDevices = 64;
+    static std::atomic<bool> ready[kDevices];
+    const auto kern = linear_w4_tc_kernel<NT, G>;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= kDevices) return cudaErrorInvalidDevice;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+        if (e != cudaSuccess) return e;
+        ready[dev].store(true, std::memory_order_release);
+    }
+    const int tiles = (a.row_tiles + kLtTiles - 1) / kLtTiles, blocks = (a.M + NT - 1) / NT;
+    unsigned char *image = static_cast<unsigned char *>(workspace);
+    float *inv = reinterpret_cast<float *>(image + (size_t)blocks * a.k_tiles * C::kX);
+    a.image = image;
+    a.inv = inv;
+    e = launch_pdl(w4_tokens_kernel, dim3(NT, (unsigned)blocks), dim3(256), s, a.x, a.ldx, a.M, a.K, NT, a.k_tiles, image, inv);
+    if (e != cudaSuccess) return e;
+    // as many splits as leave all CTAs resident at once
+    int S = 1;
+    while (S < kLtMaxSplits && (long long)tiles * (S + 1) <= (long long)sms * C::kPerSm && S + 1 <= a.k_tiles) ++S;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)tiles, (unsigned)S, (unsigned)blocks);
+    cfg.blockDim = dim3(kLtThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = g_pdl ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1;
+    attr[1].val.clusterDim.y = (unsigned)S;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+template <int G>
+static cudaError_t lt_launch_tokens(const LinearW4Args &a, void *workspace, int sms, cudaStream_t s) {
+    if (a.M <= 16) return lt_launch<16, G>(a, workspace, sms, s);
+    if (a.M <= 32) return lt_launch<32, G>(a, workspace, sms, s);
+    return lt_launch<64, G>(a, workspace, sms, s);
+}
+
+cudaError_t launch_linear_w4_tc(LinearW4Args a, void *workspace, int sms, cudaStream_t s) {
+    a.row_tiles = (a.N + kW4Rows - 1) / kW4Rows;
+    a.k_tiles = (a.K + kW4Cols - 1) / kW4Cols;
+    return a.group == 32 ? lt_launch_tokens<32>(a, workspace, sms, s)
+                         : a.group == 64 ? lt_launch_tokens<64>(a, workspace, sms, s) : lt_launch_tokens<128>(a, workspace, sms, s);
+}
+
+}  // namespace bloom

@@ -336,12 +336,18 @@ struct LinearW4Args {
     unsigned long long wait_ns = 0;    // bound of its waits (0: about 2 s)
     // set by the launch
     int row_tiles = 0, k_tiles = 0;
+    const unsigned char *image = nullptr;   // more than kLw4MaxM tokens: laid out in the workspace,
+    const float *inv = nullptr;             // and their powers of two
     int cluster = 1, passes = 1;       // CTAs that share rows of tiles; times each takes them
     int k_warps = 0, row_warps = 0;    // warps side by side on a row of tiles; rows at a time
     int chunk = 0;                     // tiles of a warp between two joints of a cluster's sums
     int wide = 0;                      // y takes four neighbouring rows at once
 };
-cudaError_t launch_linear_w4(LinearW4Args a, int sms, cudaStream_t s);
+constexpr int kLw4MaxM = 8;
+cudaError_t launch_linear_w4(LinearW4Args a, int sms, cudaStream_t s);      // M <= kLw4MaxM
+// More tokens (k_linear_w4_tc.cu); workspace of linear_w4_tc_workspace() bytes, 1024-byte aligned.
+cudaError_t launch_linear_w4_tc(LinearW4Args a, void *workspace, int sms, cudaStream_t s);
+size_t linear_w4_tc_workspace(int M, int K);
 
 struct AttnPrefillArgs {
     const uint16_t *q = nullptr;     // [B*T][n][d], prompt i's tokens at rows i*T ..

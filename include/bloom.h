@@ -592,7 +592,13 @@ bloom_status bloom_op_w4_read(const bloom_w4 *in, void *w, int64_t ld, void *str
  * that depend on it are NaN. */
 bloom_status bloom_op_linear_w4(const bloom_w4 *w, const void *x, int64_t ldx, int32_t M,
                                 const void *bias, int32_t epilogue, void *y, int64_t ldy,
-                                int32_t y_f32, int32_t *flag, void *stream);
+                                int32_t y_f32, void *workspace, size_t workspace_bytes,
+                                int32_t *flag, void *stream);
+
+/* Bytes of workspace that a call with M tokens needs (16-byte aligned device memory, its
+ * content meaningless before and after; calls whose work overlaps need one each): 0 up to
+ * 8 tokens, and on bad arguments. */
+size_t bloom_op_linear_w4_workspace(const bloom_w4 *w, int32_t M);
 
 /* Bound of the waits of this thread's calls of bloom_op_linear_w4 from now on, in
  * nanoseconds; 0 (the default): about two seconds. */
