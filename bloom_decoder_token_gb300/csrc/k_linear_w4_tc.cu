@@ -30,7 +30,7 @@
 namespace bloom {
 
 constexpr int kLtRows = 128, kLtTiles = kLtRows / kW4Rows;
-constexpr int kLtThreads = 320;      // producer, MMA issuer, 4 scaling warps, 4 widening warps
+constexpr int kLtThreads = 448;      // producer, MMA issuer, 4 scaling warps, 8 widening warps
 constexpr int kLtMaxSplits = 8;
 constexpr int kLtSteps = kW4Cols / 16;
 
@@ -40,8 +40,9 @@ struct LtCfg {
     static constexpr int kStage = kX + kW, kPerSm = NT == 64 ? 1 : 2;
     static constexpr int kStages = (kPerSm == 1 ? 216 : 104) * 1024 / kStage;
     static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
-    static constexpr uint32_t kD = 128;   // TMEM columns: two A buffers of 128 columns of weights each, then two of sums
-    static_assert(kD + 2 * NT <= 256, "TMEM");
+    static constexpr int kA = NT == 16 ? 3 : 2, kDB = NT == 64 ? 2 : 4;   // buffers; A's of 128 columns of weights, 64 of TMEM
+    static constexpr uint32_t kD = 64 * kA;                  // then two of sums
+    static_assert(kD + kDB * NT <= 256, "TMEM");
     static_assert((NT / 4 + kLtMaxSplits) * kLtRows * 16 <= kStages * kStage, "room for the cluster's sums");
 };
 
@@ -112,6 +113,19 @@ __device__ __forceinline__ void lt_store_a(uint32_t taddr, const uint32_t (&r)[3
         "r"(r[31])
         : "memory");
 }
+__device__ __forceinline__ bool lt_elect() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
+}
+// tc_mma_tmem_a with the operand's descriptor (tc_desc) by its first 14 bits.
+__device__ __forceinline__ void lt_mma(uint32_t d, uint32_t ta, uint32_t desc, uint32_t idesc, bool accumulate) {
+    constexpr uint32_t kLow = 1u << 16, kHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
+        "r"(ta), "r"(desc | kLow), "r"(kHigh), "r"(idesc), "r"((uint32_t)accumulate));
+}
 __device__ __forceinline__ void lt_store(const LinearW4Args &a, int m, int n, float bias, float v) {
     v += bias;
     if (a.epi == EPI_GELU) v = gelu_tanh(v);
@@ -131,7 +145,8 @@ __global__ void __launch_bounds__(kLtThreads, LtCfg<NT, G>::kPerSm) linear_w4_tc
     constexpr int TB = C::kTile, ST = C::kStages, SG = kW4Cols / G, GS = G / 16;   // groups of a block, products of a group
     extern __shared__ unsigned char lt_raw[];
     unsigned char *smem = lt_raw + ((0u - tc_smem(lt_raw)) & 1023u);
-    __shared__ uint64_t full[ST], empty[ST], a_full[2], a_empty[2], d_full[2], d_empty[2], done;
+    constexpr int NA = C::kA, ND = C::kDB;
+    __shared__ uint64_t full[ST], empty[ST], a_full[NA], a_empty[NA], d_full[ND], d_empty[ND], done;
     __shared__ uint32_t tmem_base;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int tile = blockIdx.x, split = blockIdx.y, S = (int)gridDim.y, m0 = (int)blockIdx.z * NT;
@@ -141,11 +156,13 @@ __global__ void __launch_bounds__(kLtThreads, LtCfg<NT, G>::kPerSm) linear_w4_tc
     if (tid == 0) {
         for (int s = 0; s < ST; ++s) {
             tc_mbar_init(&full[s], 1);
-            tc_mbar_init(&empty[s], 4 + 4 + 1);   // widening warps, scaling warps, the products' commit
+            tc_mbar_init(&empty[s], 8 + 4 + 1);   // widening warps, scaling warps, the products' commit
         }
-        for (int b = 0; b < 2; ++b) {
-            tc_mbar_init(&a_full[b], 4);
+        for (int b = 0; b < NA; ++b) {
+            tc_mbar_init(&a_full[b], 8);
             tc_mbar_init(&a_empty[b], 1);
+        }
+        for (int b = 0; b < ND; ++b) {
             tc_mbar_init(&d_full[b], 1);
             tc_mbar_init(&d_empty[b], 4);
         }
@@ -199,38 +216,57 @@ __global__ void __launch_bounds__(kLtThreads, LtCfg<NT, G>::kPerSm) linear_w4_tc
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            // ---- products
-            constexpr uint32_t idesc = tc_idesc(kLtRows, NT, true);
-            int d = 0;
-            for (int i = 0; i < my_kb && ok; ++i) {
-                const int s = i % ST;
-                ok = tc_mbar_wait_within(&full[s], (uint32_t)(i / ST & 1), a.wait_ns);
-                const uint32_t sx = tc_smem(smem + (size_t)s * C::kStage);
-                for (int hb = 0; hb < 2 && ok; ++hb) {
-                    const int h = 2 * i + hb;
-                    ok = tc_mbar_wait_within(&a_full[h & 1], (uint32_t)(h >> 1 & 1), a.wait_ns);
-                    if (!ok) break;
+        // ---- products: the warp goes along together, so that addresses stay in uniform registers (one
+        // thread alone took 130 clocks a product), and one lane issues
+        constexpr uint32_t idesc = tc_idesc(kLtRows, NT, true);
+        const uint32_t tbase = __shfl_sync(0xffffffffu, tmem, 0), sbase = __shfl_sync(0xffffffffu, tc_smem(smem), 0);
+        const bool lead = lt_elect();
+        int d = 0, s = 0, ab = 0, db = 0;
+        uint32_t sp = 0, ap = 0, dp = 1;   // the buffers' parities
+        for (int i = 0; i < my_kb && ok; ++i) {
+            ok = tc_mbar_wait_within(&full[s], sp, a.wait_ns);
+            const uint32_t desc0 = (sbase + (uint32_t)s * C::kStage) >> 4 & 0x3fffu;
 #pragma unroll
-                    for (int gr = 0; gr < SG / 2; ++gr, ++d) {
-                        if (d >= 2) ok = ok && tc_mbar_wait_within(&d_empty[d & 1], (uint32_t)(((d >> 1) - 1) & 1), a.wait_ns);
-                        if (!ok) break;
+            for (int hb = 0; hb < 2; ++hb) {
+                ok = ok && tc_mbar_wait_within(&a_full[ab], ap, a.wait_ns);
+                const uint32_t ta = tbase + (uint32_t)(ab * 64);
+#pragma unroll
+                for (int gr = 0; gr < SG / 2; ++gr) {
+                    if (d >= ND) ok = ok && tc_mbar_wait_within(&d_empty[db], dp, a.wait_ns);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (ok) {
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                        if (lead) {
+                            const uint32_t td = tbase + C::kD + (uint32_t)(db * NT);
 #pragma unroll
-                        for (int k = 0; k < GS; ++k) {
-                            const int step = gr * GS + k, at = hb * (kLtSteps / 2) + step;
-                            tc_mma_tmem_a(tmem + C::kD + (uint32_t)((d & 1) * NT), tmem + (uint32_t)((h & 1) * 64 + 8 * step),
-                                          tc_desc(sx + (uint32_t)(at / 4 * NT * 128)) + (uint64_t)(2 * (at % 4)), idesc, k > 0 ? 1u : 0u);
+                            for (int k = 0; k < GS; ++k) {
+                                const int step = gr * GS + k, at = hb * (kLtSteps / 2) + step;
+                                lt_mma(td, ta + (uint32_t)(8 * step), desc0 + (uint32_t)(at / 4 * NT * 8 + 2 * (at % 4)), idesc, k > 0);
+                            }
+                            tc_commit(&d_full[db]);
                         }
-                        tc_commit(&d_full[d & 1]);
                     }
-                    if (ok) tc_commit(&a_empty[h & 1]);
+                    ++d;
+                    if (++db == ND) {
+                        db = 0;
+                        dp ^= 1u;
+                    }
                 }
-                if (ok) tc_commit(&empty[s]);
+                if (ok && lead) tc_commit(&a_empty[ab]);
+                if (++ab == NA) {
+                    ab = 0;
+                    ap ^= 1u;
+                }
             }
-            tc_commit(&done);        // all have finished before TMEM is freed, on every path
-            ok &= tc_mbar_wait(&done, 0, kTcWaitNs);
+            if (ok && lead) tc_commit(&empty[s]);
+            if (++s == ST) {
+                s = 0;
+                sp ^= 1u;
+            }
         }
+        if (lead) tc_commit(&done);        // all have finished before TMEM is freed, on every path
+        __syncwarp();
+        ok &= tc_mbar_wait(&done, 0, kTcWaitNs);
     } else if (warp < 6) {
         // ---- sums: a thread a row
         const int r = quarter * 32 + lane, rr = r & 15;
@@ -247,19 +283,19 @@ __global__ void __launch_bounds__(kLtThreads, LtCfg<NT, G>::kPerSm) linear_w4_tc
 #pragma unroll
             for (int gr = 0; gr < SG; ++gr) {
                 const int d = i * SG + gr;
-                ok = ok && __all_sync(0xffffffffu, tc_mbar_wait_within(&d_full[d & 1], (uint32_t)(d >> 1 & 1), a.wait_ns));
+                ok = ok && __all_sync(0xffffffffu, tc_mbar_wait_within(&d_full[d % ND], (uint32_t)(d / ND & 1), a.wait_ns));
                 if (!ok) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
                 for (int c = 0; c < NT; c += 16) {
                     float v[16];
-                    tc_ld16(tquarter + C::kD + (uint32_t)((d & 1) * NT + c), v);
+                    tc_ld16(tquarter + C::kD + (uint32_t)(d % ND * NT + c), v);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) acc[c + j] = fmaf(scale[gr], v[j], acc[c + j]);
                 }
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) lt_arrive(&d_empty[d & 1]);
+                if (lane == 0) lt_arrive(&d_empty[d % ND]);
             }
         }
         if (!ok) {
@@ -267,46 +303,43 @@ __global__ void __launch_bounds__(kLtThreads, LtCfg<NT, G>::kPerSm) linear_w4_tc
             for (int i = 0; i < NT; ++i) acc[i] = __uint_as_float(0x7fc00000u);
         }
     } else {
-        // ---- codes to f16 in TMEM, 128 columns at a time: two tiles of rows a warp
+        // ---- codes to f16 in TMEM, 128 columns at a time: a warp a tile of rows
+        const int mine = 2 * quarter + (warp - 6) / 4;
         for (int i = 0; i < my_kb && ok; ++i) {
             const int s = i % ST;
             ok = __all_sync(0xffffffffu, tc_mbar_wait_within(&full[s], (uint32_t)(i / ST & 1), a.wait_ns));
             if (!ok) break;
-            const unsigned char *tiles = smem + (size_t)s * C::kStage + C::kX + 2 * quarter * TB + lane * 16;
+            const unsigned char *tile = smem + (size_t)s * C::kStage + C::kX + mine * TB + lane * 16;
+            uint4 v[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[c] = *reinterpret_cast<const uint4 *>(tile + c * 512);
+            __syncwarp();
+            if (lane == 0) lt_arrive(&empty[s]);
 #pragma unroll
             for (int hb = 0; hb < 2; ++hb) {
                 const int h = 2 * i + hb;
-                uint4 v[2][2];
+                uint32_t r[32];
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int j = 0; j < 4; ++j) {
+                    const uint4 &c = v[2 * hb + (j >> 1)];
+                    const uint32_t w0 = j & 1 ? c.z : c.x, w1 = j & 1 ? c.w : c.y;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) v[t][c] = *reinterpret_cast<const uint4 *>(tiles + t * TB + (2 * hb + c) * 512);
-                if (h >= 2) ok = ok && __all_sync(0xffffffffu, tc_mbar_wait_within(&a_empty[h & 1], (uint32_t)(((h >> 1) - 1) & 1), a.wait_ns));
+                    for (int o = 0; o < 2; ++o) {
+                        r[8 * j + 4 * o] = w4_pair(w0, 2 * o);
+                        r[8 * j + 4 * o + 1] = w4_pair(w0, 2 * o + 1);
+                        r[8 * j + 4 * o + 2] = w4_pair(w1, 2 * o);
+                        r[8 * j + 4 * o + 3] = w4_pair(w1, 2 * o + 1);
+                    }
+                }
+                if (h >= NA) ok = ok && __all_sync(0xffffffffu, tc_mbar_wait_within(&a_empty[h % NA], (uint32_t)((h / NA - 1) & 1), a.wait_ns));
                 if (!ok) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    uint32_t r[32];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t w0 = (&v[t][j >> 1].x)[2 * (j & 1)], w1 = (&v[t][j >> 1].x)[2 * (j & 1) + 1];
-#pragma unroll
-                        for (int o = 0; o < 2; ++o) {
-                            r[8 * j + 4 * o] = w4_pair(w0, 2 * o);
-                            r[8 * j + 4 * o + 1] = w4_pair(w0, 2 * o + 1);
-                            r[8 * j + 4 * o + 2] = w4_pair(w1, 2 * o);
-                            r[8 * j + 4 * o + 3] = w4_pair(w1, 2 * o + 1);
-                        }
-                    }
-                    lt_store_a(tquarter + ((uint32_t)(16 * t) << 16) + (uint32_t)((h & 1) * 64), r);
-                }
+                lt_store_a(tquarter + ((uint32_t)(16 * (mine & 1)) << 16) + (uint32_t)(h % NA * 64), r);
                 tc_wait_st();
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) lt_arrive(&a_full[h & 1]);
+                if (lane == 0) lt_arrive(&a_full[h % NA]);
             }
-            if (!ok) break;
-            if (lane == 0) lt_arrive(&empty[s]);
         }
     }
     if (!ok && a.err) atomicOr(a.err, kErrTimeout);
