@@ -118,6 +118,19 @@ __device__ __forceinline__ bool lt_elect() {
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
     return r != 0;
 }
+// Waits for three phases at once: three tests in flight together where all have come to pass.
+__device__ __forceinline__ bool lt_wait3(uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1, uint64_t *b2, uint32_t p2,
+                                         unsigned long long limit_ns) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q, r;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n mbarrier.test_wait.parity.shared::cta.b64 r, [%5], %6;\n"
+        " and.pred p, p, q;\n and.pred p, p, r;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(r)
+        : "r"(tc_smem(b0)), "r"(p0), "r"(tc_smem(b1)), "r"(p1), "r"(tc_smem(b2)), "r"(p2)
+        : "memory");
+    return r || (tc_mbar_wait_within(b0, p0, limit_ns) && tc_mbar_wait_within(b1, p1, limit_ns) && tc_mbar_wait_within(b2, p2, limit_ns));
+}
 // tc_mma_tmem_a with the operand's descriptor (tc_desc) by its first 14 bits.
 __device__ __forceinline__ void lt_mma(uint32_t d, uint32_t ta, uint32_t desc, uint32_t idesc, bool accumulate) {
     constexpr uint32_t kLow = 1u << 16, kHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
@@ -221,33 +234,38 @@ __global__ void __launch_bounds__(kLtThreads, LtCfg<NT, G>::kPerSm) linear_w4_tc
         constexpr uint32_t idesc = tc_idesc(kLtRows, NT, true);
         const uint32_t tbase = __shfl_sync(0xffffffffu, tmem, 0), sbase = __shfl_sync(0xffffffffu, tc_smem(smem), 0);
         const bool lead = lt_elect();
-        int d = 0, s = 0, ab = 0, db = 0;
+        // groups at a time: a half block's, of half of the accumulators at most
+        constexpr int BG = SG / 2 < ND / 2 ? SG / 2 : ND / 2;
+        static_assert(ND % BG == 0 && SG / 2 % BG == 0, "groups at a time");
+        int s = 0, ab = 0, db = 0;
         uint32_t sp = 0, ap = 0, dp = 1;   // the buffers' parities
         for (int i = 0; i < my_kb && ok; ++i) {
-            ok = tc_mbar_wait_within(&full[s], sp, a.wait_ns);
             const uint32_t desc0 = (sbase + (uint32_t)s * C::kStage) >> 4 & 0x3fffu;
 #pragma unroll
             for (int hb = 0; hb < 2; ++hb) {
-                ok = ok && tc_mbar_wait_within(&a_full[ab], ap, a.wait_ns);
-                const uint32_t ta = tbase + (uint32_t)(ab * 64);
 #pragma unroll
-                for (int gr = 0; gr < SG / 2; ++gr) {
-                    if (d >= ND) ok = ok && tc_mbar_wait_within(&d_empty[db], dp, a.wait_ns);
+                for (int g0 = 0; g0 < SG / 2; g0 += BG) {
+                    // what the next groups need, in one round trip; the accumulators come free in order
+                    uint64_t *const last = &d_empty[db + BG - 1];
+                    ok = ok && lt_wait3(hb == 0 && g0 == 0 ? &full[s] : last, hb == 0 && g0 == 0 ? sp : dp, g0 == 0 ? &a_full[ab] : last,
+                                        g0 == 0 ? ap : dp, last, dp, a.wait_ns);
                     ok = __all_sync(0xffffffffu, ok);
                     if (ok) {
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                         if (lead) {
-                            const uint32_t td = tbase + C::kD + (uint32_t)(db * NT);
 #pragma unroll
-                            for (int k = 0; k < GS; ++k) {
-                                const int step = gr * GS + k, at = hb * (kLtSteps / 2) + step;
-                                lt_mma(td, ta + (uint32_t)(8 * step), desc0 + (uint32_t)(at / 4 * NT * 8 + 2 * (at % 4)), idesc, k > 0);
+                            for (int gr = g0; gr < g0 + BG; ++gr) {
+                                const uint32_t td = tbase + C::kD + (uint32_t)((db + gr - g0) * NT), ta = tbase + (uint32_t)(ab * 64);
+#pragma unroll
+                                for (int k = 0; k < GS; ++k) {
+                                    const int step = gr * GS + k, at = hb * (kLtSteps / 2) + step;
+                                    lt_mma(td, ta + (uint32_t)(8 * step), desc0 + (uint32_t)(at / 4 * NT * 8 + 2 * (at % 4)), idesc, k > 0);
+                                }
+                                tc_commit(&d_full[db + gr - g0]);
                             }
-                            tc_commit(&d_full[db]);
                         }
                     }
-                    ++d;
-                    if (++db == ND) {
+                    if ((db += BG) == ND) {
                         db = 0;
                         dp ^= 1u;
                     }
