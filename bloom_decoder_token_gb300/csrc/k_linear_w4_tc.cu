@@ -161,6 +161,7 @@ __global__ void __launch_bounds__(kLtThreads, LtCfg<NT, G>::kPerSm) linear_w4_tc
     constexpr int NA = C::kA, ND = C::kDB;
     __shared__ uint64_t full[ST], empty[ST], a_full[NA], a_empty[NA], d_full[ND], d_empty[ND], done;
     __shared__ uint32_t tmem_base;
+    __shared__ float s_inv[NT];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int tile = blockIdx.x, split = blockIdx.y, S = (int)gridDim.y, m0 = (int)blockIdx.z * NT;
     const int kb0 = (int)((long long)a.k_tiles * split / S), my_kb = (int)((long long)a.k_tiles * (split + 1) / S) - kb0;
@@ -197,6 +198,7 @@ __global__ void __launch_bounds__(kLtThreads, LtCfg<NT, G>::kPerSm) linear_w4_tc
     float acc[NT];                   // scaling warps: this thread's row
 #pragma unroll
     for (int i = 0; i < NT; ++i) acc[i] = 0.f;
+    float bias = 0.f;
     bool ok = true;
 
     if (warp == 0) {
@@ -234,6 +236,8 @@ __global__ void __launch_bounds__(kLtThreads, LtCfg<NT, G>::kPerSm) linear_w4_tc
         constexpr uint32_t idesc = tc_idesc(kLtRows, NT, true);
         const uint32_t tbase = __shfl_sync(0xffffffffu, tmem, 0), sbase = __shfl_sync(0xffffffffu, tc_smem(smem), 0);
         const bool lead = lt_elect();
+        griddep_wait();
+        for (int n = lane; n < NT; n += 32) s_inv[n] = a.inv[m0 + n];
         // groups at a time: a half block's, of half of the accumulators at most
         constexpr int BG = SG / 2 < ND / 2 ? SG / 2 : ND / 2;
         static_assert(ND % BG == 0 && SG / 2 % BG == 0, "groups at a time");
@@ -288,6 +292,8 @@ __global__ void __launch_bounds__(kLtThreads, LtCfg<NT, G>::kPerSm) linear_w4_tc
     } else if (warp < 6) {
         // ---- sums: a thread a row
         const int r = quarter * 32 + lane, rr = r & 15;
+        griddep_wait();
+        if (a.bias && tile * kLtRows + r < a.N) bias = bf2f(a.bias[tile * kLtRows + r]);
         for (int i = 0; i < my_kb && ok; ++i) {
             const int s = i % ST;
             ok = __all_sync(0xffffffffu, tc_mbar_wait_within(&full[s], (uint32_t)(i / ST & 1), a.wait_ns));
@@ -363,15 +369,13 @@ __global__ void __launch_bounds__(kLtThreads, LtCfg<NT, G>::kPerSm) linear_w4_tc
     if (!ok && a.err) atomicOr(a.err, kErrTimeout);
     __syncwarp();
 
-    // ---- the codes' 2^-16 back, the activations' power of two, and the epilogue
+    // ---- the activations' power of two, and the epilogue
     const bool sums = warp >= 2 && warp < 6;
     const int r = quarter * 32 + lane, n = tile * kLtRows + r, mmax = min(a.M - m0, NT);
-    griddep_wait();                  // the tokens' powers, y
-    float bias = 0.f;
+    __syncthreads();                 // the tokens' powers
     if (sums) {
-        if (a.bias && n < a.N) bias = bf2f(a.bias[n]);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) acc[i] = acc[i] * 0x1p16f * a.inv[m0 + i];
+        for (int i = 0; i < NT; ++i) acc[i] = acc[i] * 0x1p16f * s_inv[i];   // and the codes' 2^-16 back
     }
     if (S == 1) {
         if (sums && n < a.N) {
