@@ -16,7 +16,7 @@
 //  * A warp owns 256 columns, whose activations stay in its registers, and goes down the
 //    matrix: tile after tile of 16 rows, by bulk copies into a ring of its own.  The
 //    warps of a CTA that share the rows hold the CTA's columns together; their sums
-//    meet in shared memory, in the warps' order, once a row of tiles.
+//    meet in shared memory, in the warps' order, every 32 rows.
 //  * Longer rows are split over the CTAs of a cluster, whose sums meet through distributed
 //    shared memory, in rank order; still longer ones are taken in passes.
 #include <atomic>
@@ -31,20 +31,17 @@ namespace bloom {
 
 constexpr int kLw4Warps = 16;
 constexpr int kLw4Unit = 2;                      // tiles of a step: 32 rows
-constexpr int kLw4Buffers = 2;                   // steps whose sums are on their way
 constexpr int kLw4Partial = 16384;               // bytes of a buffer of sums that wait for the cluster
 constexpr int kLw4Stride = 20;                   // floats of a token's 16 rows in a warp's sums: no bank twice
 constexpr int kLw4MaxCluster = 8;
 
-// NT: column tiles of a warp, eight tokens each; TW: warps that share tiles, each with tokens of its own.
-template <int NT, int TW, int G>
+template <int G>
 struct Lw4Smem {
-    static constexpr int kSlots = kLw4Warps / TW, kStages = (NT == 1 ? 4 : 3) * TW, kTile = w4_tile_bytes(G);
-    static constexpr int kTokens = 8 * NT * TW, kSum = kTokens * kLw4Stride;   // floats of a tile's sums
-    static constexpr int kSums = kSlots * kLw4Unit * kSum;                     // of a buffer
-    static constexpr int kRing = kSlots * kStages * kTile;
-    static constexpr int kBars = kSlots * kStages + 2 * kLw4Buffers;
-    static constexpr int kBytes = kRing + 4 * kLw4Buffers * kSums + 2 * kLw4Partial + 8 * kBars;
+    static constexpr int kStages = 4, kTile = w4_tile_bytes(G);
+    static constexpr int kSum = kLw4MaxM * kLw4Stride;                 // floats of a row of tiles' sums
+    static constexpr int kSums = kLw4Warps * kLw4Unit * kSum;          // of one of the two buffers
+    static constexpr int kRing = kLw4Warps * kStages * kTile;
+    static constexpr int kBytes = kRing + 8 * kSums + 2 * kLw4Partial + 8 * kLw4Warps * kStages;
     static_assert(kBytes <= 227 * 1024, "shared memory of an SM");
 };
 
@@ -64,9 +61,6 @@ __device__ __forceinline__ void lw4_bulk(void *dst, const void *src, uint32_t by
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(tc_smem(dst)),
                  "l"(src), "r"(bytes), "r"(tc_smem(bar))
                  : "memory");
-}
-__device__ __forceinline__ void lw4_arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc_smem(bar)) : "memory");
 }
 __device__ __forceinline__ void lw4_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -109,43 +103,34 @@ __device__ __forceinline__ void lw4_store(const LinearW4Args &a, int m, int row,
     }
 }
 
-template <int NT, int TW, int G>
+template <int G>
 __global__ void __launch_bounds__(32 * kLw4Warps, 1) linear_w4_kernel(const LinearW4Args a) {
-    using Smem = Lw4Smem<NT, TW, G>;
-    constexpr int NW = kLw4Warps, ST = Smem::kStages, TB = Smem::kTile, THREADS = 32 * NW, UT = kLw4Unit;
-    constexpr int NB = kLw4Buffers, TOKENS = Smem::kTokens, SG = kW4Cols / G;
+    using Smem = Lw4Smem<G>;
+    constexpr int NW = kLw4Warps, ST = Smem::kStages, TB = Smem::kTile, THREADS = 32 * NW, UT = kLw4Unit, SG = kW4Cols / G;
     extern __shared__ __align__(128) unsigned char lw4_smem[];
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, q = lane & 3;
-    const int ks = w / TW, tw = w - ks * TW;   // place among the tiles' warps, among the tokens'
-    unsigned char *ring = lw4_smem + ks * ST * TB;
-    float *sums = reinterpret_cast<float *>(lw4_smem + Smem::kRing);              // [NB][slots][UT][TOKENS][kLw4Stride]
-    float *part = sums + NB * Smem::kSums;                                        // [2][tiles][TOKENS][16]
-    uint64_t *full = reinterpret_cast<uint64_t *>(part + 2 * (kLw4Partial / 4)), *empty = full + NB;
-    uint64_t *bar = empty + NB + ks * ST;
-
-    const int P = a.cluster, cl = (int)blockIdx.x / P, rank = (int)blockIdx.x - cl * P, clusters = (int)gridDim.x / P;
-    const int KW = a.k_warps, RW = a.row_warps, slot = ks / KW, kw = ks - slot * KW;
-    const int m0 = (int)blockIdx.y * TOKENS, Mt = min(a.M - m0, TOKENS);
-    const int items = RW * UT * Mt * 4, NR = min(NW, (items + 31) / 32);   // a step's sums, four rows a lane; warps for them
-    if (lane == 0 && tw == 0)
+    unsigned char *ring = lw4_smem + w * ST * TB;
+    float *sums = reinterpret_cast<float *>(lw4_smem + Smem::kRing);              // [2][NW][UT][kLw4MaxM][kLw4Stride]
+    float *part = sums + 2 * Smem::kSums;                                         // [2][tiles][kLw4MaxM][16]
+    uint64_t *bar = reinterpret_cast<uint64_t *>(part + 2 * (kLw4Partial / 4)) + w * ST;
+    if (lane == 0) {
         for (int i = 0; i < ST; ++i) tc_mbar_init(&bar[i], 1);
-    if (tid == 0)
-        for (int i = 0; i < NB; ++i) {
-            tc_mbar_init(&full[i], NW);
-            tc_mbar_init(&empty[i], NR);
-        }
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    __syncthreads();
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
+    const int P = a.cluster, cl = (int)blockIdx.x / P, rank = (int)blockIdx.x - cl * P, clusters = (int)gridDim.x / P;
+    const int KW = a.k_warps, RW = a.row_warps, slot = w / KW, kw = w - slot * KW, M = a.M;
+    const int items = RW * UT * M * 4, NR = (items + 31) / 32;   // a step's sums, four rows a lane; warps for them
     griddep_wait();
     griddep_launch();
 
     // The cluster's tiles of rows, [r0, r0 + n), in RW runs of at most `run`, one for each KW
-    // slots side by side; a slot's own: len from `row` on.
+    // warps side by side; a warp's own: len from `row` on.
     const int r0 = (int)((long long)a.row_tiles * cl / clusters), n = (int)((long long)a.row_tiles * (cl + 1) / clusters) - r0;
     const int each = n / RW, more = n - each * RW;
     auto first_of = [&](int s) { return s * each + min(s, more); };
-    // i / Mt for the products of tiles and tokens that come up, less than 2^20 / Mt
-    const uint32_t per_token = (1u << 20) / (uint32_t)Mt + 1u;
+    // i / M for the products of tiles and tokens that come up, less than 2^20 / M
+    const uint32_t per_token = (1u << 20) / (uint32_t)M + 1u;
     auto by_tokens = [&](int i) { return (int)((uint32_t)i * per_token >> 20); };
     const int run = (n + RW - 1) / RW, row = r0 + first_of(slot), len = slot < RW ? r0 + first_of(slot + 1) - row : 0;
     const bool direct = P == 1 && a.passes == 1;
@@ -169,7 +154,7 @@ __global__ void __launch_bounds__(32 * kLw4Warps, 1) linear_w4_kernel(const Line
             left = min(a.chunk, len - ahead);
             src = a.tiles + ((long long)kt * a.row_tiles + row + ahead) * TB;
         }
-        if (lane == 0 && tw == 0) {
+        if (lane == 0) {
             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(tc_smem(&bar[st])), "r"(TB) : "memory");
             lw4_bulk(ring + st * TB, src, TB, &bar[st]);
         }
@@ -180,41 +165,37 @@ __global__ void __launch_bounds__(32 * kLw4Warps, 1) linear_w4_kernel(const Line
     int flying = 0;
     for (int i = 0; i < ST; ++i) flying += issue(i);
 
-    uint32_t b[NT][8][4];   // activations: token g of a column tile, elements 32 j + 8 q + (0, 1 | 2, 3 | 4, 5 | 6, 7)
-    float inv[NT][2];       // 2^-up of tokens 2 q and 2 q + 1 of it
-    auto load_x = [&](int kt) {
+    uint32_t b[8][4];       // activations: token g, elements 32 j + 8 q + (0, 1 | 2, 3 | 4, 5 | 6, 7)
+    float inv[2];           // 2^-up of tokens 2 q and 2 q + 1
+    auto load_x = [&](int k0) {
+        const uint16_t *x = a.x + g * a.ldx + k0 + 8 * q;
+        uint32_t m2 = 0;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int token = 8 * (NT * tw + nt) + g;
-            const uint16_t *x = a.x + (m0 + token) * a.ldx + kt * kW4Cols + 8 * q;
-            uint32_t m2 = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-                if (token < Mt && kt * kW4Cols + 32 * j + 8 * q < a.K) raw = ld_act(x + 32 * j);
-                b[nt][j][0] = raw.x; b[nt][j][1] = raw.y; b[nt][j][2] = raw.z; b[nt][j][3] = raw.w;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) m2 = __vmaxu2(m2, b[nt][j][e] & 0x7fff7fffu);
-            uint32_t amax = max(m2 & 0xffffu, m2 >> 16);
-            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            // 2^up brings the largest element to [2^14, 2^15); an infinity or NaN makes the token NaN
-            const int up = min(120, 14 + 127 - (int)(amax >> 7));
-            const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
-            const float back = amax >= 0x7f80u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(127 - up) << 23);
-            inv[nt][0] = __shfl_sync(0xffffffffu, back, 8 * q);
-            inv[nt][1] = __shfl_sync(0xffffffffu, back, 8 * q + 4);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) b[nt][j][e] = lw4_f16x2(bf_lo(b[nt][j][e]) * mul, bf_hi(b[nt][j][e]) * mul);
+        for (int j = 0; j < 8; ++j) {
+            uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+            if (g < M && k0 + 32 * j + 8 * q < a.K) raw = ld_act(x + 32 * j);
+            b[j][0] = raw.x; b[j][1] = raw.y; b[j][2] = raw.z; b[j][3] = raw.w;
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m2 = __vmaxu2(m2, b[j][e] & 0x7fff7fffu);
+        uint32_t amax = max(m2 & 0xffffu, m2 >> 16);
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // 2^up brings the largest element to [2^14, 2^15); an infinity or NaN makes the token NaN
+        const int up = min(120, 14 + 127 - (int)(amax >> 7));
+        const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
+        const float back = amax >= 0x7f80u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(127 - up) << 23);
+        inv[0] = __shfl_sync(0xffffffffu, back, 8 * q);
+        inv[1] = __shfl_sync(0xffffffffu, back, 8 * q + 4);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) b[j][e] = lw4_f16x2(bf_lo(b[j][e]) * mul, bf_hi(b[j][e]) * mul);
     };
 
-    int st = 0, turn = 0, fill = 0;   // turn: buffer of the slots' sums; fill: of those that wait for the cluster
+    int st = 0, turn = 0, fill = 0;   // turn: buffer of the warps' sums; fill: of those that wait for the cluster
     int first_warp = 0;               // of those that add a step's sums: they take turns
     uint32_t parity = 0;              // of the ring
     bool lost = false;                // a wait expired
@@ -223,31 +204,19 @@ __global__ void __launch_bounds__(32 * kLw4Warps, 1) linear_w4_kernel(const Line
         float *mine = part + fill * (kLw4Partial / 4);
         for (int pass = 0; pass < a.passes; ++pass) {
             const int kt = kt_of(pass);
-            const int own = kt < a.k_tiles ? min(c1, len) : 0;   // this slot's tiles of the chunk end here
-            if (own > 0 && (a.passes > 1 || c0 == 0)) load_x(kt);
-            const int nk = min(KW, a.k_tiles - (pass * P + rank) * KW);   // slots side by side that have columns
+            const int own = kt < a.k_tiles ? min(c1, len) : 0;   // this warp's tiles of the chunk end here
+            if (own > 0 && (a.passes > 1 || c0 == 0)) load_x(kt * kW4Cols);
+            const int nk = min(KW, a.k_tiles - (pass * P + rank) * KW);   // warps side by side that have columns
             for (int t0 = c0; t0 < c1; t0 += UT) {
                 float *sum = sums + turn * Smem::kSums;
-                float *to = sum + ks * (UT * Smem::kSum) + (8 * NT * tw + 2 * q) * kLw4Stride + g;
+                float *to = sum + w * (UT * Smem::kSum) + 2 * q * kLw4Stride + g;
 #pragma unroll 1
                 for (int t = t0; t < min(t0 + UT, own); ++t, to += Smem::kSum) {
                     lost = lost || !tc_mbar_wait_within(&bar[st], parity, a.wait_ns);
-                    if (TW == 1) {
-                        lost = __any_sync(0xffffffffu, lost);
-                    } else {   // the warps that share the ring stop together
-                        int any;
-                        asm volatile("{\n .reg .pred p, o;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred o, %2, %3, p;\n"
-                                     " selp.b32 %0, 1, 0, o;\n}\n"
-                                     : "=r"(any)
-                                     : "r"((int)lost), "r"(1 + ks), "n"(32 * TW)
-                                     : "memory");
-                        lost = any != 0;
-                    }
-                    float acc[NT][4];   // row g, tokens 2 q and 2 q + 1; row g + 8
+                    lost = __any_sync(0xffffffffu, lost);
+                    float acc[4];   // row g, tokens 2 q and 2 q + 1; row g + 8
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[nt][e] = lost ? __uint_as_float(0x7fc00000u) : 0.f;
+                    for (int e = 0; e < 4; ++e) acc[e] = lost ? __uint_as_float(0x7fc00000u) : 0.f;
                     if (!lost) {
                         const unsigned char *tile = ring + st * TB;
                         uint4 v[4];
@@ -256,9 +225,7 @@ __global__ void __launch_bounds__(32 * kLw4Warps, 1) linear_w4_kernel(const Line
                         for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4 *>(tile + i * 512 + lane * 16);
 #pragma unroll
                         for (int i = 0; i < SG; ++i) sc[i] = *reinterpret_cast<const uint32_t *>(tile + 2048 + i * 32 + g * 4);
-                        // the tile has been read
-                        if (TW == 1) __syncwarp();
-                        else asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + ks), "n"(32 * TW) : "memory");
+                        __syncwarp();   // the tile has been read
                         if (!issue(st)) --flying;
                         if (++st == ST) {
                             st = 0;
@@ -266,40 +233,29 @@ __global__ void __launch_bounds__(32 * kLw4Warps, 1) linear_w4_kernel(const Line
                         }
 #pragma unroll
                         for (int gr = 0; gr < SG; ++gr) {
-                            float c[NT][4];
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) c[nt][e] = 0.f;
+                            float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                             for (int j = gr * (G / 32); j < (gr + 1) * (G / 32); ++j) {
                                 const uint32_t w0 = (&v[j / 2].x)[2 * (j & 1)], w1 = (&v[j / 2].x)[2 * (j & 1) + 1];
 #pragma unroll
-                                for (int h = 0; h < 2; ++h) {
-                                    const uint32_t a0 = w4_pair(w0, 2 * h), a1 = w4_pair(w1, 2 * h);
-                                    const uint32_t a2 = w4_pair(w0, 2 * h + 1), a3 = w4_pair(w1, 2 * h + 1);
-#pragma unroll
-                                    for (int nt = 0; nt < NT; ++nt) lw4_mma(c[nt], a0, a1, a2, a3, b[nt][j][2 * h], b[nt][j][2 * h + 1]);
-                                }
+                                for (int h = 0; h < 2; ++h)
+                                    lw4_mma(c, w4_pair(w0, 2 * h), w4_pair(w1, 2 * h), w4_pair(w0, 2 * h + 1), w4_pair(w1, 2 * h + 1),
+                                            b[j][2 * h], b[j][2 * h + 1]);
                             }
                             const float s0 = bf_lo(sc[gr]), s1 = bf_hi(sc[gr]);
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) acc[nt][e] += (e < 2 ? s0 : s1) * c[nt][e];
+                            for (int e = 0; e < 4; ++e) acc[e] += (e < 2 ? s0 : s1) * c[e];
                         }
                     }
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)   // the codes' 2^-16 back, then the activations' power of two
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            to[(8 * nt + (e & 1)) * kLw4Stride + 8 * (e >> 1)] = acc[nt][e] * 0x1p16f * inv[nt][e & 1];
+                    for (int e = 0; e < 4; ++e)   // the codes' 2^-16 back, then the activations' power of two
+                        to[(e & 1) * kLw4Stride + 8 * (e >> 1)] = acc[e] * 0x1p16f * inv[e & 1];
                 }
                 __syncthreads();
-                // the slots' sums, in their order; each step other warps begin
+                // the warps' sums, in their order; each step other warps begin
                 {
                     for (int i = (tid - 32 * first_warp) & (THREADS - 1); i < items; i += THREADS) {
-                        const int r = 4 * (i & 3), um = i >> 2, u = by_tokens(um), m = um - u * Mt, s = u / UT, t = t0 + u - s * UT;
+                        const int r = 4 * (i & 3), um = i >> 2, u = by_tokens(um), m = um - u * M, s = u / UT, t = t0 + u - s * UT;
                         const int first = first_of(s);
                         if (t >= min(c1, first_of(s + 1) - first)) continue;
                         const float *from = sum + (s * KW * UT + u - s * UT) * Smem::kSum + m * kLw4Stride + r;
@@ -307,9 +263,9 @@ __global__ void __launch_bounds__(32 * kLw4Warps, 1) linear_w4_kernel(const Line
 #pragma unroll 4
                         for (int k = 0; k < nk; ++k) lw4_add(v, *reinterpret_cast<const float4 *>(from + k * (UT * Smem::kSum)));
                         if (direct) {
-                            lw4_store(a, m0 + m, (r0 + first + t) * kW4Rows + r, v);
+                            lw4_store(a, m, (r0 + first + t) * kW4Rows + r, v);
                         } else {
-                            float4 *p = reinterpret_cast<float4 *>(mine + ((s * a.chunk + t - c0) * TOKENS + m) * 16 + r);
+                            float4 *p = reinterpret_cast<float4 *>(mine + ((s * a.chunk + t - c0) * kLw4MaxM + m) * 16 + r);
                             if (pass > 0) lw4_add(v, *p);
                             *p = v;
                         }
@@ -323,18 +279,18 @@ __global__ void __launch_bounds__(32 * kLw4Warps, 1) linear_w4_kernel(const Line
         // the ranks' sums.  A buffer is written again after the next one's barrier, which
         // every rank reaches when it has read this one.
         lw4_cluster_sync();
-        for (int i = rank * THREADS + tid; i < RW * (c1 - c0) * Mt * 4; i += P * THREADS) {
-            const int r = 4 * (i & 3), um = i >> 2, u = um / Mt, m = um - u * Mt, s = u / (c1 - c0), t = c0 + u - s * (c1 - c0);
+        for (int i = rank * THREADS + tid; i < RW * (c1 - c0) * M * 4; i += P * THREADS) {
+            const int r = 4 * (i & 3), um = i >> 2, u = by_tokens(um), m = um - u * M, s = u / (c1 - c0), t = c0 + u - s * (c1 - c0);
             const int first = first_of(s);
             if (t >= first_of(s + 1) - first) continue;
-            const float *p = mine + ((s * a.chunk + t - c0) * TOKENS + m) * 16 + r;
+            const float *p = mine + ((s * a.chunk + t - c0) * kLw4MaxM + m) * 16 + r;
             float4 f[kLw4MaxCluster], v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < kLw4MaxCluster; ++k) f[k] = k < P ? lw4_peer(p, k) : v;
 #pragma unroll
             for (int k = 0; k < kLw4MaxCluster; ++k)
                 if (k < P) lw4_add(v, f[k]);
-            lw4_store(a, m0 + m, (r0 + first + t) * kW4Rows + r, v);
+            lw4_store(a, m, (r0 + first + t) * kW4Rows + r, v);
         }
     }
     if (lost && a.err && lane == 0) atomicOr(a.err, kErrTimeout);
@@ -349,12 +305,12 @@ __global__ void __launch_bounds__(32 * kLw4Warps, 1) linear_w4_kernel(const Line
     }
 }
 
-template <int NT, int TW, int G>
+template <int G>
 static cudaError_t lw4_launch(LinearW4Args a, int sms, cudaStream_t s) {
-    using Smem = Lw4Smem<NT, TW, G>;
-    constexpr int kDevices = 64, NW = Smem::kSlots, TOKENS = Smem::kTokens;
+    using Smem = Lw4Smem<G>;
+    constexpr int kDevices = 64, NW = kLw4Warps;
     static std::atomic<int> known[kDevices][kLw4MaxCluster + 1];   // clusters that are resident at once
-    const auto kern = linear_w4_kernel<NT, TW, G>;
+    const auto kern = linear_w4_kernel<G>;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(32 * kLw4Warps);
     cfg.dynamicSmemBytes = Smem::kBytes;
@@ -385,7 +341,7 @@ static cudaError_t lw4_launch(LinearW4Args a, int sms, cudaStream_t s) {
             known[dev][P].store(most < 1 ? 1 : most < sms / P ? most : sms / P, std::memory_order_release);
         }
     }
-    // The cluster that keeps most slots busy; of equals the smallest.  One pass if eight CTAs' slots
+    // The cluster that keeps most warps busy; of equals the smallest.  One pass if eight CTAs' warps
     // hold the columns.
     long long best = -1;
     for (int P = 1; P <= kLw4MaxCluster; ++P) {
@@ -402,31 +358,22 @@ static cudaError_t lw4_launch(LinearW4Args a, int sms, cudaStream_t s) {
     if (clusters > a.row_tiles) clusters = a.row_tiles;
     const int rows = (a.row_tiles + clusters - 1) / clusters;   // of tiles, at most, of a cluster
     const bool direct = a.cluster == 1 && a.passes == 1;
-    const int fit = kLw4Partial / (TOKENS * 16 * 4);
+    const int fit = kLw4Partial / (kLw4MaxM * 16 * 4);
     a.row_warps = NW / a.k_warps < rows ? NW / a.k_warps : rows;
     if (!direct && a.row_warps * kLw4Unit > fit) a.row_warps = fit / kLw4Unit;
     const int run = (rows + a.row_warps - 1) / a.row_warps;
     a.chunk = direct ? run : fit / a.row_warps / kLw4Unit * kLw4Unit;
     a.wide = a.ldy % 4 == 0 && ((uintptr_t)a.y & (a.f32 ? 15u : 7u)) == 0;
     attr[0].val.clusterDim.x = (unsigned)a.cluster;
-    cfg.gridDim = dim3((unsigned)(clusters * a.cluster), (unsigned)((a.M + TOKENS - 1) / TOKENS));
+    cfg.gridDim = dim3((unsigned)(clusters * a.cluster));
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, a);
-}
-
-template <int G>
-static cudaError_t lw4_launch_tokens(const LinearW4Args &a, int sms, cudaStream_t s) {
-    if (a.M <= 8) return lw4_launch<1, 1, G>(a, sms, s);
-    if (a.M <= 16) return lw4_launch<2, 1, G>(a, sms, s);
-    if (a.M <= 32) return lw4_launch<2, 2, G>(a, sms, s);
-    return lw4_launch<2, 4, G>(a, sms, s);
 }
 
 cudaError_t launch_linear_w4(LinearW4Args a, int sms, cudaStream_t s) {
     a.row_tiles = (a.N + kW4Rows - 1) / kW4Rows;
     a.k_tiles = (a.K + kW4Cols - 1) / kW4Cols;
-    return a.group == 32 ? lw4_launch_tokens<32>(a, sms, s)
-                         : a.group == 64 ? lw4_launch_tokens<64>(a, sms, s) : lw4_launch_tokens<128>(a, sms, s);
+    return a.group == 32 ? lw4_launch<32>(a, sms, s) : a.group == 64 ? lw4_launch<64>(a, sms, s) : lw4_launch<128>(a, sms, s);
 }
 
 }  // namespace bloom
