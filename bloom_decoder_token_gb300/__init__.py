@@ -732,26 +732,22 @@ def _w4_bytes(n: int, k: int, group: int) -> int:
     return size
 
 
-class W4(NamedTuple):
+class W4:
     """4-bit weights [n][k] with group scales: value = code * scale, codes -7 .. 7, a
     bf16 scale for every `group` (32, 64 or 128) neighbouring weights of a row.  tiles:
     uint8 [bloom_w4_bytes(n, k, group)], in the order that the linear layer reads them."""
-    tiles: torch.Tensor
-    n: int
-    k: int
-    group: int
+    __slots__ = ("tiles", "n", "k", "group", "device", "ref", "_c")
+
+    def __init__(self, tiles: torch.Tensor, n: int, k: int, group: int):
+        size = _w4_bytes(n, k, group)
+        self._c = W4C(_dev("tiles", tiles, _U8, (size,), tiles.device), n, k, group)
+        self.ref = C.byref(self._c)         # the C descriptor (bloom_w4)
+        self.tiles, self.n, self.k, self.group, self.device = tiles, n, k, group, tiles.device
 
     @classmethod
     def empty(cls, n: int, k: int, group: int = 64, device="cuda"):
         """Room for [n][k] weights (k a multiple of 8), not initialised."""
-        size = _w4_bytes(n, k, group)
-        return cls(torch.empty(size, dtype=_U8, device=device), n, k, group)
-
-    def c(self) -> W4C:
-        """The C descriptor (bloom_w4), after checking type, size and layout."""
-        t, n, k, group = self
-        size = _w4_bytes(n, k, group)
-        return W4C(_dev("tiles", t, _U8, (size,), t.device), n, k, group)
+        return cls(torch.empty(_w4_bytes(n, k, group), dtype=_U8, device=device), n, k, group)
 
 
 def _rows(name: str, t, dtype, shape, device):
@@ -775,9 +771,9 @@ def op_w4_quantize(w, group: int = 64, out: Optional[W4] = None, stream=None) ->
     wp, ld = _rows("w", w, _BF16, (n, k), dev)
     if out is None:
         out = W4.empty(n, k, group, dev)
-    elif (out.n, out.k, out.tiles.device) != (n, k, dev):
-        _bad(f"out: weights {(n, k)} on {dev} expected, got {(out.n, out.k)} on {out.tiles.device}")
-    st = lib().bloom_op_w4_quantize(wp, ld, C.byref(out.c()), _raw_stream(dev))
+    elif (out.n, out.k, out.device) != (n, k, dev):
+        _bad(f"out: weights {(n, k)} on {dev} expected, got {(out.n, out.k)} on {out.device}")
+    st = lib().bloom_op_w4_quantize(wp, ld, out.ref, _raw_stream(dev))
     if st:
         check(st)
     return out
@@ -786,16 +782,16 @@ def op_w4_quantize(w, group: int = 64, out: Optional[W4] = None, stream=None) ->
 def op_w4_read(w4: W4, out=None, stream=None):
     """The weights back as bf16 [n][k] (rows of `out` may be strided): for prompts, which
     run on op_gemm, or to look at what the codes stand for."""
-    dev = w4.tiles.device
+    dev = w4.device
     there = _elsewhere(dev, stream)
     if there is not None:
         with there:
             return op_w4_read(w4, out)
-    c = w4.c()
+    n, k = w4.n, w4.k
     if out is None:
-        out = torch.empty((c.n, c.k), dtype=_BF16, device=dev)
-    wp, ld = _rows("out", out, _BF16, (c.n, c.k), dev)
-    st = lib().bloom_op_w4_read(C.byref(c), wp, ld, _raw_stream(dev))
+        out = torch.empty((n, k), dtype=_BF16, device=dev)
+    wp, ld = _rows("out", out, _BF16, (n, k), dev)
+    st = lib().bloom_op_w4_read(w4.ref, wp, ld, _raw_stream(dev))
     if st:
         check(st)
     return out
@@ -814,11 +810,10 @@ def op_linear_w4(x, w4: W4, bias=None, epilogue=EPI_STORE, y=None, dtype=torch.b
     if there is not None:
         with there:
             return op_linear_w4(x, w4, bias, epilogue, y, dtype, workspace, flag)
-    c = w4.c()
-    if w4.tiles.device != dev:
-        _bad(f"weights on {w4.tiles.device}, x on {dev}")
-    M = x.shape[0]
-    xp, ldx = _rows("x", x, _BF16, (M, c.k), dev)
+    if w4.device != dev:
+        _bad(f"weights on {w4.device}, x on {dev}")
+    M, n = x.shape[0], w4.n
+    xp, ldx = _rows("x", x, _BF16, (M, w4.k), dev)
     if M > 1 << 20:
         _bad(f"M={M}: at most {1 << 20} tokens")
     if y is None:
@@ -826,10 +821,15 @@ def op_linear_w4(x, w4: W4, bias=None, epilogue=EPI_STORE, y=None, dtype=torch.b
             _bad("y: EPI_RESID adds to it")
         if dtype is not _BF16 and dtype is not _F32:
             _bad(f"dtype={dtype}: bfloat16 or float32 expected")
-        y = torch.empty((M, c.n), dtype=dtype, device=dev)
-    f32 = y.dtype is _F32
-    yp, ldy = _rows("y", y, _F32 if f32 else _BF16, (M, c.n), dev)
-    L, cr = lib(), C.byref(c)
+        f32 = dtype is _F32
+        y = torch.empty((M, n), dtype=dtype, device=dev)
+        yp, ldy = y.data_ptr(), n
+    else:
+        f32 = y.dtype is _F32
+        yp, ldy = _rows("y", y, _F32 if f32 else _BF16, (M, n), dev)
+    bp = None if bias is None else _dev("bias", bias, _BF16, (n,), dev)
+    fp = None if flag is None else _dev("flag", flag, _I32, (1,), dev)
+    L = lib()
     wp, wn = None, 0
     if workspace is not None:
         if workspace.dtype is not _U8 or workspace.dim() != 1:
@@ -837,11 +837,10 @@ def op_linear_w4(x, w4: W4, bias=None, epilogue=EPI_STORE, y=None, dtype=torch.b
         wn = workspace.numel()
         wp = _dev("workspace", workspace, _U8, (wn,), dev)
     elif M > 8:
-        wn = L.bloom_op_linear_w4_workspace(cr, M)
+        wn = L.bloom_op_linear_w4_workspace(w4.ref, M)
         workspace = torch.empty(wn, dtype=_U8, device=dev)
         wp = workspace.data_ptr()
-    st = L.bloom_op_linear_w4(cr, xp, ldx, M, _dev("bias", bias, _BF16, (c.n,), dev), epilogue, yp, ldy, f32, wp, wn,
-                              _dev("flag", flag, _I32, (1,), dev), _raw_stream(dev))
+    st = L.bloom_op_linear_w4(w4.ref, xp, ldx, M, bp, epilogue, yp, ldy, f32, wp, wn, fp, _raw_stream(dev))
     if st:
         check(st)
     return y
