@@ -674,6 +674,8 @@ def op_sample_filtered(logits, u, temperature=None, top_k=None, top_p=None, min_
             return op_sample_filtered(logits, u, temperature, top_k, top_p, min_p, out)
     J = u.shape[1] if u.dim() == 2 else 1
     shape = (B, J) if u.dim() == 2 else (B,)
+    if max(B, V, J) >= 2 ** 31:         # would wrap in the call
+        _bad(f"logits {(B, V)}, {J} draws: sizes below 2^31 expected")
     up, row = _dev("u", u, _F32, shape, dev), (B,)
     if out is None:
         out = torch.empty(shape, dtype=_I32, device=dev)

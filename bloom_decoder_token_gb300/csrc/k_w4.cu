@@ -3,14 +3,18 @@
 //
 // scale = bf16(amax / 7), code = w / scale rounded half to even.  Both come out as
 // in exact arithmetic: amax and w have 8 significant bits, so amax / 7 lies 2^-13 of
-// itself or more from a border between two bf16 numbers (float32 division is off by
-// 2^-24), and w / scale is a half or lies 2^-10 or more from one, so a product with
-// 1 / scale, off by 2^-20 at most, rounded to multiples of 2^-13, is a half where
-// the quotient is.  A division an element would cost more than the loads.
+// itself or more from a border between two bf16 numbers (below 2^-126: 2^-137 or more),
+// while a product with the float 1 / 7 is off by 2^-23 of itself and 2^-150; and
+// w / scale is a half or lies 2^-10 or more from one, so a product with 1 / scale, off
+// by 2^-19 at most (rcp.approx: 2^-23 of itself), rounded to multiples of 2^-13, is a
+// half where the quotient is.
 //
 // Bound by HBM: 2 bytes a weight in and half a byte out, or the other way round.  One
 // warp a tile; a row's 8 columns are one 16-byte access, 64 bytes of a row for the
-// four lanes that hold it.
+// four lanes that hold it.  57344 x 14336 in groups of 64: quantised in 304 us, 6850
+// GB/s (a copy: 6690), read back in 334, 6240; 14336 x 57344 in groups of 32: 336 and 332;
+// 16384 x 4096 in groups of 64: 30 each.  (With scales by IEEE division, and codes by conversions
+// to integers and comparisons, it was bound by instructions: 88 us for these two.)
 #include "common.cuh"
 #include "kernels.h"
 #include "w4_ops.cuh"
@@ -19,36 +23,44 @@ namespace bloom {
 
 constexpr int kW4Threads = 128;
 
-// A word from its eight codes, for w4_pair().
-__device__ __forceinline__ uint32_t w4_word(const int (&c)[8]) {
-    uint32_t w = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t half = (uint32_t)abs(c[e]) << 8 | (c[e] < 0 ? 0x8000u : 0u);
-        const uint32_t both = half << (16 * (e & 1));
-        w |= e < 6 ? __funnelshift_r(both, both, 4 * (e >> 1)) : __funnelshift_l(both, both, 4);
-    }
-    return w;
+// A word from its pairs, each as w4_pair() gives it.
+__device__ __forceinline__ uint32_t w4_word(const uint32_t (&p)[4]) {
+    return p[0] | p[1] >> 4 | p[2] >> 8 | __funnelshift_l(p[3], p[3], 4);
 }
 
 struct W4Scale {
-    float up, inv;    // code = (x * up) * inv rounded
+    float inv, up;    // |code| = |x| * inv, rounded; where `rare`, min(|x| * up * inv, 7), rounded
     uint16_t bits;
+    bool rare;        // a scale whose reciprocal may be no float or whose bits are few, or NaN
     __device__ __forceinline__ explicit W4Scale(uint32_t amax) {   // |bf16| bits
-        bits = amax >= 0x7f80u ? (uint16_t)0x7fc0u : f2bf(__fdiv_rn(bf2f((uint16_t)amax), 7.f));
+        asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(bits) : "f"(bf2f((uint16_t)amax) * (1.f / 7.f)));
+        if (amax >= 0x7f80u) bits = 0x7fc0u;
         const float s = bf2f(bits);
-        up = s < 0x1p-64f ? 0x1p64f : 1.f;    // 1 / scale stays a float
-        inv = s > 0.f ? __frcp_rn(s * up) : 0.f;   // 0 and NaN: codes 0
-    }
-    __device__ __forceinline__ int code(float x) const {
-        const float t = inv > 0.f ? x * up * inv : 0.f;
-        return max(-7, min(7, __float2int_rn((t + 1536.f) - 1536.f)));
+        rare = amax != 0u && !(s >= 0x1p-64f);
+        up = rare ? 0x1p64f : 1.f;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s * up));
+        inv = s > 0.f ? inv : 0.f;    // 0 and NaN: codes 0
     }
 };
 
+// Two codes of the bf16 numbers x, as w4_pair() gives them.  |x| * inv + 1536 is a multiple of 2^-13, and
+// adding what is missing to 1.5 * 2^23 rounds it to an integer, the code in the last byte.
+template <bool RARE>
+__device__ __forceinline__ uint32_t w4_codes(uint32_t x, const W4Scale &s) {
+    float t[2] = {fabsf(bf_lo(x)), fabsf(bf_hi(x))};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        if (RARE) t[e] = s.inv > 0.f ? fminf(t[e] * s.up * s.inv, 7.f) : 0.f;
+        else t[e] = __fmul_rn(t[e], s.inv);
+        t[e] = __fadd_rn(__fadd_rn(t[e], 1536.f), 12582912.f - 1536.f);
+    }
+    const uint32_t m = __byte_perm(__float_as_uint(t[0]), __float_as_uint(t[1]), 0x4501);   // |code| << 8
+    return m | (x & (m * 16u + 0x70007000u) & 0x80008000u);                                 // 0 has no sign
+}
+
 template <int G>
 __global__ void __launch_bounds__(kW4Threads) w4_quantize_kernel(const W4Args a) {
-    constexpr int U = G < 64 ? 64 : G, J = U / 32, GJ = G / 32;   // columns of a pass; 32-column steps of it, of a group
+    constexpr int U = 128, J = U / 32, GJ = G / 32;   // columns of a pass (64 and 256: the same); 32-column steps of it, of a group
     griddep_launch();
     griddep_wait();
     const long long tile = (long long)blockIdx.x * (kW4Threads / 32) + (threadIdx.x >> 5);
@@ -89,14 +101,19 @@ __global__ void __launch_bounds__(kW4Threads) w4_quantize_kernel(const W4Args a)
                 amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
                 const W4Scale s(amax);
                 scales |= (uint32_t)s.bits << (16 * r);
+                const bool rare = __any_sync(0xffffffffu, s.rare);
 #pragma unroll
                 for (int j = gr * GJ; j < (gr + 1) * GJ; ++j) {
-                    float f[8];
-                    unpack8(x[j][r], f);
-                    int c[8];
+                    const uint32_t v[4] = {x[j][r].x, x[j][r].y, x[j][r].z, x[j][r].w};
+                    uint32_t p[4];
+                    if (rare) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) c[e] = s.code(f[e]);
-                    words[j][r] = w4_word(c);
+                        for (int e = 0; e < 4; ++e) p[e] = w4_codes<true>(v[e], s);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) p[e] = w4_codes<false>(v[e], s);
+                    }
+                    words[j][r] = w4_word(p);
                 }
             }
             if (q == 0) *reinterpret_cast<uint32_t *>(out + 2048 + ((u * U) / G + gr) * 32 + g * 4) = scales;
@@ -108,16 +125,20 @@ __global__ void __launch_bounds__(kW4Threads) w4_quantize_kernel(const W4Args a)
     }
 }
 
-// Code e of the eight of a word.
-__device__ __forceinline__ float w4_code(uint32_t w, int e) {
-    const uint32_t half = w4_pair(w, e >> 1) >> (16 * (e & 1));
-    const float m = (float)(half >> 8 & 7u);
-    return half & 0x8000u ? -m : m;
+// Codes 2 i and 2 i + 1 of a word times the scale, as bf16: 128 + |code| is a bf16 number, and the
+// product is rounded once.
+__device__ __forceinline__ uint32_t w4_values(uint32_t w, int i, uint32_t scales) {
+    const uint32_t p = w4_pair(w, i), m = (p >> 8 & 0x00070007u) | 0x43004300u, s = scales ^ (p & 0x80008000u);
+    uint32_t c, v;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(m), "r"(0x43004300u));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(c), "r"(s));
+    return v;
 }
 
 template <int G>
 __global__ void __launch_bounds__(kW4Threads) w4_read_kernel(const W4Args a) {
-    griddep_launch();
+    // No early start of the kernel after this one: the linear layers that read the matrix as their
+    // weights load it before they wait.
     griddep_wait();
     const long long tile = (long long)blockIdx.x * (kW4Threads / 32) + (threadIdx.x >> 5);
     const int ktiles = (a.K + kW4Cols - 1) / kW4Cols, row_tiles = (a.N + kW4Rows - 1) / kW4Rows;
@@ -140,13 +161,14 @@ __global__ void __launch_bounds__(kW4Threads) w4_read_kernel(const W4Args a) {
             const int row = rt * kW4Rows + g + 8 * r;
             if (row >= a.N) continue;
             const uint32_t w = (&v[j / 2].x)[2 * (j & 1) + r];
-            const float scale = r ? bf_hi(s[32 * j / G]) : bf_lo(s[32 * j / G]);
+            const uint32_t scales = __byte_perm(s[32 * j / G], 0u, r ? 0x3232 : 0x1010);
             uint32_t o[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = pack_bf2(w4_code(w, 2 * e) * scale, w4_code(w, 2 * e + 1) * scale);
+            for (int i = 0; i < 4; ++i) o[i] = w4_values(w, i, scales);
             *reinterpret_cast<uint4 *>(a.w + row * a.ld + k) = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
+    __threadfence();
 }
 
 template <typename K>

@@ -345,7 +345,7 @@ struct LinearW4Args {
 };
 constexpr int kLw4MaxM = 8;
 cudaError_t launch_linear_w4(LinearW4Args a, int sms, cudaStream_t s);      // M <= kLw4MaxM
-// More tokens (k_linear_w4_tc.cu); workspace of linear_w4_tc_workspace() bytes, 1024-byte aligned.
+// More tokens (k_linear_w4_tc.cu); workspace of linear_w4_tc_workspace() bytes, 16-byte aligned.
 cudaError_t launch_linear_w4_tc(LinearW4Args a, void *workspace, int sms, cudaStream_t s);
 size_t linear_w4_tc_workspace(int M, int K);
 

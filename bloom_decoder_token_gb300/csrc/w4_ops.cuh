@@ -3,7 +3,7 @@
 //
 // value = code * scale, codes -7 .. 7, one bf16 scale for every `group` (32, 64 or
 // 128) neighbouring weights of a row.  The matrix [N][K] lies in tiles of 16 rows x
-// 256 columns, [ceil(N / 16)][ceil(K / 256)], zeros beyond N and K, so that a warp
+// 256 columns, [ceil(K / 256)][ceil(N / 16)], zeros beyond N and K, so that a warp
 // streams whole tiles with one bulk copy each and finds its fragments of mma.sync
 // m16n8k16 in place:
 //  * codes, 2048 bytes: lane (g, q) = 4 g + q holds rows g and g + 8, of every 32

@@ -583,9 +583,11 @@ bloom_status bloom_op_w4_read(const bloom_w4 *in, void *w, int64_t ld, void *str
  * rows ldx apart (ldx >= k, ldx % 8 == 0; 16-byte aligned); bias: bf16 [n] or
  * NULL; y: bf16 (y_f32 = 0) or float (1) [M][n], rows ldy >= n apart, aligned to
  * its elements; epilogue as bloom_op_linear (BLOOM_EPI_RESID adds to y in
- * place).  Any M >= 0; the weights are read once for every 64 tokens.  An
- * activation smaller than 2^-31 of the largest of its token's 256 columns
- * (256 i .. 256 i + 255) is taken to within 2^-39 of that one; others exactly.
+ * place).  M up to 2^20; the weights are read once for every 64 tokens.  An
+ * activation smaller than 2^-31 of the largest of its token (up to 8 tokens: of
+ * its token's 256 columns 256 i .. 256 i + 255) is taken to within 2^-39 of that
+ * one; others exactly.  That largest one goes into the sums as about 2^15: scales
+ * from 2^-90 to 2^70 neither lose bits there nor overflow.
  * A token with an infinity or NaN among its activations has NaN outputs.  y
  * must not overlap x, the tiles or the bias.
  * `flag`: as for the 8-bit cache; bit 8: a bounded wait expired, the outputs

@@ -35,20 +35,22 @@ def gelu(v):
     return v * 0.5 * (1.0 + torch.tanh(0.79788456 * v * (1.0 + 0.044715 * v * v)))
 
 
-def linear(x, wide, bias=None, epilogue=0, y=None):
+def linear(x, wide, bias=None, epilogue=0, y=None, group=32):
     """(y, tolerance) of the linear layer over the values `wide`, float64 [M][n].
 
-    The tolerance, before the output's own rounding: a float32 sum of products in chains
-    of at most 64 additions (8 of a tensor core's sums a group, 8 groups a warp, 16 warps, 8 ranks, passes), each
-    off by 2^-23 of the sum of magnitudes at most; activations below 2^-31 of the largest
-    of their 256 columns, off by 2^-39 of it; the GeLU's slope is below 1.13, its own
-    arithmetic off by 2^-20 of its result or 2^-22 of its argument at most."""
+    The tolerance, before the output's own rounding: a float32 sum of products in chains of
+    additions, each off by 2^-23 of the sum of magnitudes at most: up to 8 tokens 64 (8 of a tensor
+    core's sums a group, 8 groups a warp, 16 warps, 8 ranks, passes); more: group / 16, 8 ranks, and one
+    for every group, those to the nearest (2^-24); activations below 2^-31 of the largest
+    of their 256 columns (more than 8 tokens: of all), off by 2^-39 of it; the GeLU's slope is below
+    1.13, its own arithmetic off by 2^-20 of its result or 2^-22 of its argument at most."""
     x = x.double()
-    k = x.shape[1]
+    M, k = x.shape
     v = x @ wide.t()
-    far = x.abs() @ wide.abs().t() * (64 * 2.0 ** -23)
-    for a in range(0, k, 256):
-        far += x[:, a: a + 256].abs().amax(1, keepdim=True) * wide[:, a: a + 256].abs().sum(1) * 2.0 ** -39
+    far = x.abs() @ wide.abs().t() * ((64 if M <= 8 else group / 16 + 8 + -(-k // group) / 2) * 2.0 ** -23)
+    block = 256 if M <= 8 else k
+    for a in range(0, k, block):
+        far += x[:, a: a + block].abs().amax(1, keepdim=True) * wide[:, a: a + block].abs().sum(1) * 2.0 ** -39
     if bias is not None:
         v = v + bias.double()
         far += v.abs() * 2.0 ** -23
