@@ -19,6 +19,12 @@
 //    meet in shared memory, in the warps' order, every 32 rows.
 //  * Longer rows are split over the CTAs of a cluster, whose sums meet through distributed
 //    shared memory, in rank order; still longer ones are taken in passes.
+// The first tiles are loaded before the wait for the kernel before (behind a layer norm 12288 x 4096,
+// one token: 12.3 -> 12.0 us, 4096 x 16384 17.8 -> 16.1); so what writes tiles starts nothing early.
+// One token, from HBM: 4096 x 1024 3.7 us, 12288 x 4096 10.4 (4.0 to read the weights), 4096 x 16384
+// 12.3 (5.2, groups of 128), 57344 x 14336 94 (65), 14336 x 57344 111 (65); 8 tokens, 250880 x 4096: 107
+// (83).  Long matrices: bound by instructions as much as by HBM (a step of 32 rows takes the 16 warps
+// about as long as its tiles take to come); short ones by the start, 3 us, and the last tiles' way.
 #include <atomic>
 #include <math.h>
 
@@ -111,7 +117,7 @@ __global__ void __launch_bounds__(32 * kLw4Warps, 1) linear_w4_kernel(const Line
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, q = lane & 3;
     unsigned char *ring = lw4_smem + w * ST * TB;
     float *sums = reinterpret_cast<float *>(lw4_smem + Smem::kRing);              // [2][NW][UT][kLw4MaxM][kLw4Stride]
-    float *part = sums + 2 * Smem::kSums;                                         // [2][tiles][kLw4MaxM][16]
+    float *part = sums + 2 * Smem::kSums;                                         // [2][tiles][M][16]
     uint64_t *bar = reinterpret_cast<uint64_t *>(part + 2 * (kLw4Partial / 4)) + w * ST;
     if (lane == 0) {
         for (int i = 0; i < ST; ++i) tc_mbar_init(&bar[i], 1);
@@ -121,7 +127,6 @@ __global__ void __launch_bounds__(32 * kLw4Warps, 1) linear_w4_kernel(const Line
     const int P = a.cluster, cl = (int)blockIdx.x / P, rank = (int)blockIdx.x - cl * P, clusters = (int)gridDim.x / P;
     const int KW = a.k_warps, RW = a.row_warps, slot = w / KW, kw = w - slot * KW, M = a.M;
     const int items = RW * UT * M * 4, NR = (items + 31) / 32;   // a step's sums, four rows a lane; warps for them
-    griddep_wait();
     griddep_launch();
 
     // The cluster's tiles of rows, [r0, r0 + n), in RW runs of at most `run`, one for each KW
@@ -164,6 +169,7 @@ __global__ void __launch_bounds__(32 * kLw4Warps, 1) linear_w4_kernel(const Line
     };
     int flying = 0;
     for (int i = 0; i < ST; ++i) flying += issue(i);
+    griddep_wait();   // the activations and y
 
     uint32_t b[8][4];       // activations: token g, elements 32 j + 8 q + (0, 1 | 2, 3 | 4, 5 | 6, 7)
     float inv[2];           // 2^-up of tokens 2 q and 2 q + 1
@@ -265,7 +271,7 @@ __global__ void __launch_bounds__(32 * kLw4Warps, 1) linear_w4_kernel(const Line
                         if (direct) {
                             lw4_store(a, m, (r0 + first + t) * kW4Rows + r, v);
                         } else {
-                            float4 *p = reinterpret_cast<float4 *>(mine + ((s * a.chunk + t - c0) * kLw4MaxM + m) * 16 + r);
+                            float4 *p = reinterpret_cast<float4 *>(mine + ((s * a.chunk + t - c0) * M + m) * 16 + r);
                             if (pass > 0) lw4_add(v, *p);
                             *p = v;
                         }
@@ -283,7 +289,7 @@ __global__ void __launch_bounds__(32 * kLw4Warps, 1) linear_w4_kernel(const Line
             const int r = 4 * (i & 3), um = i >> 2, u = by_tokens(um), m = um - u * M, s = u / (c1 - c0), t = c0 + u - s * (c1 - c0);
             const int first = first_of(s);
             if (t >= first_of(s + 1) - first) continue;
-            const float *p = mine + ((s * a.chunk + t - c0) * kLw4MaxM + m) * 16 + r;
+            const float *p = mine + ((s * a.chunk + t - c0) * M + m) * 16 + r;
             float4 f[kLw4MaxCluster], v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < kLw4MaxCluster; ++k) f[k] = k < P ? lw4_peer(p, k) : v;
@@ -358,7 +364,7 @@ static cudaError_t lw4_launch(LinearW4Args a, int sms, cudaStream_t s) {
     if (clusters > a.row_tiles) clusters = a.row_tiles;
     const int rows = (a.row_tiles + clusters - 1) / clusters;   // of tiles, at most, of a cluster
     const bool direct = a.cluster == 1 && a.passes == 1;
-    const int fit = kLw4Partial / (kLw4MaxM * 16 * 4);
+    const int fit = kLw4Partial / (a.M * 16 * 4);   // tiles of sums that wait for the cluster
     a.row_warps = NW / a.k_warps < rows ? NW / a.k_warps : rows;
     if (!direct && a.row_warps * kLw4Unit > fit) a.row_warps = fit / kLw4Unit;
     const int run = (rows + a.row_warps - 1) / a.row_warps;

@@ -11,9 +11,9 @@
 //
 // Bound by HBM: 2 bytes a weight in and half a byte out, or the other way round.  One
 // warp a tile; a row's 8 columns are one 16-byte access, 64 bytes of a row for the
-// four lanes that hold it.  57344 x 14336 in groups of 64: quantised in 304 us, 6850
-// GB/s (a copy: 6690), read back in 334, 6240; 14336 x 57344 in groups of 32: 336 and 332;
-// 16384 x 4096 in groups of 64: 30 each.  (With scales by IEEE division, and codes by conversions
+// four lanes that hold it.  57344 x 14336 in groups of 64: quantised in 311 us, 6690
+// GB/s (as a copy), read back in 331, 6290; 14336 x 57344 in groups of 32: 342 and 328;
+// 16384 x 4096 in groups of 64: 31 and 30.  (With scales by IEEE division, and codes by conversions
 // to integers and comparisons, it was bound by instructions: 88 us for these two.)
 #include "common.cuh"
 #include "kernels.h"
@@ -61,8 +61,7 @@ __device__ __forceinline__ uint32_t w4_codes(uint32_t x, const W4Scale &s) {
 template <int G>
 __global__ void __launch_bounds__(kW4Threads) w4_quantize_kernel(const W4Args a) {
     constexpr int U = 128, J = U / 32, GJ = G / 32;   // columns of a pass (64 and 256: the same); 32-column steps of it, of a group
-    griddep_launch();
-    griddep_wait();
+    griddep_wait();   // no early start of the kernel after this one: linear layers load weights before they wait
     const long long tile = (long long)blockIdx.x * (kW4Threads / 32) + (threadIdx.x >> 5);
     const int ktiles = (a.K + kW4Cols - 1) / kW4Cols, row_tiles = (a.N + kW4Rows - 1) / kW4Rows;
     if (tile >= (long long)ktiles * row_tiles) return;
@@ -123,6 +122,7 @@ __global__ void __launch_bounds__(kW4Threads) w4_quantize_kernel(const W4Args a)
             *reinterpret_cast<uint4 *>(out + (u * U / 64 + j / 2) * 512 + lane * 16) =
                 make_uint4(words[j][0], words[j][1], words[j + 1][0], words[j + 1][1]);
     }
+    __threadfence();
 }
 
 // Codes 2 i and 2 i + 1 of a word times the scale, as bf16: 128 + |code| is a bf16 number, and the
@@ -137,8 +137,7 @@ __device__ __forceinline__ uint32_t w4_values(uint32_t w, int i, uint32_t scales
 
 template <int G>
 __global__ void __launch_bounds__(kW4Threads) w4_read_kernel(const W4Args a) {
-    // No early start of the kernel after this one: the linear layers that read the matrix as their
-    // weights load it before they wait.
+    // No early start here either: the matrix may be another linear layer's weights.
     griddep_wait();
     const long long tile = (long long)blockIdx.x * (kW4Threads / 32) + (threadIdx.x >> 5);
     const int ktiles = (a.K + kW4Cols - 1) / kW4Cols, row_tiles = (a.N + kW4Rows - 1) / kW4Rows;
