@@ -14,7 +14,10 @@
 // exponent (max z - z) log2(e) / t is carried in two floats, or the rounding of 1 / t would
 // shift all far tokens the same way.
 //
-// Bound by the logits' first read; then by the instructions of the passes over them in L2.  One cluster of up to 8 CTAs a row, each a slice of the vocabulary:
+// The logits are read once from HBM (few rows) and then from L2: one row is bound by the latency of
+// its phases (1 x 250880: greedy 9 us, top-k 50 13, top-p 0.95 30), many by instructions, 60 % of the
+// issue slots (509 x 250880, 76 us from HBM: greedy 189, top-k 50 194, top-p 0.95 of normal logits 462:
+// some 70 instructions a logit).  One cluster of up to 16 CTAs a row, each a slice of the vocabulary:
 //  1. the maximum and minimum, and every thread's own maximum;
 //  2. where few tokens can be kept, these come to the first CTA, which ranks them and does the
 //     rest: of the top 192, those that reach a bound from the maxima of groups of threads; the
@@ -666,7 +669,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     bool ready = false;   // the segments' masses are those of the cut
     if (!infinite && k != 1 && (k > 1 || nucleus)) {
         const float far = fminf(row.exponent(sf_unkey(kmin)), kSfFar);
-        SfBins bins = {false, far > 0.f ? (kSfBins - 1) / far : 0.f, 0u, 0u, 0};
+        SfBins bins = {false, far > 0.f ? (kSfBins - 2) / far : 0.f, 0u, 0u, 0};
         if (!(bins.per_binade < 1e30f)) bins.per_binade = 0.f;   // logits that differ by next to nothing
         // the cluster's counts of `bins`; by exponent with the whole mass, by keys with the bins'
         // masses, in the place of the list
@@ -690,12 +693,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
                         float x;
                         uint32_t f;
                         const uint32_t n = row.mass(v[e], x, f);
-                        const int i = bins.near(x);
                         own += (sf_u64)n * f;
-                        if (x < kSfFar) {
-                            atomicAdd(&sm.hist[i], 1u);
-                            if (f > 1u) atomicAdd(&rest_own[i], (int)(((float)i * binades - x) * (0.6931471805599453f * 1048576.f)));
-                        }
+                        const int i = x < kSfFar ? bins.near(x) : kSfBins - 1;   // NaN too: to the bin that no other logit has
+                        atomicAdd(&sm.hist[i], 1u);
+                        if (f > 1u) atomicAdd(&rest_own[i], (int)(((float)i * binades - x) * (0.6931471805599453f * 1048576.f)));
                     }
                 }, no_segment);
                 publish(kSfWhole, block_sum(own));
@@ -711,6 +712,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
                     }
                 }, no_segment);
             }
+            if (whole && tid == 0) sm.hist[kSfBins - 1] = 0u;
             sf_sync();
             const int share = kSfBins / CS;    // this rank adds up its share of the bins for all
             for (int i = (int)rank * share + tid; i < ((int)rank + 1) * share; i += THREADS) {
