@@ -1425,7 +1425,7 @@ extern "C" bloom_status bloom_op_sample_filtered(const float *logits, int32_t B,
                                                  const float *u, int32_t J, int32_t *out_tokens,
                                                  void *stream) {
     g_pdl = true;
-    if (B < 0 || B > 65535 || V < 1 || ld < V || J < 0)
+    if (B < 0 || B > 65535 || V < 1 || V > kSfMaxV || ld < V || J < 0 || J > kSfMaxJ)
         return fail(BLOOM_E_INVALID, "B=%d V=%d ld=%lld J=%d", B, V, (long long)ld, J);
     if (B == 0 || J == 0) return BLOOM_OK;
     if (!logits || !u || !out_tokens) return fail(BLOOM_E_INVALID, "null argument");

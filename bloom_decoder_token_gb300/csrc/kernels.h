@@ -246,6 +246,8 @@ struct SampleFilteredArgs {
     const float *u = nullptr;             // [B][J]
     int32_t *out = nullptr;               // [B][J]
 };
+constexpr int kSfMaxV = 1 << 22;   // masses of 2^40 at most: a row's sum stays below 2^63
+constexpr int kSfMaxJ = 1 << 30;   // loops over the draws stay below 2^31
 cudaError_t launch_sample_filtered(const SampleFilteredArgs &a, cudaStream_t s);
 
 // Log probabilities of given tokens, entropy and the top alternatives of B rows of

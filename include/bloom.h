@@ -427,7 +427,8 @@ bloom_status bloom_op_sample(const float *logits, int32_t B, int32_t V, int64_t 
  * maximum; +inf logits share the whole mass.  Masses are 2^-40 fixed point, summed in
  * 64-bit integers: the result does not depend on the order of summation.  A row
  * where nothing takes part gives -1.  BLOOM_E_INVALID for null or misaligned
- * pointers, B outside 0..65535, V < 1, ld < V, J < 0 (B = 0 or J = 0 does nothing). */
+ * pointers, B outside 0..65535, V outside 1..2^22, ld < V, J outside 0..2^30 (B = 0 or
+ * J = 0 does nothing). */
 bloom_status bloom_op_sample_filtered(const float *logits, int32_t B, int32_t V, int64_t ld,
                                       const float *temperature, const int32_t *top_k,
                                       const float *top_p, const float *min_p, const float *u,

@@ -202,3 +202,27 @@ def test_streams_and_graphs():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, res)
+
+
+@pytest.mark.parametrize("k,p", [(0, 0.5), (0, 1.0), (3000000, 1.0), (100, 0.5)])
+@pytest.mark.parametrize("B", [1, 310])
+def test_longest_rows_of_equal_logits(B, k, p):
+    """The largest sums of masses that there are: 2^22 tokens of the maximum's."""
+    V = 1 << 22
+    z = torch.full((1, V), -1.5, device=DEV).expand(B, V).contiguous()
+    u = np.tile(np.array([[0.0, 0.25, 0.5, 0.75, 1.0 - 2.0 ** -24]], dtype=np.float32), (B, 1))
+    got = run(z, u, [0.7] * B, [k] * B, [p] * B).cpu()
+    kept = min(k or V, V)
+    kept = kept if p == 1.0 else int(kept * p)
+    want = [min(int(float(x) * kept), kept - 1) for x in u[0]]
+    assert (got == torch.tensor(want, dtype=torch.int32)).all()
+
+
+def test_rows_of_other_lengths_side_by_side():
+    """Lengths around those at which clusters and lists change."""
+    for V in (511, 512, 513, 8191, 8192, 8193, 65535, 65536, 131072):
+        z = logits(3, V, 2.0)
+        check(z, uniforms(3, 5), [0.9] * 3, [0, 60, 0], [0.8, 1.0, 1.0], [0.0, 0.0, 0.02])
+    for B in (4, 5, 38, 39, 152, 153, 304, 305):
+        z = logits(B, 70000 if B > 300 else 9000, 2.0)
+        check(z, uniforms(B, 1), [0.9] * B, [0] * B, [0.5 + 0.4 * (b % 3) / 2 for b in range(B)], None)

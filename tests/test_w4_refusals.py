@@ -94,7 +94,7 @@ def test_sampling_refusals(lib):
     f = lib.bloom_op_sample_filtered
     ok = dict(z=X, B=2, V=8, ld=8, t=None, k=None, p=None, m=None, u=X, J=1, out=X)
     odd = C.c_void_p(18)
-    for kw in [dict(z=None), dict(z=odd), dict(B=-1), dict(B=65536), dict(V=0), dict(V=-8), dict(ld=7), dict(ld=-8), dict(t=odd),
+    for kw in [dict(z=None), dict(z=odd), dict(B=-1), dict(B=65536), dict(V=0), dict(V=-8), dict(V=2 ** 22 + 1, ld=2 ** 23), dict(J=2 ** 30 + 1), dict(ld=7), dict(ld=-8), dict(t=odd),
                dict(k=odd), dict(p=odd), dict(m=odd), dict(u=None), dict(u=odd), dict(J=-1), dict(out=None), dict(out=odd)]:
         a = dict(ok, **kw)
         assert f(a["z"], a["B"], a["V"], a["ld"], a["t"], a["k"], a["p"], a["m"], a["u"], a["J"], a["out"], None) == 1, kw
