@@ -11,14 +11,25 @@
 //    those of an mma.sync fragment.
 //  * The tokens are the N operand: f16 after a power of two for each token, in the order and
 //    swizzle of the shared-memory operand, so that a block of 256 columns is one bulk copy.
-//    A small kernel before this one lays them out (done here, the conversion would
-//    be repeated by every tile of rows: 100 instructions for a tile's 240).
-//  * A group's products make an accumulator of their own, in one of two TMEM buffers; four
-//    warps, a thread a row, add it times the row's scale to float32 sums in registers.
+//    A small kernel before this one lays them out (done here, every tile of rows would repeat
+//    the conversion).
+//  * A group's products make an accumulator of their own; four warps, a thread a row, add them times
+//    the rows' scales to float32 sums in registers, as many groups a wait as half of the accumulators hold.
 //  * Few tiles of rows: the columns are split over a cluster, whose sums meet through
-//    distributed shared memory, in rank order.
+//    distributed shared memory, in rank order.  Many: a CTA goes from tile to tile, and copies and
+//    products of the next one go on while the sums of the last are stored (250880 x 4096, 64 tokens: 312
+//    -> 262 us, 12 tokens: 143 -> 139).
 // Weights are loaded before the wait for the kernel before: that is the one that lays out
 // the tokens, and it starts its successors only after its own wait, when all work before it is done.
+// (Started at once, as the layer norms' successors are, this kernel's CTAs found the SMs partly taken: 12288
+// x 4096, 16 tokens, 15 -> 21 us.)
+//
+// 16 tokens, 12288 x 4096: 14.7 us (4.1 to read the weights); 32, 16384 x 4096, groups of 128 18.4 (5.4), of
+// 32 22; 64 25.8 (5.6); 12, 250880 x 4096 139 (83); 64 262 (84).  Bound by instructions: a block of 128 x
+// 256 takes about 3000 warp instructions, 900 of them the codes', a third the scales' and most others waits
+// and their polling; and at 64 tokens by L2, which gives a block's tokens, 32 KB, beside 17 KB of weights.  Four
+// widening warps, two tiles each, against eight: 12 tokens, 250880 x 4096 154 -> 151; scales by two groups a
+// wait: 151 -> 143, and 32 tokens in groups of 32 24.8 -> 20.6.
 #include <atomic>
 #include <math.h>
 
@@ -30,7 +41,7 @@
 namespace bloom {
 
 constexpr int kLtRows = 128, kLtTiles = kLtRows / kW4Rows;
-constexpr int kLtThreads = 448;      // producer, MMA issuer, 4 scaling warps, 8 widening warps
+constexpr int kLtThreads = 320;      // producer, MMA issuer, 4 scaling warps, 4 widening warps
 constexpr int kLtMaxSplits = 8;
 constexpr int kLtSteps = kW4Cols / 16;
 
@@ -113,6 +124,31 @@ __device__ __forceinline__ void lt_store_a(uint32_t taddr, const uint32_t (&r)[3
         "r"(r[31])
         : "memory");
 }
+// 32 columns of this thread's TMEM lane, on their way until tc_wait_ld().
+__device__ __forceinline__ void lt_load32(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+        "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void lt_load16(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+// Orders the loaded registers' uses behind the wait.
+template <int N>
+__device__ __forceinline__ void lt_wait_ld(uint32_t (&r)[N]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
 __device__ __forceinline__ bool lt_elect() {
     uint32_t r;
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
@@ -159,21 +195,26 @@ __global__ void __launch_bounds__(kLtThreads, LtCfg<NT, G>::kPerSm) linear_w4_tc
     extern __shared__ unsigned char lt_raw[];
     unsigned char *smem = lt_raw + ((0u - tc_smem(lt_raw)) & 1023u);
     constexpr int NA = C::kA, ND = C::kDB;
+    // groups at a time: a half block's, of half of the accumulators at most
+    constexpr int BG = SG / 2 < ND / 2 ? SG / 2 : ND / 2;
+    static_assert(ND % BG == 0 && SG / 2 % BG == 0, "groups at a time");
     __shared__ uint64_t full[ST], empty[ST], a_full[NA], a_empty[NA], d_full[ND], d_empty[ND], done;
     __shared__ uint32_t tmem_base;
     __shared__ float s_inv[NT];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int tile = blockIdx.x, split = blockIdx.y, S = (int)gridDim.y, m0 = (int)blockIdx.z * NT;
+    const int split = blockIdx.y, S = (int)gridDim.y, m0 = (int)blockIdx.z * NT;
     const int kb0 = (int)((long long)a.k_tiles * split / S), my_kb = (int)((long long)a.k_tiles * (split + 1) / S) - kb0;
-    const int here = min(kLtTiles, a.row_tiles - tile * kLtTiles);   // tiles of rows that there are
+    // this CTA's blocks: 128 rows at a time (every gridDim.x-th; with S > 1 one), their columns from kb0 on
+    const int of_rows = (a.row_tiles + kLtTiles - 1) / kLtTiles, mine_rows = (of_rows - (int)blockIdx.x - 1) / (int)gridDim.x + 1;
+    const int total = mine_rows * my_kb;   // fits: a block has 17 KB of weights
 
     if (tid == 0) {
         for (int s = 0; s < ST; ++s) {
             tc_mbar_init(&full[s], 1);
-            tc_mbar_init(&empty[s], 8 + 4 + 1);   // widening warps, scaling warps, the products' commit
+            tc_mbar_init(&empty[s], 4 + 4 + 1);   // widening warps, scaling warps, the products' commit
         }
         for (int b = 0; b < NA; ++b) {
-            tc_mbar_init(&a_full[b], 8);
+            tc_mbar_init(&a_full[b], 4);
             tc_mbar_init(&a_empty[b], 1);
         }
         for (int b = 0; b < ND; ++b) {
@@ -204,30 +245,46 @@ __global__ void __launch_bounds__(kLtThreads, LtCfg<NT, G>::kPerSm) linear_w4_tc
     if (warp == 0) {
         if (lane == 0) {
             // ---- copies: the weights of the first stages before the wait for the tokens
-            const uint32_t bytes = (uint32_t)(here * TB);
-            const unsigned char *wsrc = a.tiles + ((long long)kb0 * a.row_tiles + tile * kLtTiles) * TB;
-            const unsigned char *xsrc = a.image + ((size_t)blockIdx.z * a.k_tiles + kb0) * C::kX;
-            auto weights = [&](int i, int s) {
+            int tile = blockIdx.x, kb = 0;   // the next block of weights
+            auto weights = [&](int s) {
+                const uint32_t bytes = (uint32_t)(min(kLtTiles, a.row_tiles - tile * kLtTiles) * TB);
                 asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(tc_smem(&full[s])), "r"(bytes + C::kX) : "memory");
-                lt_bulk(smem + (size_t)s * C::kStage + C::kX, wsrc + (long long)i * a.row_tiles * TB, bytes, &full[s]);
+                lt_bulk(smem + (size_t)s * C::kStage + C::kX, a.tiles + ((long long)(kb0 + kb) * a.row_tiles + tile * kLtTiles) * TB, bytes,
+                        &full[s]);
+                if (++kb == my_kb) {
+                    kb = 0;
+                    tile += (int)gridDim.x;
+                }
             };
-            auto tokens = [&](int i, int s) { lt_bulk(smem + (size_t)s * C::kStage, xsrc + (size_t)i * C::kX, C::kX, &full[s]); };
-            const int pre = min(my_kb, ST);
-            for (int i = 0; i < pre; ++i) weights(i, i);
+            const unsigned char *xsrc = a.image + ((size_t)blockIdx.z * a.k_tiles + kb0) * C::kX;
+            int xb = 0;                      // and of tokens
+            auto tokens = [&](int s) {
+                lt_bulk(smem + (size_t)s * C::kStage, xsrc + (size_t)xb * C::kX, C::kX, &full[s]);
+                if (++xb == my_kb) xb = 0;
+            };
+            const int pre = min(total, ST);
+            for (int i = 0; i < pre; ++i) weights(i);
             griddep_wait();
-            for (int i = 0; i < pre; ++i) tokens(i, i);
-            int issued = pre;
-            for (int i = pre; i < my_kb && ok; ++i) {
-                const int s = i % ST;
-                ok = tc_mbar_wait_within(&empty[s], (uint32_t)((i / ST & 1) ^ 1), a.wait_ns);
+            for (int i = 0; i < pre; ++i) tokens(i);
+            int s = 0;
+            uint32_t parity = 0;
+            for (int i = pre; i < total; ++i) {
+                ok = tc_mbar_wait_within(&empty[s], parity, a.wait_ns);
                 if (!ok) break;
-                weights(i, s);
-                tokens(i, s);
-                ++issued;
+                weights(s);
+                tokens(s);
+                if (++s == ST) {
+                    s = 0;
+                    parity ^= 1u;
+                }
             }
-            for (int j = 0; j < ST && j < issued; ++j) {   // no copy lands after the CTA has ended
-                const int i = issued - 1 - j;
-                ok &= tc_mbar_wait(&full[i % ST], (uint32_t)(i / ST & 1), kTcWaitNs);
+            // no copy lands after the CTA has ended: the stages' last fills, oldest first
+            for (int j = 0; j < pre; ++j) {
+                ok &= tc_mbar_wait(&full[s], parity, kTcWaitNs);
+                if (++s == pre) {
+                    s = 0;
+                    parity ^= 1u;
+                }
             }
         }
     } else if (warp == 1) {
@@ -237,20 +294,16 @@ __global__ void __launch_bounds__(kLtThreads, LtCfg<NT, G>::kPerSm) linear_w4_tc
         const uint32_t tbase = __shfl_sync(0xffffffffu, tmem, 0), sbase = __shfl_sync(0xffffffffu, tc_smem(smem), 0);
         const bool lead = lt_elect();
         griddep_wait();
-        for (int n = lane; n < NT; n += 32) s_inv[n] = a.inv[m0 + n];
-        // groups at a time: a half block's, of half of the accumulators at most
-        constexpr int BG = SG / 2 < ND / 2 ? SG / 2 : ND / 2;
-        static_assert(ND % BG == 0 && SG / 2 % BG == 0, "groups at a time");
         int s = 0, ab = 0, db = 0;
         uint32_t sp = 0, ap = 0, dp = 1;   // the buffers' parities
-        for (int i = 0; i < my_kb && ok; ++i) {
+        for (int i = 0; i < total && ok; ++i) {
             const uint32_t desc0 = (sbase + (uint32_t)s * C::kStage) >> 4 & 0x3fffu;
 #pragma unroll
             for (int hb = 0; hb < 2; ++hb) {
 #pragma unroll
                 for (int g0 = 0; g0 < SG / 2; g0 += BG) {
                     // what the next groups need, in one round trip; the accumulators come free in order
-                    uint64_t *const last = &d_empty[db + BG - 1];
+                    uint64_t *const last = &d_empty[db];
                     ok = ok && lt_wait3(hb == 0 && g0 == 0 ? &full[s] : last, hb == 0 && g0 == 0 ? sp : dp, g0 == 0 ? &a_full[ab] : last,
                                         g0 == 0 ? ap : dp, last, dp, a.wait_ns);
                     ok = __all_sync(0xffffffffu, ok);
@@ -265,8 +318,8 @@ __global__ void __launch_bounds__(kLtThreads, LtCfg<NT, G>::kPerSm) linear_w4_tc
                                     const int step = gr * GS + k, at = hb * (kLtSteps / 2) + step;
                                     lt_mma(td, ta + (uint32_t)(8 * step), desc0 + (uint32_t)(at / 4 * NT * 8 + 2 * (at % 4)), idesc, k > 0);
                                 }
-                                tc_commit(&d_full[db + gr - g0]);
                             }
+                            tc_commit(&d_full[db]);
                         }
                     }
                     if ((db += BG) == ND) {
@@ -293,72 +346,100 @@ __global__ void __launch_bounds__(kLtThreads, LtCfg<NT, G>::kPerSm) linear_w4_tc
         // ---- sums: a thread a row
         const int r = quarter * 32 + lane, rr = r & 15;
         griddep_wait();
-        if (a.bias && tile * kLtRows + r < a.N) bias = bf2f(a.bias[tile * kLtRows + r]);
-        for (int i = 0; i < my_kb && ok; ++i) {
-            const int s = i % ST;
-            ok = __all_sync(0xffffffffu, tc_mbar_wait_within(&full[s], (uint32_t)(i / ST & 1), a.wait_ns));
-            if (!ok) break;
-            const unsigned char *sc = smem + (size_t)s * C::kStage + C::kX + (r >> 4) * TB + 2048 + (rr & 7) * 4 + (rr >> 3) * 2;
-            float scale[SG];
+        const float inv = r < NT ? a.inv[m0 + r] : 0.f;
+        int block = 0;
+        for (int tile = blockIdx.x; tile < of_rows; tile += (int)gridDim.x) {
+            const int n = tile * kLtRows + r;
+            bias = a.bias && n < a.N ? bf2f(a.bias[n]) : 0.f;
 #pragma unroll
-            for (int gr = 0; gr < SG; ++gr) scale[gr] = bf2f(*reinterpret_cast<const uint16_t *>(sc + gr * 32));
-            __syncwarp();
-            if (lane == 0) lt_arrive(&empty[s]);
-#pragma unroll
-            for (int gr = 0; gr < SG; ++gr) {
-                const int d = i * SG + gr;
-                ok = ok && __all_sync(0xffffffffu, tc_mbar_wait_within(&d_full[d % ND], (uint32_t)(d / ND & 1), a.wait_ns));
+            for (int i = 0; i < NT; ++i) acc[i] = 0.f;
+            for (int kb = 0; kb < my_kb && ok; ++kb, ++block) {
+                const int s = block % ST;
+                ok = __all_sync(0xffffffffu, tc_mbar_wait_within(&full[s], (uint32_t)(block / ST & 1), a.wait_ns));
                 if (!ok) break;
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const unsigned char *sc = smem + (size_t)s * C::kStage + C::kX + (r >> 4) * TB + 2048 + (rr & 7) * 4 + (rr >> 3) * 2;
+                float scale[SG];
 #pragma unroll
-                for (int c = 0; c < NT; c += 16) {
-                    float v[16];
-                    tc_ld16(tquarter + C::kD + (uint32_t)(d % ND * NT + c), v);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) acc[c + j] = fmaf(scale[gr], v[j], acc[c + j]);
-                }
-                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                for (int gr = 0; gr < SG; ++gr) scale[gr] = bf2f(*reinterpret_cast<const uint16_t *>(sc + gr * 32));
                 __syncwarp();
-                if (lane == 0) lt_arrive(&d_empty[d % ND]);
+                if (lane == 0) lt_arrive(&empty[s]);
+#pragma unroll
+                for (int g0 = 0; g0 < SG; g0 += BG) {
+                    const int d = block * SG + g0, db = d % ND;
+                    ok = ok && __all_sync(0xffffffffu, tc_mbar_wait_within(&d_full[db], (uint32_t)(d / ND & 1), a.wait_ns));
+                    if (!ok) break;
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    constexpr int COLS = BG * NT, AT = COLS < 32 || NT == 64 ? COLS : 32;   // columns; those of one wait
+#pragma unroll
+                    for (int c0 = 0; c0 < COLS; c0 += AT) {
+                        uint32_t v[AT];
+                        const uint32_t from = tquarter + C::kD + (uint32_t)(db * NT + c0);
+                        if constexpr (AT == 16) lt_load16(from, v);
+                        else
+#pragma unroll
+                            for (int c = 0; c < AT; c += 32) lt_load32(from + (uint32_t)c, v + c);
+                        lt_wait_ld(v);
+#pragma unroll
+                        for (int j = 0; j < AT; ++j)
+                            acc[(c0 + j) % NT] = fmaf(scale[g0 + (c0 + j) / NT], __uint_as_float(v[j]), acc[(c0 + j) % NT]);
+                    }
+                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) lt_arrive(&d_empty[db]);
+                }
+            }
+            // the activations' power of two
+            if (r < NT) s_inv[r] = inv;
+            asm volatile("bar.sync 1, 128;" ::: "memory");   // these four warps
+#pragma unroll
+            for (int i = 0; i < NT; ++i)                     // and the codes' 2^-16 back
+                acc[i] = ok ? acc[i] * 0x1p16f * s_inv[i] : __uint_as_float(0x7fc00000u);
+            if (S == 1 && n < a.N) {
+                const int mmax = min(a.M - m0, NT);
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+                    if (i < mmax) lt_store(a, m0 + i, n, bias, acc[i]);
             }
         }
-        if (!ok) {
-#pragma unroll
-            for (int i = 0; i < NT; ++i) acc[i] = __uint_as_float(0x7fc00000u);
-        }
     } else {
-        // ---- codes to f16 in TMEM, 128 columns at a time: a warp a tile of rows
-        const int mine = 2 * quarter + (warp - 6) / 4;
-        for (int i = 0; i < my_kb && ok; ++i) {
+        // ---- codes to f16 in TMEM, 128 columns at a time: a warp two tiles of rows
+        for (int i = 0; i < total && ok; ++i) {
             const int s = i % ST;
             ok = __all_sync(0xffffffffu, tc_mbar_wait_within(&full[s], (uint32_t)(i / ST & 1), a.wait_ns));
             if (!ok) break;
-            const unsigned char *tile = smem + (size_t)s * C::kStage + C::kX + mine * TB + lane * 16;
-            uint4 v[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) v[c] = *reinterpret_cast<const uint4 *>(tile + c * 512);
-            __syncwarp();
-            if (lane == 0) lt_arrive(&empty[s]);
+            const unsigned char *tile = smem + (size_t)s * C::kStage + C::kX + 2 * quarter * TB + lane * 16;
 #pragma unroll
             for (int hb = 0; hb < 2; ++hb) {
-                const int h = 2 * i + hb;
-                uint32_t r[32];
+                uint4 v[2][2];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint4 &c = v[2 * hb + (j >> 1)];
-                    const uint32_t w0 = j & 1 ? c.z : c.x, w1 = j & 1 ? c.w : c.y;
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int o = 0; o < 2; ++o) {
-                        r[8 * j + 4 * o] = w4_pair(w0, 2 * o);
-                        r[8 * j + 4 * o + 1] = w4_pair(w0, 2 * o + 1);
-                        r[8 * j + 4 * o + 2] = w4_pair(w1, 2 * o);
-                        r[8 * j + 4 * o + 3] = w4_pair(w1, 2 * o + 1);
-                    }
+                    for (int c = 0; c < 2; ++c) v[t][c] = *reinterpret_cast<const uint4 *>(tile + t * TB + (2 * hb + c) * 512);
+                if (hb == 1) {
+                    __syncwarp();
+                    if (lane == 0) lt_arrive(&empty[s]);
                 }
+                const int h = 2 * i + hb;
                 if (h >= NA) ok = ok && __all_sync(0xffffffffu, tc_mbar_wait_within(&a_empty[h % NA], (uint32_t)((h / NA - 1) & 1), a.wait_ns));
                 if (!ok) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                lt_store_a(tquarter + ((uint32_t)(16 * (mine & 1)) << 16) + (uint32_t)(h % NA * 64), r);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    uint32_t r[32];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint4 &c = v[t][j >> 1];
+                        const uint32_t w0 = j & 1 ? c.z : c.x, w1 = j & 1 ? c.w : c.y;
+#pragma unroll
+                        for (int o = 0; o < 2; ++o) {
+                            r[8 * j + 4 * o] = w4_pair(w0, 2 * o);
+                            r[8 * j + 4 * o + 1] = w4_pair(w0, 2 * o + 1);
+                            r[8 * j + 4 * o + 2] = w4_pair(w1, 2 * o);
+                            r[8 * j + 4 * o + 3] = w4_pair(w1, 2 * o + 1);
+                        }
+                    }
+                    lt_store_a(tquarter + ((uint32_t)(16 * t) << 16) + (uint32_t)(h % NA * 64), r);
+                }
                 tc_wait_st();
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                 __syncwarp();
@@ -369,21 +450,10 @@ __global__ void __launch_bounds__(kLtThreads, LtCfg<NT, G>::kPerSm) linear_w4_tc
     if (!ok && a.err) atomicOr(a.err, kErrTimeout);
     __syncwarp();
 
-    // ---- the activations' power of two, and the epilogue
-    const bool sums = warp >= 2 && warp < 6;
-    const int r = quarter * 32 + lane, n = tile * kLtRows + r, mmax = min(a.M - m0, NT);
-    __syncthreads();                 // the tokens' powers
-    if (sums) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i) acc[i] = acc[i] * 0x1p16f * s_inv[i];   // and the codes' 2^-16 back
-    }
-    if (S == 1) {
-        if (sums && n < a.N) {
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-                if (i < mmax) lt_store(a, m0 + i, n, bias, acc[i]);
-        }
-    } else {
+    if (S > 1) {
+        // ---- the splits' sums
+        const bool sums = warp >= 2 && warp < 6;
+        const int r = quarter * 32 + lane, n = (int)blockIdx.x * kLtRows + r, mmax = min(a.M - m0, NT);
         // Four tokens at a time to the rank that finishes them, into its ring: [split][row][its groups]
         const int groups = (mmax + 3) / 4, each = (groups + S - 1) / S;
         float4 *recv = reinterpret_cast<float4 *>(smem);
@@ -461,8 +531,11 @@ static cudaError_t lt_launch(LinearW4Args a, void *workspace, int sms, cudaStrea
     // as many splits as leave all CTAs resident at once
     int S = 1;
     while (S < kLtMaxSplits && (long long)tiles * (S + 1) <= (long long)sms * C::kPerSm && S + 1 <= a.k_tiles) ++S;
+    // more tiles than that: each CTA takes several, as many as the others
+    const int slots = sms * C::kPerSm, wide = blocks < slots ? slots / blocks : 1;
+    const int each = S > 1 || tiles < wide ? 1 : (tiles + wide - 1) / wide;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)tiles, (unsigned)S, (unsigned)blocks);
+    cfg.gridDim = dim3((unsigned)((tiles + each - 1) / each), (unsigned)S, (unsigned)blocks);
     cfg.blockDim = dim3(kLtThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = s;
