@@ -24,8 +24,8 @@
 // (Started at once, as the layer norms' successors are, this kernel's CTAs found the SMs partly taken: 12288
 // x 4096, 16 tokens, 15 -> 21 us.)
 //
-// 16 tokens, 12288 x 4096: 14.7 us (4.1 to read the weights); 32, 16384 x 4096, groups of 128 18.4 (5.4), of
-// 32 22; 64 25.8 (5.6); 12, 250880 x 4096 139 (83); 64 262 (84).  Bound by instructions: a block of 128 x
+// 16 tokens, 12288 x 4096: 14.3 us (4.1 to read the weights); 32, 16384 x 4096, groups of 128 17.6 (5.4), of
+// 32 21; 64 25.8 (5.6); 12, 250880 x 4096 139 (83); 64 262 (84).  Bound by instructions: a block of 128 x
 // 256 takes about 3000 warp instructions, 900 of them the codes', a third the scales' and most others waits
 // and their polling; and at 64 tokens by L2, which gives a block's tokens, 32 KB, beside 17 KB of weights.  Four
 // widening warps, two tiles each, against eight: 12 tokens, 250880 x 4096 154 -> 151; scales by two groups a
@@ -239,7 +239,6 @@ __global__ void __launch_bounds__(kLtThreads, LtCfg<NT, G>::kPerSm) linear_w4_tc
     float acc[NT];                   // scaling warps: this thread's row
 #pragma unroll
     for (int i = 0; i < NT; ++i) acc[i] = 0.f;
-    float bias = 0.f;
     bool ok = true;
 
     if (warp == 0) {
@@ -350,7 +349,7 @@ __global__ void __launch_bounds__(kLtThreads, LtCfg<NT, G>::kPerSm) linear_w4_tc
         int block = 0;
         for (int tile = blockIdx.x; tile < of_rows; tile += (int)gridDim.x) {
             const int n = tile * kLtRows + r;
-            bias = a.bias && n < a.N ? bf2f(a.bias[n]) : 0.f;
+            const float bias = S == 1 && a.bias && n < a.N ? bf2f(a.bias[n]) : 0.f;
 #pragma unroll
             for (int i = 0; i < NT; ++i) acc[i] = 0.f;
             for (int kb = 0; kb < my_kb && ok; ++kb, ++block) {
@@ -453,7 +452,7 @@ __global__ void __launch_bounds__(kLtThreads, LtCfg<NT, G>::kPerSm) linear_w4_tc
     if (S > 1) {
         // ---- the splits' sums
         const bool sums = warp >= 2 && warp < 6;
-        const int r = quarter * 32 + lane, n = (int)blockIdx.x * kLtRows + r, mmax = min(a.M - m0, NT);
+        const int r = quarter * 32 + lane, mmax = min(a.M - m0, NT);
         // Four tokens at a time to the rank that finishes them, into its ring: [split][row][its groups]
         const int groups = (mmax + 3) / 4, each = (groups + S - 1) / S;
         float4 *recv = reinterpret_cast<float4 *>(smem);
@@ -472,23 +471,22 @@ __global__ void __launch_bounds__(kLtThreads, LtCfg<NT, G>::kPerSm) linear_w4_tc
             }
         }
         lt_cluster_sync();
-        if (sums && n < a.N) {
-            for (int l = 0; l < each; ++l) {
-                const int q = l * S + split;
-                if (q >= groups) break;
-                float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int p = 0; p < S; ++p) {
-                    const float4 v = recv[(p * kLtRows + r) * each + l];
-                    t.x += v.x;
-                    t.y += v.y;
-                    t.z += v.z;
-                    t.w += v.w;
-                }
-                const float f[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (4 * q + j < mmax) lt_store(a, m0 + 4 * q + j, n, bias, f[j]);
+        for (int i = tid; i < each * kLtRows; i += kLtThreads) {   // all warps: a row's four tokens each
+            const int l = i / kLtRows, row = i % kLtRows, q = l * S + split, n = (int)blockIdx.x * kLtRows + row;
+            if (q >= groups || n >= a.N) continue;
+            const float bias = a.bias ? bf2f(a.bias[n]) : 0.f;
+            float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int p = 0; p < S; ++p) {
+                const float4 v = recv[(p * kLtRows + row) * each + l];
+                t.x += v.x;
+                t.y += v.y;
+                t.z += v.z;
+                t.w += v.w;
             }
+            const float f[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (4 * q + j < mmax) lt_store(a, m0 + 4 * q + j, n, bias, f[j]);
         }
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
