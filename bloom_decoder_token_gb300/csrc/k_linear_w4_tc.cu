@@ -59,44 +59,62 @@ struct LtCfg {
 
 // Where a token's elements lie in a block of 256 columns: four boxes of 64 columns, rows of 128
 // bytes (a token each), 16-byte pieces swizzled by the row.  A product of 16 columns takes, as the weights'
-// fragments have it, place 4 q + i of product 2 j + o from column 32 j + 8 q + 4 o + i.
-__global__ void __launch_bounds__(256) w4_tokens_kernel(const uint16_t *x, long long ldx, int M, int K, int NT, int k_tiles,
-                                                        unsigned char *image, float *inv) {
-    __shared__ uint32_t red[8];
+// fragments have it, place 4 q + i of product 2 j + o from column 32 j + 8 q + 4 o + i: half of eight columns goes
+// to the left or right half of piece 4 (j & 1) + 2 o + q / 2.
+// One CTA a token; up to 8192 columns are read once (behind a layer norm 12 tokens, 4096 x 16384: 23.0 -> 22.1 us
+// against two readings of all).  With 512 threads it took so much of its SMs that the next kernel's clusters found
+// no room until it had ended: 16 tokens, 12288 x 4096, 14.3 -> 15.5.
+constexpr int kLtTokenThreads = 256;
+__global__ void __launch_bounds__(kLtTokenThreads) w4_tokens_kernel(const uint16_t *x, long long ldx, int M, int K, int NT, int k_tiles,
+                                                                    unsigned char *image, float *inv) {
+    constexpr int T = kLtTokenThreads, R = 4;
+    __shared__ uint32_t red[T / 32];
     griddep_wait();
     griddep_launch();
-    const int n = blockIdx.x, m = blockIdx.y * NT + n, tid = threadIdx.x;
+    const int n = blockIdx.x, m = blockIdx.y * NT + n, tid = threadIdx.x, chunks = k_tiles * 32;   // of eight columns
     const uint16_t *row = x + (long long)m * ldx;
-    uint32_t m2 = 0;
-    if (m < M)
-        for (int k = 8 * tid; k < K; k += 8 * 256) {
-            const uint4 v = ld_act(row + k);
-            m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+    uint4 v[R];
+    auto load = [&](int c0) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int c = c0 + i * T + tid;
+            v[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (m < M && 8 * c < K) v[i] = ld_act(row + 8 * c);
         }
+    };
+    uint32_t m2 = 0;
+    for (int c0 = 0; c0 < chunks; c0 += R * T) {
+        load(c0);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu), __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu)));
+    }
     uint32_t amax = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
     if ((tid & 31) == 0) red[tid >> 5] = amax;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = max(amax, red[i]);
+    for (int i = 0; i < T / 32; ++i) amax = max(amax, red[i]);
     // 2^up brings the largest element to [2^14, 2^15); an infinity or NaN makes the token NaN
     const int up = min(120, 14 + 127 - (int)(amax >> 7));
     const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
     if (tid == 0)
         inv[m] = amax >= 0x7f80u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(127 - up) << 23);
-    image += (size_t)blockIdx.y * k_tiles * NT * 512;
-    for (int p = tid; p < k_tiles * 32; p += 256) {   // 16-byte pieces: block p / 32, box, piece
-        const int box = p / 8, c = p & 7;
-        const int k = 64 * box + 32 * (c >> 2) + 16 * (c & 1) + 4 * ((c >> 1) & 1);
-        uint32_t o[4];
+    image += (size_t)blockIdx.y * k_tiles * NT * 512 + n * 128;
+    for (int c0 = 0; c0 < chunks; c0 += R * T) {
+        if (chunks > R * T) load(c0);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint2 v = make_uint2(0u, 0u);
-            if (m < M && k + 8 * h < K) v = __ldg(reinterpret_cast<const uint2 *>(row + k + 8 * h));
-            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[2 * h]) : "f"(bf_hi(v.x) * mul), "f"(bf_lo(v.x) * mul));
-            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[2 * h + 1]) : "f"(bf_hi(v.y) * mul), "f"(bf_lo(v.y) * mul));
+        for (int i = 0; i < R; ++i) {
+            const int c = c0 + i * T + tid;
+            if (c >= chunks) break;
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[e]) : "f"(bf_hi(w[e]) * mul), "f"(bf_lo(w[e]) * mul));
+            const int piece = (c & 4) | (c >> 1 & 1);
+            unsigned char *box = image + (size_t)(c >> 3) * NT * 128 + 8 * (c & 1);
+            *reinterpret_cast<uint2 *>(box + ((piece ^ (n & 7)) << 4)) = make_uint2(o[0], o[1]);
+            *reinterpret_cast<uint2 *>(box + (((piece | 2) ^ (n & 7)) << 4)) = make_uint2(o[2], o[3]);
         }
-        *reinterpret_cast<uint4 *>(image + ((size_t)(box / 4) * 4 + box % 4) * NT * 128 + n * 128 + ((c ^ (n & 7)) << 4)) =
-            make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
@@ -524,7 +542,7 @@ static cudaError_t lt_launch(LinearW4Args a, void *workspace, int sms, cudaStrea
     float *inv = reinterpret_cast<float *>(image + (size_t)blocks * a.k_tiles * C::kX);
     a.image = image;
     a.inv = inv;
-    e = launch_pdl(w4_tokens_kernel, dim3(NT, (unsigned)blocks), dim3(256), s, a.x, a.ldx, a.M, a.K, NT, a.k_tiles, image, inv);
+    e = launch_pdl(w4_tokens_kernel, dim3(NT, (unsigned)blocks), dim3(kLtTokenThreads), s, a.x, a.ldx, a.M, a.K, NT, a.k_tiles, image, inv);
     if (e != cudaSuccess) return e;
     // as many splits as leave all CTAs resident at once
     int S = 1;
