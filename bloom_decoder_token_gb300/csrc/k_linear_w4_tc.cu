@@ -25,7 +25,7 @@
 // x 4096, 16 tokens, 15 -> 21 us.)
 //
 // 16 tokens, 12288 x 4096: 14.3 us (4.1 to read the weights); 32, 16384 x 4096, groups of 128 17.6 (5.4), of
-// 32 21; 64 25.8 (5.6); 12, 250880 x 4096 139 (83); 64 262 (84).  Bound by instructions: a block of 128 x
+// 32 21; 64 25.8 (5.6); 12, 250880 x 4096 137 (83); 64 262 (84).  Bound by instructions: a block of 128 x
 // 256 takes about 3000 warp instructions, 900 of them the codes', a third the scales' and most others waits
 // and their polling; and at 64 tokens by L2, which gives a block's tokens, 32 KB, beside 17 KB of weights.  Four
 // widening warps, two tiles each, against eight: 12 tokens, 250880 x 4096 154 -> 151; scales by two groups a
@@ -406,8 +406,10 @@ __global__ void __launch_bounds__(kLtThreads, LtCfg<NT, G>::kPerSm) linear_w4_tc
                 }
             }
             // the activations' power of two
-            if (r < NT) s_inv[r] = inv;
-            asm volatile("bar.sync 1, 128;" ::: "memory");   // these four warps
+            if (tile == (int)blockIdx.x) {
+                if (r < NT) s_inv[r] = inv;
+                asm volatile("bar.sync 1, 128;" ::: "memory");   // these four warps
+            }
 #pragma unroll
             for (int i = 0; i < NT; ++i)                     // and the codes' 2^-16 back
                 acc[i] = ok ? acc[i] * 0x1p16f * s_inv[i] : __uint_as_float(0x7fc00000u);
@@ -469,6 +471,7 @@ __global__ void __launch_bounds__(kLtThreads, LtCfg<NT, G>::kPerSm) linear_w4_tc
 
     if (S > 1) {
         // ---- the splits' sums
+        griddep_wait();              // every thread's own, for the bias and y
         const bool sums = warp >= 2 && warp < 6;
         const int r = quarter * 32 + lane, mmax = min(a.M - m0, NT);
         // Four tokens at a time to the rank that finishes them, into its ring: [split][row][its groups]

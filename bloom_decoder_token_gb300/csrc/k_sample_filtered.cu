@@ -16,7 +16,7 @@
 //
 // The logits are read once from HBM (few rows) and then from L2: one row is bound by the latency of
 // its phases (1 x 250880: greedy 9 us, top-k 50 13, top-p 0.95 30), many by instructions, 60 % of the
-// issue slots (509 x 250880, 76 us from HBM: greedy 189, top-k 50 194, top-p 0.95 of normal logits 462:
+// issue slots (509 x 250880, 76 us from HBM: greedy 189, top-k 50 194, top-p 0.95 of normal logits 435:
 // some 70 instructions a logit).  One cluster of up to 16 CTAs a row, each a slice of the vocabulary:
 //  1. the maximum and minimum, and every thread's own maximum;
 //  2. where few tokens can be kept, these come to the first CTA, which ranks them and does the
