@@ -226,3 +226,17 @@ def test_rows_of_other_lengths_side_by_side():
     for B in (4, 5, 38, 39, 152, 153, 304, 305):
         z = logits(B, 70000 if B > 300 else 9000, 2.0)
         check(z, uniforms(B, 1), [0.9] * B, [0] * B, [0.5 + 0.4 * (b % 3) / 2 for b in range(B)], None)
+
+
+def test_the_most_rows():
+    """65535 short rows: as many rows of the same values in smaller calls."""
+    z = logits(65535, 9, 2.0).to(DEV)
+    u = torch.rand(65535, generator=torch.Generator(device=DEV).manual_seed(3), device=DEV)
+    t, p = torch.full((65535,), 0.8, device=DEV), torch.full((65535,), 0.9, device=DEV)
+    k = torch.arange(65535, device=DEV, dtype=torch.int32) % 7
+    got = bg.op_sample_filtered(z, u, t, k, p)
+    for a in (0, 30000, 65435):
+        at = slice(a, a + 100)
+        assert torch.equal(got[at], bg.op_sample_filtered(z[at], u[at], t[at], k[at], p[at]))
+        for b in range(a, a + 100):
+            assert plain.agrees(int(got[b]), z[b].cpu().numpy(), float(t[b]), int(k[b]), float(p[b]), 0.0, float(u[b]))

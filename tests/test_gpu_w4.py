@@ -101,7 +101,7 @@ SHAPES = [  # tokens in one to eight column tiles and several blocks; one to eig
     (7, 2100, 8200), (8, 64, 16384), (9, 48, 520), (16, 1003, 4096), (13, 40, 12296), (17, 129, 2048), (31, 500, 2056),
     (32, 4096, 1024), (24, 64, 16392), (33, 100, 776), (64, 257, 2304), (65, 33, 264), (200, 40, 512),
     (2, 33, 33000), (12, 20, 40968), (20, 24, 20000), (1, 90000, 4360), (20, 12000, 2112), (10, 20000, 4608),
-    (1, 40000, 64),
+    (1, 40000, 64), (12, 90000, 520), (50, 45000, 264), (300, 5000, 512),
 ]
 
 
@@ -220,7 +220,7 @@ def test_no_tokens():
     assert bg.op_linear_w4(torch.empty(0, 64, dtype=torch.bfloat16, device=DEV), w4).shape == (0, 40)
 
 
-@pytest.mark.parametrize("M,n,k", [(3, 40000, 4608), (1, 40000, 2048), (12, 9000, 33000), (32, 20000, 4096)])
+@pytest.mark.parametrize("M,n,k", [(3, 40000, 4608), (1, 40000, 2048), (12, 9000, 33000), (32, 20000, 4096), (12, 90000, 520)])
 def test_expired_waits(M, n, k):
     """Waits bounded by a few nanoseconds: the call ends, flag 8 says so, whole outputs are NaN or as ever.  (Up to
     8 tokens the copies may land while the activations are converted, and no wait runs out.)"""
@@ -357,3 +357,40 @@ def test_a_step_of_a_small_model(B):
                 assert sample_plain.agrees(int(tok[b, j]), zc[b], f[0], 50, f[1], f[2], float(u[b, j]))
         want = torch.log_softmax(z.double(), 1).gather(1, tok.long())
         assert ((logp.double() - want).abs() <= 2.0 ** -24 * (V / 512 + 64) + 2.0 ** -22 * want.abs()).all()
+
+
+def test_more_blocks_of_tokens_than_fit_at_once():
+    """70000 tokens: more blocks of 64 than CTAs are resident, each going through all rows."""
+    M, n, k = 70000, 300, 264
+    w, x = weights(n, k), acts(M, k)
+    w4 = bg.op_w4_quantize(w, 64)
+    y = bg.op_linear_w4(x, w4, dtype=torch.float32)
+    check(y, *plain.linear(x, plain.values(w, 64), group=64))
+    assert torch.equal(bg.op_linear_w4(x[-64:], w4, dtype=torch.float32), y[-64:])
+
+
+def test_streams_and_graphs_of_many_tokens():
+    """Two streams at once on the same weights, two graphs with a workspace each, replayed side by side."""
+    w4, xs = bg.op_w4_quantize(weights(9000, 2056), 64), [acts(24, 2056, s) for s in (0, 9)]
+    want = [bg.op_linear_w4(x, w4) for x in xs]
+    need = bg.lib().bloom_op_linear_w4_workspace(w4.ref, 24)
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    outs = [[bg.op_linear_w4(x, w4, stream=s) for x, s in zip(xs, streams)] for _ in range(20)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for pair in outs for a, b in zip(pair, want))
+    graphs, bufs, ys = [], [x.clone() for x in xs], [torch.empty_like(w) for w in want]
+    rooms = [torch.empty(need, dtype=torch.uint8, device=DEV) for _ in xs]
+    for buf, y, room in zip(bufs, ys, rooms):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            bg.op_linear_w4(buf, w4, y=y, workspace=room)
+    for turn in range(10):
+        for i in (0, 1):
+            bufs[i].copy_(xs[(i + turn) & 1])
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(ys[i], want[(i + turn) & 1]) for i in (0, 1))
