@@ -15,8 +15,8 @@
 // shift all far tokens the same way.
 //
 // The logits are read once from HBM (few rows) and then from L2: one row is bound by the latency of
-// its phases (1 x 250880: greedy 9 us, top-k 50 13, top-p 0.95 30), many by instructions, 60 % of the
-// issue slots (509 x 250880, 76 us from HBM: greedy 189, top-k 50 194, top-p 0.95 of normal logits 435:
+// its phases (1 x 250880: greedy 8 us, top-k 50 11, top-p 0.95 29), many by instructions, 60 % of the
+// issue slots (509 x 250880, 76 us from HBM: greedy 183, top-k 50 186, top-p 0.95 of normal logits 430:
 // some 70 instructions a logit).  One cluster of up to 16 CTAs a row, each a slice of the vocabulary:
 //  1. the maximum and minimum, and every thread's own maximum;
 //  2. where few tokens can be kept, these come to the first CTA, which ranks them and does the
@@ -73,13 +73,14 @@ struct alignas(16) SfSmem {
     sf_u64 seg_mass[kSfSegments + 2];
     uint32_t seg_ties[kSfSegments + 2];
     alignas(16) uint32_t own_max[THREADS / 2];
-    uint32_t marks[kSfMaxCluster * kSfMarks];
+    alignas(16) uint32_t marks[kSfMaxCluster * kSfMarks];
     sf_u64 scan[2][kWarps];
     uint32_t scan_n[kWarps];
     sf_u64 part[kWarps][3];
     sf_u64 xch[kSfSlots][kSfMaxCluster];       // a value of every rank
     sf_u64 found[4];
-    double real[2];
+    double real;
+    float unit[3];
     int bin[4];
     uint32_t nlist;
 };
@@ -269,22 +270,28 @@ __device__ __forceinline__ uint32_t sf_select(SfSmem<THREADS> &sm, const SfRow &
 // target: the mass itself; floor: least key kept.
 template <int THREADS>
 __device__ __forceinline__ void sf_finish(SfSmem<THREADS> &sm, const SfRow &row, const SampleFilteredArgs &a, int b, int n, int k,
-                                          float part, sf_u64 target, uint32_t floor) {
+                                          float part, sf_u64 target, uint32_t floor, float first_u) {
     constexpr int PT = kSfRank / THREADS;
     const int tid = threadIdx.x;
     sf_u64 *sorted = sm.list + kSfRank, *mass = sorted + kSfRank;   // highest first
     if (tid == 0 && (n & 1)) sm.list[n] = 0ull;
     __syncthreads();
-    for (int i = tid; i < n; i += THREADS) {
-        const sf_u64 mine = sm.list[i];
+    const int parts = 4 * n <= THREADS ? 4 : 1;   // threads a token
+    for (int i0 = 0; i0 < n; i0 += THREADS) {
+        const int i = i0 + tid / parts;
+        const sf_u64 mine = i < n ? sm.list[i] : 0ull;
         int above = 0;
+        if (i < n)
 #pragma unroll 4
-        for (int j = 0; j < n; j += 2) {
-            const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(&sm.list[j]);
-            above += (v.x > mine) + (v.y > mine);
+            for (int j = 2 * (tid % parts); j < n; j += 2 * parts) {
+                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(&sm.list[j]);
+                above += (v.x > mine) + (v.y > mine);
+            }
+        for (int o = 1; o < parts; o *= 2) above += __shfl_xor_sync(0xffffffffu, above, o);
+        if (i < n && tid % parts == 0) {
+            sorted[above] = mine;
+            mass[above] = row.mass(sf_unkey((uint32_t)(mine >> 32)));
         }
-        sorted[above] = mine;
-        mass[above] = row.mass(sf_unkey((uint32_t)(mine >> 32)));
     }
     __syncthreads();
     const int upto = k > 0 ? min(n, k) : n;
@@ -336,7 +343,7 @@ __device__ __forceinline__ void sf_finish(SfSmem<THREADS> &sm, const SfRow &row,
         __syncthreads();
         const int nj = min(a.J - j0, kSfDigits);
         for (int j = tid; j < nj; j += THREADS) {
-            const float u = a.u[(long long)b * a.J + j0 + j];
+            const float u = j0 + j == tid ? first_u : a.u[(long long)b * a.J + j0 + j];
             pos[j] = min(u > 0.f ? (sf_u64)((double)u * (double)total) : 0ull, total - 1ull);
         }
         __syncthreads();
@@ -360,9 +367,15 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     uint32_t rank;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     if (tid == 0) sm.nlist = 0u;
-    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // every CTA runs: waited for before the first store to another
+    if (tid < kSfMaxCluster * kSfMarks) sm.marks[tid] = 0u;
+    sf_arrive();   // every CTA runs, and its marks are empty: waited for before the first store to another
     griddep_wait();
     const float *z = a.logits + (long long)b * a.ld;
+    // the row's settings and its first draws, on their way while the row is read
+    float t = a.temperature ? a.temperature[b] : 1.f;
+    int k = a.top_k ? a.top_k[b] : 0;
+    const float p = a.top_p ? a.top_p[b] : 1.f, mp = a.min_p ? a.min_p[b] : 0.f;
+    const float first_u = rank == 0 && tid < a.J ? a.u[(long long)b * a.J + tid] : 0.f;
 
     // this CTA's slice: whole float4s [at0, at0 + 4 nq) of the row's aligned body in segments of sq, and
     // beside them the row's ragged head (first CTA) and tail (last): indexes [s0, s1)
@@ -494,9 +507,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     block_range(kmax, kmin);
 
     // ---- the row's settings
-    float t = a.temperature ? a.temperature[b] : 1.f;
-    int k = a.top_k ? max(a.top_k[b], 0) : 0;
-    const float p = a.top_p ? a.top_p[b] : 1.f, mp = a.min_p ? a.min_p[b] : 0.f;
+    k = max(k, 0);
     const bool nucleus = p < 1.f && p > 0.f;   // NaN: off
     if (!(t > 0.f)) {
         t = 1.f;
@@ -512,41 +523,44 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
         const int wide = k <= 64 ? 4 : 2, groups = THREADS / wide;
         uint32_t g = max(thread_max, __shfl_xor_sync(0xffffffffu, thread_max, 1));
         if (wide == 4) g = max(g, __shfl_xor_sync(0xffffffffu, g, 2));
-        if (tid % wide == 0) sm.own_max[tid / wide] = g;
-        if (tid < kSfMaxCluster * kSfMarks) sm.marks[tid] = 0u;
+        const int part = tid % wide;             // of the group's threads
+        if (part == 0) sm.own_max[tid / wide] = g;
         __syncthreads();
-        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-        sf_sync();                               // every rank's marks are empty
-        if (tid < groups) {
-            const uint32_t mine = sm.own_max[tid];
-            int above = 0, upto = 0;
+        int above = 0, upto = 0;
 #pragma unroll 4
-            for (int i = 0; i < groups; i += 4) {
-                const uint4 o = *reinterpret_cast<const uint4 *>(&sm.own_max[i]);
-                above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
-                upto += (o.x >= mine) + (o.y >= mine) + (o.z >= mine) + (o.w >= mine);
-            }
-            // marks that fall on this value; equal ones write the same
-            for (int i = above / step; mine && i < kSfMarks && (i + 1) * step <= upto; ++i)
-                for (int r = 0; r < CS; ++r)
-                    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(sf_at(&sm.marks[rank * kSfMarks + i], (uint32_t)r)), "r"(mine) : "memory");
+        for (int i = 4 * part; i < groups; i += 4 * wide) {
+            const uint4 o = *reinterpret_cast<const uint4 *>(&sm.own_max[i]);
+            above += (o.x > g) + (o.y > g) + (o.z > g) + (o.w > g);
+            upto += (o.x >= g) + (o.y >= g) + (o.z >= g) + (o.w >= g);
         }
+        for (int o = 1; o < wide; o *= 2) {
+            above += __shfl_xor_sync(0xffffffffu, above, o);
+            upto += __shfl_xor_sync(0xffffffffu, upto, o);
+        }
+        sf_wait();
+        // marks that fall on this value; equal ones write the same
+        for (int i = above / step; g && i < kSfMarks && (i + 1) * step <= upto; ++i)
+            for (int r = part; r < CS; r += wide)
+                asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(sf_at(&sm.marks[rank * kSfMarks + i], (uint32_t)r)), "r"(g) : "memory");
     } else {
-        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        sf_wait();
     }
     publish(kSfRange, (sf_u64)kmax << 32 | kmin);
     sf_arrive();
     const bool floored = mp > 0.f && mp < 1.f;
     if (tid == 0) {   // in 64 bits, by one thread: few of an SM's units have them
-        sm.real[0] = fmin(1.4426950408889634 / (double)t, 3e38);
-        if (floored) sm.real[1] = (double)t * log((double)mp);
+        const double c = fmin(1.4426950408889634 / (double)t, 3e38);
+        sm.unit[0] = (float)c;
+        sm.unit[1] = (float)(c - (double)sm.unit[0]);
+        if (floored) sm.real = (double)t * log((double)mp);
     }
     __syncwarp();
     sf_wait();
     __syncthreads();   // the settings, written after that thread's arrival
-    for (int r = 0; r < CS; ++r) {
-        kmax = max(kmax, (uint32_t)(sm.xch[kSfRange][r] >> 32));
-        kmin = min(kmin, (uint32_t)sm.xch[kSfRange][r]);
+    {
+        const sf_u64 one = sm.xch[kSfRange][min(lane, CS - 1)];
+        kmax = __reduce_max_sync(0xffffffffu, (uint32_t)(one >> 32));
+        kmin = __reduce_min_sync(0xffffffffu, (uint32_t)one);
     }
     if (kmax == 0u) {
         if (rank == 0)
@@ -557,26 +571,38 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     if (bounded) {
         if (tid == 0) sm.found[0] = 0ull;
         __syncthreads();
-        if (tid < kSfMaxCluster * kSfMarks) {
-            const uint32_t mine = sm.marks[tid];
-            int above = 0, upto = 0;
-#pragma unroll 8
-            for (int i = 0; i < kSfMaxCluster * kSfMarks; ++i) {
-                above += sm.marks[i] > mine;
-                upto += sm.marks[i] >= mine;
-            }
-            if (mine && above < kSfMarks && kSfMarks <= upto) sm.found[0] = mine;
+        constexpr int PARTS = THREADS / (kSfMaxCluster * kSfMarks);   // threads a mark
+        const uint32_t mine = sm.marks[tid / PARTS];
+        int above = 0, upto = 0;
+#pragma unroll 4
+        for (int i = 4 * (tid % PARTS); i < CS * kSfMarks; i += 4 * PARTS) {
+            const uint4 o = *reinterpret_cast<const uint4 *>(&sm.marks[i]);
+            above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+            upto += (o.x >= mine) + (o.y >= mine) + (o.z >= mine) + (o.w >= mine);
         }
+#pragma unroll
+        for (int o = 1; o < PARTS; o *= 2) {
+            above += __shfl_xor_sync(0xffffffffu, above, o);
+            upto += __shfl_xor_sync(0xffffffffu, upto, o);
+        }
+        if (mine && above < kSfMarks && kSfMarks <= upto) sm.found[0] = mine;
         __syncthreads();
         bound = (uint32_t)sm.found[0];
     }
     SfRow row;
     row.top = sf_unkey(kmax);
-    row.c = (float)sm.real[0];
-    row.c_low = (float)(sm.real[0] - (double)row.c);
+    row.c = sm.unit[0];
+    row.c_low = sm.unit[1];
     SfCut cut = {0u, ~0u};
-    if (mp > 0.f)   // the least logit with exp((z - top) / t) >= min_p
-        cut.tighten(sf_key(floored && row.top < INFINITY ? fminf(__double2float_ru((double)row.top + sm.real[1]), row.top) : row.top), ~0u);
+    if (mp > 0.f) {   // the least logit with exp((z - top) / t) >= min_p
+        float least = row.top;
+        if (floored && row.top < INFINITY) {
+            if (tid == 0) sm.unit[2] = fminf(__double2float_ru((double)row.top + sm.real), row.top);
+            __syncthreads();
+            least = sm.unit[2];
+        }
+        cut.tighten(sf_key(least), ~0u);
+    }
     const uint32_t floor_key = cut.key;
     if (k == 1) cut.tighten(kmax, 1u);
 
@@ -595,9 +621,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
         __syncthreads();
         publish(kSfCount, sm.nlist);
         sf_sync();
-        uint32_t all = 0;
-        for (int r = 0; r < CS; ++r) all += (uint32_t)min(sm.xch[kSfCount][r], 1ull << 28);
-        return all;
+        return __reduce_add_sync(0xffffffffu, lane < CS ? (uint32_t)sm.xch[kSfCount][lane] : 0u);   // below 2^23
     };
     // The first CTA: the other ranks' lists behind its own.
     auto gather = [&]() {
@@ -626,7 +650,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     auto finish = [&](float part, sf_u64 target) {
         if (rank == 0) {
             const int n = min(gather(), kSfRank);
-            sf_finish(sm, row, a, b, n, k, part, target, max(floor_key, 1u));
+            sf_finish(sm, row, a, b, n, k, part, target, max(floor_key, 1u), first_u);
         }
         sf_sync();   // the lists have been read
     };
