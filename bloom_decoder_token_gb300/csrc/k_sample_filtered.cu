@@ -15,8 +15,8 @@
 // shift all far tokens the same way.
 //
 // The logits are read once from HBM (few rows) and then from L2: one row is bound by the latency of
-// its phases (1 x 250880: greedy 8 us, top-k 50 11, top-p 0.95 29), many by instructions, 60 % of the
-// issue slots (509 x 250880, 76 us from HBM: greedy 183, top-k 50 186, top-p 0.95 of normal logits 430:
+// its phases (1 x 250880: greedy 8 us, top-k 50 10.6, top-p 0.95 28), many by instructions, 60 % of the
+// issue slots (509 x 250880, 76 us from HBM: greedy 183, top-k 50 186, top-p 0.95 of normal logits 415:
 // some 70 instructions a logit).  One cluster of up to 16 CTAs a row, each a slice of the vocabulary:
 //  1. the maximum and minimum, and every thread's own maximum;
 //  2. where few tokens can be kept, these come to the first CTA, which ranks them and does the
@@ -80,7 +80,7 @@ struct alignas(16) SfSmem {
     sf_u64 xch[kSfSlots][kSfMaxCluster];       // a value of every rank
     sf_u64 found[4];
     double real;
-    float unit[3];
+    float unit[2], least;
     int bin[4];
     uint32_t nlist;
 };
@@ -183,6 +183,16 @@ struct SfBins {
         return m > less ? m - less : 0ull;
     }
 };
+
+// part * whole, 0 <= part < 1, rounded down or (up) up.  In integers: an SM has next to no 64-bit floating-point units.
+__device__ __forceinline__ sf_u64 sf_part(float part, sf_u64 whole, bool up) {
+    const uint32_t bits = __float_as_uint(part), e = bits >> 23, m = (bits & 0x7fffffu) | (e ? 0x800000u : 0u);
+    const int shift = 150 - (int)(e ? e : 1u);   // part = m * 2^-shift, shift >= 24
+    const sf_u64 low = whole * m, high = __umul64hi(whole, m);
+    const sf_u64 n = shift < 64 ? low >> shift | high << (64 - shift) : shift < 128 ? high >> (shift - 64) : 0ull;
+    const bool more = shift < 64 ? (low & ((1ull << shift) - 1ull)) != 0ull : true;   // of 64 and more digits some are not 0
+    return n + (up && more ? 1ull : 0ull);
+}
 
 __device__ __forceinline__ sf_u64 sf_warp_sum(sf_u64 v) {
 #pragma unroll
@@ -303,12 +313,7 @@ __device__ __forceinline__ void sf_finish(SfSmem<THREADS> &sm, const SfRow &row,
     }
     sf_u64 run = sf_block_scan(sm, sum, total);
     if (part < 1.f) {
-        if (tid == 0) {
-            const double want = ceil((double)part * (double)total);
-            sm.found[0] = want < 1.0 ? 1ull : min((sf_u64)want, total);
-        }
-        __syncthreads();
-        target = sm.found[0];
+        target = max(sf_part(part, total, true), 1ull);
     }
     // of the tokens up to top-k: those before which the target is not reached, down to the floor
     uint32_t kept = 0;
@@ -344,7 +349,7 @@ __device__ __forceinline__ void sf_finish(SfSmem<THREADS> &sm, const SfRow &row,
         const int nj = min(a.J - j0, kSfDigits);
         for (int j = tid; j < nj; j += THREADS) {
             const float u = j0 + j == tid ? first_u : a.u[(long long)b * a.J + j0 + j];
-            pos[j] = min(u > 0.f ? (sf_u64)((double)u * (double)total) : 0ull, total - 1ull);
+            pos[j] = u < 1.f ? sf_part(fmaxf(u, 0.f), total, false) : u >= 1.f ? total - 1ull : 0ull;
         }
         __syncthreads();
 #pragma unroll
@@ -548,10 +553,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     publish(kSfRange, (sf_u64)kmax << 32 | kmin);
     sf_arrive();
     const bool floored = mp > 0.f && mp < 1.f;
-    if (tid == 0) {   // in 64 bits, by one thread: few of an SM's units have them
-        const double c = fmin(1.4426950408889634 / (double)t, 3e38);
-        sm.unit[0] = (float)c;
-        sm.unit[1] = (float)(c - (double)sm.unit[0]);
+    if (tid == 0) {
+        // log2(e) / t: the quotient, and what it leaves of the numerator
+        constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = (float)(1.4426950408889634 - (double)1.4426950408889634f);
+        const float c = fminf(__fdiv_rn(kLog2e, t), 3e38f), low = __fdiv_rn(fmaf(-c, t, kLog2e) + kLog2eLow, t);
+        sm.unit[0] = c;
+        sm.unit[1] = fabsf(low) < c * 1e-6f ? low : 0.f;   // 0 where t is infinite, or next to 0
+        // in 64 bits, by one thread: few of an SM's units have them
         if (floored) sm.real = (double)t * log((double)mp);
     }
     __syncwarp();
@@ -597,9 +605,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     if (mp > 0.f) {   // the least logit with exp((z - top) / t) >= min_p
         float least = row.top;
         if (floored && row.top < INFINITY) {
-            if (tid == 0) sm.unit[2] = fminf(__double2float_ru((double)row.top + sm.real), row.top);
+            if (tid == 0) sm.least = fminf(__double2float_ru((double)row.top + sm.real), row.top);
             __syncthreads();
-            least = sm.unit[2];
+            least = sm.least;
         }
         cut.tighten(sf_key(least), ~0u);
     }
@@ -610,12 +618,16 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     auto collect = [&](uint32_t least) {
         const float from = sf_unkey(least);
         each([&](const float (&v)[kSfBatch], int at) {
-            if (!any_from(v, from)) return;
+            uint32_t in = 0;
+#pragma unroll
+            for (int e = 0; e < kSfBatch; ++e) in |= v[e] >= from ? 1u << e : 0u;
+            if (in == 0u) return;
+            uint32_t n = atomicAdd(&sm.nlist, (uint32_t)__popc(in));
 #pragma unroll
             for (int e = 0; e < kSfBatch; ++e)
-                if (v[e] >= from) {
-                    const uint32_t n = atomicAdd(&sm.nlist, 1u);
+                if (in >> e & 1u) {
                     if (n < kSfList) sm.list[n] = (sf_u64)sf_key(v[e]) << 32 | (uint32_t)~index_of(at, e);
+                    ++n;
                 }
         }, no_segment);
         __syncthreads();
@@ -668,7 +680,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
         n = 0ull;
         for (int r = 0; r < CS; ++r) n += sm.xch[kSfWhole][r];
         if (k > 0) n = min(n, (sf_u64)k);
-        if (nucleus && k != 1) n = max(1ull, min(n, (sf_u64)ceil((double)p * (double)n)));
+        if (nucleus && k != 1) n = max(1ull, min(n, sf_part(p, n, true)));
         cut.tighten(kmax, (uint32_t)n);
     }
 
@@ -1026,13 +1038,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
             }
         }
         if (nucleus) {
-            __syncthreads();
-            if (tid == 0) {
-                const double want = ceil((double)p * (double)whole);
-                sm.found[2] = want < 1.0 ? 1ull : min((sf_u64)want, whole);
-            }
-            __syncthreads();
-            const sf_u64 target = sm.found[2];
+            const sf_u64 target = max(sf_part(p, whole, true), 1ull);
             SfCut by_p = {0u, ~0u};
             sf_u64 held;
             const int r = find(true, target, false, by_p, held);
@@ -1095,8 +1101,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     for (int j = w; j < a.J; j += WARPS) {
         const long long out = (long long)b * a.J + j;
         const float u = a.u[out];
-        sf_u64 pos = u > 0.f ? (sf_u64)((double)u * (double)kept) : 0ull;
-        if (pos >= kept) pos = kept - 1ull;
+        const sf_u64 pos = u < 1.f ? sf_part(fmaxf(u, 0.f), kept, false) : u >= 1.f ? kept - 1ull : 0ull;
         // the place whose mass the draw falls into, with the ties and the mass before it
         sf_u64 tb = ties_before + sf_warp_scan(tie_sum) - tie_sum, own = 0ull, m3[3], t3[3];
 #pragma unroll
