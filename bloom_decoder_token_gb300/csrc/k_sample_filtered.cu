@@ -186,7 +186,7 @@ struct SfBins {
 
 // part * whole, 0 <= part < 1, rounded down or (up) up.  In integers: an SM has next to no 64-bit floating-point units.
 __device__ __forceinline__ sf_u64 sf_part(float part, sf_u64 whole, bool up) {
-    const uint32_t bits = __float_as_uint(part), e = bits >> 23, m = (bits & 0x7fffffu) | (e ? 0x800000u : 0u);
+    const uint32_t bits = __float_as_uint(part) & 0x7fffffffu, e = bits >> 23, m = (bits & 0x7fffffu) | (e ? 0x800000u : 0u);
     const int shift = 150 - (int)(e ? e : 1u);   // part = m * 2^-shift, shift >= 24
     const sf_u64 low = whole * m, high = __umul64hi(whole, m);
     const sf_u64 n = shift < 64 ? low >> shift | high << (64 - shift) : shift < 128 ? high >> (shift - 64) : 0ull;

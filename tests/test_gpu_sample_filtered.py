@@ -120,6 +120,18 @@ def test_uniforms_at_the_ends():
     assert got == [tokens[0]] * 3 + [tokens[-1]] * 4
 
 
+@pytest.mark.parametrize("k", [50, 0])
+@pytest.mark.parametrize("V", [1000, 90000])
+def test_the_smallest_uniforms(V, k):
+    """-0, subnormal and tiny numbers take the first kept token; so does a top-p next to 0."""
+    z = logits(1, V, 1.0)
+    u = np.array([[-0.0, 1e-45, 1e-40, 1.2e-38, 1e-30, -1e-40]], dtype=np.float32)
+    got = run(z.to(DEV), u, [1.0], [k], [0.9]).cpu()[0]
+    assert (got == int(plain.kept_of(z[0].numpy(), 1.0, k, 0.9, 0.0)[0][0])).all()
+    for p in (1e-45, 1e-39, 1e-20):
+        assert (run(z.to(DEV), u, [1.0], [k], [p]).cpu() == int(z[0].argmax())).all()
+
+
 def test_infinities_nan_and_empty_rows():
     z = logits(8, 6000, 1.5)
     z[0] = -torch.inf
