@@ -288,32 +288,53 @@ def test_workspace(M):
             bg.op_linear_w4(x, w4, workspace=bad)
 
 
-@pytest.mark.parametrize("M", [1, 300])
-def test_read_back_then_other_layers(M):
+def chained(step, turns=20):
+    """The results of step(0), step(1), ... launched back to back from one graph."""
+    step(0)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [step(i) for i in range(turns)]
+    graph.replay()
+    torch.cuda.synchronize()
+    return got
+
+
+SOON = [(256, 512), (1024, 1024), (4096, 1024), (16384, 4096)]     # from one wave of CTAs to many
+
+
+@pytest.mark.parametrize("n,k", SOON)
+@pytest.mark.parametrize("M", [1, 8, 300])
+def test_read_back_then_other_layers(M, n, k):
     """The matrix read back is another layer's weights at once, though that layer loads weights ahead."""
-    n, k = 16384, 4096
     x = acts(M, k)
     w4s = [bg.op_w4_quantize(weights(n, k, s), 64) for s in (0, 1)]
     out = torch.zeros(n, k, dtype=torch.bfloat16, device=DEV)
-    layer = bg.op_linear if M == 1 else bg.op_gemm
+    layer = {1: bg.op_linear, 8: bg.op_linear_tc, 300: bg.op_gemm}[M]
     want = [layer(x, bg.op_w4_read(w)) for w in w4s]
-    torch.cuda.synchronize()
-    for i in range(10):
+
+    def step(i):
         bg.op_w4_read(w4s[i & 1], out)
-        assert torch.equal(layer(x, out), want[i & 1])
+        return layer(x, out)
+
+    for i, y in enumerate(chained(step)):
+        assert torch.equal(y, want[i & 1])
 
 
-def test_quantized_anew_before_each_layer():
+@pytest.mark.parametrize("n,k", SOON)
+@pytest.mark.parametrize("M", [1, 12])
+def test_quantized_anew_before_each_layer(M, n, k):
     """Tiles that are written just before the layer that reads them, on both of its forms."""
-    w, w2 = weights(16384, 4096), weights(16384, 4096, 1)
-    q = bg.op_w4_quantize(w, 64)
-    for M in (1, 12):
-        x = acts(M, 4096)
-        want = [bg.op_linear_w4(x, bg.op_w4_quantize(v, 64)) for v in (w, w2)]
-        torch.cuda.synchronize()
-        for i in range(10):
-            bg.op_w4_quantize((w, w2)[i & 1], 64, out=q)
-            assert torch.equal(bg.op_linear_w4(x, q), want[i & 1])
+    ws, x = [weights(n, k, s) for s in (0, 1)], acts(M, k)
+    want = [bg.op_linear_w4(x, bg.op_w4_quantize(w, 64)) for w in ws]
+    q = bg.op_w4_quantize(ws[0], 64)
+
+    def step(i):
+        bg.op_w4_quantize(ws[i & 1], 64, out=q)
+        return bg.op_linear_w4(x, q)
+
+    for i, y in enumerate(chained(step)):
+        assert torch.equal(y, want[i & 1])
 
 
 @pytest.mark.parametrize("B", [3, 12])
