@@ -41,7 +41,8 @@ __device__ __forceinline__ void unpack8(const uint4 &v, float *f) {
 }
 
 // ---- loads ----
-// Weight stream: read once per step, so keep it out of L1.
+// Weight stream: read once per step, so keep it out of L1.  Non-coherent, so only of memory that
+// nothing writes from this kernel's start on, which may come before the end of the kernel before.
 __device__ __forceinline__ uint4 ld_stream(const void *p) {
     uint4 r;
     asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -49,9 +50,15 @@ __device__ __forceinline__ uint4 ld_stream(const void *p) {
                  : "l"(p));
     return r;
 }
-// Activations: small, re-read by every warp of the SM; cache in L1.
+// Activations: small, re-read by every warp of the SM; cache in L1.  The kernel before may
+// have been writing them when this one started: coherent, and behind griddep_wait().
 __device__ __forceinline__ uint4 ld_act(const void *p) {
-    return __ldg(reinterpret_cast<const uint4 *>(p));
+    uint4 r;
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p)
+                 : "memory");
+    return r;
 }
 
 // ---- asynchronous global -> shared copies (one 16-byte piece per call) ----

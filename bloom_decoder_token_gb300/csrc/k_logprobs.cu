@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(const LogprobsArgs a)
         for (int k = 0; k < kLpUnroll; ++k) {
             const int i = i0 + k * THREADS;
             float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-            if (inside || i < nq) f = __ldg(zq + i);
+            if (inside || i < nq) f = zq[i];
             v[4 * k] = f.x;
             v[4 * k + 1] = f.y;
             v[4 * k + 2] = f.z;
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(const LogprobsArgs a)
         int n = sm.ncand;
         auto each = [&](auto see) {   // the slice's logits and their indexes
             for (int i = tid; i < nq; i += THREADS) {
-                const float4 v = __ldg(zq + i);
+                const float4 v = zq[i];
                 see(v.x, at0 + 4 * i);
                 see(v.y, at0 + 4 * i + 1);
                 see(v.z, at0 + 4 * i + 2);

@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
             float4 v[6];
 #pragma unroll
             for (int k = 0; k < 6; ++k)
-                v[k] = i + k * THREADS < nq ? __ldg(body + i + k * THREADS) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                v[k] = i + k * THREADS < nq ? body[i + k * THREADS] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
 #pragma unroll
             for (int k = 0; k < 6; ++k) {
                 see(v[k].x);
