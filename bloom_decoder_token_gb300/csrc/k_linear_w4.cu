@@ -19,8 +19,8 @@
 //    meet in shared memory, in the warps' order, every 32 rows.
 //  * Longer rows are split over the CTAs of a cluster, whose sums meet through distributed
 //    shared memory, in rank order; still longer ones are taken in passes.
-// The first tiles are loaded before the wait for the kernel before (behind a layer norm 12288 x 4096,
-// one token: 12.3 -> 12.0 us, 4096 x 16384 17.8 -> 16.1); so what writes tiles starts nothing early.
+// Before the wait for the kernel before, which may be what writes the tiles, the first of them are only brought to
+// L2 (behind a layer norm 12288 x 4096, one token: 12.0 -> 11.4 us, 4096 x 16384 17.0 -> 16.0).
 // One token, from HBM: 4096 x 1024 3.6 us, 12288 x 4096 10.1 (4.0 to read the weights), 4096 x 16384
 // 12.0 (5.2, groups of 128), 57344 x 14336 94 (65), 14336 x 57344 111 (65); 8 tokens, 250880 x 4096: 107
 // (83).  Long matrices: bound by instructions as much as by HBM (a step of 32 rows takes the 16 warps
@@ -40,6 +40,10 @@ constexpr int kLw4Unit = 2;                      // tiles of a step: 32 rows
 constexpr int kLw4Partial = 16384;               // bytes of a buffer of sums that wait for the cluster
 constexpr int kLw4Stride = 20;                   // floats of a token's 16 rows in a warp's sums: no bank twice
 constexpr int kLw4MaxCluster = 8;
+// Tiles of a warp from 2 up to which its first ones are asked for ahead of the wait (one token, columns 4096, with
+// and without: 5 tiles 10.1 and 10.8 us, 11 15.6 and 16.0, 14 19.3 and 19.3, 27 33.7 and 32.7; 1 tile, 4096 x 1024,
+// 3.8 and 3.6).
+constexpr int kLw4Short = 16;
 
 template <int G>
 struct Lw4Smem {
@@ -67,6 +71,9 @@ __device__ __forceinline__ void lw4_bulk(void *dst, const void *src, uint32_t by
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(tc_smem(dst)),
                  "l"(src), "r"(bytes), "r"(tc_smem(bar))
                  : "memory");
+}
+__device__ __forceinline__ void lw4_prefetch(const void *src, uint32_t bytes) {   // both multiples of 16
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void lw4_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -109,7 +116,9 @@ __device__ __forceinline__ void lw4_store(const LinearW4Args &a, int m, int row,
     }
 }
 
-template <int G>
+// AHEAD: a form of its own, for with these lines in it the kernel took 109 us instead of 107 (8 tokens, 250880
+// x 4096) even where they were passed over.
+template <int G, bool AHEAD>
 __global__ void __launch_bounds__(32 * kLw4Warps, 1) linear_w4_kernel(const LinearW4Args a) {
     using Smem = Lw4Smem<G>;
     constexpr int NW = kLw4Warps, ST = Smem::kStages, TB = Smem::kTile, THREADS = 32 * NW, UT = kLw4Unit, SG = kW4Cols / G;
@@ -167,9 +176,13 @@ __global__ void __launch_bounds__(32 * kLw4Warps, 1) linear_w4_kernel(const Line
         --left;
         return true;
     };
+    // The first tiles go to L2 while the kernel before still runs; read they are behind the wait, for it may be
+    // what writes them.
+    if (AHEAD && lane == 0 && len > 0 && kt_of(0) < a.k_tiles)
+        lw4_prefetch(a.tiles + ((long long)kt_of(0) * a.row_tiles + row) * TB, (uint32_t)(min(min(ST, a.chunk), len) * TB));
+    griddep_wait();   // the tiles, the activations and y
     int flying = 0;
     for (int i = 0; i < ST; ++i) flying += issue(i);
-    griddep_wait();   // the activations and y
 
     uint32_t b[8][4];       // activations: token g, elements 32 j + 8 q + (0, 1 | 2, 3 | 4, 5 | 6, 7)
     float inv[2];           // 2^-up of tokens 2 q and 2 q + 1
@@ -316,7 +329,7 @@ static cudaError_t lw4_launch(LinearW4Args a, int sms, cudaStream_t s) {
     using Smem = Lw4Smem<G>;
     constexpr int kDevices = 64, NW = kLw4Warps;
     static std::atomic<int> known[kDevices][kLw4MaxCluster + 1];   // clusters that are resident at once
-    const auto kern = linear_w4_kernel<G>;
+    const auto kern = linear_w4_kernel<G, false>, ahead = linear_w4_kernel<G, true>;   // alike in what they need
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(32 * kLw4Warps);
     cfg.dynamicSmemBytes = Smem::kBytes;
@@ -334,6 +347,7 @@ static cudaError_t lw4_launch(LinearW4Args a, int sms, cudaStream_t s) {
     if (dev >= kDevices) return cudaErrorInvalidDevice;
     if (known[dev][1].load(std::memory_order_acquire) == 0) {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::kBytes);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(ahead, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::kBytes);
         if (e != cudaSuccess) return e;
         for (int P = kLw4MaxCluster; P >= 1; --P) {   // fewer than sms / P where a GPC's SMs are no multiple of P
             int most = sms / P;
@@ -373,7 +387,7 @@ static cudaError_t lw4_launch(LinearW4Args a, int sms, cudaStream_t s) {
     attr[0].val.clusterDim.x = (unsigned)a.cluster;
     cfg.gridDim = dim3((unsigned)(clusters * a.cluster));
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, a);
+    return cudaLaunchKernelEx(&cfg, run > 1 && run <= kLw4Short ? ahead : kern, a);
 }
 
 cudaError_t launch_linear_w4(LinearW4Args a, int sms, cudaStream_t s) {

@@ -61,7 +61,7 @@ __device__ __forceinline__ uint32_t w4_codes(uint32_t x, const W4Scale &s) {
 template <int G>
 __global__ void __launch_bounds__(kW4Threads) w4_quantize_kernel(const W4Args a) {
     constexpr int U = 128, J = U / 32, GJ = G / 32;   // columns of a pass (64 and 256: the same); 32-column steps of it, of a group
-    griddep_wait();   // no early start of the kernel after this one: linear layers load weights before they wait
+    griddep_wait();
     const long long tile = (long long)blockIdx.x * (kW4Threads / 32) + (threadIdx.x >> 5);
     const int ktiles = (a.K + kW4Cols - 1) / kW4Cols, row_tiles = (a.N + kW4Rows - 1) / kW4Rows;
     if (tile >= (long long)ktiles * row_tiles) return;
@@ -122,7 +122,6 @@ __global__ void __launch_bounds__(kW4Threads) w4_quantize_kernel(const W4Args a)
             *reinterpret_cast<uint4 *>(out + (u * U / 64 + j / 2) * 512 + lane * 16) =
                 make_uint4(words[j][0], words[j][1], words[j + 1][0], words[j + 1][1]);
     }
-    __threadfence();
 }
 
 // Codes 2 i and 2 i + 1 of a word times the scale, as bf16: 128 + |code| is a bf16 number, and the
@@ -137,7 +136,7 @@ __device__ __forceinline__ uint32_t w4_values(uint32_t w, int i, uint32_t scales
 
 template <int G>
 __global__ void __launch_bounds__(kW4Threads) w4_read_kernel(const W4Args a) {
-    // No early start here either: the matrix may be another linear layer's weights.
+    // No early start of the kernel after this one: the matrix may be its weights, loaded before it waits.
     griddep_wait();
     const long long tile = (long long)blockIdx.x * (kW4Threads / 32) + (threadIdx.x >> 5);
     const int ktiles = (a.K + kW4Cols - 1) / kW4Cols, row_tiles = (a.N + kW4Rows - 1) / kW4Rows;

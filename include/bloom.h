@@ -555,9 +555,7 @@ bloom_status bloom_op_attn_decode_kv8_wait_us(int32_t wait_us);
 /* ------------------------------------------------------------------------
  * 4-bit weights with group scales: value = code * scale, codes -7 .. 7, one
  * bf16 scale for every `group` neighbouring weights of a row of [n][k].  4.25
- * bits a weight at groups of 64 for a decode step to read.  The linear
- * layer may load tiles while kernels before it still run: what writes tiles (quantising, a
- * copy, a kernel of yours) must not let the kernel after it start early.
+ * bits a weight at groups of 64 for a decode step to read.
  * ------------------------------------------------------------------------ */
 typedef struct {
     void *tiles;           /* bloom_w4_bytes() bytes, 16-byte aligned, device: tiles of 16 rows x

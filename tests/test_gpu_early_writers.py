@@ -1,5 +1,5 @@
 """Operators behind a kernel that lets them start early and writes what they read late: whatever the kernel before
-writes (activations, rows that are added to, logits, settings), a call finds it written."""
+writes (tiles, activations, rows that are added to, logits, settings), a call finds it written."""
 import pytest
 import torch
 
@@ -38,6 +38,14 @@ def late(buf, contents, call, turns=6):
     torch.cuda.synchronize()
     for i, out in enumerate(got):
         assert all(torch.equal(a, b) for a, b in zip(out, want[i & 1])), i
+
+
+@pytest.mark.parametrize("n,k", SIZES)
+@pytest.mark.parametrize("M", [1, 8, 12, 40])
+def test_tiles(M, n, k):
+    q, x = [bg.op_w4_quantize(rand(n, k, seed=s, std=0.02), 64) for s in (0, 1)], rand(M, k)
+    w4 = bg.W4.empty(n, k, 64)
+    late(w4.tiles, [w.tiles for w in q], lambda: (bg.op_linear_w4(x, w4),))
 
 
 @pytest.mark.parametrize("n,k", SIZES)
