@@ -1267,7 +1267,7 @@ extern "C" bloom_status bloom_op_layernorm(const void *x, const void *g, const v
 extern "C" bloom_status bloom_op_linear(const bloom_linear *lin, int32_t int8, const void *x,
                                         int32_t M, int32_t N, int32_t K, int32_t epilogue, void *y,
                                         void *stream) {
-    g_pdl = true;
+    g_pdl = false;   // weights are loaded ahead, as a model's: here the kernel before may be writing them
     if (!lin) return fail(BLOOM_E_INVALID, "null argument");
     bloom_status st = check_linear(*lin, int8, N, K, "op", -1);
     if (st) return st;
@@ -1312,7 +1312,7 @@ extern "C" bloom_status bloom_op_gemm(const bloom_linear *lin, const void *x, in
 extern "C" bloom_status bloom_op_linear_tc(const bloom_linear *lin, int32_t int8, const void *x,
                                            int32_t M, int32_t N, int32_t K, int32_t epilogue,
                                            void *y, void *stream) {
-    g_pdl = true;
+    g_pdl = false;   // weights are loaded ahead, as a model's: here the kernel before may be writing them
     if (!lin) return fail(BLOOM_E_INVALID, "null argument");
     bloom_status st = check_linear(*lin, int8, N, K, "op", -1);
     if (st) return st;

@@ -136,7 +136,8 @@ __device__ __forceinline__ uint32_t w4_values(uint32_t w, int i, uint32_t scales
 
 template <int G>
 __global__ void __launch_bounds__(kW4Threads) w4_read_kernel(const W4Args a) {
-    // No early start of the kernel after this one: the matrix may be its weights, loaded before it waits.
+    // No early start of the kernel after this one: the matrix may be a model's weights, which its layers load before
+    // they wait.
     griddep_wait();
     const long long tile = (long long)blockIdx.x * (kW4Threads / 32) + (threadIdx.x >> 5);
     const int ktiles = (a.K + kW4Cols - 1) / kW4Cols, row_tiles = (a.N + kW4Rows - 1) / kW4Rows;

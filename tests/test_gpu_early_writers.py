@@ -1,5 +1,5 @@
 """Operators behind a kernel that lets them start early and writes what they read late: whatever the kernel before
-writes (tiles, activations, rows that are added to, logits, settings), a call finds it written."""
+writes (tiles, weights, activations, rows that are added to, logits, settings), a call finds it written."""
 import pytest
 import torch
 
@@ -98,3 +98,52 @@ def test_logits_and_settings(B, V):
     late(t, [row(0.1), row(2.0)], lambda: (bg.op_sample_filtered(z, hot, t),))
     tok = torch.zeros(B, 1, dtype=torch.int32, device=DEV)
     late(z, zs, lambda: bg.op_logprobs(z, tok, 5))
+
+
+@pytest.mark.parametrize("n,k", SIZES)
+@pytest.mark.parametrize("op,M", [("op_linear", 1), ("op_linear", 5), ("op_linear", 40), ("op_linear_tc", 1), ("op_linear_tc", 8),
+                                  ("op_linear_tc", 40), ("op_gemm", 300)])
+def test_bf16_weights(op, M, n, k):
+    layer, x, ws = getattr(bg, op), rand(M, k), [rand(n, k, seed=s, std=0.02) for s in (0, 1)]
+    w, xs = ws[0].clone(), [rand(M, k, seed=s) for s in (0, 1)]
+    late(w, ws, lambda: (layer(x, w),))
+    late(x, xs, lambda: (layer(x, w),))
+
+
+@pytest.mark.parametrize("n,k", [(256, 512), (16384, 4096)])
+@pytest.mark.parametrize("op,M", [("op_linear", 1), ("op_linear", 5), ("op_linear_tc", 8), ("op_linear_tc", 40)])
+def test_int8_weights(op, M, n, k):
+    g = torch.Generator(device=DEV).manual_seed(3)
+    qs = [torch.randint(-127, 128, (n, k), generator=g, device=DEV, dtype=torch.int8) for _ in range(2)]
+    layer, x, q, scale = getattr(bg, op), rand(M, k), qs[0].clone(), rand(n, std=0.001)
+    late(q, qs, lambda: (layer(x, q=q, scale=scale),))
+
+
+@pytest.mark.parametrize("M", [1, 8])
+def test_a_layers_output_as_weights(M):
+    """Normalised rows, and another layer's output, as the next layer's matrix."""
+    n, k = 2048, 1024
+    layer = {1: bg.op_linear, 8: bg.op_linear_tc}[M]
+    rows, x, one, zero = [rand(n, k, seed=s) for s in (0, 1)], rand(M, k), torch.ones(k, dtype=BF, device=DEV), torch.zeros(k, dtype=BF, device=DEV)
+    square, w = rand(k, k, std=0.03), torch.empty(n, k, dtype=BF, device=DEV)
+    for make in (lambda r: bg.op_layernorm(r, one, zero, y=w), lambda r: bg.op_gemm(r, square, y=w)):
+        want = []
+        for r in rows:
+            make(r)
+            torch.cuda.synchronize()
+            want.append(layer(x, w))
+            torch.cuda.synchronize()
+        got = []
+        for i in range(10):
+            make(rows[i & 1])
+            got.append(layer(x, w))
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, want[i & 1]) for i, y in enumerate(got))
+
+
+def test_lm_head():
+    """Its scratch is cleared between the writer and the layer."""
+    x, es = rand(4, 1024), [rand(30000, 1024, seed=s) for s in (0, 1)]
+    e = es[0].clone()
+    late(e, es, lambda: bg.op_lmhead_argmax(x, e))
+    late(e, es, lambda: bg.op_lmhead_argmax_noalloc(x, e))
