@@ -759,22 +759,24 @@ def _rows(name: str, t, dtype, shape, device):
     return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]   # one row: its stride means nothing
 
 
-def op_w4_quantize(w, group: int = 64, out: Optional[W4] = None, stream=None) -> W4:
+def op_w4_quantize(w, group: Optional[int] = None, out: Optional[W4] = None, stream=None) -> W4:
     """bf16 weights w [n][k] (rows may be strided, k a multiple of 8) in 4 bits: into
-    `out`, or new tiles."""
+    `out`, in its groups, or new tiles in groups of `group` (64 unless given)."""
     dev = w.device
     if w.dim() != 2:
         _bad(f"w: [n][k] expected, got {tuple(w.shape)}")
+    n, k = w.shape
+    if out is not None and (out.n, out.k, out.device) != (n, k, dev):
+        _bad(f"out: weights {(n, k)} on {dev} expected, got {(out.n, out.k)} on {out.device}")
+    if out is not None and group is not None and group != out.group:
+        _bad(f"group={group}: out has groups of {out.group}")
     there = _elsewhere(dev, stream)
     if there is not None:
         with there:
             return op_w4_quantize(w, group, out)
-    n, k = w.shape
     wp, ld = _rows("w", w, _BF16, (n, k), dev)
     if out is None:
-        out = W4.empty(n, k, group, dev)
-    elif (out.n, out.k, out.device) != (n, k, dev):
-        _bad(f"out: weights {(n, k)} on {dev} expected, got {(out.n, out.k)} on {out.device}")
+        out = W4.empty(n, k, 64 if group is None else group, dev)
     st = lib().bloom_op_w4_quantize(wp, ld, out.ref, _raw_stream(dev))
     if st:
         check(st)
