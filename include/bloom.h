@@ -420,10 +420,11 @@ bloom_status bloom_op_sample(const float *logits, int32_t B, int32_t V, int64_t 
  * those the shortest prefix that holds top_p of their mass, and of those the
  * ones with p >= min_p * max p.  Each draw takes the token where the kept mass,
  * summed in vocabulary order, first exceeds u times the whole of it.
- * temperature <= 0 or NaN, or top_p <= 0: the most probable token.  Off: top_k <= 0,
+ * temperature <= 0 or NaN, or top_p <= 0: the most probable token; a temperature
+ * below 2^-126 counts as that.  Off: top_k <= 0,
  * top_p >= 1 or NaN, min_p <= 0 or NaN; min_p >= 1 keeps the tokens of the largest
  * logit.  u < 0 or NaN counts as 0, u >= 1 takes the last kept token with mass.
- * NaN and -inf logits take no part, nor do logits 40 or more binades of mass below the
+ * NaN and -inf logits take no part, nor do logits 40 or more binades of mass, or 2^128, below the
  * maximum; +inf logits share the whole mass.  Masses are 2^-40 fixed point, summed in
  * 64-bit integers: the result does not depend on the order of summation.  A row
  * where nothing takes part gives -1.  BLOOM_E_INVALID for null or misaligned
