@@ -6,9 +6,8 @@
 //  * The products run on mma.sync m16n8k16 with 16 rows of weights as one operand and 8
 //    tokens as the other.  The codes are f16 numbers but for a turn and a mask a pair
 //    (w4_ops.cuh): 7 instructions for 8 codes, exact.  (e4m3 numbers and m16n8k32 would take 3,
-//    but that instruction is made of two f16 ones and conversions here: 5.1 clocks an SM
-//    against 2.5, and bf16 activations need two e4m3 columns.  12288 x 4096, one token:
-//    11.1 us with them.)
+//    but that instruction takes 5.1 clocks of an SM against 2.5 of the f16 one, and bf16
+//    activations need two e4m3 columns.  12288 x 4096, one token: 11.1 us with them.)
 //  * An activation goes in as f16 after a power of two that brings the largest of the
 //    token's 256 values to [2^14, 2^15): exact down to 2^-31 of that largest value; smaller
 //    ones are off by 2^-39 of it at most.  Sums are float32.
@@ -378,9 +377,9 @@ static cudaError_t lw4_launch(LinearW4Args a, int sms, cudaStream_t s) {
     if (clusters > a.row_tiles) clusters = a.row_tiles;
     const int rows = (a.row_tiles + clusters - 1) / clusters;   // of tiles, at most, of a cluster
     const bool direct = a.cluster == 1 && a.passes == 1;
-    const int fit = kLw4Partial / (a.M * 16 * 4);   // tiles of sums that wait for the cluster
+    const int fit = kLw4Partial / (a.M * kW4Rows * 4);   // tiles of sums that wait for the cluster
+    static_assert(kLw4Partial >= NW * kLw4Unit * kLw4MaxM * kW4Rows * 4, "a step's");
     a.row_warps = NW / a.k_warps < rows ? NW / a.k_warps : rows;
-    if (!direct && a.row_warps * kLw4Unit > fit) a.row_warps = fit / kLw4Unit;
     const int run = (rows + a.row_warps - 1) / a.row_warps;
     a.chunk = direct ? run : fit / a.row_warps / kLw4Unit * kLw4Unit;
     a.wide = a.ldy % 4 == 0 && ((uintptr_t)a.y & (a.f32 ? 15u : 7u)) == 0;
