@@ -547,7 +547,10 @@ static cudaError_t lt_launch(LinearW4Args a, void *workspace, int sms, cudaStrea
     a.inv = inv;
     e = launch_pdl(w4_tokens_kernel, dim3(NT, (unsigned)blocks), dim3(kLtTokenThreads), s, a.x, a.ldx, a.M, a.K, NT, a.k_tiles, image, inv);
     if (e != cudaSuccess) return e;
-    // as many splits as leave all CTAs resident at once
+    // As many splits as leave the CTAs of one block of tokens resident at once, however many blocks there are: a
+    // token's sums are the same beside any number of others (of more than 32).  That costs many tokens on a matrix of few
+    // rows: 1024 x 2048, 65 tokens 11.5 us, 300 24, 4096 271, where fewer splits as blocks fill the GPU take 11.5, 12.4
+    // and 76; 4096 x 4096, 300 57 (55), 4096 633 (435).  (Read the weights back and use the GEMM there.)
     int S = 1;
     while (S < kLtMaxSplits && (long long)tiles * (S + 1) <= (long long)sms * C::kPerSm && S + 1 <= a.k_tiles) ++S;
     // more tiles than that: each CTA takes several, as many as the others
