@@ -21,7 +21,7 @@
 // Before the wait for the kernel before, which may be what writes the tiles, the first of them are only brought to
 // L2 (behind a layer norm 12288 x 4096, one token: 12.0 -> 11.4 us, 4096 x 16384 17.0 -> 16.0).
 // One token, from HBM: 4096 x 1024 3.6 us, 12288 x 4096 10.1 (4.0 to read the weights), 4096 x 16384
-// 12.0 (5.2, groups of 128), 57344 x 14336 94 (65), 14336 x 57344 111 (65); 8 tokens, 250880 x 4096: 107
+// 12.1 (5.2, groups of 128), 57344 x 14336 94 (65), 14336 x 57344 111 (65); 8 tokens, 250880 x 4096: 107
 // (83).  Long matrices: bound by instructions as much as by HBM (a step of 32 rows takes the 16 warps
 // about as long as its tiles take to come); short ones by the start, 3 us, and the last tiles' way.
 #include <atomic>

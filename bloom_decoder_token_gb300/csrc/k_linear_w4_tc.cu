@@ -17,15 +17,15 @@
 //    the rows' scales to float32 sums in registers, as many groups a wait as half of the accumulators hold.
 //  * Few tiles of rows: the columns are split over a cluster, whose sums meet through
 //    distributed shared memory, in rank order.  Many: a CTA goes from tile to tile, and copies and
-//    products of the next one go on while the sums of the last are stored (250880 x 4096, 64 tokens: 312
-//    -> 262 us, 12 tokens: 143 -> 139).
+//    products of the next one go on while the sums of the last are stored (250880 x 4096, 64 tokens, groups of
+//    128: some 310 -> 262 us, 12 tokens, of 64: 143 -> 139).
 // Weights are loaded before the wait for the kernel before: that is the one that lays out
 // the tokens, and it starts its successors only after its own wait, when all work before it is done.
 // (Started at once, as the layer norms' successors are, this kernel's CTAs found the SMs partly taken: 12288
 // x 4096, 16 tokens, 15 -> 21 us.)
 //
 // 16 tokens, 12288 x 4096: 14.3 us (4.1 to read the weights); 32, 16384 x 4096, groups of 128 17.6 (5.4), of
-// 32 21; 64 25.8 (5.6); 12, 250880 x 4096 137 (83); 64 262 (84).  Bound by instructions: a block of 128 x
+// 32 21; 64 25.8 (5.6); 12, 250880 x 4096 137 (83); 64 in groups of 128 262 (84), of 64 346 (86).  Bound by instructions: a block of 128 x
 // 256 takes about 3000 warp instructions, 900 of them the codes', a third the scales' and most others waits
 // and their polling; and at 64 tokens by L2, which gives a block's tokens, 32 KB, beside 17 KB of weights.  Four
 // widening warps, two tiles each, against eight: 12 tokens, 250880 x 4096 154 -> 151; scales by two groups a

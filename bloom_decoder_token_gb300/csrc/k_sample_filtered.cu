@@ -14,10 +14,12 @@
 // exponent (max z - z) log2(e) / t is carried in two floats, or the rounding of 1 / t would
 // shift all far tokens the same way.
 //
-// The logits are read once from HBM (few rows) and then from L2: one row is bound by the latency of
-// its phases (1 x 250880: greedy 8 us, top-k 50 10.6, top-p 0.95 28), many by instructions, 60 % of the
-// issue slots (509 x 250880, 76 us from HBM: greedy 183, top-k 50 186, top-p 0.95 of normal logits 415:
-// some 70 instructions a logit).  One cluster of up to 16 CTAs a row, each a slice of the vocabulary:
+// Normal logits of deviation 2.5 at temperature 0.8.  A few rows are read once from HBM and then from L2,
+// bound by the latency of their phases (1 x 250880: greedy 7.6 us, top-k 50 10.4, min-p 0.05 or no filter
+// 11.9, top-p 0.95 30).  Of many rows more are under way than L2 holds, and every pass reads HBM (509 x
+// 250880, 76 us to read once): greedy 183 and top-k 50 185 us, two readings at 70 % of the DRAM's peak;
+// min-p 226, no filter 249, two; top-p 452, three, and bound by instructions too, some 70 a logit at 60 %
+// of the issue slots.  One cluster of up to 16 CTAs a row, each a slice of the vocabulary:
 //  1. the maximum and minimum, and every thread's own maximum;
 //  2. where few tokens can be kept, these come to the first CTA, which ranks them and does the
 //     rest: of the top 192, those that reach a bound from the maxima of groups of threads; the
